@@ -22,6 +22,7 @@ __all__ = [
     "LIB_PATH", "DwconvError", "abi_version",
     "dwconv1d_fwd", "dwconv1d_stream_fwd", "dwconv1d_bwd", "dwconv1d_bwd_workspace_bytes", "dwsub_fused_fwd", "dwsub_fused_bwd", "dwsub_fused_bwd_workspace_bytes",
     "dwconv2d_fwd", "dwconv2d_bwd", "dwconv2d_bwd_workspace_bytes", "dwconv2d_bwd_noalloc",
+    "dwnorm_fwd", "dwnorm_bwd", "dwnorm_bwd_workspace_bytes", "dwdrop_fwd", "dwdrop_bwd",
     "conv2d_out_shape", "CAUSAL_PADS_2D", "front_out_shape", "out_len",
 ]
 
@@ -46,6 +47,7 @@ if not os.path.exists(LIB_PATH):
         "(python conv_subsampling_amd/build.py, or __graft_entry__.build())")
 
 _vp, _i64, _sz, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 
 
 def _bind(path: str) -> ctypes.CDLL:
@@ -89,6 +91,16 @@ def _bind(path: str) -> ctypes.CDLL:
     lib.dwconv2d_bwd_ex.argtypes = [_vp] * 8 + [_sz] + [_i64] * 11 + [_int, _vp]
     lib.dwconv2d_bwd_noalloc.restype = _int
     lib.dwconv2d_bwd_noalloc.argtypes = [_vp] * 7 + [_i64] * 11 + [_int, _vp]
+    lib.dwdrop_fwd.restype = _int
+    lib.dwdrop_fwd.argtypes = [_vp] * 4 + [_i64] * 2 + [_f64, _f32, _int, _vp]
+    lib.dwdrop_bwd.restype = _int
+    lib.dwdrop_bwd.argtypes = [_vp] * 3 + [_i64] * 2 + [_f64, _f32, _int, _vp]
+    lib.dwnorm_fwd.restype = _int
+    lib.dwnorm_fwd.argtypes = [_vp] * 10 + [_i64] * 3 + [_f32, _f32, _f64, _int, _vp]
+    lib.dwnorm_bwd_workspace_bytes.restype = _sz
+    lib.dwnorm_bwd_workspace_bytes.argtypes = [_i64] * 3
+    lib.dwnorm_bwd.restype = _int
+    lib.dwnorm_bwd.argtypes = [_vp] * 13 + [_sz] + [_i64] * 3 + [_f32, _f64, _int, _vp]
     return lib
 
 
@@ -423,3 +435,132 @@ def dwconv2d_bwd_noalloc(x, w, lengths, dy, dx=None, dw=None, db=None, stride: i
     _check(_lib.dwconv2d_bwd_noalloc(_ptr(x), _ptr(w), _ptr(lengths), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
                                      B, T, F, C, KH, KW, stride, pt0, pt1, pf0, pf1, code, _stream(dev)))
     return dx, dw, db
+
+
+def _rng(rng, p, device):
+    """The dropout generator's state: int64 [2] (seed, stream) on the device."""
+    return _dev_tensor("rng", rng, torch.int64, device, (2,), allow_none=p == 0)
+
+
+def _rows(t):
+    """[rows, C] of a tensor whose last axis is the channels."""
+    if t.dim() < 1:
+        raise ValueError("dropout takes a tensor with a channel axis")
+    C = t.shape[-1]
+    rows = 1
+    for n in t.shape[:-1]:
+        rows *= n
+    return rows, C
+
+
+def dwdrop_fwd(x, rng, p: float, residual=None, alpha: float = 1.0, y=None):
+    """residual + alpha * dropout(x); x [..., C] (float32 or bfloat16).  rng is
+    an int64 tensor [2] on the device, (seed, stream), from which the mask
+    follows; it is never stored."""
+    dev = x.device
+    st, code = _storage(x)
+    _dev_tensor("x", x, st, dev)
+    _dev_tensor("residual", residual, st, dev, x.shape, allow_none=True)
+    if y is None:
+        y = torch.empty_like(x)
+    _dev_tensor("y", y, st, dev, x.shape)
+    rows, C = _rows(x)
+    _check(_lib.dwdrop_fwd(_ptr(x), _ptr(residual), _ptr(y), _ptr(_rng(rng, p, dev)), rows, C, p, alpha, code,
+                           _stream(dev)))
+    return y
+
+
+def dwdrop_bwd(dy, rng, p: float, alpha: float = 1.0, dx=None):
+    """dx of dwdrop_fwd given dy, with the forward's rng, p and alpha."""
+    dev = dy.device
+    st, code = _storage(dy)
+    _dev_tensor("dy", dy, st, dev)
+    if dx is None:
+        dx = torch.empty_like(dy)
+    _dev_tensor("dx", dx, st, dev, dy.shape)
+    rows, C = _rows(dy)
+    _check(_lib.dwdrop_bwd(_ptr(dy), _ptr(dx), _ptr(_rng(rng, p, dev)), rows, C, p, alpha, code, _stream(dev)))
+    return dx
+
+
+def dwnorm_fwd(x, gamma=None, beta=None, lengths=None, residual=None, rng=None, p: float = 0.0, alpha: float = 1.0,
+               eps: float = 1e-5, y=None, sum=None, mean=None, rstd=None, need=("y", "sum", "mean", "rstd")):
+    """Layer norm of s = residual + alpha * dropout(x) over the channels; x
+    [B,T,C].  Returns (y, s, mean, rstd): s in x's storage type (x itself where
+    there is neither a residual, a scale nor a dropout and no `sum` is given),
+    mean and rstd float32 [B,T].  s, mean and rstd not in `need` are skipped
+    (None)."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    dev, f32 = x.device, torch.float32
+    st, code = _storage(x)
+    B, T, C = x.shape
+    _dev_tensor("x", x, st, dev)
+    _dev_tensor("gamma", gamma, st, dev, (C,), allow_none=True)
+    _dev_tensor("beta", beta, st, dev, (C,), allow_none=True)
+    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
+    _dev_tensor("residual", residual, st, dev, (B, T, C), allow_none=True)
+    _rng(rng, p, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    plain = residual is None and p == 0 and alpha == 1.0 and sum is None
+    if sum is None and "sum" in need and not plain:
+        sum = torch.empty_like(x)
+    if mean is None and "mean" in need:
+        mean = torch.empty((B, T), dtype=f32, device=dev)
+    if rstd is None and "rstd" in need:
+        rstd = torch.empty((B, T), dtype=f32, device=dev)
+    _dev_tensor("y", y, st, dev, (B, T, C))
+    _dev_tensor("sum", sum, st, dev, (B, T, C), allow_none=True)
+    _dev_tensor("mean", mean, f32, dev, (B, T), allow_none=True)
+    _dev_tensor("rstd", rstd, f32, dev, (B, T), allow_none=True)
+    _check(_lib.dwnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(beta), _ptr(lengths), _ptr(rng), _ptr(y),
+                           _ptr(sum), _ptr(mean), _ptr(rstd), B, T, C, eps, alpha, p, code, _stream(dev)))
+    return y, x if plain and "sum" in need else sum, mean, rstd
+
+
+def dwnorm_bwd_workspace_bytes(B, T, C) -> int:
+    return int(_lib.dwnorm_bwd_workspace_bytes(B, T, C))
+
+
+def dwnorm_bwd(sum, gamma, lengths, mean, rstd, dy, dsum=None, rng=None, p: float = 0.0, alpha: float = 1.0, dx=None,
+               dres=None, dgamma=None, dbeta=None, workspace=None, need=("dx", "dres", "dgamma", "dbeta")):
+    """Gradients (dx, dres, dgamma, dbeta) of dwnorm_fwd given dy and, along
+    the residual, dsum; sum, mean and rstd are the forward's.  dx and dres are
+    in the storage type, dgamma and dbeta float32; those not in `need` are
+    skipped (None)."""
+    if sum.dim() != 3:
+        raise ValueError("sum must be [B, T, C]")
+    dev, f32 = sum.device, torch.float32
+    st, code = _storage(sum)
+    B, T, C = sum.shape
+    _dev_tensor("sum", sum, st, dev)
+    _dev_tensor("gamma", gamma, st, dev, (C,), allow_none=True)
+    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
+    _dev_tensor("mean", mean, f32, dev, (B, T))
+    _dev_tensor("rstd", rstd, f32, dev, (B, T))
+    _dev_tensor("dy", dy, st, dev, (B, T, C))
+    _dev_tensor("dsum", dsum, st, dev, (B, T, C), allow_none=True)
+    _rng(rng, p, dev)
+    if dx is None and "dx" in need:
+        dx = torch.empty_like(sum)
+    if dres is None and "dres" in need:
+        dres = torch.empty_like(sum)
+    if dgamma is None and "dgamma" in need:
+        dgamma = torch.empty((C,), dtype=f32, device=dev)
+    if dbeta is None and "dbeta" in need:
+        dbeta = torch.empty((C,), dtype=f32, device=dev)
+    _dev_tensor("dx", dx, st, dev, (B, T, C), allow_none=True)
+    _dev_tensor("dres", dres, st, dev, (B, T, C), allow_none=True)
+    _dev_tensor("dgamma", dgamma, f32, dev, (C,), allow_none=True)
+    _dev_tensor("dbeta", dbeta, f32, dev, (C,), allow_none=True)
+    ws_bytes = 0
+    if dgamma is not None or dbeta is not None:
+        if workspace is None:
+            workspace = torch.empty((max(dwnorm_bwd_workspace_bytes(B, T, C), 1),), dtype=torch.uint8, device=dev)
+        _dev_tensor("workspace", workspace, torch.uint8, dev)
+        ws_bytes = workspace.numel()
+    _check(_lib.dwnorm_bwd(_ptr(sum), _ptr(gamma), _ptr(lengths), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dsum),
+                           _ptr(rng), _ptr(dx), _ptr(dres), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), ws_bytes,
+                           B, T, C, alpha, p, code, _stream(dev)))
+    return dx, dres, dgamma, dbeta

@@ -77,6 +77,40 @@ dw_status check_pad(const char* fn, dw_pad pad) {
     return DW_OK;
 }
 
+dw_status check_dtype(const char* fn, dw_dtype dtype) {
+    if (dtype != DW_F32 && dtype != DW_BF16) return fail(DW_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
+    return DW_OK;
+}
+
+// A dropout probability, and the generator's state where it drops anything.
+dw_status check_dropout(const char* fn, double p, const uint64_t* rng) {
+    if (!(p >= 0.0 && p < 1.0))
+        return fail(DW_ERR_INVALID_ARG, "%s: dropout probability %g is not in [0, 1)", fn, p);
+    if (p > 0.0 && !rng) return fail(DW_ERR_INVALID_ARG, "%s: rng must not be NULL when p > 0", fn);
+    return DW_OK;
+}
+
+dw_status check_norm_sizes(const char* fn, int64_t B, int64_t T, int64_t C) {
+    if (B < 0 || T < 0 || C < 0) return fail(DW_ERR_INVALID_ARG, "%s: negative size", fn);
+    if (!dw::dwnorm_width_supported(C))
+        return fail(DW_ERR_UNSUPPORTED, "%s: rows of C=%lld columns have no kernel (at most 8192)", fn, (long long)C);
+    if (!extents_ok(B, T) || !dw::product_below(dw::kMaxExtent, {B, T})) return too_large(fn);
+    return DW_OK;
+}
+
+dw_status dropout(const char* fn, const void* x, const void* residual, void* y, const uint64_t* rng, int64_t rows,
+                  int64_t C, double p, float alpha, dw_dtype dtype, void* stream) {
+    if (rows < 0 || C < 0) return fail(DW_ERR_INVALID_ARG, "%s: negative size", fn);
+    dw_status s = check_dtype(fn, dtype);
+    if (s == DW_OK) s = check_dropout(fn, p, rng);
+    if (s != DW_OK) return s;
+    if (rows == 0 || C == 0) return ok();
+    if (!extents_ok(C) || !dw::dwdrop_fits(rows, C)) return too_large(fn);
+    if (!x || !y) return fail(DW_ERR_INVALID_ARG, "%s: the input and the output must not be NULL", fn);
+    return from_hip(dw::launch_dwdrop(x, residual, y, p > 0.0 ? rng : nullptr, rows, C, p, alpha, dtype == DW_BF16,
+                                      (hipStream_t)stream), fn);
+}
+
 }  // namespace
 
 extern "C" {
@@ -350,6 +384,63 @@ dw_status dwconv2d_bwd(const float* x, const float* w, const int32_t* lengths, c
                        void* stream) {
     return dwconv2d_bwd_ex(x, w, lengths, dy, dx, dw_, db, workspace, workspace_bytes, B, T, F, C, KH, KW, stride,
                            pad, pad, pad, pad, DW_F32, stream);
+}
+
+dw_status dwdrop_fwd(const void* x, const void* residual, void* y, const uint64_t* rng, int64_t rows, int64_t C,
+                     double p, float alpha, dw_dtype dtype, void* stream) {
+    return dropout("dwdrop_fwd", x, residual, y, rng, rows, C, p, alpha, dtype, stream);
+}
+
+dw_status dwdrop_bwd(const void* dy, void* dx, const uint64_t* rng, int64_t rows, int64_t C, double p, float alpha,
+                     dw_dtype dtype, void* stream) {
+    return dropout("dwdrop_bwd", dy, nullptr, dx, rng, rows, C, p, alpha, dtype, stream);
+}
+
+dw_status dwnorm_fwd(const void* x, const void* residual, const void* gamma, const void* beta, const int32_t* lengths,
+                     const uint64_t* rng, void* y, void* sum, float* mean, float* rstd, int64_t B, int64_t T,
+                     int64_t C, float eps, float alpha, double p, dw_dtype dtype, void* stream) {
+    const char* fn = "dwnorm_fwd";
+    dw_status s = check_norm_sizes(fn, B, T, C);
+    if (s == DW_OK) s = check_dtype(fn, dtype);
+    if (s == DW_OK) s = check_dropout(fn, p, rng);
+    if (s != DW_OK) return s;
+    if (!(eps >= 0.0f)) return fail(DW_ERR_INVALID_ARG, "%s: eps must not be negative", fn);
+    if (B == 0 || T == 0 || C == 0) return ok();
+    if (!x || !y) return fail(DW_ERR_INVALID_ARG, "%s: x and y must not be NULL", fn);
+    if (y == sum) return fail(DW_ERR_INVALID_ARG, "%s: y must not alias sum", fn);
+    return from_hip(dw::launch_dwnorm_fwd(x, residual, gamma, beta, lengths, p > 0.0 ? rng : nullptr, y, sum, mean,
+                                          rstd, B, T, C, eps, alpha, p, dtype == DW_BF16, (hipStream_t)stream), fn);
+}
+
+size_t dwnorm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C) {
+    if (B < 0 || T < 0 || C < 0 || !dw::dwnorm_width_supported(C)) return 0;
+    if (!extents_ok(B, T) || !dw::product_below(dw::kMaxExtent, {B, T})) return 0;
+    return dw::dwnorm_bwd_workspace(B, T, C);
+}
+
+dw_status dwnorm_bwd(const void* sum, const void* gamma, const int32_t* lengths, const float* mean, const float* rstd,
+                     const void* dy, const void* dsum, const uint64_t* rng, void* dx, void* dres, float* dgamma,
+                     float* dbeta, void* workspace, size_t workspace_bytes, int64_t B, int64_t T, int64_t C,
+                     float alpha, double p, dw_dtype dtype, void* stream) {
+    const char* fn = "dwnorm_bwd";
+    dw_status s = check_norm_sizes(fn, B, T, C);
+    if (s == DW_OK) s = check_dtype(fn, dtype);
+    if (s == DW_OK) s = check_dropout(fn, p, rng);
+    if (s != DW_OK) return s;
+    const bool params = dgamma || dbeta;
+    if ((!dx && !dres && !params) || C == 0) return ok();
+    if (nonempty(B, T) && (!sum || !mean || !rstd || !dy))
+        return fail(DW_ERR_INVALID_ARG, "%s: sum, mean, rstd and dy must not be NULL (unless empty)", fn);
+    if (dx && dx == dres) return fail(DW_ERR_INVALID_ARG, "%s: dx must not alias dres", fn);
+    if (params) {
+        const size_t need = dw::dwnorm_bwd_workspace(B, T, C);
+        if (need && (!workspace || workspace_bytes < need))
+            return fail(DW_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
+                        workspace ? workspace_bytes : (size_t)0, need);
+    }
+    return from_hip(dw::launch_dwnorm_bwd(sum, gamma, lengths, mean, rstd, dy, dsum, p > 0.0 ? rng : nullptr, dx, dres,
+                                          dgamma, dbeta, workspace, B, T, C, alpha, p, dtype == DW_BF16,
+                                          (hipStream_t)stream), fn);
 }
 
 }  // extern "C"

@@ -123,4 +123,20 @@ hipError_t launch_dwconv2d_bwd(const void* x, const void* w, const int32_t* leng
                                float* dw, float* db, void* workspace, int64_t B, const Conv2dGeom& g, bool bf16,
                                int vec, hipStream_t stream);
 
+// Layer norm with the residual add and dropout in front of it, and dropout
+// alone.  rng is NULL where nothing is dropped.
+bool dwnorm_width_supported(int64_t C);
+hipError_t launch_dwnorm_fwd(const void* x, const void* residual, const void* gamma, const void* beta,
+                             const int32_t* lengths, const uint64_t* rng, void* y, void* sum, float* mean,
+                             float* rstd, int64_t B, int64_t T, int64_t C, float eps, float alpha, double p, bool bf16,
+                             hipStream_t stream);
+size_t dwnorm_bwd_workspace(int64_t B, int64_t T, int64_t C);
+hipError_t launch_dwnorm_bwd(const void* s, const void* gamma, const int32_t* lengths, const float* mean,
+                             const float* rstd, const void* dy, const void* dsum, const uint64_t* rng, void* dx,
+                             void* dres, float* dgamma, float* dbeta, void* workspace, int64_t B, int64_t T, int64_t C,
+                             float alpha, double p, bool bf16, hipStream_t stream);
+bool dwdrop_fits(int64_t rows, int64_t C);
+hipError_t launch_dwdrop(const void* x, const void* residual, void* y, const uint64_t* rng, int64_t rows, int64_t C,
+                         double p, float alpha, bool bf16, hipStream_t stream);
+
 }  // namespace dw

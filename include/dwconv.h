@@ -414,6 +414,97 @@ dw_status dwconv2d_bwd_noalloc(const void *x, const void *w, const int32_t *leng
                                int64_t KW, int64_t stride, int64_t pad_t0, int64_t pad_t1, int64_t pad_f0,
                                int64_t pad_f1, dw_dtype dtype, void *stream);
 
+/*
+ * Dropout: which elements stay.
+ *
+ * The entry points that drop elements take a probability p in [0, 1) and the
+ * generator's state rng, two uint64 in DEVICE memory: rng[0] the seed, rng[1]
+ * a stream number (one for each use: a call site, a training step).  A
+ * captured HIP graph reads them anew on every replay.  No mask is stored: the
+ * backward call gives the same two numbers and sees the same mask.
+ * For element (row, c) of a tensor of rows of C elements, let (w0, w1, w2, w3)
+ * be Philox4x32-10 with key rng[0] and the 128-bit counter whose low 64 bits
+ * are row * ceil(C / 8) + floor(c / 8) and whose high 64 bits are rng[1]
+ * (low 32-bit words first), and u the half word c mod 8 of those 128 bits (the
+ * low half of w0 first).  The element stays if u >= n, where
+ * n = min(65535, floor(65536 p + 1/2)), and is then scaled by
+ * 65536 / (65536 - n).  p is thus resolved to 1/65536, and the scale is that
+ * of the resolved p.  The mask depends on neither the storage type nor the
+ * launch.  rng may be NULL when p = 0.
+ */
+
+/*
+ * dwdrop_fwd -- dropout of x, scaled and added to a residual:
+ *   y[r, c] = residual[r, c] + alpha * drop(x)[r, c]
+ * x, residual (or NULL), y: [rows][C] in the storage type dtype.  The products
+ * and the sum are float32, rounded once.  y may be x or residual (in place);
+ * other overlaps race.
+ * Errors: DW_ERR_INVALID_ARG for a null x or y, a negative size, a bad dtype,
+ * p outside [0, 1) or a null rng with p > 0.
+ */
+dw_status dwdrop_fwd(const void *x, const void *residual, void *y, const uint64_t *rng, int64_t rows, int64_t C,
+                     double p, float alpha, dw_dtype dtype, void *stream);
+
+/*
+ * dwdrop_bwd -- the gradient of dwdrop_fwd with respect to x:
+ * dx = alpha * drop(dy) with the forward's rng, p and alpha (the residual's
+ * gradient is dy itself).  Layout and errors as dwdrop_fwd; dx may be dy.
+ */
+dw_status dwdrop_bwd(const void *dy, void *dx, const uint64_t *rng, int64_t rows, int64_t C, double p, float alpha,
+                     dw_dtype dtype, void *stream);
+
+/*
+ * dwnorm_fwd -- layer norm over the channels, with the residual add and the
+ * dropout of a pre-norm encoder block in front of it.  For each frame of
+ * [B][T] with t < len_b:
+ *   s[c]  = residual[c] + alpha * drop(x)[c]      (drop: row b * T + t)
+ *   mean  = sum_c s[c] / C,  rstd = 1 / sqrt(sum_c (s[c] - mean)^2 / C + eps)
+ *   y[c]  = (s[c] - mean) * rstd * gamma[c] + beta[c]
+ * Frames t >= len_b: s = y = 0, mean = rstd = 0, and their inputs are not read.
+ * A NULL residual is zero, a NULL gamma one, a NULL beta zero.  With
+ * residual NULL, alpha = 1 and p = 0 this is a plain layer norm, and s is x.
+ *
+ * x, residual, y, sum: [B][T][C]; gamma, beta: [C]; all in the storage type
+ * dtype.  mean, rstd: [B][T] float.  sum (which receives s), mean and rstd may
+ * be NULL (not written).  Everything is carried in float32; the statistics and
+ * y are those of the unrounded s, in two passes over registers.  In place:
+ * each of y and sum may be x or residual; y must not be sum.
+ * Errors: DW_ERR_UNSUPPORTED for C > 8192; DW_ERR_INVALID_ARG for a null x or
+ * y, a negative size or eps, a bad dtype, p outside [0, 1), a null rng with
+ * p > 0, or y == sum.
+ */
+dw_status dwnorm_fwd(const void *x, const void *residual, const void *gamma, const void *beta, const int32_t *lengths,
+                     const uint64_t *rng, void *y, void *sum, float *mean, float *rstd, int64_t B, int64_t T,
+                     int64_t C, float eps, float alpha, double p, dw_dtype dtype, void *stream);
+
+/* Bytes of device workspace dwnorm_bwd needs when it computes dgamma or dbeta
+ * (0 for an empty batch, and for sizes that the call refuses). */
+size_t dwnorm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C);
+
+/*
+ * dwnorm_bwd -- gradients of dwnorm_fwd.  sum, mean and rstd are what the
+ * forward wrote (sum is x itself for a plain layer norm); dy is the gradient of
+ * y and dsum (or NULL: zero) that of s along the residual stream.  For frames
+ * t < len_b, with xh = (s - mean) * rstd and g = dy * gamma:
+ *   ds[c]     = dsum[c] + rstd * (g[c] - sum(g)/C - xh[c] * sum(g xh)/C)
+ *   dres[c]   = ds[c]
+ *   dx[c]     = alpha * drop(ds)[c]               (the forward's rng and p)
+ *   dgamma[c] = sum_{b,t} dy[c] * xh[c],  dbeta[c] = sum_{b,t} dy[c]
+ * and dx = dres = 0 at frames t >= len_b, whose inputs are not read.  dgamma
+ * and dbeta are float, added in a fixed order (float32 over each workgroup's
+ * frames, fp64 across workgroups), so repeated calls agree bit for bit.
+ * dx, dres ([B][T][C], dtype), dgamma, dbeta ([C]) may be NULL (not computed).
+ * In place: each of dx and dres may be sum, dy or dsum; dx must not be dres.
+ * An empty batch still writes dgamma = dbeta = 0.
+ * Errors: as dwnorm_fwd, DW_ERR_INVALID_ARG for a null sum, mean, rstd or dy
+ * that holds elements or dx == dres, and DW_ERR_WORKSPACE for a missing or
+ * short workspace.
+ */
+dw_status dwnorm_bwd(const void *sum, const void *gamma, const int32_t *lengths, const float *mean, const float *rstd,
+                     const void *dy, const void *dsum, const uint64_t *rng, void *dx, void *dres, float *dgamma,
+                     float *dbeta, void *workspace, size_t workspace_bytes, int64_t B, int64_t T, int64_t C,
+                     float alpha, double p, dw_dtype dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
