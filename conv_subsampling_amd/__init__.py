@@ -22,6 +22,7 @@ __all__ = [
     "LIB_PATH", "DwconvError", "abi_version",
     "dwconv1d_fwd", "dwconv1d_stream_fwd", "dwconv1d_bwd", "dwconv1d_bwd_workspace_bytes", "dwsub_fused_fwd", "dwsub_fused_bwd", "dwsub_fused_bwd_workspace_bytes",
     "dwconv2d_fwd", "dwconv2d_bwd", "dwconv2d_bwd_workspace_bytes", "dwconv2d_bwd_noalloc",
+    "dwattn_fwd", "dwattn_fwd_workspace_bytes", "rel_buckets",
     "dwnorm_fwd", "dwnorm_bwd", "dwnorm_bwd_workspace_bytes", "dwdrop_fwd", "dwdrop_bwd",
     "conv2d_out_shape", "CAUSAL_PADS_2D", "front_out_shape", "out_len",
 ]
@@ -48,6 +49,16 @@ if not os.path.exists(LIB_PATH):
 
 _vp, _i64, _sz, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
 _f32, _f64 = ctypes.c_float, ctypes.c_double
+
+
+class _Strides(ctypes.Structure):
+    _fields_ = [("item", _i64), ("frame", _i64), ("head", _i64)]
+
+
+class _Attn(ctypes.Structure):
+    _fields_ = ([(n, _i64) for n in ("B", "Tq", "Tk", "H", "Hkv", "D")] +
+                [(n, _Strides) for n in ("q", "k", "v", "dq", "dk", "dv")] +
+                [(n, _i64) for n in ("buckets", "reach", "left", "right")] + [("scale", _f32), ("dtype", _int)])
 
 
 def _bind(path: str) -> ctypes.CDLL:
@@ -101,6 +112,13 @@ def _bind(path: str) -> ctypes.CDLL:
     lib.dwnorm_bwd_workspace_bytes.argtypes = [_i64] * 3
     lib.dwnorm_bwd.restype = _int
     lib.dwnorm_bwd.argtypes = [_vp] * 13 + [_sz] + [_i64] * 3 + [_f32, _f64, _int, _vp]
+    attn = ctypes.POINTER(_Attn)
+    lib.dwattn_rel_buckets.restype = _int
+    lib.dwattn_rel_buckets.argtypes = [_vp, _i64, _i64, _int]
+    lib.dwattn_fwd_workspace_bytes.restype = _sz
+    lib.dwattn_fwd_workspace_bytes.argtypes = [attn]
+    lib.dwattn_fwd.restype = _int
+    lib.dwattn_fwd.argtypes = [attn] + [_vp] * 11 + [_sz, _vp]
     return lib
 
 
@@ -564,3 +582,93 @@ def dwnorm_bwd(sum, gamma, lengths, mean, rstd, dy, dsum=None, rng=None, p: floa
                            _ptr(rng), _ptr(dx), _ptr(dres), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), ws_bytes,
                            B, T, C, alpha, p, code, _stream(dev)))
     return dx, dres, dgamma, dbeta
+
+
+def rel_buckets(num_buckets: int, reach: int, bidirectional: bool = True, device="cuda"):
+    """The usual map of relative positions to buckets for `dwattn_fwd`: int32
+    [2 * reach + 1], entry r + reach the bucket of a key r frames after its
+    query.  One distance a bucket up to a quarter of `num_buckets` (half of
+    them, in one direction), then equal ratios up to `reach`."""
+    if reach < 0 or reach > 1 << 20:
+        raise ValueError("reach must be between 1 and 1024")
+    m = torch.empty((2 * reach + 1,), dtype=torch.int32)
+    _check(_lib.dwattn_rel_buckets(_ptr(m), num_buckets, reach, int(bool(bidirectional))))
+    return m.to(device)
+
+
+def _heads(name, t, st, device, shape):
+    """A [B, frames, heads, D] tensor whose head elements lie next to each other."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != st:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {st}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name} must have the elements of a head next to each other")
+    return t
+
+
+def _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, right, scale):
+    """The problem's sizes for the C ABI, its tensors checked; and its storage type."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, Tq, H, D], k and v [B, Tk, Hkv, D]")
+    dev = q.device
+    st, code = _storage(q)
+    B, Tq, H, D = q.shape
+    Tk, Hkv = k.shape[1], k.shape[2]
+    _heads("q", q, st, dev, q.shape)
+    _heads("k", k, st, dev, (B, Tk, Hkv, D))
+    _heads("v", v, st, dev, (B, Tk, Hkv, D))
+    if (table is None) != (buckets is None):
+        raise ValueError("a bias needs both its table and its buckets")
+    NB = reach = 0
+    if table is not None:
+        if table.dim() != 2 or table.shape[1] != H:
+            raise ValueError("table must be [num_buckets, H]")
+        if buckets.dim() != 1 or buckets.shape[0] % 2 == 0:
+            raise ValueError("buckets must be [2 * reach + 1]")
+        _dev_tensor("table", table, st, dev)
+        _dev_tensor("buckets", buckets, torch.int32, dev)
+        NB, reach = table.shape[0], buckets.shape[0] // 2
+    for name, t in (("q_lengths", q_lengths), ("k_lengths", k_lengths), ("q_pos", q_pos)):
+        _dev_tensor(name, t, torch.int32, dev, (B,), allow_none=True)
+    strides = [_Strides(*t.stride()[:3]) for t in (q, k, v)]
+    return _Attn(B, Tq, Tk, H, Hkv, D, *strides, buckets=NB, reach=reach, left=left, right=right,
+                 scale=D ** -0.5 if scale is None else scale, dtype=code), st
+
+
+def dwattn_fwd_workspace_bytes(q, k, v, left: int = -1, right: int = -1) -> int:
+    """Bytes of workspace `dwattn_fwd` takes for tensors of these sizes."""
+    return int(_lib.dwattn_fwd_workspace_bytes(_attn_shape(q, k, v, None, None, None, None, None, left, right, None)[0]))
+
+
+def dwattn_fwd(q, k, v, table=None, buckets=None, q_lengths=None, k_lengths=None, q_pos=None, left: int = -1,
+               right: int = -1, scale=None, out=None, lse=None, workspace=None, need=("out", "lse")):
+    """Softmax attention with a learned relative position bias: q [B,Tq,H,D],
+    k, v [B,Tk,Hkv,D] (float32 or bfloat16, any strides above the last), table
+    [num_buckets,H], buckets int32 [2*reach+1] (see `rel_buckets`).  q_pos
+    int32 [B] places query 0 on the key axis (the cached frames before a
+    streaming chunk); left and right limit the context, negative for all of
+    it.  Returns (out [B,Tq,H,D], lse float32 [B,H,Tq] or None if not in
+    `need`); queries without a key give 0 and -inf."""
+    shape, st = _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, right, scale)
+    dev = q.device
+    B, Tq, H, D = q.shape
+    if out is None:
+        out = torch.empty((B, Tq, H, D), dtype=st, device=dev)
+    if lse is None and "lse" in need:
+        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=dev)
+    _dev_tensor("out", out, st, dev, (B, Tq, H, D))
+    _dev_tensor("lse", lse, torch.float32, dev, (B, H, Tq), allow_none=True)
+    if workspace is None:
+        need_ws = int(_lib.dwattn_fwd_workspace_bytes(shape))
+        if need_ws:
+            workspace = torch.empty((need_ws,), dtype=torch.uint8, device=dev)
+    _dev_tensor("workspace", workspace, torch.uint8, dev, allow_none=True)
+    _check(_lib.dwattn_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(table), _ptr(buckets), _ptr(q_lengths),
+                           _ptr(k_lengths), _ptr(q_pos), _ptr(out), _ptr(lse), _ptr(workspace),
+                           0 if workspace is None else workspace.numel(), _stream(dev)))
+    return out, lse

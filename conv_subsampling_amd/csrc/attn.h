@@ -1,0 +1,296 @@
+// Shared pieces of the attention kernels (forward, gradients): arguments,
+// matrix fragments, tiles in LDS, the relative position bias and the masks.
+//
+// Every product runs on 32x32 matrix instructions with the OWNED axis (the
+// queries in the forward and in dq, the keys in dk and dv) in the columns, so
+// that a lane holds one row of the softmax and its neighbour 32 lanes away the
+// rest of it:
+//   columns: owned index lane % 32
+//   rows:    streamed index 8 * (r / 4) + 4 * (lane / 32) + r % 4 of register r
+// The next product contracts over those rows.  A contraction may take its
+// index in any order as long as both operands agree, so the probabilities go
+// from the accumulator registers straight into the next instruction's operand,
+// and it is the other operand that is read from LDS in that order (transposed).
+#pragma once
+
+#include "launch.h"
+#include "rowops.h"
+
+#include <type_traits>
+
+namespace dw {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kAttnThreads = 256;
+constexpr int kTile = 32;          // owned and streamed frames of one matrix tile
+constexpr int kBiasMargin = 64;    // entries beyond the map's ends: a tile that touches it reads without a clamp
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+// The 16-deep operand of one 32x32 product: 8 values a lane, of the streamed
+// depth 8 * (lane / 32) + e.
+template <typename S>
+struct Frag;
+template <>
+struct Frag<uint16_t> {
+    u32x4 r;
+};
+template <>
+struct Frag<float> {
+    f32x4 r[2];
+};
+
+__device__ __forceinline__ f32x16 mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.r), __builtin_bit_cast(bf16x8, b.r),
+                                                   c, 0, 0, 0);
+}
+
+// float32 keeps its 24 bits: eight 2-deep products, the e-th of which pairs
+// depths e and 8 + e.
+__device__ __forceinline__ f32x16 mma(const Frag<float>& a, const Frag<float>& b, f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.r[e / 4][e % 4], b.r[e / 4][e % 4], c, 0, 0, 0);
+    return c;
+}
+
+// Accumulator registers 8k .. 8k + 7 as the operand of the next product,
+// rounded to the storage type (bf16: the matrix instruction takes no wider
+// operand; the sums of a softmax are taken before the rounding).
+template <typename S>
+__device__ __forceinline__ Frag<S> to_frag(const f32x16& c, int k) {
+    Frag<S> f;
+    if constexpr (sizeof(S) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.r[e / 4][e % 4] = c[8 * k + e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.r[e] = pack_bf16x2(c[8 * k + 2 * e], c[8 * k + 2 * e + 1]);
+    }
+    return f;
+}
+
+template <typename S>
+__device__ __forceinline__ Frag<S> to_frag(const RawGroup<S>& g) {
+    Frag<S> f;
+    if constexpr (sizeof(S) == 4) {
+        f.r[0] = __builtin_bit_cast(f32x4, g.r[0]);
+        f.r[1] = __builtin_bit_cast(f32x4, g.r[1]);
+    } else {
+        f.r = g.r[0];
+    }
+    return f;
+}
+
+// ---------------------------------------------------------------------------
+// A tile of ROWS frames x DP head elements in LDS, each row followed by a pad
+// that puts neighbouring rows on other banks.
+// ---------------------------------------------------------------------------
+template <typename S, int DP>
+struct Tile {
+    static constexpr int kPad = (sizeof(S) == 2 ? 32 : 16) / (int)sizeof(S);
+    static constexpr int kStride = DP + kPad;
+    static constexpr int kGroups = DP / kGroup;  // 8-element groups of a row
+
+    static constexpr int bytes(int rows) { return rows * kStride * (int)sizeof(S); }
+
+    // Operand whose rows are frames row0 + lane % 32 and whose depth is the
+    // 16 head elements from 16 * c.
+    static __device__ __forceinline__ Frag<S> rows(const S* t, int row0, int c, int lane) {
+        const S* p = t + (row0 + lane % 32) * kStride + 16 * c + 8 * (lane / 32);
+        Frag<S> f;
+        if constexpr (sizeof(S) == 4) {
+            f.r[0] = *reinterpret_cast<const f32x4*>(p);
+            f.r[1] = *reinterpret_cast<const f32x4*>(p + 4);
+        } else {
+            f.r = *reinterpret_cast<const u32x4*>(p);
+        }
+        return f;
+    }
+
+    // Operand whose rows are head elements 32 * d + lane % 32 and whose depth
+    // is the 16 frames from row0, in the order of the accumulator's registers:
+    // frames 4 * (lane / 32) + e, then 8 + 4 * (lane / 32) + e - 4.  bf16: one
+    // transposing read brings lane i of 16 the i-th column of four rows, whose
+    // 4-element pieces the 16 lanes address.
+    static __device__ __forceinline__ Frag<S> columns(const S* t, int row0, int d, int lane) {
+        Frag<S> f;
+        if constexpr (sizeof(S) == 4) {
+            const S* p = t + (row0 + 4 * (lane / 32)) * kStride + 32 * d + lane % 32;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f.r[e / 4][e % 4] = p[((e / 4) * 8 + e % 4) * kStride];
+        } else {
+            const S* p = t + (row0 + 4 * (lane / 32) + lane % 16 / 4) * kStride + 32 * d + 16 * (lane / 16 % 2) +
+                         4 * (lane % 4);
+            typedef __attribute__((address_space(3))) s16x4* lds;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p + 8 * kStride));
+            const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+            f.r = u32x4{a.x, a.y, b.x, b.y};
+        }
+        return f;
+    }
+};
+
+// A workgroup's share of a tile on its way from memory to LDS.  Rows from
+// `live` on and head elements from D on become zero and are not read.
+template <typename S, int DP, int ROWS>
+struct TileLoad {
+    static constexpr int N = ROWS * Tile<S, DP>::kGroups / kAttnThreads;
+    static_assert(ROWS * Tile<S, DP>::kGroups % kAttnThreads == 0, "every thread takes the same number of groups");
+    RawGroup<S> g[N];
+
+    __device__ __forceinline__ void load(const S* base, int64_t stride, int live, int D) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int at = threadIdx.x + n * kAttnThreads;
+            const int row = at / Tile<S, DP>::kGroups, col = at % Tile<S, DP>::kGroups * kGroup;
+            g[n] = load_group<S, true>(base + row * stride, col, row < live ? D : 0);
+        }
+    }
+
+    __device__ __forceinline__ void store(S* tile) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int at = threadIdx.x + n * kAttnThreads;
+            const int row = at / Tile<S, DP>::kGroups, col = at % Tile<S, DP>::kGroups * kGroup;
+            u32x4* p = reinterpret_cast<u32x4*>(tile + row * Tile<S, DP>::kStride + col);
+#pragma unroll
+            for (int i = 0; i < RawGroup<S>::N; ++i) p[i] = g[n].r[i];
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Arguments
+// ---------------------------------------------------------------------------
+struct AttnArgs {
+    const void *q, *k, *v, *table;
+    const int32_t *buckets, *q_lengths, *k_lengths, *q_pos;
+    AttnStride qs, ks, vs;
+    int32_t B, Tq, Tk, H, Hkv, D;
+    int32_t NB, R;         // buckets of the table, reach of the map
+    int32_t left, right;   // kNoLimit: none
+    float scale, scale2;   // of the scores, and times log2(e)
+};
+
+inline AttnArgs attn_args(const AttnPtrs& p, const AttnShape& s) {
+    AttnArgs a;
+    a.q = p.q, a.k = p.k, a.v = p.v, a.table = p.table;
+    a.buckets = p.buckets, a.q_lengths = p.q_lengths, a.k_lengths = p.k_lengths, a.q_pos = p.q_pos;
+    a.qs = s.q, a.ks = s.k, a.vs = s.v;
+    a.B = (int32_t)s.B, a.Tq = (int32_t)s.Tq, a.Tk = (int32_t)s.Tk;
+    a.H = (int32_t)s.H, a.Hkv = (int32_t)s.Hkv, a.D = (int32_t)s.D;
+    a.NB = (int32_t)s.buckets, a.R = (int32_t)s.reach;
+    a.left = (int32_t)s.left, a.right = (int32_t)s.right;
+    a.scale = s.scale, a.scale2 = s.scale * kLog2e;
+    return a;
+}
+
+// Calls f with the padded head width that holds D.
+template <typename F>
+hipError_t with_head_width(int64_t D, F&& f) {
+    if (D <= 32) return f(std::integral_constant<int, 32>());
+    if (D <= 64) return f(std::integral_constant<int, 64>());
+    if (D <= 96) return f(std::integral_constant<int, 96>());
+    return f(std::integral_constant<int, 128>());
+}
+
+// One item's valid frames and the position of its first query on the key axis.
+struct AttnItem {
+    int32_t nq, nk;
+    int64_t pos;
+    int32_t pos32;  // pos where it can matter: beyond, every distance is past the map's reach on the same side
+
+    __device__ __forceinline__ AttnItem(const AttnArgs& a, int b)
+        : nq((int32_t)item_length(a.q_lengths, b, a.Tq)), nk((int32_t)item_length(a.k_lengths, b, a.Tk)),
+          pos(a.q_pos ? a.q_pos[b] : 0) {
+        const int64_t far = (int64_t)1 << 29;
+        pos32 = (int32_t)(pos < -far ? -far : pos > far ? far : pos);
+    }
+
+    // Keys [first, last] that queries i0 .. i1 may see between them.
+    __device__ __forceinline__ int32_t first_key(const AttnArgs& a, int32_t i0) const {
+        const int64_t j = a.left == kNoLimit ? 0 : i0 + pos - a.left;
+        return (int32_t)(j < 0 ? 0 : j > nk ? nk : j);
+    }
+    __device__ __forceinline__ int32_t last_key(const AttnArgs& a, int32_t i1) const {
+        const int64_t j = a.right == kNoLimit ? nk - 1 : i1 + pos + a.right;
+        return (int32_t)(j < -1 ? -1 : j > nk - 1 ? nk - 1 : j);
+    }
+    // Queries [first, last] that see a key of j0 .. j1.
+    __device__ __forceinline__ int32_t first_query(const AttnArgs& a, int32_t j0) const {
+        const int64_t i = a.right == kNoLimit ? 0 : j0 - pos - a.right;
+        return (int32_t)(i < 0 ? 0 : i > nq ? nq : i);
+    }
+    __device__ __forceinline__ int32_t last_query(const AttnArgs& a, int32_t j1) const {
+        const int64_t i = a.left == kNoLimit ? nq - 1 : j1 - pos + a.left;
+        return (int32_t)(i < -1 ? -1 : i > nq - 1 ? nq - 1 : i);
+    }
+};
+
+// The head's bias for every distance -R .. R in units of log2, with the ends
+// repeated kBiasMargin times on both sides.  A table may hold its type's lowest
+// value: times log2(e) that must stay a number, so that rows which hold nothing
+// else still weigh their keys alike.  Bucket numbers are held to the table.
+template <typename S>
+__device__ __forceinline__ void fill_bias(const AttnArgs& a, int h, float* bias) {
+    const int n = 2 * a.R + 1 + 2 * kBiasMargin;
+    for (int x = threadIdx.x; x < n; x += kAttnThreads) {
+        int rel = x - kBiasMargin;
+        rel = rel < 0 ? 0 : rel > 2 * a.R ? 2 * a.R : rel;
+        int bucket = a.buckets[rel];
+        bucket = bucket < 0 ? 0 : bucket >= a.NB ? a.NB - 1 : bucket;
+        const float t = to_f32(((const S*)a.table)[(int64_t)bucket * a.H + h]);
+        const float v = t * kLog2e, lowest = -3.0e38f;
+        bias[x] = v < lowest && t > -__builtin_inff() ? lowest : v;
+    }
+}
+
+inline int attn_bias_bytes(int32_t R) { return (2 * R + 1 + 2 * kBiasMargin) * 4; }
+
+// The distance key - query of a tile's first key and first query says what the
+// tile's bias is: past the map's reach on either side one value, else looked up.
+enum class Span { kLow, kNear, kHigh };
+__device__ __forceinline__ Span span_of(int base, int R) {
+    return base + (kTile - 1) <= -R ? Span::kLow : base - (kTile - 1) >= R ? Span::kHigh : Span::kNear;
+}
+
+__device__ __forceinline__ float swap_halves(float v) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(threadIdx.x & 32 ? s[0] : s[1]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Row of register r of a 32x32 accumulator in lanes of half h.
+__device__ __forceinline__ constexpr int acc_row(int r, int half) { return 8 * (r / 4) + 4 * half + r % 4; }
+
+// Four neighbouring head elements d .. d + 3 of one frame.
+template <typename S>
+__device__ __forceinline__ void store4(S* row, int d, int D, float v0, float v1, float v2, float v3) {
+    const float v[4] = {v0, v1, v2, v3};
+    if (d + 4 <= D) {
+        if constexpr (sizeof(S) == 4) {
+            typedef f32x4 vec __attribute__((aligned(4)));
+            *reinterpret_cast<vec*>(row + d) = f32x4{v0, v1, v2, v3};
+        } else {
+            typedef u32x2 vec __attribute__((aligned(2)));
+            *reinterpret_cast<vec*>(row + d) = u32x2{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            if (d + e < D) {
+                if constexpr (sizeof(S) == 4)
+                    row[d + e] = v[e];
+                else
+                    row[d + e] = (uint16_t)bf16_bits_rne(v[e]);
+            }
+        }
+    }
+}
+
+}  // namespace dw

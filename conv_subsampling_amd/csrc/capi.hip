@@ -1,6 +1,7 @@
 // The library's C ABI (declared in include/dwconv.h): host-side argument
 // validation, the thread-local error message, and dispatch to the kernel
 // launchers.  Nothing here allocates, frees or synchronises.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -109,6 +110,72 @@ dw_status dropout(const char* fn, const void* x, const void* residual, void* y, 
     if (!x || !y) return fail(DW_ERR_INVALID_ARG, "%s: the input and the output must not be NULL", fn);
     return from_hip(dw::launch_dwdrop(x, residual, y, p > 0.0 ? rng : nullptr, rows, C, p, alpha, dtype == DW_BF16,
                                       (hipStream_t)stream), fn);
+}
+
+bool strides_ok(const dw_strides& s) { return s.item >= 0 && s.frame >= 0 && s.head >= 0; }
+
+dw::AttnStride stride_of(const dw_strides& s) { return {s.item, s.frame, s.head}; }
+
+// Offsets inside [n items][t frames][h heads] stay far below 2^63.
+bool strides_fit(const dw_strides& s, int64_t n, int64_t t, int64_t h) {
+    const int64_t far = (int64_t)1 << 58;
+    return dw::product_below(far, {n, s.item}) && dw::product_below(far, {t + 256, s.frame}) &&
+           dw::product_below(far, {h, s.head});
+}
+
+// The problem as the launchers take it.
+dw_status check_attn(const char* fn, const dw_attn* a, bool bias, dw::AttnShape* s) {
+    if (!a) return fail(DW_ERR_INVALID_ARG, "%s: shape must not be NULL", fn);
+    if (a->B < 0 || a->Tq < 0 || a->Tk < 0 || a->H < 0 || a->Hkv < 0 || a->D < 0)
+        return fail(DW_ERR_INVALID_ARG, "%s: negative size", fn);
+    if (!strides_ok(a->q) || !strides_ok(a->k) || !strides_ok(a->v))
+        return fail(DW_ERR_INVALID_ARG, "%s: negative stride", fn);
+    const dw_status t = check_dtype(fn, a->dtype);
+    if (t != DW_OK) return t;
+    if (a->H > 0 && (a->Hkv < 1 || a->H % a->Hkv != 0))
+        return fail(DW_ERR_INVALID_ARG, "%s: H=%lld is not a multiple of Hkv=%lld", fn, (long long)a->H, (long long)a->Hkv);
+    if (bias && (a->buckets < 1 || a->reach < 1))
+        return fail(DW_ERR_INVALID_ARG, "%s: a bias needs at least one bucket and a reach of one frame", fn);
+    if (a->D > dw::kAttnMaxHead)
+        return fail(DW_ERR_UNSUPPORTED, "%s: heads of D=%lld have no kernel (at most 128)", fn, (long long)a->D);
+    if (bias && a->reach > dw::kAttnMaxReach)
+        return fail(DW_ERR_UNSUPPORTED, "%s: a reach of %lld frames has no kernel (at most 1024)", fn, (long long)a->reach);
+    if (bias && !extents_ok(a->buckets)) return too_large(fn);
+    if (!extents_ok(a->B, a->H, a->Hkv) || a->Tq > dw::kAttnMaxFrames || a->Tk > dw::kAttnMaxFrames ||
+        !strides_fit(a->q, a->B, a->Tq, a->H) || !strides_fit(a->k, a->B, a->Tk, a->Hkv) ||
+        !strides_fit(a->v, a->B, a->Tk, a->Hkv))
+        return too_large(fn);
+    const int64_t none = dw::kNoLimit;
+    s->B = a->B, s->Tq = a->Tq, s->Tk = a->Tk, s->H = a->H, s->Hkv = a->Hkv, s->D = a->D;
+    s->q = stride_of(a->q), s->k = stride_of(a->k), s->v = stride_of(a->v);
+    s->dq = stride_of(a->dq), s->dk = stride_of(a->dk), s->dv = stride_of(a->dv);
+    s->buckets = bias ? a->buckets : 0, s->reach = bias ? a->reach : 0;
+    s->left = a->left < 0 || a->left > none ? none : a->left;
+    s->right = a->right < 0 || a->right > none ? none : a->right;
+    s->scale = a->scale;
+    if (!dw::dwattn_fits(*s)) return too_large(fn);
+    return DW_OK;
+}
+
+// How often p divides n.
+int times_divides(int64_t p, int64_t n) {
+    int e = 0;
+    for (; n % p == 0; n /= p) ++e;
+    return e;
+}
+
+// floor(m log(n/e) / log(reach/e)) for n >= e.  The quotient is a whole number
+// k exactly where n^m e^k = reach^k e^m, which the exponents of the primes
+// decide; elsewhere long double tells the floor.
+int64_t log_steps(int64_t n, int64_t e, int64_t reach, int64_t m) {
+    const long double t = m * (logl((long double)n / e) / logl((long double)reach / e));
+    const int64_t k = llroundl(t);
+    if (fabsl(t - k) > 1e-6L) return (int64_t)floorl(t);
+    bool equal = true;
+    for (int64_t p = 2; p <= reach; ++p)
+        equal = equal && m * times_divides(p, n) + k * times_divides(p, e) ==
+                             k * times_divides(p, reach) + m * times_divides(p, e);
+    return equal ? k : (int64_t)floorl(t);
 }
 
 }  // namespace
@@ -441,6 +508,53 @@ dw_status dwnorm_bwd(const void* sum, const void* gamma, const int32_t* lengths,
     return from_hip(dw::launch_dwnorm_bwd(sum, gamma, lengths, mean, rstd, dy, dsum, p > 0.0 ? rng : nullptr, dx, dres,
                                           dgamma, dbeta, workspace, B, T, C, alpha, p, dtype == DW_BF16,
                                           (hipStream_t)stream), fn);
+}
+
+dw_status dwattn_rel_buckets(int32_t* map, int64_t buckets, int64_t reach, int bidirectional) {
+    const char* fn = "dwattn_rel_buckets";
+    const int64_t per = bidirectional ? buckets / 2 : buckets, e = per / 2;
+    if (!map) return fail(DW_ERR_INVALID_ARG, "%s: map must not be NULL", fn);
+    if (buckets < 1 || per < 1) return fail(DW_ERR_INVALID_ARG, "%s: fewer than one bucket a direction", fn);
+    if (buckets > 65536) return fail(DW_ERR_UNSUPPORTED, "%s: over 65536 buckets", fn);
+    if (reach < 1 || reach <= e)
+        return fail(DW_ERR_INVALID_ARG, "%s: the reach must be past the %lld distances with a bucket each", fn, (long long)e);
+    if (reach > dw::kAttnMaxReach) return fail(DW_ERR_UNSUPPORTED, "%s: a reach over 1024 frames", fn);
+    for (int64_t n = 0; n <= reach; ++n) {
+        int64_t b = n;
+        if (n >= e) {
+            const int64_t k = e > 0 ? log_steps(n, e, reach, per - e) : 0;
+            b = e + (k < per - e ? k : per - e - 1);
+        }
+        map[reach - n] = (int32_t)b;
+        if (n > 0) map[reach + n] = (int32_t)(bidirectional ? per + b : 0);
+    }
+    return ok();
+}
+
+size_t dwattn_fwd_workspace_bytes(const dw_attn* shape) {
+    dw::AttnShape s;
+    if (check_attn("dwattn_fwd_workspace_bytes", shape, false, &s) != DW_OK) return 0;
+    return dw::dwattn_fwd_workspace(s);
+}
+
+dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const void* v, const void* table,
+                     const int32_t* map, const int32_t* q_lengths, const int32_t* k_lengths, const int32_t* q_pos,
+                     void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "dwattn_fwd";
+    if (!table != !map) return fail(DW_ERR_INVALID_ARG, "%s: a bias needs both its table and its map", fn);
+    dw::AttnShape s;
+    const dw_status c = check_attn(fn, shape, table != nullptr, &s);
+    if (c != DW_OK) return c;
+    if (!nonempty(s.B, s.Tq, s.H, s.D)) return ok();
+    if (!q || !out || (s.Tk > 0 && (!k || !v)))
+        return fail(DW_ERR_INVALID_ARG, "%s: q, k, v and out must not be NULL (unless empty)", fn);
+    if (out == q || out == k || out == v) return fail(DW_ERR_INVALID_ARG, "%s: out must not alias an input", fn);
+    const size_t need = dw::dwattn_fwd_workspace(s);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(DW_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
+                    workspace ? workspace_bytes : (size_t)0, need);
+    const dw::AttnPtrs p = {q, k, v, table, map, q_lengths, k_lengths, q_pos};
+    return from_hip(dw::launch_dwattn_fwd(p, s, out, lse, workspace, shape->dtype == DW_BF16, (hipStream_t)stream), fn);
 }
 
 }  // extern "C"

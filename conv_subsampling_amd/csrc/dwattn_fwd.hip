@@ -1,0 +1,349 @@
+// Self-attention with a learned relative position bias by buckets: forward.
+//
+//   S_ij = scale * q_i . k_j + bias[j - i - pos],  out_i = sum_j softmax_j(S_ij) v_j
+//
+// One pass over the keys with the running maximum and sum of a softmax.  A
+// workgroup of four waves owns 32 * QW queries of one head: with QW = 4 each
+// wave owns 32 queries and all share the tiles of 64 keys; with QW = 1 (few
+// queries: streaming, short utterances) the waves share 32 queries and divide
+// tiles of 128 keys, and their results are joined in LDS.  Where even that
+// leaves compute units idle, the key axis is split over workgroups, whose
+// results attn_join adds.
+#include "attn.h"
+
+namespace dw {
+
+struct AttnFwd : AttnArgs {
+    void* out;     // [B][Tq][H][D]
+    float* lse;    // [B][H][Tq] or NULL
+    float* part;   // splits > 1: [splits][B * H * Tq][D4] unnormalised sums, then [splits][B * H * Tq][2] maxima and sums
+    int32_t splits, nqb;
+};
+
+// The scores are kept in units of log2.  The running maximum follows the true
+// one only when that has grown by more than kSlack: the weights then stay
+// below 2^kSlack, and most tiles need no rescaling of the accumulators.
+constexpr float kSlack = 8.0f;
+
+// Keys of a tile, and the waves per SIMD its registers are to allow: float rows
+// over 96 wide hold twice the registers in flight.
+template <typename S, int DP, int QW>
+struct FwdShape {
+    static constexpr bool kHeavy = sizeof(S) == 4 && DP > 96;
+    static constexpr int BN = QW == 1 ? 128 : kHeavy ? 32 : 64;
+    static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : 2;
+};
+
+template <typename S, int DP, int QW>
+__global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW>::kWaves)) void attn_fwd_kernel(const AttnFwd a) {
+    constexpr int KW = 4 / QW, BN = FwdShape<S, DP, QW>::BN, KT = BN / kTile / KW, NC = DP / 16, ND = DP / 32;
+    typedef Tile<S, DP> T;
+    extern __shared__ __align__(16) char smem[];
+    S* ktile = (S*)smem;
+    S* vtile = (S*)(smem + T::bytes(BN));
+    float* bias = (float*)(smem + 2 * T::bytes(BN));
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, half = lane / 32;
+    const int wq = QW == 4 ? wave : 0, wk = QW == 4 ? 0 : wave;
+
+    uint32_t id = xcd_contiguous_block(blockIdx.x, gridDim.x);
+    const int split = id % a.splits;
+    id /= a.splits;
+    const int qb = id % a.nqb;
+    id /= a.nqb;
+    const int h = id % a.H, b = id / a.H;
+    const AttnItem item(a, b);
+    const int i0 = qb * (kTile * QW), iw = i0 + wq * kTile, i = iw + lane % 32;
+    const bool live = i < item.nq;
+
+    if (a.table) fill_bias<S>(a, h, bias);
+
+    Frag<S> q[NC];
+    {
+        const S* row = (const S*)a.q + b * a.qs.item + (int64_t)(live ? i : 0) * a.qs.frame + h * a.qs.head;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) q[c] = to_frag<S>(load_group<S, true>(row, 16 * c + 8 * half, live ? a.D : 0));
+    }
+    // this lane's keys: [mine0, mine0 + mine)
+    const int mine0 = item.first_key(a, i);
+    const int mine1 = item.last_key(a, i);
+    const uint32_t mine = live && mine1 >= mine0 ? mine1 - mine0 + 1 : 0;
+
+    // the workgroup's keys, and this split's share of them
+    int j0 = 0, j1 = 0;
+    if (i0 < item.nq) {
+        const int ilast = min(i0 + kTile * QW, item.nq) - 1;
+        j0 = item.first_key(a, i0);
+        j1 = item.last_key(a, ilast) + 1;
+    }
+    const int tiles = j1 > j0 ? (j1 - j0 + BN - 1) / BN : 0, share = (tiles + a.splits - 1) / a.splits;
+    const int t0 = min(split * share, tiles), t1 = min(t0 + share, tiles);
+    // the wave's keys, for the tiles that it can pass over or take unmasked
+    const int iwl = min(iw + kTile, item.nq) - 1;
+    const int some0 = item.first_key(a, iw), some1 = iw < item.nq ? item.last_key(a, iwl) : -1;
+    const int all0 = item.first_key(a, iwl), all1 = iw + kTile <= item.nq ? item.last_key(a, iw) : -1;
+
+    const S* kbase = (const S*)a.k + b * a.ks.item + (int64_t)(h / (a.H / a.Hkv)) * a.ks.head;
+    const S* vbase = (const S*)a.v + b * a.vs.item + (int64_t)(h / (a.H / a.Hkv)) * a.vs.head;
+    TileLoad<S, DP, BN> kl, vl;
+    if (t0 < t1) {
+        const int64_t j = j0 + t0 * BN;
+        kl.load(kbase + j * a.ks.frame, a.ks.frame, j1 - (int)j, a.D);
+        vl.load(vbase + j * a.vs.frame, a.vs.frame, j1 - (int)j, a.D);
+    }
+
+    f32x16 o[ND] = {};
+    float top = -__builtin_inff(), sum = 0.0f;
+    for (int t = t0; t < t1; ++t) {
+        __syncthreads();
+        kl.store(ktile);
+        vl.store(vtile);
+        __syncthreads();
+        if (t + 1 < t1) {
+            const int64_t j = j0 + (t + 1) * BN;
+            kl.load(kbase + j * a.ks.frame, a.ks.frame, j1 - (int)j, a.D);
+            vl.load(vbase + j * a.vs.frame, a.vs.frame, j1 - (int)j, a.D);
+        }
+        f32x16 s[KT];
+        bool any = false;
+#pragma unroll
+        for (int u = 0; u < KT; ++u) {
+            const int row0 = (wk * KT + u) * kTile, j = j0 + t * BN + row0;
+            if (j > some1 || j + kTile <= some0) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[u][r] = -__builtin_inff();
+                continue;
+            }
+            any = true;
+            s[u] = f32x16{};
+#pragma unroll
+            for (int c = 0; c < NC; ++c) s[u] = mma(T::rows(ktile, row0, c, lane), q[c], s[u]);
+            const int base = j - iw - item.pos32;
+            if (a.table) {
+                const Span span = span_of(base, a.R);
+                if (span == Span::kNear) {
+                    const float* p = bias + (base + a.R + kBiasMargin + 4 * half - lane % 32);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[u][r] = fmaf(s[u][r], a.scale2, p[acc_row(r, 0)]);
+                } else {
+                    const float v = bias[span == Span::kLow ? 0 : 2 * a.R + 2 * kBiasMargin];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[u][r] = fmaf(s[u][r], a.scale2, v);
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[u][r] *= a.scale2;
+            }
+            if (j < all0 || j + kTile - 1 > all1) {
+                const uint32_t at = j + 4 * half - mine0;
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    s[u][r] = at + acc_row(r, 0) < mine ? s[u][r] : -__builtin_inff();
+            }
+        }
+        if (!any) continue;
+        float m = s[0][0];
+#pragma unroll
+        for (int u = 0; u < KT; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) m = fmaxf(m, s[u][r]);
+        m = fmaxf(m, swap_halves(m));
+        if (__any(m > top + kSlack)) {
+            m = fmaxf(m, top);
+            const float f = m == -__builtin_inff() ? 1.0f : exp2_fast(top - m);
+            sum *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[d][r] *= f;
+            top = m;
+        }
+        const float ref = top == -__builtin_inff() ? 0.0f : top;
+#pragma unroll
+        for (int u = 0; u < KT; ++u) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[u][r] = exp2_fast(s[u][r] - ref);
+                sum += s[u][r];
+            }
+            const int row0 = (wk * KT + u) * kTile;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const Frag<S> p = to_frag<S>(s[u], k);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) o[d] = mma(T::columns(vtile, row0 + 16 * k, d, lane), p, o[d]);
+            }
+        }
+    }
+    sum += swap_halves(sum);
+
+    if constexpr (KW > 1) {  // join the waves: wave w takes head elements 32 w ..
+        float* opart = (float*)smem;                                    // [KW][ND * 16][64]
+        float* stat = (float*)(smem + KW * ND * 16 * 64 * 4);           // [KW][2][32]
+        static_assert(KW * ND * 16 * 64 * 4 + KW * 2 * 32 * 4 <= 2 * T::bytes(BN), "the tiles' room holds the join");
+        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) opart[((wave * ND + d) * 16 + r) * 64 + lane] = o[d][r];
+        if (half == 0) {
+            stat[wave * 64 + lane] = top;
+            stat[wave * 64 + 32 + lane] = sum;
+        }
+        __syncthreads();
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < KW; ++w) m = fmaxf(m, stat[w * 64 + lane % 32]);
+        float f[KW], total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+            f[w] = m == -__builtin_inff() ? 0.0f : exp2_fast(stat[w * 64 + lane % 32] - m);
+            total += f[w] * stat[w * 64 + 32 + lane % 32];
+        }
+        top = m;
+        sum = total;
+        if (wave < ND) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < KW; ++w) v += f[w] * opart[((w * ND + wave) * 16 + r) * 64 + lane];
+                o[0][r] = v;
+            }
+        }
+    }
+    if (i >= a.Tq) return;
+    const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
+    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // a row without keys is zero; NaN stays
+#pragma unroll
+    for (int d = 0; d < (KW > 1 ? 1 : ND); ++d) {
+        const int d0 = 32 * (KW > 1 ? wave : d) + 4 * half;
+        if (KW > 1 && wave >= ND) break;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            if (a.splits > 1) {
+                const int64_t rows = (int64_t)a.B * a.H * a.Tq;
+                const int D4 = (a.D + 3) / 4 * 4;
+                store4<float>(a.part + (split * rows + row) * D4, d0 + 8 * g, D4, o[d][4 * g], o[d][4 * g + 1],
+                              o[d][4 * g + 2], o[d][4 * g + 3]);
+            } else {
+                store4<S>((S*)a.out + (((int64_t)b * a.Tq + i) * a.H + h) * a.D, d0 + 8 * g, a.D, o[d][4 * g] * inv,
+                          o[d][4 * g + 1] * inv, o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv);
+            }
+        }
+    }
+    if (half == 0 && wk == 0) {
+        if (a.splits > 1) {
+            const int64_t rows = (int64_t)a.B * a.H * a.Tq;
+            float* stat = a.part + a.splits * rows * ((a.D + 3) / 4 * 4) + (split * rows + row) * 2;
+            stat[0] = top;
+            stat[1] = sum;
+        } else if (a.lse) {
+            a.lse[row] = sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * kLn2;
+        }
+    }
+}
+
+// Joins the splits of the key axis: one thread takes 4 head elements of a row.
+template <typename S>
+__global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnFwd a) {
+    const int D4 = (a.D + 3) / 4;
+    const int64_t rows = (int64_t)a.B * a.H * a.Tq, at = (int64_t)blockIdx.x * kAttnThreads + threadIdx.x;
+    if (at >= rows * D4) return;
+    const int64_t row = at / D4;
+    const int d = (int)(at - row * D4);
+    const float* stat = a.part + a.splits * rows * D4 * 4;
+    float m = -__builtin_inff();
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, stat[(s * rows + row) * 2]);
+    f32x4 o = {};
+    float sum = 0.0f;
+    for (int s = 0; s < a.splits; ++s) {
+        const float f = m == -__builtin_inff() ? 0.0f : exp2_fast(stat[(s * rows + row) * 2] - m);
+        sum += f * stat[(s * rows + row) * 2 + 1];
+        o += f * *reinterpret_cast<const f32x4*>(a.part + ((s * rows + row) * D4 + d) * 4);
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+    const int64_t i = row % a.Tq, bh = row / a.Tq;
+    S* out = (S*)a.out + (((bh / a.H) * a.Tq + i) * a.H + bh % a.H) * a.D;
+    store4<S>(out, 4 * d, a.D, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -__builtin_inff() : (m + log2f(sum)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// Launch plan
+// ---------------------------------------------------------------------------
+struct FwdPlan {
+    int qw, splits;
+    int64_t nqb;
+};
+
+// 128 queries a workgroup read each key tile once for four waves, so they are
+// taken where that leaves enough workgroups; else 32 queries, and where those
+// are few too, the keys are split until about two workgroups per compute unit
+// are there.  The plan goes by the sizes alone (lengths are on the device).
+static FwdPlan fwd_plan(const AttnShape& s) {
+    constexpr int64_t kUnits = 256;
+    FwdPlan p;
+    const int64_t wide = (s.Tq + 127) / 128, narrow = (s.Tq + 31) / 32;
+    p.qw = s.Tq > 32 && s.B * s.H * wide >= kUnits * 3 / 4 ? 4 : 1;
+    p.nqb = p.qw == 4 ? wide : narrow;
+    const int64_t queries = p.qw == 4 ? 128 : 32, keys = p.qw == 4 ? 64 : 128;
+    int64_t span = s.Tk;
+    if (s.left < kNoLimit && s.right < kNoLimit) {
+        const int64_t window = s.left + s.right + queries;
+        span = window < 1 ? 1 : window < span ? window : span;
+    }
+    const int64_t blocks = s.B * s.H * p.nqb, tiles = (span + keys - 1) / keys;
+    int64_t n = 2 * kUnits / (blocks ? blocks : 1);
+    n = n < tiles ? n : tiles;
+    p.splits = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+    return p;
+}
+
+static int64_t part_floats(const AttnShape& s, int splits) {
+    return splits > 1 ? splits * s.B * s.H * s.Tq * ((s.D + 3) / 4 * 4 + 2) : 0;
+}
+
+size_t dwattn_fwd_workspace(const AttnShape& s) { return (size_t)part_floats(s, fwd_plan(s).splits) * sizeof(float); }
+
+bool dwattn_fits(const AttnShape& s) {
+    // workgroups of the narrowest tiles times the most splits, and the threads of the join
+    const int64_t q32 = (s.Tq + 31) / 32, k32 = (s.Tk + 31) / 32;
+    return product_below(kMaxExtent, {s.B, s.H, q32}) && product_below(kMaxExtent, {s.B, s.H, k32}) &&
+           product_below(kMaxExtent, {s.B, s.H, s.Tq}) && product_below(kMaxExtent, {s.B, s.H, s.Tq, (s.D + 3) / 4 + 1});
+}
+
+template <typename S, int DP, int QW>
+static hipError_t launch_fwd(const AttnFwd& a, hipStream_t stream) {
+    constexpr int BN = FwdShape<S, DP, QW>::BN;
+    const int lds = 2 * Tile<S, DP>::bytes(BN) + (a.table ? attn_bias_bytes(a.R) : 0);
+    hipLaunchKernelGGL((attn_fwd_kernel<S, DP, QW>), dim3((uint32_t)(a.B * a.H) * a.nqb * a.splits), dim3(kAttnThreads),
+                       lds, stream, a);
+    return hipGetLastError();
+}
+
+template <typename S>
+static hipError_t fwd_of_type(const AttnFwd& a, int qw, hipStream_t stream) {
+    const hipError_t e = with_head_width(a.D, [&](auto dp) {
+        return qw == 4 ? launch_fwd<S, dp.value, 4>(a, stream) : launch_fwd<S, dp.value, 1>(a, stream);
+    });
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t threads = (int64_t)a.B * a.H * a.Tq * ((a.D + 3) / 4);
+    hipLaunchKernelGGL(attn_join<S>, dim3((uint32_t)((threads + kAttnThreads - 1) / kAttnThreads)), dim3(kAttnThreads), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_dwattn_fwd(const AttnPtrs& p, const AttnShape& s, void* out, float* lse, void* workspace, bool bf16,
+                             hipStream_t stream) {
+    const FwdPlan plan = fwd_plan(s);
+    AttnFwd a;
+    (AttnArgs&)a = attn_args(p, s);
+    a.out = out;
+    a.lse = lse;
+    a.part = (float*)workspace;
+    a.splits = plan.splits;
+    a.nqb = (int32_t)plan.nqb;
+    return bf16 ? fwd_of_type<uint16_t>(a, plan.qw, stream) : fwd_of_type<float>(a, plan.qw, stream);
+}
+
+}  // namespace dw

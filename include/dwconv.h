@@ -505,6 +505,85 @@ dw_status dwnorm_bwd(const void *sum, const void *gamma, const int32_t *lengths,
                      float *dbeta, void *workspace, size_t workspace_bytes, int64_t B, int64_t T, int64_t C,
                      float alpha, double p, dw_dtype dtype, void *stream);
 
+/*
+ * Attention with a learned relative position bias by buckets.
+ *
+ * Sizes and layout of one problem.  q, k, v, dq, dk, dv are [B][frames][heads][D]
+ * with the D elements of a head next to each other and any distance between
+ * items, frames and heads, given in elements (so slices of one projection's
+ * output, or a cache with room to grow, need no copy; an input's distance may
+ * be 0).  out and dout are dense [B][Tq][H][D], lse dense [B][H][Tq].  Query
+ * head h reads key head h / (H / Hkv).
+ */
+typedef struct {
+    int64_t item, frame, head; /* elements from one to the next */
+} dw_strides;
+
+typedef struct {
+    int64_t B, Tq, Tk; /* items; queries and keys of each, at most 2^28 */
+    int64_t H, Hkv;    /* query heads, key heads (H a multiple of Hkv) */
+    int64_t D;         /* elements of a head, 1 to 128 */
+    dw_strides q, k, v;
+    dw_strides dq, dk, dv;  /* dwattn_bwd only */
+    int64_t buckets, reach; /* of the bias: rows of the table; the map covers -reach .. reach, 1 to 1024 */
+    int64_t left, right;    /* frames of context each side of a query; negative: all of them */
+    float scale;            /* of q . k, usually 1 / sqrt(D) */
+    dw_dtype dtype;         /* of q, k, v, table, out, dout, dq, dk, dv */
+} dw_attn;
+
+/*
+ * dwattn_rel_buckets -- the usual map of distances to buckets, into HOST memory:
+ * map[r + reach] is the bucket of a key r frames after (r > 0) or before
+ * (r < 0) its query, for -reach <= r <= reach; the ends stand for everything
+ * beyond.  With n = |r| and P buckets for one direction (buckets / 2 where
+ * both are told apart, keys after the query then counting from buckets / 2;
+ * else buckets, and r > 0 counts as 0), e = floor(P / 2):
+ *   n < e:  n      n >= e:  e + min(P - e - 1, floor((P - e) log(n/e) / log(reach/e)))
+ * evaluated exactly.  Errors: DW_ERR_INVALID_ARG for a null map, fewer than
+ * one bucket a direction, or a reach that is not past e; DW_ERR_UNSUPPORTED for
+ * a reach over 1024 or over 65536 buckets.
+ */
+dw_status dwattn_rel_buckets(int32_t *map, int64_t buckets, int64_t reach, int bidirectional);
+
+/*
+ * Bytes of device workspace dwattn_fwd needs: none where there are queries
+ * enough to fill the GPU; where there are few (streaming) the key axis is
+ * split, and the parts are joined from the workspace.  0 for sizes that the
+ * call refuses.
+ */
+size_t dwattn_fwd_workspace_bytes(const dw_attn *shape);
+
+/*
+ * dwattn_fwd -- softmax attention whose scores carry a learned bias:
+ *   S_ij    = scale * q_i . k_j + table[map[clamp(r, -reach, reach) + reach], h],  r = j - i - pos_b
+ *   allowed: i < q_lengths[b], j < k_lengths[b], r >= -left (left >= 0), r <= right (right >= 0)
+ *   out_i   = sum_j p_ij v_j,  p_i = softmax of S_i over the allowed j
+ *   lse_i   = log(sum_j exp(S_ij))
+ * pos_b = q_pos[b] is the place of query 0 on the key axis: 0 (q_pos NULL) for
+ * whole utterances, the number of cached frames for a streaming chunk whose
+ * keys are already in the cache.  right = 0 makes it causal.  A query without
+ * an allowed key, and one at or past its item's length, gives out = 0 and
+ * lse = -inf.  Keys and values at or past the length are not read.  Keys and
+ * values below it are expected to be finite.
+ *
+ * table: [buckets][H] in the storage type; map: [2 * reach + 1] int32 in device
+ * memory, from dwattn_rel_buckets or any other (entries are held to the table);
+ * both NULL: no bias.  A table entry of -inf forbids its bucket.  lengths and
+ * positions: int32 [B] or NULL (full lengths, position 0); lengths are clamped
+ * to the tensors.  lse may be NULL.
+ * Scores, softmax and sums are float32.  DW_BF16 rounds the weights p to bf16
+ * for their product with v (their sum is taken before), and out once.
+ * Repeated calls agree bit for bit.
+ * Errors: DW_ERR_INVALID_ARG for a null pointer that holds elements, a negative
+ * size or stride, H not a multiple of Hkv, a table without a map or the other
+ * way round, buckets or reach below 1, a bad dtype, or out aliasing an input;
+ * DW_ERR_UNSUPPORTED for D > 128, reach > 1024 or sizes too large for one
+ * launch; DW_ERR_WORKSPACE for a missing or short workspace.
+ */
+dw_status dwattn_fwd(const dw_attn *shape, const void *q, const void *k, const void *v, const void *table,
+                     const int32_t *map, const int32_t *q_lengths, const int32_t *k_lengths, const int32_t *q_pos,
+                     void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

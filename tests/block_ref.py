@@ -62,3 +62,66 @@ def norm_bwd(s, gamma, lengths, mean, rstd, dy, dsum, factor, alpha):
             ag += np.abs(dy[b, t] * xh)
             ab += np.abs(dy[b, t])
     return dx, dres, dg, db, ag, ab
+
+
+def bucket(rel, buckets, reach, bidirectional):
+    """The bucket of one distance, in whole numbers."""
+    per = buckets // 2 if bidirectional else buckets
+    n = abs(rel) if bidirectional else max(0, -rel)
+    n, e = min(n, reach), per // 2
+    b = n
+    if n >= e:
+        m, k = per - e, 0
+        while k + 1 < m and n ** m * e ** (k + 1) >= reach ** (k + 1) * e ** m:
+            k += 1
+        b = e + k
+    return b + (per if bidirectional and rel > 0 else 0)
+
+
+def attn(q, k, v, table, buckets, q_len, k_len, pos, left, right, scale, dout=None, out=None, lse=None):
+    """Attention of [B,T,H,D] arrays.  Returns (out, lse), or with dout (dq, dk, dv, dtable) and the sums of the
+    absolute terms of dtable; there out and lse are the forward's as given."""
+    B, Tq, H, D = q.shape
+    Tk, G = k.shape[1], H // k.shape[2]
+    R = 0 if buckets is None else len(buckets) // 2
+    bwd = dout is not None
+    if not bwd:
+        out, lse = np.zeros_like(q), np.full((B, H, Tq), -np.inf)
+    dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    dt = None if table is None else np.zeros_like(table)
+    at = None if table is None else np.zeros_like(table)
+    for b in range(B):
+        nq, nk = int(np.clip(q_len[b], 0, Tq)), int(np.clip(k_len[b], 0, Tk))
+        if not nq or not nk:
+            continue
+        rel = np.arange(nk)[None, :] - np.arange(nq)[:, None] - int(pos[b])
+        seen = np.ones((nq, nk), bool)
+        if left >= 0:
+            seen &= rel >= -left
+        if right >= 0:
+            seen &= rel <= right
+        place = None if buckets is None else np.asarray(buckets)[np.clip(rel, -R, R) + R]
+        for h in range(H):
+            kk, vv = k[b, :nk, h // G], v[b, :nk, h // G]
+            S = scale * (q[b, :nq, h] @ kk.T) + (0.0 if table is None else table[place, h])
+            S = np.where(seen, S, -np.inf)
+            if not bwd:
+                m = S.max(1, keepdims=True)
+                m = np.where(np.isinf(m), 0.0, m)
+                P = np.exp(S - m)
+                total = P.sum(1, keepdims=True)
+                out[b, :nq, h] = np.where(total > 0, P @ vv / np.where(total > 0, total, 1), 0.0)
+                with np.errstate(divide="ignore"):
+                    lse[b, h, :nq] = (m + np.log(total))[:, 0]
+                continue
+            ls = lse[b, h, :nq, None]
+            P = np.where(np.isinf(ls) | ~seen, 0.0, np.exp(S - np.where(np.isinf(ls), 0.0, ls)))
+            do, o = dout[b, :nq, h], out[b, :nq, h]
+            dS = P * (do @ vv.T - (do * o).sum(1, keepdims=True))
+            dq[b, :nq, h] = scale * dS @ kk
+            dk[b, :nk, h // G] += scale * dS.T @ q[b, :nq, h]
+            dv[b, :nk, h // G] += P.T @ do
+            if table is not None:
+                np.add.at(dt[:, h], place, dS)
+                np.add.at(at[:, h], place, np.abs(dS))
+    return (dq, dk, dv, dt, at) if bwd else (out, lse)
