@@ -22,7 +22,7 @@ __all__ = [
     "LIB_PATH", "DwconvError", "abi_version",
     "dwconv1d_fwd", "dwconv1d_stream_fwd", "dwconv1d_bwd", "dwconv1d_bwd_workspace_bytes", "dwsub_fused_fwd", "dwsub_fused_bwd", "dwsub_fused_bwd_workspace_bytes",
     "dwconv2d_fwd", "dwconv2d_bwd", "dwconv2d_bwd_workspace_bytes", "dwconv2d_bwd_noalloc",
-    "dwattn_fwd", "dwattn_fwd_workspace_bytes", "rel_buckets",
+    "dwattn_fwd", "dwattn_fwd_workspace_bytes", "dwattn_bwd", "dwattn_bwd_workspace_bytes", "rel_buckets",
     "dwnorm_fwd", "dwnorm_bwd", "dwnorm_bwd_workspace_bytes", "dwdrop_fwd", "dwdrop_bwd",
     "conv2d_out_shape", "CAUSAL_PADS_2D", "front_out_shape", "out_len",
 ]
@@ -119,6 +119,10 @@ def _bind(path: str) -> ctypes.CDLL:
     lib.dwattn_fwd_workspace_bytes.argtypes = [attn]
     lib.dwattn_fwd.restype = _int
     lib.dwattn_fwd.argtypes = [attn] + [_vp] * 11 + [_sz, _vp]
+    lib.dwattn_bwd_workspace_bytes.restype = _sz
+    lib.dwattn_bwd_workspace_bytes.argtypes = [attn]
+    lib.dwattn_bwd.restype = _int
+    lib.dwattn_bwd.argtypes = [attn] + [_vp] * 16 + [_sz, _vp]
     return lib
 
 
@@ -672,3 +676,45 @@ def dwattn_fwd(q, k, v, table=None, buckets=None, q_lengths=None, k_lengths=None
                            _ptr(k_lengths), _ptr(q_pos), _ptr(out), _ptr(lse), _ptr(workspace),
                            0 if workspace is None else workspace.numel(), _stream(dev)))
     return out, lse
+
+
+def dwattn_bwd_workspace_bytes(q, k, v, table=None, buckets=None) -> int:
+    """Bytes of workspace `dwattn_bwd` takes for tensors of these sizes."""
+    return int(_lib.dwattn_bwd_workspace_bytes(_attn_shape(q, k, v, table, buckets, None, None, None, -1, -1, None)[0]))
+
+
+def dwattn_bwd(q, k, v, out, lse, dout, table=None, buckets=None, q_lengths=None, k_lengths=None, q_pos=None,
+               left: int = -1, right: int = -1, scale=None, dq=None, dk=None, dv=None, dtable=None, workspace=None,
+               need=("dq", "dk", "dv", "dtable")):
+    """Gradients (dq, dk, dv, dtable) of dwattn_fwd given its out and lse and
+    dout; the other arguments are the forward's.  dq, dk and dv are in the
+    storage type (given ones may have any strides above the last), dtable
+    float32 [num_buckets,H]; those not in `need`, and dtable without a table,
+    are skipped (None)."""
+    shape, st = _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, right, scale)
+    dev = q.device
+    B, Tq, H, D = q.shape
+    kv = tuple(k.shape)
+    _dev_tensor("out", out, st, dev, (B, Tq, H, D))
+    _dev_tensor("lse", lse, torch.float32, dev, (B, H, Tq))
+    _dev_tensor("dout", dout, st, dev, (B, Tq, H, D))
+    if dq is None and "dq" in need:
+        dq = torch.empty((B, Tq, H, D), dtype=st, device=dev)
+    if dk is None and "dk" in need:
+        dk = torch.empty(kv, dtype=st, device=dev)
+    if dv is None and "dv" in need:
+        dv = torch.empty(kv, dtype=st, device=dev)
+    if dtable is None and "dtable" in need and table is not None:
+        dtable = torch.empty(tuple(table.shape), dtype=torch.float32, device=dev)
+    for name, t, like in (("dq", dq, (B, Tq, H, D)), ("dk", dk, kv), ("dv", dv, kv)):
+        if t is not None:
+            _heads(name, t, st, dev, like)
+            setattr(shape, name, _Strides(*t.stride()[:3]))
+    _dev_tensor("dtable", dtable, torch.float32, dev, None if table is None else table.shape, allow_none=True)
+    if workspace is None:
+        workspace = torch.empty((max(int(_lib.dwattn_bwd_workspace_bytes(shape)), 1),), dtype=torch.uint8, device=dev)
+    _dev_tensor("workspace", workspace, torch.uint8, dev)
+    _check(_lib.dwattn_bwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(table), _ptr(buckets), _ptr(q_lengths),
+                           _ptr(k_lengths), _ptr(q_pos), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
+                           _ptr(dtable), _ptr(workspace), workspace.numel(), _stream(dev)))
+    return dq, dk, dv, dtable

@@ -557,4 +557,45 @@ dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const v
     return from_hip(dw::launch_dwattn_fwd(p, s, out, lse, workspace, shape->dtype == DW_BF16, (hipStream_t)stream), fn);
 }
 
+size_t dwattn_bwd_workspace_bytes(const dw_attn* shape) {
+    dw::AttnShape s;
+    if (!shape || check_attn("dwattn_bwd_workspace_bytes", shape, shape->buckets > 0, &s) != DW_OK) return 0;
+    return dw::dwattn_bwd_workspace(s);
+}
+
+dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const void* v, const void* table,
+                     const int32_t* map, const int32_t* q_lengths, const int32_t* k_lengths, const int32_t* q_pos,
+                     const void* out, const float* lse, const void* dout, void* dq, void* dk, void* dv, float* dtable,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "dwattn_bwd";
+    if (!table != !map) return fail(DW_ERR_INVALID_ARG, "%s: a bias needs both its table and its map", fn);
+    if (dtable && !table) return fail(DW_ERR_INVALID_ARG, "%s: dtable needs a table", fn);
+    dw::AttnShape s;
+    const dw_status c = check_attn(fn, shape, table != nullptr, &s);
+    if (c != DW_OK) return c;
+    if (!strides_ok(shape->dq) || !strides_ok(shape->dk) || !strides_ok(shape->dv))
+        return fail(DW_ERR_INVALID_ARG, "%s: negative stride", fn);
+    if ((dq && !strides_fit(shape->dq, s.B, s.Tq, s.H)) || (dk && !strides_fit(shape->dk, s.B, s.Tk, s.Hkv)) ||
+        (dv && !strides_fit(shape->dv, s.B, s.Tk, s.Hkv)))
+        return too_large(fn);
+    if ((!dq && !dk && !dv && !dtable) || s.H == 0) return ok();
+    if (!dtable && (s.B == 0 || s.D == 0)) return ok();
+    if (nonempty(s.B, s.Tq) && (!lse || (s.D > 0 && (!q || !out || !dout))))
+        return fail(DW_ERR_INVALID_ARG, "%s: q, out, lse and dout must not be NULL (unless empty)", fn);
+    if (nonempty(s.B, s.Tk, s.D) && (!k || !v))
+        return fail(DW_ERR_INVALID_ARG, "%s: k and v must not be NULL (unless empty)", fn);
+    for (const void* o : {(const void*)dq, (const void*)dk, (const void*)dv})
+        if (o && (o == q || o == k || o == v || o == out || o == dout))
+            return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
+    if ((dq && (dq == dk || dq == dv)) || (dk && dk == dv))
+        return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
+    const size_t need = dw::dwattn_bwd_workspace(s);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(DW_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
+                    workspace ? workspace_bytes : (size_t)0, need);
+    const dw::AttnPtrs p = {q, k, v, table, map, q_lengths, k_lengths, q_pos};
+    return from_hip(dw::launch_dwattn_bwd(p, s, out, lse, dout, dq, dk, dv, dtable, workspace, shape->dtype == DW_BF16,
+                                          (hipStream_t)stream), fn);
+}
+
 }  // extern "C"

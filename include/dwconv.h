@@ -584,6 +584,35 @@ dw_status dwattn_fwd(const dw_attn *shape, const void *q, const void *k, const v
                      const int32_t *map, const int32_t *q_lengths, const int32_t *k_lengths, const int32_t *q_pos,
                      void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
+/* Bytes of device workspace dwattn_bwd needs; shape->buckets and reach count
+ * when buckets > 0.  0 for sizes that the call refuses. */
+size_t dwattn_bwd_workspace_bytes(const dw_attn *shape);
+
+/*
+ * dwattn_bwd -- gradients of dwattn_fwd, given its out and lse and the gradient
+ * dout of out.  With P_ij = exp(S_ij - lse_i) over the allowed pairs (0 where
+ * lse_i = -inf) and delta_i = sum_d dout_i[d] * out_i[d]:
+ *   dS_ij = P_ij * (dout_i . v_j - delta_i)
+ *   dq_i  = scale * sum_j dS_ij k_j
+ *   dk_j  = scale * sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i    (summed over the heads that share j)
+ *   dtable[n, h] = sum of dS_ij of head h over the pairs in bucket n
+ * Frames at or past the lengths get zero gradients, and q, k, v, out, lse and
+ * dout are not read there.  The maps P and dS are recomputed, never stored.
+ *
+ * dq [B][Tq][H][D], dk, dv [B][Tk][Hkv][D] have the strides shape->dq, dk, dv
+ * and must not overlap each other or an input; dtable [buckets][H] is float.
+ * Each may be NULL (not computed).  An empty batch still writes dtable = 0.
+ * Scores, P, delta and all sums are float32 (dtable's across workgroups fp64);
+ * DW_BF16 rounds P and dS to bf16 for their products with dout, q and k, but
+ * not for dtable.  No atomics: repeated calls agree bit for bit.
+ * Errors: as dwattn_fwd; DW_ERR_INVALID_ARG also for a dtable without a table,
+ * a null lse or dout that holds elements, or an output aliasing an input.
+ */
+dw_status dwattn_bwd(const dw_attn *shape, const void *q, const void *k, const void *v, const void *table,
+                     const int32_t *map, const int32_t *q_lengths, const int32_t *k_lengths, const int32_t *q_pos,
+                     const void *out, const float *lse, const void *dout, void *dq, void *dk, void *dv, float *dtable,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -84,3 +84,108 @@ def test_norm_backward_validation(lib):
     assert f(P, N, N, P, P, P, N, N, N, N, N, N, N, 0, *a) == OK  # nothing asked for
     assert f(P, N, N, P, P, P, N, N, Q, N, N, N, N, 0, 16, 750, 1024, 1.0, 0.1, 0, N) == INVALID and "rng" in err(lib)
     assert f(P, N, N, P, P, P, N, N, Q, N, N, N, N, 0, 16, 750, 1024, 1.0, 0.0, 3, N) == INVALID
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("item", "frame", "head")]
+
+
+class Attn(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "Tq", "Tk", "H", "Hkv", "D")] +
+                [(n, Strides) for n in ("q", "k", "v", "dq", "dk", "dv")] +
+                [(n, ctypes.c_int64) for n in ("buckets", "reach", "left", "right")] +
+                [("scale", ctypes.c_float), ("dtype", ctypes.c_int)])
+
+
+def attn(B=2, Tq=100, Tk=100, H=4, Hkv=2, D=64, buckets=32, reach=128, dtype=0, **more):
+    s = Attn(B, Tq, Tk, H, Hkv, D, buckets=buckets, reach=reach, left=-1, right=-1, scale=0.125, dtype=dtype)
+    for n, heads, frames in (("q", H, Tq), ("k", Hkv, Tk), ("v", Hkv, Tk), ("dq", H, Tq), ("dk", Hkv, Tk), ("dv", Hkv, Tk)):
+        setattr(s, n, Strides(frames * heads * D, heads * D, D))
+    for n, v in more.items():
+        setattr(s, n, v)
+    return s
+
+
+@pytest.fixture(scope="module")
+def alib(lib):
+    vp, sz, p = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(Attn)
+    lib.dwattn_rel_buckets.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
+    for n in ("fwd", "bwd"):
+        getattr(lib, f"dwattn_{n}_workspace_bytes").argtypes = [p]
+        getattr(lib, f"dwattn_{n}_workspace_bytes").restype = sz
+    lib.dwattn_fwd.argtypes = [p] + [vp] * 11 + [sz, vp]
+    lib.dwattn_bwd.argtypes = [p] + [vp] * 16 + [sz, vp]
+    return lib
+
+
+BAD_SHAPES = [(dict(B=-1), INVALID), (dict(D=-1), INVALID), (dict(H=3), INVALID), (dict(Hkv=0), INVALID),
+              (dict(dtype=2), INVALID), (dict(q=Strides(-1, 1, 1)), INVALID), (dict(buckets=0), INVALID),
+              (dict(reach=0), INVALID), (dict(D=129), UNSUPPORTED), (dict(reach=1025), UNSUPPORTED),
+              (dict(Tq=(1 << 28) + 1), UNSUPPORTED), (dict(Tk=1 << 40), UNSUPPORTED), (dict(B=1 << 40), UNSUPPORTED),
+              (dict(B=1 << 20, H=1 << 10, Hkv=1 << 10), UNSUPPORTED), (dict(k=Strides(1 << 60, 1, 1)), UNSUPPORTED),
+              (dict(v=Strides(1, (1 << 62), 1)), UNSUPPORTED)]
+
+
+def test_attention_validation(alib):
+    f = alib.dwattn_fwd
+    good = attn()
+    # shape, q, k, v, table, map, q_lengths, k_lengths, q_pos, out, lse, workspace, bytes, stream
+    for bad, status in BAD_SHAPES:
+        assert f(attn(**bad), P, P, P, P, P, N, N, N, Q, N, W, 1 << 40, N) == status, bad
+    assert f(None, P, P, P, P, P, N, N, N, Q, N, W, 1 << 40, N) == INVALID
+    assert f(good, P, P, P, P, N, N, N, N, Q, N, W, 1 << 40, N) == INVALID and "map" in err(alib)
+    assert f(good, P, P, P, N, P, N, N, N, Q, N, W, 1 << 40, N) == INVALID
+    for i in (0, 1, 2, 8):
+        args = [P, R, S, P, P, N, N, N, Q, N, W, 1 << 40, N]
+        args[i] = N
+        assert f(good, *args) == INVALID and "NULL" in err(alib)
+    for alias in (P, R, S):
+        assert f(good, P, R, S, P, P, N, N, N, alias, N, W, 1 << 40, N) == INVALID and "alias" in err(alib)
+    few = attn(B=1, Tq=1, Tk=5000)
+    need = alib.dwattn_fwd_workspace_bytes(few)
+    assert need > 0 and f(few, P, P, P, P, P, N, N, N, Q, N, W, need - 1, N) == WORKSPACE
+    assert f(few, P, P, P, P, P, N, N, N, Q, N, N, need, N) == WORKSPACE and "workspace" in err(alib)
+    assert alib.dwattn_fwd_workspace_bytes(attn(B=64, Tq=1000, Tk=1000)) == 0
+    assert alib.dwattn_fwd_workspace_bytes(attn(D=500)) == 0 and alib.dwattn_fwd_workspace_bytes(None) == 0
+    for empty in (dict(B=0), dict(Tq=0), dict(H=0, Hkv=0), dict(D=0)):
+        assert f(attn(**empty), N, N, N, N, N, N, N, N, N, N, N, 0, N) == OK
+
+
+def test_attention_backward_validation(alib):
+    f, good = alib.dwattn_bwd, attn()
+    big = 1 << 40
+    X = [ctypes.c_void_p(0x10000 * i) for i in range(1, 12)]
+    # q, k, v, table, map, q_lengths, k_lengths, q_pos, out, lse, dout, dq, dk, dv, dtable, workspace
+    a = [X[0], X[1], X[2], X[3], X[4], N, N, N, X[5], X[6], X[7], X[8], X[9], X[10], P, W]
+    for bad, status in BAD_SHAPES + [(dict(dq=Strides(-1, 1, 1)), INVALID), (dict(dk=Strides(1 << 60, 1, 1)), UNSUPPORTED)]:
+        assert f(attn(**bad), *a, big, N) == status, bad
+
+    def with_(**k):
+        names = "q k v table map q_lengths k_lengths q_pos out lse dout dq dk dv dtable workspace".split()
+        return [k.get(n, v) for n, v in zip(names, a)]
+
+    for n in ("q", "k", "v", "out", "lse", "dout"):
+        assert f(good, *with_(**{n: N}), big, N) == INVALID and "NULL" in err(alib), n
+    assert f(good, *with_(table=N, map=N), big, N) == INVALID and "dtable" in err(alib)
+    assert f(good, *with_(map=N), big, N) == INVALID
+    for n in ("dq", "dk", "dv"):
+        for o in (X[0], X[1], X[2], X[5], X[7]):
+            assert f(good, *with_(**{n: o}), big, N) == INVALID and "alias" in err(alib)
+    assert f(good, *with_(dq=X[9]), big, N) == INVALID and f(good, *with_(dv=X[9]), big, N) == INVALID
+    need = alib.dwattn_bwd_workspace_bytes(good)
+    assert need > 0 and f(good, *a, need - 1, N) == WORKSPACE and f(good, *with_(workspace=N), need, N) == WORKSPACE
+    assert alib.dwattn_bwd_workspace_bytes(attn(reach=2000)) == 0 and alib.dwattn_bwd_workspace_bytes(None) == 0
+    assert 0 < alib.dwattn_bwd_workspace_bytes(attn(buckets=0)) < need
+    assert f(good, *with_(dq=N, dk=N, dv=N, dtable=N), 0, N) == OK  # nothing asked for
+    assert f(attn(B=0), *[N] * 11, Q, R, S, N, N, 0, N) == OK
+
+
+def test_bucket_map_validation(alib):
+    f = alib.dwattn_rel_buckets
+    m = (ctypes.c_int32 * 4096)()
+    assert f(m, 32, 128, 1) == OK and f(m, 2, 1, 1) == OK and f(m, 1, 1, 0) == OK
+    assert f(None, 32, 128, 1) == INVALID and "NULL" in err(alib)
+    assert f(m, 1, 128, 1) == INVALID and f(m, 0, 128, 0) == INVALID and f(m, -4, 128, 0) == INVALID
+    assert f(m, 32, 8, 1) == INVALID and f(m, 32, 16, 0) == INVALID and f(m, 32, 9, 1) == OK
+    assert f(m, 1, 0, 0) == INVALID and f(m, 32, -5, 1) == INVALID
+    assert f(m, 32, 1025, 1) == UNSUPPORTED and f(m, 1 << 40, 1 << 50, 1) == UNSUPPORTED

@@ -3,9 +3,10 @@ definition in 64 bits.
 
 Tolerances.  Scores here stay below 32 in units of log2, so float32 arithmetic
 moves a weight by at most a few 2^-24 * 32 of itself, and out, a weighted mean
-of values below 6, by less than 2e-5.  bf16: the weights are rounded once (each
-moves by 2^-9 of itself at most, and their mean with them) and out once more:
-2^-8 * (max |v| that the head holds) bounds both together.
+of values below 6, by less than 2e-5.  bf16: each weight is rounded once, by at
+most 2^-8 of itself, and so is out: 2^-8 * (max |v|) holds the two together
+unless the weights' errors all have the sign of their values while the values
+all lie near the largest.
 """
 import numpy as np
 import pytest
@@ -13,7 +14,7 @@ import torch
 
 import block_ref as ref
 import datagen
-from gpu_util import Guarded, host64, say
+from gpu_util import Guarded, host64
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
