@@ -29,6 +29,8 @@ constexpr int kTile = 32;          // owned and streamed frames of one matrix ti
 constexpr int kBiasMargin = 64;    // entries beyond the map's ends: a tile that touches it reads without a clamp
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
+__device__ __forceinline__ int wave_of_block() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
+
 // The 16-deep operand of one 32x32 product: 8 values a lane, of the streamed
 // depth 8 * (lane / 32) + e.
 template <typename S>
@@ -72,6 +74,11 @@ __device__ __forceinline__ Frag<S> to_frag(const f32x16& c, int k) {
     return f;
 }
 
+// Waits here for an operand that was loaded from memory.  Left to its first use
+// inside the loop over tiles, the wait would hold up that loop's own loads.
+__device__ __forceinline__ void arrived(Frag<uint16_t>& f) { asm volatile("" : "+v"(f.r)); }
+__device__ __forceinline__ void arrived(Frag<float>& f) { asm volatile("" : "+v"(f.r[0]), "+v"(f.r[1])); }
+
 template <typename S>
 __device__ __forceinline__ Frag<S> to_frag(const RawGroup<S>& g) {
     Frag<S> f;
@@ -85,16 +92,20 @@ __device__ __forceinline__ Frag<S> to_frag(const RawGroup<S>& g) {
 }
 
 // ---------------------------------------------------------------------------
-// A tile of ROWS frames x DP head elements in LDS, each row followed by a pad
-// that puts neighbouring rows on other banks.
+// A tile of frames x DP head elements in LDS.  A row is a whole number of
+// 16-byte chunks and a pad that puts the rows that one instruction touches on
+// different banks: eight neighbouring rows for a 16-byte read, four for a
+// transposing one (measured, a 16-byte read from every lane: 8.5 cycles with
+// these strides as from linear addresses, 64 without the pad at 128 elements).
 // ---------------------------------------------------------------------------
 template <typename S, int DP>
 struct Tile {
-    static constexpr int kPad = (sizeof(S) == 2 ? 32 : 16) / (int)sizeof(S);
-    static constexpr int kStride = DP + kPad;
+    static constexpr int kChunks = DP * (int)sizeof(S) / 16;
+    static constexpr int kSlots = kChunks + (kChunks == 16 && sizeof(S) == 2 ? 3 : 1);  // with the pad
+    static constexpr int kStride = kSlots * 16 / (int)sizeof(S);
     static constexpr int kGroups = DP / kGroup;  // 8-element groups of a row
 
-    static constexpr int bytes(int rows) { return rows * kStride * (int)sizeof(S); }
+    static constexpr int bytes(int rows) { return rows * kSlots * 16; }
 
     // Operand whose rows are frames row0 + lane % 32 and whose depth is the
     // 16 head elements from 16 * c.
@@ -134,34 +145,97 @@ struct Tile {
     }
 };
 
-// A workgroup's share of a tile on its way from memory to LDS.  Rows from
-// `live` on and head elements from D on become zero and are not read.
+// A workgroup's share of a tile on its way from memory to LDS through
+// registers: start() reads, finish() writes.  Rows from `live` on and head
+// elements from D on become zero and are not read.
 template <typename S, int DP, int ROWS>
-struct TileLoad {
-    static constexpr int N = ROWS * Tile<S, DP>::kGroups / kAttnThreads;
-    static_assert(ROWS * Tile<S, DP>::kGroups % kAttnThreads == 0, "every thread takes the same number of groups");
+struct TileRegs {
+    static constexpr int kTotal = ROWS * Tile<S, DP>::kGroups;
+    static constexpr int N = (kTotal + kAttnThreads - 1) / kAttnThreads;
     RawGroup<S> g[N];
 
-    __device__ __forceinline__ void load(const S* base, int64_t stride, int live, int D) {
+    __device__ __forceinline__ void setup(int64_t, int) {}
+
+    __device__ __forceinline__ void start(const S* base, int64_t frame, int live, int D, S*) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int at = threadIdx.x + n * kAttnThreads;
             const int row = at / Tile<S, DP>::kGroups, col = at % Tile<S, DP>::kGroups * kGroup;
-            g[n] = load_group<S, true>(base + row * stride, col, row < live ? D : 0);
+            g[n] = load_group<S, true>(base + row * frame, col, row < live && at < kTotal ? D : 0);
         }
     }
 
-    __device__ __forceinline__ void store(S* tile) const {
+    __device__ __forceinline__ void finish(S* tile) const {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int at = threadIdx.x + n * kAttnThreads;
             const int row = at / Tile<S, DP>::kGroups, col = at % Tile<S, DP>::kGroups * kGroup;
+            if (kTotal % kAttnThreads != 0 && at >= kTotal) continue;
             u32x4* p = reinterpret_cast<u32x4*>(tile + row * Tile<S, DP>::kStride + col);
 #pragma unroll
             for (int i = 0; i < RawGroup<S>::N; ++i) p[i] = g[n].r[i];
         }
     }
 };
+
+// The same without registers: loads that write LDS themselves, 16 bytes a lane
+// to the wave's LDS address (m0) plus 16 times the lane.  A lane works out once
+// which row and chunk its place in the tile is; lanes on a pad sit out.  The
+// buffer ends at the last live row, so what lies past it arrives as zero.
+// start() returns with the loads in flight: wave_loads_done() and a barrier
+// come before the tile is read.  (Written as inline assembly, without a result
+// register, because the compiler would else wait for them before any LDS read.
+// Nothing else in these kernels takes its operand from m0.)
+template <typename S, int DP, int ROWS>
+struct TileDma {
+    static constexpr int kTotal = ROWS * Tile<S, DP>::kSlots;
+    static constexpr int N = (kTotal + kAttnThreads - 1) / kAttnThreads;
+    static constexpr uint32_t kSkip = 0xffffffffu, kZero = 0xfffffff0u;
+    uint32_t off[N];
+
+    __device__ __forceinline__ void setup(int64_t frame, int D) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int at = threadIdx.x + n * kAttnThreads;
+            const int row = at / Tile<S, DP>::kSlots, chunk = at % Tile<S, DP>::kSlots;
+            off[n] = at >= kTotal || chunk >= Tile<S, DP>::kChunks ? kSkip
+                     : chunk * 16 >= D * (int)sizeof(S)             ? kZero
+                                                        : (uint32_t)(row * frame * (int)sizeof(S)) + chunk * 16;
+        }
+    }
+
+    __device__ __forceinline__ void start(const S* base, int64_t frame, int live, int D, S* tile) {
+        if (live > ROWS) live = ROWS;
+        const uint32_t bytes = (uint32_t)(((live - 1) * frame + D) * (int)sizeof(S));
+        const uint64_t at = (uint64_t)base;
+        const u32x4 rsrc = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, (uint32_t)kBufferFlags};
+        const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)tile +
+                             wave_of_block() * 1024;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if (off[n] != kSkip)
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                             :: "s"(lds + n * kAttnThreads * 16), "v"(off[n]), "s"(rsrc)
+                             : "memory");
+        }
+    }
+
+    __device__ __forceinline__ void finish(S*) const {}
+};
+
+// What direct loads ask of a tensor: whole groups of 8 elements, aligned 16-byte
+// chunks, frames that do not overlap, and a tile's offsets in 31 bits.
+template <typename S>
+bool dma_fits(const void* base, const AttnStride& s, int64_t D) {
+    const int64_t chunk = 16 / (int64_t)sizeof(S);
+    return (uintptr_t)base % 16 == 0 && D % kGroup == 0 && s.item % chunk == 0 && s.frame % chunk == 0 &&
+           s.head % chunk == 0 && s.frame >= D && s.frame <= ((int64_t)1 << 29) / 256;
+}
+
+template <typename S, int DP, int ROWS, bool DMA>
+using TileLoad = std::conditional_t<DMA, TileDma<S, DP, ROWS>, TileRegs<S, DP, ROWS>>;
+
+__device__ __forceinline__ void wave_loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 // Arguments
@@ -197,6 +271,26 @@ hipError_t with_head_width(int64_t D, F&& f) {
     if (D <= 96) return f(std::integral_constant<int, 96>());
     return f(std::integral_constant<int, 128>());
 }
+
+// The workgroup's place: its block of owned frames and its (item, head) pair.
+// Workgroups go round the XCDs, and a pair's blocks share its keys and values
+// in one XCD's L2, so whole pairs are dealt to the XCDs in turn (in turn, not in
+// runs: an XCD then gets short and long items alike).  Pairs beyond a multiple
+// of the XCDs are dealt block by block.
+struct AttnPlace {
+    uint32_t block, pair;
+    __device__ __forceinline__ AttnPlace(uint32_t id, uint32_t blocks, uint32_t pairs) {
+        const uint32_t even = pairs / kNumXcd * kNumXcd;
+        if (id < even * blocks) {
+            const uint32_t slot = id / kNumXcd;
+            pair = slot / blocks * kNumXcd + id % kNumXcd;
+            block = slot % blocks;
+        } else {
+            pair = id / blocks;
+            block = id % blocks;
+        }
+    }
+};
 
 // One item's valid frames and the position of its first query on the key axis.
 struct AttnItem {

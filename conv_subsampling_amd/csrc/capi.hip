@@ -134,6 +134,7 @@ dw_status check_attn(const char* fn, const dw_attn* a, bool bias, dw::AttnShape*
     if (t != DW_OK) return t;
     if (a->H > 0 && (a->Hkv < 1 || a->H % a->Hkv != 0))
         return fail(DW_ERR_INVALID_ARG, "%s: H=%lld is not a multiple of Hkv=%lld", fn, (long long)a->H, (long long)a->Hkv);
+    if (!(a->scale > 0.0f)) return fail(DW_ERR_INVALID_ARG, "%s: scale must be positive", fn);
     if (bias && (a->buckets < 1 || a->reach < 1))
         return fail(DW_ERR_INVALID_ARG, "%s: a bias needs at least one bucket and a reach of one frame", fn);
     if (a->D > dw::kAttnMaxHead)

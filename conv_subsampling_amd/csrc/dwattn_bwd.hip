@@ -44,29 +44,23 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// Streamed frames of a tile (two tiles of each tensor are in LDS).
 template <typename S, int DP>
-struct DqShape {
-    static constexpr int BN = sizeof(S) == 4 && DP > 96 ? 32 : 64;
-    static constexpr int kWaves = DP > 64 ? 1 : 2;
-};
+constexpr int kBwdRows = sizeof(S) * DP <= 128 ? 64 : 32;
 
-template <typename S, int DP>
-__global__ __launch_bounds__(kAttnThreads, (DqShape<S, DP>::kWaves)) void attn_dq_kernel(const AttnBwd a) {
-    constexpr int BN = DqShape<S, DP>::BN, KT = BN / kTile, NC = DP / 16, ND = DP / 32;
+template <typename S, int DP, bool DMA>
+__global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) ? 1 : 2)) void attn_dq_kernel(const AttnBwd a) {
+    constexpr int BN = kBwdRows<S, DP>, KT = BN / kTile, NC = DP / 16, ND = DP / 32;
     typedef Tile<S, DP> T;
     extern __shared__ __align__(16) char smem[];
-    S* ktile = (S*)smem;
-    S* vtile = (S*)(smem + T::bytes(BN));
-    float* bias = (float*)(smem + 2 * T::bytes(BN));
+    float* bias = (float*)(smem + 4 * T::bytes(BN));
     const int nbias = 2 * a.R + 1 + 2 * kBiasMargin;
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, half = lane / 32;
+    const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
     float* square = bias + (nbias + 3) / 4 * 4 + wave * kTile * kDiag;                      // a tile of dS
     float* sums = bias + (nbias + 3) / 4 * 4 + 4 * kTile * kDiag + wave * nbias;            // by distance, of this wave
 
-    uint32_t id = xcd_contiguous_block(blockIdx.x, gridDim.x);
-    const int qb = id % a.nqb;
-    id /= a.nqb;
-    const int h = id % a.H, b = id / a.H;
+    const AttnPlace place(blockIdx.x, a.nqb, a.B * a.H);
+    const int qb = place.block, h = place.pair % a.H, b = place.pair / a.H;
     const AttnItem item(a, b);
     const int i0 = qb * kBwdOwned, iw = i0 + wave * kTile, i = iw + lane % 32;
     const bool live = i < item.nq;
@@ -84,10 +78,10 @@ __global__ __launch_bounds__(kAttnThreads, (DqShape<S, DP>::kWaves)) void attn_d
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int d = 16 * c + 8 * half, D = live ? a.D : 0;
-            const RawGroup<S> gr = load_group<S, true>((const S*)a.dout + at, d, D);
-            q[c] = to_frag<S>(load_group<S, true>(row, d, D));
+            const RawGroup<S> gr = load_group<S, !DMA>((const S*)a.dout + at, d, D);
+            q[c] = to_frag<S>(load_group<S, !DMA>(row, d, D));
             g[c] = to_frag<S>(gr);
-            const Vf<kGroup> x = widen<S>(gr), o = widen<S>(load_group<S, true>((const S*)a.out + at, d, D));
+            const Vf<kGroup> x = widen<S>(gr), o = widen<S>(load_group<S, !DMA>((const S*)a.out + at, d, D));
 #pragma unroll
             for (int e = 0; e < kGroup; ++e) delta = fmaf(x.v[e], o.v[e], delta);
         }
@@ -110,23 +104,37 @@ __global__ __launch_bounds__(kAttnThreads, (DqShape<S, DP>::kWaves)) void attn_d
 
     const S* kbase = (const S*)a.k + b * a.ks.item + (int64_t)(h / (a.H / a.Hkv)) * a.ks.head;
     const S* vbase = (const S*)a.v + b * a.vs.item + (int64_t)(h / (a.H / a.Hkv)) * a.vs.head;
-    TileLoad<S, DP, BN> kl, vl;
-    if (j0 < j1) {
-        kl.load(kbase + (int64_t)j0 * a.ks.frame, a.ks.frame, j1 - j0, a.D);
-        vl.load(vbase + (int64_t)j0 * a.vs.frame, a.vs.frame, j1 - j0, a.D);
+    TileLoad<S, DP, BN, DMA> kl, vl;
+    kl.setup(a.ks.frame, a.D);
+    vl.setup(a.vs.frame, a.D);
+    auto ktile_of = [&](int t) { return (S*)(smem + (t & 1) * 2 * T::bytes(BN)); };
+    auto vtile_of = [&](int t) { return (S*)((char*)ktile_of(t) + T::bytes(BN)); };
+    auto start = [&](int t) {
+        const int64_t j = j0 + t * BN;
+        kl.start(kbase + j * a.ks.frame, a.ks.frame, j1 - (int)j, a.D, ktile_of(t));
+        vl.start(vbase + j * a.vs.frame, a.vs.frame, j1 - (int)j, a.D, vtile_of(t));
+    };
+    auto finish = [&](int t) {
+        kl.finish(ktile_of(t));
+        vl.finish(vtile_of(t));
+    };
+    const int tiles = j1 > j0 ? (j1 - j0 + BN - 1) / BN : 0;
+    if (tiles) {
+        start(0);
+        finish(0);
     }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) arrived(q[c]), arrived(g[c]);
+    asm volatile("" : "+v"(lse2), "+v"(delta));
     f32x16 acc[ND] = {};
     float low = 0.0f, high = 0.0f;  // sums of dS past the map's reach
-    for (int jt = j0; jt < j1; jt += BN) {
+    for (int t = 0; t < tiles; ++t) {
+        wave_loads_done();
         __syncthreads();
-        kl.store(ktile);
-        vl.store(vtile);
-        __syncthreads();
-        if (jt + BN < j1) {
-            const int64_t j = jt + BN;
-            kl.load(kbase + j * a.ks.frame, a.ks.frame, j1 - (int)j, a.D);
-            vl.load(vbase + j * a.vs.frame, a.vs.frame, j1 - (int)j, a.D);
-        }
+        if (t + 1 < tiles) start(t + 1);
+        const S* ktile = ktile_of(t);
+        const S* vtile = vtile_of(t);
+        const int jt = j0 + t * BN;
 #pragma unroll
         for (int u = 0; u < KT; ++u) {
             const int row0 = u * kTile, j = jt + row0;
@@ -196,6 +204,7 @@ __global__ __launch_bounds__(kAttnThreads, (DqShape<S, DP>::kWaves)) void attn_d
                 }
             }
         }
+        if (t + 1 < tiles) finish(t + 1);
     }
     if (a.dq && i < a.Tq) {
         S* row = (S*)a.dq + b * a.dqs.item + (int64_t)i * a.dqs.frame + h * a.dqs.head;
@@ -269,28 +278,18 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dtable(const double* __rest
 }
 
 // ---------------------------------------------------------------------------
-template <typename S, int DP>
-struct DkvShape {
-    static constexpr int BQ = sizeof(S) == 4 && DP > 96 ? 32 : 64;
-    static constexpr int kWaves = DP > 64 || sizeof(S) == 4 ? 1 : 2;
-};
-
-template <typename S, int DP>
-__global__ __launch_bounds__(kAttnThreads, (DkvShape<S, DP>::kWaves)) void attn_dkv_kernel(const AttnBwd a) {
-    constexpr int BQ = DkvShape<S, DP>::BQ, QT = BQ / kTile, NC = DP / 16, ND = DP / 32;
+template <typename S, int DP, bool DMA>
+__global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) void attn_dkv_kernel(const AttnBwd a) {
+    constexpr int BQ = kBwdRows<S, DP>, QT = BQ / kTile, NC = DP / 16, ND = DP / 32;
     typedef Tile<S, DP> T;
     extern __shared__ __align__(16) char smem[];
-    S* qtile = (S*)smem;
-    S* gtile = (S*)(smem + T::bytes(BQ));
-    float* stat = (float*)(smem + 2 * T::bytes(BQ));  // [2][BQ]: lse in units of log2, delta
-    float* bias = stat + 2 * BQ;
+    float* stats = (float*)(smem + 4 * T::bytes(BQ));  // of two tiles: [2][2][BQ], lse in units of log2, then delta
+    float* bias = stats + 4 * BQ;
     const int nbias = 2 * a.R + 1 + 2 * kBiasMargin;
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, half = lane / 32;
+    const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
 
-    uint32_t id = xcd_contiguous_block(blockIdx.x, gridDim.x);
-    const int kb = id % a.nkb;
-    id /= a.nkb;
-    const int hk = id % a.Hkv, b = id / a.Hkv, group = a.H / a.Hkv;
+    const AttnPlace place(blockIdx.x, a.nkb, a.B * a.Hkv);
+    const int kb = place.block, hk = place.pair % a.Hkv, b = place.pair / a.Hkv, group = a.H / a.Hkv;
     const AttnItem item(a, b);
     const int j0 = kb * kBwdOwned, jw = j0 + wave * kTile, j = jw + lane % 32;
     const bool live = j < item.nk;
@@ -301,8 +300,8 @@ __global__ __launch_bounds__(kAttnThreads, (DkvShape<S, DP>::kWaves)) void attn_
         const S* vr = (const S*)a.v + b * a.vs.item + (int64_t)(live ? j : 0) * a.vs.frame + hk * a.vs.head;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            k[c] = to_frag<S>(load_group<S, true>(kr, 16 * c + 8 * half, live ? a.D : 0));
-            v[c] = to_frag<S>(load_group<S, true>(vr, 16 * c + 8 * half, live ? a.D : 0));
+            k[c] = to_frag<S>(load_group<S, !DMA>(kr, 16 * c + 8 * half, live ? a.D : 0));
+            v[c] = to_frag<S>(load_group<S, !DMA>(vr, 16 * c + 8 * half, live ? a.D : 0));
         }
     }
     const int mine0 = item.first_query(a, j), mine1 = item.last_query(a, j);
@@ -319,33 +318,48 @@ __global__ __launch_bounds__(kAttnThreads, (DkvShape<S, DP>::kWaves)) void attn_
     f32x16 dk[ND] = {}, dv[ND] = {};
     for (int n = 0; n < group; ++n) {
         const int h = hk * group + n;
-        if (a.table) {
-            __syncthreads();
-            fill_bias<S>(a, h, bias);
-        }
+        __syncthreads();  // the head before is done with the tiles and its bias
+        if (a.table) fill_bias<S>(a, h, bias);
         const S* qbase = (const S*)a.q + b * a.qs.item + h * a.qs.head;
         const S* gbase = (const S*)a.dout + ((int64_t)b * a.Tq * a.H + h) * a.D;
         const int64_t gstride = (int64_t)a.H * a.D, srow = ((int64_t)b * a.H + h) * a.Tq;
-        TileLoad<S, DP, BQ> ql, gl;
-        if (i0 < i1) {
-            ql.load(qbase + (int64_t)i0 * a.qs.frame, a.qs.frame, i1 - i0, a.D);
-            gl.load(gbase + (int64_t)i0 * gstride, gstride, i1 - i0, a.D);
-        }
-        for (int it = i0; it < i1; it += BQ) {
-            __syncthreads();
-            ql.store(qtile);
-            gl.store(gtile);
+        TileLoad<S, DP, BQ, DMA> ql, gl;
+        ql.setup(a.qs.frame, a.D);
+        gl.setup(gstride, a.D);
+        float row_lse = 0.0f, row_delta = 0.0f;
+        auto qtile_of = [&](int t) { return (S*)(smem + (t & 1) * 2 * T::bytes(BQ)); };
+        auto gtile_of = [&](int t) { return (S*)((char*)qtile_of(t) + T::bytes(BQ)); };
+        auto start = [&](int t) {
+            const int64_t i = i0 + t * BQ;
+            const bool mine = threadIdx.x < BQ && i + threadIdx.x < i1;
+            row_lse = mine ? a.lse[srow + i + threadIdx.x] : -__builtin_inff();
+            row_delta = mine ? a.delta[srow + i + threadIdx.x] : 0.0f;
+            ql.start(qbase + i * a.qs.frame, a.qs.frame, i1 - (int)i, a.D, qtile_of(t));
+            gl.start(gbase + i * gstride, gstride, i1 - (int)i, a.D, gtile_of(t));
+        };
+        auto finish = [&](int t) {
+            ql.finish(qtile_of(t));
+            gl.finish(gtile_of(t));
             if (threadIdx.x < BQ) {
-                const int i = it + threadIdx.x;
-                stat[threadIdx.x] = i < i1 ? lse_or_inf(a.lse[srow + i]) : __builtin_inff();
-                stat[BQ + threadIdx.x] = i < i1 ? a.delta[srow + i] : 0.0f;
+                stats[(t & 1) * 2 * BQ + threadIdx.x] = lse_or_inf(row_lse);
+                stats[(t & 1) * 2 * BQ + BQ + threadIdx.x] = row_delta;
             }
+        };
+        const int tiles = i1 > i0 ? (i1 - i0 + BQ - 1) / BQ : 0;
+        if (tiles) {
+            start(0);
+            finish(0);
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) arrived(k[c]), arrived(v[c]);
+        for (int t = 0; t < tiles; ++t) {
+            wave_loads_done();
             __syncthreads();
-            if (it + BQ < i1) {
-                const int64_t i = it + BQ;
-                ql.load(qbase + i * a.qs.frame, a.qs.frame, i1 - (int)i, a.D);
-                gl.load(gbase + i * gstride, gstride, i1 - (int)i, a.D);
-            }
+            if (t + 1 < tiles) start(t + 1);
+            const S* qtile = qtile_of(t);
+            const S* gtile = gtile_of(t);
+            const float* stat = stats + (t & 1) * 2 * BQ;
+            const int it = i0 + t * BQ;
 #pragma unroll
             for (int u = 0; u < QT; ++u) {
                 const int row0 = u * kTile, i = it + row0;
@@ -393,6 +407,7 @@ __global__ __launch_bounds__(kAttnThreads, (DkvShape<S, DP>::kWaves)) void attn_
                     }
                 }
             }
+            if (t + 1 < tiles) finish(t + 1);
         }
     }
     if (j >= a.Tk) return;
@@ -429,19 +444,23 @@ size_t dwattn_bwd_workspace(const AttnShape& s) {
 
 template <typename S, int DP>
 static hipError_t launch_bwd(const AttnBwd& a, hipStream_t stream) {
-    typedef Tile<S, DP> T;
+    constexpr int kRows = kBwdRows<S, DP>;
     const int nbias = a.table ? 2 * a.R + 1 + 2 * kBiasMargin : 0;
     if (a.nqb > 0) {
-        const int lds = 2 * T::bytes(DqShape<S, DP>::BN) + (nbias + 3) / 4 * 16 +
+        const int lds = 4 * Tile<S, DP>::bytes(kRows) + (nbias + 3) / 4 * 16 +
                         (a.dist ? 4 * kTile * kDiag * 4 + 4 * nbias * 4 : 0);
-        hipLaunchKernelGGL((attn_dq_kernel<S, DP>), dim3((uint32_t)(a.B * a.H) * a.nqb), dim3(kAttnThreads), lds, stream, a);
+        const bool dma = dma_fits<S>(a.k, a.ks, a.D) && dma_fits<S>(a.v, a.vs, a.D);
+        hipLaunchKernelGGL((dma ? attn_dq_kernel<S, DP, true> : attn_dq_kernel<S, DP, false>),
+                           dim3((uint32_t)(a.B * a.H) * a.nqb), dim3(kAttnThreads), lds, stream, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (a.nkb > 0 && (a.dk || a.dv)) {
-        constexpr int BQ = DkvShape<S, DP>::BQ;
-        const int lds = 2 * T::bytes(BQ) + 2 * BQ * 4 + nbias * 4;
-        hipLaunchKernelGGL((attn_dkv_kernel<S, DP>), dim3((uint32_t)(a.B * a.Hkv) * a.nkb), dim3(kAttnThreads), lds, stream, a);
+        const int lds = 4 * Tile<S, DP>::bytes(kRows) + 4 * kRows * 4 + nbias * 4;
+        const AttnStride rows = {(int64_t)a.Tq * a.H * a.D, (int64_t)a.H * a.D, a.D};
+        const bool dma = dma_fits<S>(a.q, a.qs, a.D) && dma_fits<S>(a.dout, rows, a.D);
+        hipLaunchKernelGGL((dma ? attn_dkv_kernel<S, DP, true> : attn_dkv_kernel<S, DP, false>),
+                           dim3((uint32_t)(a.B * a.Hkv) * a.nkb), dim3(kAttnThreads), lds, stream, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -25,32 +25,27 @@ struct AttnFwd : AttnArgs {
 // below 2^kSlack, and most tiles need no rescaling of the accumulators.
 constexpr float kSlack = 8.0f;
 
-// Keys of a tile, and the waves per SIMD its registers are to allow: float rows
-// over 96 wide hold twice the registers in flight.
-template <typename S, int DP, int QW>
+// Keys of a tile, and the waves per SIMD its registers are to allow.
+template <typename S, int DP, int QW, bool DMA>
 struct FwdShape {
-    static constexpr bool kHeavy = sizeof(S) == 4 && DP > 96;
-    static constexpr int BN = QW == 1 ? 128 : kHeavy ? 32 : 64;
-    static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : 2;
+    static constexpr int BN = QW == 1 ? 128 : sizeof(S) * DP <= 128 ? 64 : 32;
+    static constexpr int kBuffers = QW == 1 ? 1 : 2;  // of the tiles
+    static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : DMA && sizeof(S) == 2 ? 3 : 2;
 };
 
-template <typename S, int DP, int QW>
-__global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW>::kWaves)) void attn_fwd_kernel(const AttnFwd a) {
-    constexpr int KW = 4 / QW, BN = FwdShape<S, DP, QW>::BN, KT = BN / kTile / KW, NC = DP / 16, ND = DP / 32;
+template <typename S, int DP, int QW, bool DMA>
+__global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) void attn_fwd_kernel(const AttnFwd a) {
+    constexpr int KW = 4 / QW, BN = FwdShape<S, DP, QW, DMA>::BN, KT = BN / kTile / KW, NC = DP / 16, ND = DP / 32;
+    constexpr int kBuffers = FwdShape<S, DP, QW, DMA>::kBuffers;
     typedef Tile<S, DP> T;
     extern __shared__ __align__(16) char smem[];
-    S* ktile = (S*)smem;
-    S* vtile = (S*)(smem + T::bytes(BN));
-    float* bias = (float*)(smem + 2 * T::bytes(BN));
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, half = lane / 32;
+    float* bias = (float*)(smem + 2 * kBuffers * T::bytes(BN));
+    const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
     const int wq = QW == 4 ? wave : 0, wk = QW == 4 ? 0 : wave;
 
-    uint32_t id = xcd_contiguous_block(blockIdx.x, gridDim.x);
-    const int split = id % a.splits;
-    id /= a.splits;
-    const int qb = id % a.nqb;
-    id /= a.nqb;
-    const int h = id % a.H, b = id / a.H;
+    const AttnPlace place(blockIdx.x, a.nqb * a.splits, a.B * a.H);
+    const int split = place.block % a.splits, qb = place.block / a.splits;
+    const int h = place.pair % a.H, b = place.pair / a.H;
     const AttnItem item(a, b);
     const int i0 = qb * (kTile * QW), iw = i0 + wq * kTile, i = iw + lane % 32;
     const bool live = i < item.nq;
@@ -61,7 +56,7 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW>::kWaves)) void a
     {
         const S* row = (const S*)a.q + b * a.qs.item + (int64_t)(live ? i : 0) * a.qs.frame + h * a.qs.head;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) q[c] = to_frag<S>(load_group<S, true>(row, 16 * c + 8 * half, live ? a.D : 0));
+        for (int c = 0; c < NC; ++c) q[c] = to_frag<S>(load_group<S, !DMA>(row, 16 * c + 8 * half, live ? a.D : 0));
     }
     // this lane's keys: [mine0, mine0 + mine)
     const int mine0 = item.first_key(a, i);
@@ -84,102 +79,111 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW>::kWaves)) void a
 
     const S* kbase = (const S*)a.k + b * a.ks.item + (int64_t)(h / (a.H / a.Hkv)) * a.ks.head;
     const S* vbase = (const S*)a.v + b * a.vs.item + (int64_t)(h / (a.H / a.Hkv)) * a.vs.head;
-    TileLoad<S, DP, BN> kl, vl;
-    if (t0 < t1) {
-        const int64_t j = j0 + t0 * BN;
-        kl.load(kbase + j * a.ks.frame, a.ks.frame, j1 - (int)j, a.D);
-        vl.load(vbase + j * a.vs.frame, a.vs.frame, j1 - (int)j, a.D);
-    }
+    TileLoad<S, DP, BN, DMA> kl, vl;
+    kl.setup(a.ks.frame, a.D);
+    vl.setup(a.vs.frame, a.D);
+    auto ktile = [&](int t) { return (S*)(smem + (kBuffers == 2 && (t & 1) ? 2 * T::bytes(BN) : 0)); };
+    auto vtile = [&](int t) { return (S*)((char*)ktile(t) + T::bytes(BN)); };
+    auto start = [&](int t) {
+        const int64_t j = j0 + t * BN;
+        kl.start(kbase + j * a.ks.frame, a.ks.frame, j1 - (int)j, a.D, ktile(t));
+        vl.start(vbase + j * a.vs.frame, a.vs.frame, j1 - (int)j, a.D, vtile(t));
+    };
+    auto finish = [&](int t) {
+        kl.finish(ktile(t));
+        vl.finish(vtile(t));
+    };
 
     f32x16 o[ND] = {};
     float top = -__builtin_inff(), sum = 0.0f;
+    if (t0 < t1) {
+        start(t0);
+        if (kBuffers == 2) finish(t0);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) arrived(q[c]);
     for (int t = t0; t < t1; ++t) {
-        __syncthreads();
-        kl.store(ktile);
-        vl.store(vtile);
-        __syncthreads();
-        if (t + 1 < t1) {
-            const int64_t j = j0 + (t + 1) * BN;
-            kl.load(kbase + j * a.ks.frame, a.ks.frame, j1 - (int)j, a.D);
-            vl.load(vbase + j * a.vs.frame, a.vs.frame, j1 - (int)j, a.D);
+        if (kBuffers == 1) {
+            __syncthreads();
+            finish(t);
         }
-        f32x16 s[KT];
-        bool any = false;
+        wave_loads_done();
+        __syncthreads();
+        if (t + 1 < t1) start(t + 1);
+        const S* kt = ktile(t);
+        const S* vt = vtile(t);
 #pragma unroll
         for (int u = 0; u < KT; ++u) {
             const int row0 = (wk * KT + u) * kTile, j = j0 + t * BN + row0;
-            if (j > some1 || j + kTile <= some0) {
+            if (j > some1 || j + kTile <= some0) continue;
+            Frag<S> k[NC];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[u][r] = -__builtin_inff();
-                continue;
-            }
-            any = true;
-            s[u] = f32x16{};
+            for (int c = 0; c < NC; ++c) k[c] = T::rows(kt, row0, c, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            f32x16 s = {};
 #pragma unroll
-            for (int c = 0; c < NC; ++c) s[u] = mma(T::rows(ktile, row0, c, lane), q[c], s[u]);
+            for (int c = 0; c < NC; ++c) s = mma(k[c], q[c], s);
             const int base = j - iw - item.pos32;
-            if (a.table) {
-                const Span span = span_of(base, a.R);
-                if (span == Span::kNear) {
-                    const float* p = bias + (base + a.R + kBiasMargin + 4 * half - lane % 32);
+            const Span span = span_of(base, a.R);
+            const bool looked_up = a.table && span == Span::kNear;
+            float m;
+            const bool edge = j < all0 || j + kTile - 1 > all1;
+            const uint32_t at = j + 4 * half - mine0;
+            // s becomes scale2 * s + bias - ref: looked up, the bias is added
+            // first; flat, it rides on the multiply (scale2 > 0, so the
+            // largest score is that of the largest product).
+            float flat = 0.0f;
+            if (looked_up) {
+                const float* p = bias + (base + a.R + kBiasMargin + 4 * half - lane % 32);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[u][r] = fmaf(s[u][r], a.scale2, p[acc_row(r, 0)]);
-                } else {
-                    const float v = bias[span == Span::kLow ? 0 : 2 * a.R + 2 * kBiasMargin];
+                for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale2, p[acc_row(r, 0)]);
+            } else if (a.table) {
+                flat = bias[span == Span::kLow ? 0 : 2 * a.R + 2 * kBiasMargin];
+            }
+            if (edge) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[u][r] = fmaf(s[u][r], a.scale2, v);
-                }
+                for (int r = 0; r < 16; ++r) s[r] = at + acc_row(r, 0) < mine ? s[r] : -__builtin_inff();
+            }
+            m = s[0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) m = fmaxf(m, s[r]);
+            m = fmaxf(m, swap_halves(m));
+            if (!looked_up) m = fmaf(m, a.scale2, flat);
+            if (__any(m > top + kSlack)) {
+                m = fmaxf(m, top);
+                const float f = m == -__builtin_inff() ? 1.0f : exp2_fast(top - m);
+                sum *= f;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[d][r] *= f;
+                top = m;
+            }
+            const float ref = top == -__builtin_inff() ? 0.0f : top;
+            if (looked_up) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = exp2_fast(s[r] - ref);
             } else {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[u][r] *= a.scale2;
+                for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], a.scale2, flat - ref));
             }
-            if (j < all0 || j + kTile - 1 > all1) {
-                const uint32_t at = j + 4 * half - mine0;
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[u][r] = at + acc_row(r, 0) < mine ? s[u][r] : -__builtin_inff();
-            }
-        }
-        if (!any) continue;
-        float m = s[0][0];
-#pragma unroll
-        for (int u = 0; u < KT; ++u)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) m = fmaxf(m, s[u][r]);
-        m = fmaxf(m, swap_halves(m));
-        if (__any(m > top + kSlack)) {
-            m = fmaxf(m, top);
-            const float f = m == -__builtin_inff() ? 1.0f : exp2_fast(top - m);
-            sum *= f;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[d][r] *= f;
-            top = m;
-        }
-        const float ref = top == -__builtin_inff() ? 0.0f : top;
-#pragma unroll
-        for (int u = 0; u < KT; ++u) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                s[u][r] = exp2_fast(s[u][r] - ref);
-                sum += s[u][r];
-            }
-            const int row0 = (wk * KT + u) * kTile;
+            for (int r = 0; r < 16; ++r) sum += s[r];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const Frag<S> p = to_frag<S>(s[u], k);
+                const Frag<S> p = to_frag<S>(s, k);
 #pragma unroll
-                for (int d = 0; d < ND; ++d) o[d] = mma(T::columns(vtile, row0 + 16 * k, d, lane), p, o[d]);
+                for (int d = 0; d < ND; ++d) o[d] = mma(T::columns(vt, row0 + 16 * k, d, lane), p, o[d]);
             }
         }
+        if (kBuffers == 2 && t + 1 < t1) finish(t + 1);
     }
     sum += swap_halves(sum);
 
     if constexpr (KW > 1) {  // join the waves: wave w takes head elements 32 w ..
         float* opart = (float*)smem;                                    // [KW][ND * 16][64]
         float* stat = (float*)(smem + KW * ND * 16 * 64 * 4);           // [KW][2][32]
-        static_assert(KW * ND * 16 * 64 * 4 + KW * 2 * 32 * 4 <= 2 * T::bytes(BN), "the tiles' room holds the join");
+        static_assert(KW * ND * 16 * 64 * 4 + KW * 2 * 32 * 4 <= 2 * kBuffers * T::bytes(BN), "the tiles' room holds the join");
         __syncthreads();
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -312,19 +316,22 @@ bool dwattn_fits(const AttnShape& s) {
            product_below(kMaxExtent, {s.B, s.H, s.Tq}) && product_below(kMaxExtent, {s.B, s.H, s.Tq, (s.D + 3) / 4 + 1});
 }
 
-template <typename S, int DP, int QW>
+template <typename S, int DP, int QW, bool DMA>
 static hipError_t launch_fwd(const AttnFwd& a, hipStream_t stream) {
-    constexpr int BN = FwdShape<S, DP, QW>::BN;
-    const int lds = 2 * Tile<S, DP>::bytes(BN) + (a.table ? attn_bias_bytes(a.R) : 0);
-    hipLaunchKernelGGL((attn_fwd_kernel<S, DP, QW>), dim3((uint32_t)(a.B * a.H) * a.nqb * a.splits), dim3(kAttnThreads),
-                       lds, stream, a);
+    typedef FwdShape<S, DP, QW, DMA> F;
+    const int lds = 2 * F::kBuffers * Tile<S, DP>::bytes(F::BN) + (a.table ? attn_bias_bytes(a.R) : 0);
+    hipLaunchKernelGGL((attn_fwd_kernel<S, DP, QW, DMA>), dim3((uint32_t)(a.B * a.H) * a.nqb * a.splits),
+                       dim3(kAttnThreads), lds, stream, a);
     return hipGetLastError();
 }
 
 template <typename S>
 static hipError_t fwd_of_type(const AttnFwd& a, int qw, hipStream_t stream) {
+    const bool dma = dma_fits<S>(a.k, a.ks, a.D) && dma_fits<S>(a.v, a.vs, a.D);
     const hipError_t e = with_head_width(a.D, [&](auto dp) {
-        return qw == 4 ? launch_fwd<S, dp.value, 4>(a, stream) : launch_fwd<S, dp.value, 1>(a, stream);
+        return qw != 4 ? launch_fwd<S, dp.value, 1, false>(a, stream)
+               : dma   ? launch_fwd<S, dp.value, 4, true>(a, stream)
+                       : launch_fwd<S, dp.value, 4, false>(a, stream);
     });
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t threads = (int64_t)a.B * a.H * a.Tq * ((a.D + 3) / 4);

@@ -527,7 +527,7 @@ typedef struct {
     dw_strides dq, dk, dv;  /* dwattn_bwd only */
     int64_t buckets, reach; /* of the bias: rows of the table; the map covers -reach .. reach, 1 to 1024 */
     int64_t left, right;    /* frames of context each side of a query; negative: all of them */
-    float scale;            /* of q . k, usually 1 / sqrt(D) */
+    float scale;            /* of q . k, positive, usually 1 / sqrt(D) */
     dw_dtype dtype;         /* of q, k, v, table, out, dout, dq, dk, dv */
 } dw_attn;
 
@@ -575,7 +575,7 @@ size_t dwattn_fwd_workspace_bytes(const dw_attn *shape);
  * for their product with v (their sum is taken before), and out once.
  * Repeated calls agree bit for bit.
  * Errors: DW_ERR_INVALID_ARG for a null pointer that holds elements, a negative
- * size or stride, H not a multiple of Hkv, a table without a map or the other
+ * size or stride, a scale that is not positive, H not a multiple of Hkv, a table without a map or the other
  * way round, buckets or reach below 1, a bad dtype, or out aliasing an input;
  * DW_ERR_UNSUPPORTED for D > 128, reach > 1024 or sizes too large for one
  * launch; DW_ERR_WORKSPACE for a missing or short workspace.
