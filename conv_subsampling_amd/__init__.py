@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -51,14 +52,9 @@ _vp, _i64, _sz, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.
 _f32, _f64 = ctypes.c_float, ctypes.c_double
 
 
-class _Strides(ctypes.Structure):
-    _fields_ = [("item", _i64), ("frame", _i64), ("head", _i64)]
-
-
-class _Attn(ctypes.Structure):
-    _fields_ = ([(n, _i64) for n in ("B", "Tq", "Tk", "H", "Hkv", "D")] +
-                [(n, _Strides) for n in ("q", "k", "v", "dq", "dk", "dv")] +
-                [(n, _i64) for n in ("buckets", "reach", "left", "right")] + [("scale", _f32), ("dtype", _int)])
+# struct dw_attn: 6 sizes, the strides of q, k, v, dq, dk and dv, buckets, reach,
+# left, right; scale, dtype.
+_attn_struct = struct.Struct("=28qfi")
 
 
 def _bind(path: str) -> ctypes.CDLL:
@@ -112,7 +108,7 @@ def _bind(path: str) -> ctypes.CDLL:
     lib.dwnorm_bwd_workspace_bytes.argtypes = [_i64] * 3
     lib.dwnorm_bwd.restype = _int
     lib.dwnorm_bwd.argtypes = [_vp] * 13 + [_sz] + [_i64] * 3 + [_f32, _f64, _int, _vp]
-    attn = ctypes.POINTER(_Attn)
+    attn = ctypes.c_char_p  # a packed dw_attn
     lib.dwattn_rel_buckets.restype = _int
     lib.dwattn_rel_buckets.argtypes = [_vp, _i64, _i64, _int]
     lib.dwattn_fwd_workspace_bytes.restype = _sz
@@ -143,6 +139,9 @@ def _ptr(t):
 
 
 def _dev_tensor(name, t, dtype, device, shape=None, allow_none=False):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t  # the usual case, in one test: small calls are bound by the host
     if t is None:
         if allow_none:
             return None
@@ -160,7 +159,14 @@ def _dev_tensor(name, t, dtype, device, shape=None, allow_none=False):
     return t
 
 
+# The stream's handle without a torch.cuda.Stream object around it, which costs
+# as much as a small kernel.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -483,9 +489,7 @@ def dwdrop_fwd(x, rng, p: float, residual=None, alpha: float = 1.0, y=None):
     st, code = _storage(x)
     _dev_tensor("x", x, st, dev)
     _dev_tensor("residual", residual, st, dev, x.shape, allow_none=True)
-    if y is None:
-        y = torch.empty_like(x)
-    _dev_tensor("y", y, st, dev, x.shape)
+    y = torch.empty_like(x) if y is None else _dev_tensor("y", y, st, dev, x.shape)
     rows, C = _rows(x)
     _check(_lib.dwdrop_fwd(_ptr(x), _ptr(residual), _ptr(y), _ptr(_rng(rng, p, dev)), rows, C, p, alpha, code,
                            _stream(dev)))
@@ -497,9 +501,7 @@ def dwdrop_bwd(dy, rng, p: float, alpha: float = 1.0, dx=None):
     dev = dy.device
     st, code = _storage(dy)
     _dev_tensor("dy", dy, st, dev)
-    if dx is None:
-        dx = torch.empty_like(dy)
-    _dev_tensor("dx", dx, st, dev, dy.shape)
+    dx = torch.empty_like(dy) if dx is None else _dev_tensor("dx", dx, st, dev, dy.shape)
     rows, C = _rows(dy)
     _check(_lib.dwdrop_bwd(_ptr(dy), _ptr(dx), _ptr(_rng(rng, p, dev)), rows, C, p, alpha, code, _stream(dev)))
     return dx
@@ -523,19 +525,20 @@ def dwnorm_fwd(x, gamma=None, beta=None, lengths=None, residual=None, rng=None, 
     _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
     _dev_tensor("residual", residual, st, dev, (B, T, C), allow_none=True)
     _rng(rng, p, dev)
-    if y is None:
-        y = torch.empty_like(x)
     plain = residual is None and p == 0 and alpha == 1.0 and sum is None
-    if sum is None and "sum" in need and not plain:
+    y = torch.empty_like(x) if y is None else _dev_tensor("y", y, st, dev, (B, T, C))
+    if sum is not None:
+        _dev_tensor("sum", sum, st, dev, (B, T, C))
+    elif "sum" in need and not plain:
         sum = torch.empty_like(x)
-    if mean is None and "mean" in need:
+    if mean is not None:
+        _dev_tensor("mean", mean, f32, dev, (B, T))
+    elif "mean" in need:
         mean = torch.empty((B, T), dtype=f32, device=dev)
-    if rstd is None and "rstd" in need:
-        rstd = torch.empty((B, T), dtype=f32, device=dev)
-    _dev_tensor("y", y, st, dev, (B, T, C))
-    _dev_tensor("sum", sum, st, dev, (B, T, C), allow_none=True)
-    _dev_tensor("mean", mean, f32, dev, (B, T), allow_none=True)
-    _dev_tensor("rstd", rstd, f32, dev, (B, T), allow_none=True)
+    if rstd is not None:
+        _dev_tensor("rstd", rstd, f32, dev, (B, T))
+    elif "rstd" in need:
+        rstd = torch.empty((B, T), dtype=f32, device=dev) if mean is None else torch.empty_like(mean)
     _check(_lib.dwnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(beta), _ptr(lengths), _ptr(rng), _ptr(y),
                            _ptr(sum), _ptr(mean), _ptr(rstd), B, T, C, eps, alpha, p, code, _stream(dev)))
     return y, x if plain and "sum" in need else sum, mean, rstd
@@ -564,18 +567,22 @@ def dwnorm_bwd(sum, gamma, lengths, mean, rstd, dy, dsum=None, rng=None, p: floa
     _dev_tensor("dy", dy, st, dev, (B, T, C))
     _dev_tensor("dsum", dsum, st, dev, (B, T, C), allow_none=True)
     _rng(rng, p, dev)
-    if dx is None and "dx" in need:
+    if dx is not None:
+        _dev_tensor("dx", dx, st, dev, (B, T, C))
+    elif "dx" in need:
         dx = torch.empty_like(sum)
-    if dres is None and "dres" in need:
+    if dres is not None:
+        _dev_tensor("dres", dres, st, dev, (B, T, C))
+    elif "dres" in need:
         dres = torch.empty_like(sum)
-    if dgamma is None and "dgamma" in need:
+    if dgamma is not None:
+        _dev_tensor("dgamma", dgamma, f32, dev, (C,))
+    elif "dgamma" in need:
         dgamma = torch.empty((C,), dtype=f32, device=dev)
-    if dbeta is None and "dbeta" in need:
-        dbeta = torch.empty((C,), dtype=f32, device=dev)
-    _dev_tensor("dx", dx, st, dev, (B, T, C), allow_none=True)
-    _dev_tensor("dres", dres, st, dev, (B, T, C), allow_none=True)
-    _dev_tensor("dgamma", dgamma, f32, dev, (C,), allow_none=True)
-    _dev_tensor("dbeta", dbeta, f32, dev, (C,), allow_none=True)
+    if dbeta is not None:
+        _dev_tensor("dbeta", dbeta, f32, dev, (C,))
+    elif "dbeta" in need:
+        dbeta = torch.empty((C,), dtype=f32, device=dev) if dgamma is None else torch.empty_like(dgamma)
     ws_bytes = 0
     if dgamma is not None or dbeta is not None:
         if workspace is None:
@@ -616,7 +623,8 @@ def _heads(name, t, st, device, shape):
 
 
 def _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, right, scale):
-    """The problem's sizes for the C ABI, its tensors checked; and its storage type."""
+    """Checks the tensors; the storage type, and the fields of the C ABI's dw_attn before and after the strides of
+    the gradients."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B, Tq, H, D], k and v [B, Tk, Hkv, D]")
     dev = q.device
@@ -639,14 +647,21 @@ def _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, righ
         NB, reach = table.shape[0], buckets.shape[0] // 2
     for name, t in (("q_lengths", q_lengths), ("k_lengths", k_lengths), ("q_pos", q_pos)):
         _dev_tensor(name, t, torch.int32, dev, (B,), allow_none=True)
-    strides = [_Strides(*t.stride()[:3]) for t in (q, k, v)]
-    return _Attn(B, Tq, Tk, H, Hkv, D, *strides, buckets=NB, reach=reach, left=left, right=right,
-                 scale=D ** -0.5 if scale is None else scale, dtype=code), st
+    return st, (B, Tq, Tk, H, Hkv, D, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3]), (
+        NB, reach, _limit(left), _limit(right), D ** -0.5 if scale is None else scale, code)
+
+
+_NO_STRIDES = (0,) * 9   # dq, dk, dv of a call that has none
+
+
+def _limit(n: int) -> int:
+    return n if -1 <= n < 1 << 40 else (-1 if n < 0 else 1 << 40)
 
 
 def dwattn_fwd_workspace_bytes(q, k, v, left: int = -1, right: int = -1) -> int:
     """Bytes of workspace `dwattn_fwd` takes for tensors of these sizes."""
-    return int(_lib.dwattn_fwd_workspace_bytes(_attn_shape(q, k, v, None, None, None, None, None, left, right, None)[0]))
+    _, sizes, rest = _attn_shape(q, k, v, None, None, None, None, None, left, right, None)
+    return int(_lib.dwattn_fwd_workspace_bytes(_attn_struct.pack(*sizes, *_NO_STRIDES, *rest)))
 
 
 def dwattn_fwd(q, k, v, table=None, buckets=None, q_lengths=None, k_lengths=None, q_pos=None, left: int = -1,
@@ -658,20 +673,24 @@ def dwattn_fwd(q, k, v, table=None, buckets=None, q_lengths=None, k_lengths=None
     streaming chunk); left and right limit the context, negative for all of
     it.  Returns (out [B,Tq,H,D], lse float32 [B,H,Tq] or None if not in
     `need`); queries without a key give 0 and -inf."""
-    shape, st = _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, right, scale)
+    st, sizes, rest = _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, right, scale)
+    shape = _attn_struct.pack(*sizes, *_NO_STRIDES, *rest)
     dev = q.device
-    B, Tq, H, D = q.shape
+    B, Tq, _, H, _, D = sizes[:6]
     if out is None:
         out = torch.empty((B, Tq, H, D), dtype=st, device=dev)
-    if lse is None and "lse" in need:
+    else:
+        _dev_tensor("out", out, st, dev, (B, Tq, H, D))
+    if lse is not None:
+        _dev_tensor("lse", lse, torch.float32, dev, (B, H, Tq))
+    elif "lse" in need:
         lse = torch.empty((B, H, Tq), dtype=torch.float32, device=dev)
-    _dev_tensor("out", out, st, dev, (B, Tq, H, D))
-    _dev_tensor("lse", lse, torch.float32, dev, (B, H, Tq), allow_none=True)
-    if workspace is None:
-        need_ws = int(_lib.dwattn_fwd_workspace_bytes(shape))
+    if workspace is not None:
+        _dev_tensor("workspace", workspace, torch.uint8, dev)
+    else:
+        need_ws = _lib.dwattn_fwd_workspace_bytes(shape)
         if need_ws:
             workspace = torch.empty((need_ws,), dtype=torch.uint8, device=dev)
-    _dev_tensor("workspace", workspace, torch.uint8, dev, allow_none=True)
     _check(_lib.dwattn_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(table), _ptr(buckets), _ptr(q_lengths),
                            _ptr(k_lengths), _ptr(q_pos), _ptr(out), _ptr(lse), _ptr(workspace),
                            0 if workspace is None else workspace.numel(), _stream(dev)))
@@ -680,7 +699,8 @@ def dwattn_fwd(q, k, v, table=None, buckets=None, q_lengths=None, k_lengths=None
 
 def dwattn_bwd_workspace_bytes(q, k, v, table=None, buckets=None) -> int:
     """Bytes of workspace `dwattn_bwd` takes for tensors of these sizes."""
-    return int(_lib.dwattn_bwd_workspace_bytes(_attn_shape(q, k, v, table, buckets, None, None, None, -1, -1, None)[0]))
+    _, sizes, rest = _attn_shape(q, k, v, table, buckets, None, None, None, -1, -1, None)
+    return int(_lib.dwattn_bwd_workspace_bytes(_attn_struct.pack(*sizes, *_NO_STRIDES, *rest)))
 
 
 def dwattn_bwd(q, k, v, out, lse, dout, table=None, buckets=None, q_lengths=None, k_lengths=None, q_pos=None,
@@ -691,29 +711,36 @@ def dwattn_bwd(q, k, v, out, lse, dout, table=None, buckets=None, q_lengths=None
     storage type (given ones may have any strides above the last), dtable
     float32 [num_buckets,H]; those not in `need`, and dtable without a table,
     are skipped (None)."""
-    shape, st = _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, right, scale)
-    dev = q.device
-    B, Tq, H, D = q.shape
-    kv = tuple(k.shape)
+    st, sizes, rest = _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, right, scale)
+    dev, f32 = q.device, torch.float32
+    B, Tq, _, H, _, D = sizes[:6]
     _dev_tensor("out", out, st, dev, (B, Tq, H, D))
-    _dev_tensor("lse", lse, torch.float32, dev, (B, H, Tq))
+    _dev_tensor("lse", lse, f32, dev, (B, H, Tq))
     _dev_tensor("dout", dout, st, dev, (B, Tq, H, D))
-    if dq is None and "dq" in need:
-        dq = torch.empty((B, Tq, H, D), dtype=st, device=dev)
-    if dk is None and "dk" in need:
-        dk = torch.empty(kv, dtype=st, device=dev)
-    if dv is None and "dv" in need:
-        dv = torch.empty(kv, dtype=st, device=dev)
-    if dtable is None and "dtable" in need and table is not None:
-        dtable = torch.empty(tuple(table.shape), dtype=torch.float32, device=dev)
-    for name, t, like in (("dq", dq, (B, Tq, H, D)), ("dk", dk, kv), ("dv", dv, kv)):
-        if t is not None:
-            _heads(name, t, st, dev, like)
-            setattr(shape, name, _Strides(*t.stride()[:3]))
-    _dev_tensor("dtable", dtable, torch.float32, dev, None if table is None else table.shape, allow_none=True)
-    if workspace is None:
+    if dq is not None:
+        _heads("dq", dq, st, dev, q.shape)
+    elif "dq" in need:
+        dq = torch.empty_like(dout)
+    if dk is not None:
+        _heads("dk", dk, st, dev, k.shape)
+    elif "dk" in need:
+        dk = torch.empty(k.shape, dtype=st, device=dev)
+    if dv is not None:
+        _heads("dv", dv, st, dev, k.shape)
+    elif "dv" in need:
+        dv = torch.empty(k.shape, dtype=st, device=dev)
+    if dtable is not None:
+        if table is None:
+            raise ValueError("dtable needs a table")
+        _dev_tensor("dtable", dtable, f32, dev, table.shape)
+    elif "dtable" in need and table is not None:
+        dtable = torch.empty(table.shape, dtype=f32, device=dev)
+    strides = [n for t in (dq, dk, dv) for n in ((0, 0, 0) if t is None else t.stride()[:3])]
+    shape = _attn_struct.pack(*sizes, *strides, *rest)
+    if workspace is not None:
+        _dev_tensor("workspace", workspace, torch.uint8, dev)
+    else:
         workspace = torch.empty((max(int(_lib.dwattn_bwd_workspace_bytes(shape)), 1),), dtype=torch.uint8, device=dev)
-    _dev_tensor("workspace", workspace, torch.uint8, dev)
     _check(_lib.dwattn_bwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(table), _ptr(buckets), _ptr(q_lengths),
                            _ptr(k_lengths), _ptr(q_pos), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                            _ptr(dtable), _ptr(workspace), workspace.numel(), _stream(dev)))

@@ -58,6 +58,22 @@ __device__ __forceinline__ f32x16 mma(const Frag<float>& a, const Frag<float>& b
     return c;
 }
 
+// Stands between a run of products and the first arithmetic on their sums: the
+// wait states that the last product's result asks for before a vector
+// instruction may read it (16 + 2 for a float product, 8 + 4 for a bf16 one).
+// The compiler inserts them too, but where the sums sat in accumulation
+// registers and the reads behind a branch it was found to leave 13 of a float
+// product's 18 before the last register, which then lacked the last product.
+template <typename S>
+__device__ __forceinline__ void products_done() {
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (sizeof(S) == 4)
+        asm volatile("s_nop 15\n\ts_nop 3");
+    else
+        asm volatile("s_nop 11");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // Accumulator registers 8k .. 8k + 7 as the operand of the next product,
 // rounded to the storage type (bf16: the matrix instruction takes no wider
 // operand; the sums of a softmax are taken before the rounding).
@@ -276,15 +292,16 @@ hipError_t with_head_width(int64_t D, F&& f) {
 // Workgroups go round the XCDs, and a pair's blocks share its keys and values
 // in one XCD's L2, so whole pairs are dealt to the XCDs in turn (in turn, not in
 // runs: an XCD then gets short and long items alike).  Pairs beyond a multiple
-// of the XCDs are dealt block by block.
+// of the XCDs are dealt block by block.  longest_last: a block's work grows with
+// its index, so the last blocks of all pairs go first and the short ones fill up.
 struct AttnPlace {
     uint32_t block, pair;
-    __device__ __forceinline__ AttnPlace(uint32_t id, uint32_t blocks, uint32_t pairs) {
-        const uint32_t even = pairs / kNumXcd * kNumXcd;
+    __device__ __forceinline__ AttnPlace(uint32_t id, uint32_t blocks, uint32_t pairs, bool longest_last) {
+        const uint32_t each = pairs / kNumXcd, even = each * kNumXcd;
         if (id < even * blocks) {
             const uint32_t slot = id / kNumXcd;
-            pair = slot / blocks * kNumXcd + id % kNumXcd;
-            block = slot % blocks;
+            pair = (longest_last ? slot % each : slot / blocks) * kNumXcd + id % kNumXcd;
+            block = longest_last ? blocks - 1 - slot / each : slot % blocks;
         } else {
             pair = id / blocks;
             block = id % blocks;

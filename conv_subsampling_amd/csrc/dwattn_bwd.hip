@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
     float* square = bias + (nbias + 3) / 4 * 4 + wave * kTile * kDiag;                      // a tile of dS
     float* sums = bias + (nbias + 3) / 4 * 4 + 4 * kTile * kDiag + wave * nbias;            // by distance, of this wave
 
-    const AttnPlace place(blockIdx.x, a.nqb, a.B * a.H);
+    const AttnPlace place(blockIdx.x, a.nqb, a.B * a.H, a.left == kNoLimit && a.right != kNoLimit);
     const int qb = place.block, h = place.pair % a.H, b = place.pair / a.H;
     const AttnItem item(a, b);
     const int i0 = qb * kBwdOwned, iw = i0 + wave * kTile, i = iw + lane % 32;
@@ -145,6 +145,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
                 s = mma(T::rows(ktile, row0, c, lane), q[c], s);
                 ds = mma(T::rows(vtile, row0, c, lane), g[c], ds);
             }
+            products_done<S>();
             const int base = j - iw - item.pos32;
             const Span span = span_of(base, a.R);
             if (a.table && span == Span::kNear) {
@@ -206,6 +207,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
         }
         if (t + 1 < tiles) finish(t + 1);
     }
+    products_done<S>();
     if (a.dq && i < a.Tq) {
         S* row = (S*)a.dq + b * a.dqs.item + (int64_t)i * a.dqs.frame + h * a.dqs.head;
 #pragma unroll
@@ -288,7 +290,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
     const int nbias = 2 * a.R + 1 + 2 * kBiasMargin;
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
 
-    const AttnPlace place(blockIdx.x, a.nkb, a.B * a.Hkv);
+    const AttnPlace place(blockIdx.x, a.nkb, a.B * a.Hkv, a.right == kNoLimit && a.left != kNoLimit);
     const int kb = place.block, hk = place.pair % a.Hkv, b = place.pair / a.Hkv, group = a.H / a.Hkv;
     const AttnItem item(a, b);
     const int j0 = kb * kBwdOwned, jw = j0 + wave * kTile, j = jw + lane % 32;
@@ -370,6 +372,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
                     s = mma(T::rows(qtile, row0, c, lane), k[c], s);
                     ds = mma(T::rows(gtile, row0, c, lane), v[c], ds);
                 }
+                products_done<S>();
                 // distance of the tile's first key and first query; along the registers it falls
                 const int base = jw - i - item.pos32;
                 const Span span = span_of(base, a.R);
@@ -410,6 +413,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
             if (t + 1 < tiles) finish(t + 1);
         }
     }
+    products_done<S>();
     if (j >= a.Tk) return;
     S* kr = a.dk ? (S*)a.dk + b * a.dks.item + (int64_t)j * a.dks.frame + hk * a.dks.head : nullptr;
     S* vr = a.dv ? (S*)a.dv + b * a.dvs.item + (int64_t)j * a.dvs.frame + hk * a.dvs.head : nullptr;

@@ -30,7 +30,7 @@ template <typename S, int DP, int QW, bool DMA>
 struct FwdShape {
     static constexpr int BN = QW == 1 ? 128 : sizeof(S) * DP <= 128 ? 64 : 32;
     static constexpr int kBuffers = QW == 1 ? 1 : 2;  // of the tiles
-    static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : DMA && sizeof(S) == 2 ? 3 : 2;
+    static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : DMA && sizeof(S) == 2 && DP <= 128 ? 3 : 2;
 };
 
 template <typename S, int DP, int QW, bool DMA>
@@ -43,7 +43,7 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
     const int wq = QW == 4 ? wave : 0, wk = QW == 4 ? 0 : wave;
 
-    const AttnPlace place(blockIdx.x, a.nqb * a.splits, a.B * a.H);
+    const AttnPlace place(blockIdx.x, a.nqb * a.splits, a.B * a.H, a.left == kNoLimit && a.right != kNoLimit);
     const int split = place.block % a.splits, qb = place.block / a.splits;
     const int h = place.pair % a.H, b = place.pair / a.H;
     const AttnItem item(a, b);
@@ -116,6 +116,9 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
         for (int u = 0; u < KT; ++u) {
             const int row0 = (wk * KT + u) * kTile, j = j0 + t * BN + row0;
             if (j > some1 || j + kTile <= some0) continue;
+            // The tile's operands are read ahead of their use: the keys before
+            // the first product, the first half of the values before the softmax
+            // (as many as leave three waves a SIMD their registers).
             Frag<S> k[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c) k[c] = T::rows(kt, row0, c, lane);
@@ -123,32 +126,38 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
             f32x16 s = {};
 #pragma unroll
             for (int c = 0; c < NC; ++c) s = mma(k[c], q[c], s);
+            constexpr bool kAhead = sizeof(S) == 2;  // float's values would take twice the registers
+            Frag<S> v[ND];
+            if (kAhead) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d) v[d] = T::columns(vt, row0, d, lane);
+            }
+            products_done<S>();
             const int base = j - iw - item.pos32;
             const Span span = span_of(base, a.R);
-            const bool looked_up = a.table && span == Span::kNear;
-            float m;
             const bool edge = j < all0 || j + kTile - 1 > all1;
-            const uint32_t at = j + 4 * half - mine0;
-            // s becomes scale2 * s + bias - ref: looked up, the bias is added
-            // first; flat, it rides on the multiply (scale2 > 0, so the
-            // largest score is that of the largest product).
-            float flat = 0.0f;
-            if (looked_up) {
-                const float* p = bias + (base + a.R + kBiasMargin + 4 * half - lane % 32);
+            // s becomes the weights exp2(scale2 * s + bias - top).  The flat
+            // bias of a tile past the map's reach rides on the multiply
+            // (scale2 > 0, so the largest score is that of the largest
+            // product); a looked-up one is added first.
+            float factor = a.scale2, flat = 0.0f;
+            if (a.table && span == Span::kNear) {
+                const float* f = bias + (base + a.R + kBiasMargin + 4 * half - lane % 32);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale2, p[acc_row(r, 0)]);
+                for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale2, f[acc_row(r, 0)]);
+                factor = 1.0f;
             } else if (a.table) {
                 flat = bias[span == Span::kLow ? 0 : 2 * a.R + 2 * kBiasMargin];
             }
             if (edge) {
+                const uint32_t at = j + 4 * half - mine0;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = at + acc_row(r, 0) < mine ? s[r] : -__builtin_inff();
             }
-            m = s[0];
+            float m = s[0];
 #pragma unroll
             for (int r = 1; r < 16; ++r) m = fmaxf(m, s[r]);
-            m = fmaxf(m, swap_halves(m));
-            if (!looked_up) m = fmaf(m, a.scale2, flat);
+            m = fmaf(fmaxf(m, swap_halves(m)), factor, flat);
             if (__any(m > top + kSlack)) {
                 m = fmaxf(m, top);
                 const float f = m == -__builtin_inff() ? 1.0f : exp2_fast(top - m);
@@ -159,25 +168,22 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
                     for (int r = 0; r < 16; ++r) o[d][r] *= f;
                 top = m;
             }
-            const float ref = top == -__builtin_inff() ? 0.0f : top;
-            if (looked_up) {
+            flat -= top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = exp2_fast(s[r] - ref);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], a.scale2, flat - ref));
+            for (int r = 0; r < 16; ++r) {
+                s[r] = exp2_fast(fmaf(s[r], factor, flat));
+                sum += s[r];
             }
+            const Frag<S> p[2] = {to_frag<S>(s, 0), to_frag<S>(s, 1)};
 #pragma unroll
-            for (int r = 0; r < 16; ++r) sum += s[r];
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const Frag<S> p = to_frag<S>(s, k);
-#pragma unroll
-                for (int d = 0; d < ND; ++d) o[d] = mma(T::columns(vt, row0 + 16 * k, d, lane), p, o[d]);
-            }
+                for (int d = 0; d < ND; ++d)
+                    o[d] = mma(kAhead && c == 0 ? v[d] : T::columns(vt, row0 + 16 * c, d, lane), p[c], o[d]);
         }
         if (kBuffers == 2 && t + 1 < t1) finish(t + 1);
     }
+    products_done<S>();
     sum += swap_halves(sum);
 
     if constexpr (KW > 1) {  // join the waves: wave w takes head elements 32 w ..
