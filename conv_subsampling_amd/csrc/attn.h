@@ -309,6 +309,20 @@ struct AttnPlace {
     }
 };
 
+// The item with the rank-th most work.  The workgroups of a padded batch start
+// in this order, so that the long ones run beside short ones and not after them.
+__device__ __forceinline__ int item_of_rank(const AttnArgs& a, int rank) {
+    if (a.B == 1 || a.B > 64 || (!a.q_lengths && !a.k_lengths)) return rank;
+    const int lane = threadIdx.x % 64, b = lane < a.B ? lane : 0;
+    const float work = (float)item_length(a.q_lengths, b, a.Tq) * (float)item_length(a.k_lengths, b, a.Tk);
+    int mine = 0;
+    for (int m = 0; m < a.B; ++m) {
+        const float other = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(work), m));
+        mine += other > work || (other == work && m < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < a.B && mine == rank));
+}
+
 // One item's valid frames and the position of its first query on the key axis.
 struct AttnItem {
     int32_t nq, nk;
@@ -346,19 +360,43 @@ struct AttnItem {
 // repeated kBiasMargin times on both sides.  A table may hold its type's lowest
 // value: times log2(e) that must stay a number, so that rows which hold nothing
 // else still weigh their keys alike.  Bucket numbers are held to the table.
+// The constructor reads the map (the first entries of each thread), fill() the
+// table: what is read in between is in flight with the map.
 template <typename S>
-__device__ __forceinline__ void fill_bias(const AttnArgs& a, int h, float* bias) {
-    const int n = 2 * a.R + 1 + 2 * kBiasMargin;
-    for (int x = threadIdx.x; x < n; x += kAttnThreads) {
+struct BiasFill {
+    static constexpr int kFirst = 3;
+    int bucket[kFirst];
+
+    static __device__ __forceinline__ int map_at(const AttnArgs& a, int x) {
         int rel = x - kBiasMargin;
         rel = rel < 0 ? 0 : rel > 2 * a.R ? 2 * a.R : rel;
-        int bucket = a.buckets[rel];
-        bucket = bucket < 0 ? 0 : bucket >= a.NB ? a.NB - 1 : bucket;
-        const float t = to_f32(((const S*)a.table)[(int64_t)bucket * a.H + h]);
-        const float v = t * kLog2e, lowest = -3.0e38f;
-        bias[x] = v < lowest && t > -__builtin_inff() ? lowest : v;
+        const int b = a.buckets[rel];
+        return b < 0 ? 0 : b >= a.NB ? a.NB - 1 : b;
     }
-}
+
+    static __device__ __forceinline__ float value(const AttnArgs& a, int h, int b) {
+        const float t = to_f32(((const S*)a.table)[(int64_t)b * a.H + h]);
+        const float v = t * kLog2e, lowest = -3.0e38f;
+        return v < lowest && t > -__builtin_inff() ? lowest : v;
+    }
+
+    __device__ __forceinline__ explicit BiasFill(const AttnArgs& a) {
+        if (!a.table) return;
+#pragma unroll
+        for (int k = 0; k < kFirst; ++k) bucket[k] = map_at(a, threadIdx.x + k * kAttnThreads);
+    }
+
+    __device__ __forceinline__ void fill(const AttnArgs& a, int h, float* bias) const {
+        if (!a.table) return;
+        const int n = 2 * a.R + 1 + 2 * kBiasMargin;
+#pragma unroll
+        for (int k = 0; k < kFirst; ++k) {
+            const int x = threadIdx.x + k * kAttnThreads;
+            if (x < n) bias[x] = value(a, h, bucket[k]);
+        }
+        for (int x = threadIdx.x + kFirst * kAttnThreads; x < n; x += kAttnThreads) bias[x] = value(a, h, map_at(a, x));
+    }
+};
 
 inline int attn_bias_bytes(int32_t R) { return (2 * R + 1 + 2 * kBiasMargin) * 4; }
 

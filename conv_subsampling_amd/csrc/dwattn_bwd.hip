@@ -60,15 +60,13 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
     float* sums = bias + (nbias + 3) / 4 * 4 + 4 * kTile * kDiag + wave * nbias;            // by distance, of this wave
 
     const AttnPlace place(blockIdx.x, a.nqb, a.B * a.H, a.left == kNoLimit && a.right != kNoLimit);
-    const int qb = place.block, h = place.pair % a.H, b = place.pair / a.H;
+    const int qb = place.block, h = place.pair % a.H, b = item_of_rank(a, place.pair / a.H);
     const AttnItem item(a, b);
     const int i0 = qb * kBwdOwned, iw = i0 + wave * kTile, i = iw + lane % 32;
     const bool live = i < item.nq;
-    if (a.table) {
-        fill_bias<S>(a, h, bias);
-        if (a.dist)
-            for (int x = lane; x < nbias; x += 64) sums[x] = 0.0f;
-    }
+    const BiasFill<S> filler(a);
+    if (a.dist)
+        for (int x = lane; x < nbias; x += 64) sums[x] = 0.0f;
 
     Frag<S> q[NC], g[NC];
     float delta = 0.0f, lse2 = __builtin_inff();
@@ -91,6 +89,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
         if (half == 0 && i < a.Tq) a.delta[stat] = delta;
     }
     if (!a.dq && !a.dist) return;
+    filler.fill(a, h, bias);
     const int mine0 = item.first_key(a, i), mine1 = item.last_key(a, i);
     const uint32_t mine = live && mine1 >= mine0 ? mine1 - mine0 + 1 : 0;
     int j0 = 0, j1 = 0;
@@ -291,7 +290,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
 
     const AttnPlace place(blockIdx.x, a.nkb, a.B * a.Hkv, a.right == kNoLimit && a.left != kNoLimit);
-    const int kb = place.block, hk = place.pair % a.Hkv, b = place.pair / a.Hkv, group = a.H / a.Hkv;
+    const int kb = place.block, hk = place.pair % a.Hkv, b = item_of_rank(a, place.pair / a.Hkv), group = a.H / a.Hkv;
     const AttnItem item(a, b);
     const int j0 = kb * kBwdOwned, jw = j0 + wave * kTile, j = jw + lane % 32;
     const bool live = j < item.nk;
@@ -321,7 +320,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
     for (int n = 0; n < group; ++n) {
         const int h = hk * group + n;
         __syncthreads();  // the head before is done with the tiles and its bias
-        if (a.table) fill_bias<S>(a, h, bias);
+        const BiasFill<S> filler(a);
         const S* qbase = (const S*)a.q + b * a.qs.item + h * a.qs.head;
         const S* gbase = (const S*)a.dout + ((int64_t)b * a.Tq * a.H + h) * a.D;
         const int64_t gstride = (int64_t)a.H * a.D, srow = ((int64_t)b * a.H + h) * a.Tq;
@@ -348,10 +347,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
             }
         };
         const int tiles = i1 > i0 ? (i1 - i0 + BQ - 1) / BQ : 0;
-        if (tiles) {
-            start(0);
-            finish(0);
-        }
+        if (tiles) start(0);
+        filler.fill(a, h, bias);
+        if (tiles) finish(0);
 #pragma unroll
         for (int c = 0; c < NC; ++c) arrived(k[c]), arrived(v[c]);
         for (int t = 0; t < tiles; ++t) {

@@ -11,6 +11,13 @@
 // results attn_join adds.
 #include "attn.h"
 
+#ifndef DW_ATTN_WIDE_BF16
+#define DW_ATTN_WIDE_BF16 3
+#endif
+#ifndef DW_ATTN_WIDE_F32
+#define DW_ATTN_WIDE_F32 8
+#endif
+
 namespace dw {
 
 struct AttnFwd : AttnArgs {
@@ -28,9 +35,9 @@ constexpr float kSlack = 8.0f;
 // Keys of a tile, and the waves per SIMD its registers are to allow.
 template <typename S, int DP, int QW, bool DMA>
 struct FwdShape {
-    static constexpr int BN = QW == 1 ? 128 : sizeof(S) * DP <= 128 ? 64 : 32;
+    static constexpr int BN = QW == 1 ? 128 : QW == 2 || sizeof(S) * DP <= 128 ? 64 : 32;
     static constexpr int kBuffers = QW == 1 ? 1 : 2;  // of the tiles
-    static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : DMA && sizeof(S) == 2 && DP <= 128 ? 3 : 2;
+    static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : QW == 4 && DMA && sizeof(S) == 2 ? 3 : 2;
 };
 
 template <typename S, int DP, int QW, bool DMA>
@@ -41,23 +48,15 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
     extern __shared__ __align__(16) char smem[];
     float* bias = (float*)(smem + 2 * kBuffers * T::bytes(BN));
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
-    const int wq = QW == 4 ? wave : 0, wk = QW == 4 ? 0 : wave;
+    const int wq = wave % QW, wk = wave / QW;
 
     const AttnPlace place(blockIdx.x, a.nqb * a.splits, a.B * a.H, a.left == kNoLimit && a.right != kNoLimit);
     const int split = place.block % a.splits, qb = place.block / a.splits;
-    const int h = place.pair % a.H, b = place.pair / a.H;
+    const int h = place.pair % a.H, b = a.nqb > 1 ? item_of_rank(a, place.pair / a.H) : place.pair / a.H;
     const AttnItem item(a, b);
     const int i0 = qb * (kTile * QW), iw = i0 + wq * kTile, i = iw + lane % 32;
     const bool live = i < item.nq;
 
-    if (a.table) fill_bias<S>(a, h, bias);
-
-    Frag<S> q[NC];
-    {
-        const S* row = (const S*)a.q + b * a.qs.item + (int64_t)(live ? i : 0) * a.qs.frame + h * a.qs.head;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) q[c] = to_frag<S>(load_group<S, !DMA>(row, 16 * c + 8 * half, live ? a.D : 0));
-    }
     // this lane's keys: [mine0, mine0 + mine)
     const int mine0 = item.first_key(a, i);
     const int mine1 = item.last_key(a, i);
@@ -94,14 +93,20 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
         vl.finish(vtile(t));
     };
 
-    f32x16 o[ND] = {};
-    float top = -__builtin_inff(), sum = 0.0f;
-    if (t0 < t1) {
-        start(t0);
-        if (kBuffers == 2) finish(t0);
+    const BiasFill<S> filler(a);
+    if (t0 < t1) start(t0);
+    Frag<S> q[NC];
+    {
+        const S* row = (const S*)a.q + b * a.qs.item + (int64_t)(live ? i : 0) * a.qs.frame + h * a.qs.head;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) q[c] = to_frag<S>(load_group<S, !DMA>(row, 16 * c + 8 * half, live ? a.D : 0));
     }
+    filler.fill(a, h, bias);
+    if (kBuffers == 2 && t0 < t1) finish(t0);
 #pragma unroll
     for (int c = 0; c < NC; ++c) arrived(q[c]);
+    f32x16 o[ND] = {};
+    float top = -__builtin_inff(), sum = 0.0f;
     for (int t = t0; t < t1; ++t) {
         if (kBuffers == 1) {
             __syncthreads();
@@ -186,10 +191,13 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
     products_done<S>();
     sum += swap_halves(sum);
 
-    if constexpr (KW > 1) {  // join the waves: wave w takes head elements 32 w ..
-        float* opart = (float*)smem;                                    // [KW][ND * 16][64]
-        float* stat = (float*)(smem + KW * ND * 16 * 64 * 4);           // [KW][2][32]
-        static_assert(KW * ND * 16 * 64 * 4 + KW * 2 * 32 * 4 <= 2 * kBuffers * T::bytes(BN), "the tiles' room holds the join");
+    // Join the waves that share queries: wave wk of them takes every KW-th run
+    // of 32 head elements.
+    constexpr int NJ = (ND + KW - 1) / KW;
+    if constexpr (KW > 1) {
+        float* opart = (float*)smem;                          // [4][ND * 16][64]
+        float* stat = (float*)(smem + 4 * ND * 16 * 64 * 4);  // [4][2][32]
+        static_assert(4 * ND * 16 * 64 * 4 + 4 * 2 * 32 * 4 <= 2 * kBuffers * T::bytes(BN), "the tiles' room holds the join");
         __syncthreads();
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -202,22 +210,25 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
         __syncthreads();
         float m = -__builtin_inff();
 #pragma unroll
-        for (int w = 0; w < KW; ++w) m = fmaxf(m, stat[w * 64 + lane % 32]);
-        float f[KW], total = 0.0f;
+        for (int w = 0; w < KW; ++w) m = fmaxf(m, stat[(w * QW + wq) * 64 + lane % 32]);
+        float f[KW];
+        sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-            f[w] = m == -__builtin_inff() ? 0.0f : exp2_fast(stat[w * 64 + lane % 32] - m);
-            total += f[w] * stat[w * 64 + 32 + lane % 32];
+            f[w] = m == -__builtin_inff() ? 0.0f : exp2_fast(stat[(w * QW + wq) * 64 + lane % 32] - m);
+            sum += f[w] * stat[(w * QW + wq) * 64 + 32 + lane % 32];
         }
         top = m;
-        sum = total;
-        if (wave < ND) {
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) {
+            const int d = wk + n * KW;
+            if (d >= ND) break;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 float v = 0.0f;
 #pragma unroll
-                for (int w = 0; w < KW; ++w) v += f[w] * opart[((w * ND + wave) * 16 + r) * 64 + lane];
-                o[0][r] = v;
+                for (int w = 0; w < KW; ++w) v += f[w] * opart[(((w * QW + wq) * ND + d) * 16 + r) * 64 + lane];
+                o[n][r] = v;
             }
         }
     }
@@ -225,19 +236,19 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
     const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
     const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // a row without keys is zero; NaN stays
 #pragma unroll
-    for (int d = 0; d < (KW > 1 ? 1 : ND); ++d) {
-        const int d0 = 32 * (KW > 1 ? wave : d) + 4 * half;
-        if (KW > 1 && wave >= ND) break;
+    for (int n = 0; n < NJ; ++n) {
+        const int d0 = 32 * (wk + n * KW) + 4 * half;
+        if (wk + n * KW >= ND) break;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+            const float v[4] = {o[n][4 * g], o[n][4 * g + 1], o[n][4 * g + 2], o[n][4 * g + 3]};
             if (a.splits > 1) {
                 const int64_t rows = (int64_t)a.B * a.H * a.Tq;
                 const int D4 = (a.D + 3) / 4 * 4;
-                store4<float>(a.part + (split * rows + row) * D4, d0 + 8 * g, D4, o[d][4 * g], o[d][4 * g + 1],
-                              o[d][4 * g + 2], o[d][4 * g + 3]);
+                store4<float>(a.part + (split * rows + row) * D4, d0 + 8 * g, D4, v[0], v[1], v[2], v[3]);
             } else {
-                store4<S>((S*)a.out + (((int64_t)b * a.Tq + i) * a.H + h) * a.D, d0 + 8 * g, a.D, o[d][4 * g] * inv,
-                          o[d][4 * g + 1] * inv, o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv);
+                store4<S>((S*)a.out + (((int64_t)b * a.Tq + i) * a.H + h) * a.D, d0 + 8 * g, a.D, v[0] * inv, v[1] * inv,
+                          v[2] * inv, v[3] * inv);
             }
         }
     }
@@ -254,6 +265,8 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
 }
 
 // Joins the splits of the key axis: one thread takes 4 head elements of a row.
+constexpr int kJoin = 8;
+
 template <typename S>
 __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnFwd a) {
     const int D4 = (a.D + 3) / 4;
@@ -262,14 +275,31 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnFwd a) {
     const int64_t row = at / D4;
     const int d = (int)(at - row * D4);
     const float* stat = a.part + a.splits * rows * D4 * 4;
-    float m = -__builtin_inff();
-    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, stat[(s * rows + row) * 2]);
+    float m = -__builtin_inff(), sum = 0.0f;
     f32x4 o = {};
-    float sum = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
-        const float f = m == -__builtin_inff() ? 0.0f : exp2_fast(stat[(s * rows + row) * 2] - m);
-        sum += f * stat[(s * rows + row) * 2 + 1];
-        o += f * *reinterpret_cast<const f32x4*>(a.part + ((s * rows + row) * D4 + d) * 4);
+    for (int s0 = 0; s0 < a.splits; s0 += kJoin) {  // kJoin splits' loads are in flight together
+        float top[kJoin], part[kJoin];
+        f32x4 v[kJoin];
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) {
+            const int64_t s = min(s0 + k, a.splits - 1);
+            top[k] = stat[(s * rows + row) * 2];
+            part[k] = stat[(s * rows + row) * 2 + 1];
+            v[k] = *reinterpret_cast<const f32x4*>(a.part + ((s * rows + row) * D4 + d) * 4);
+        }
+        float next = m;
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) next = fmaxf(next, top[k]);
+        const float ref = next == -__builtin_inff() ? 0.0f : next, f = exp2_fast(m - ref);
+        sum *= f;
+        o *= f;
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) {
+            const float g = s0 + k < a.splits ? exp2_fast(top[k] - ref) : 0.0f;
+            sum += g * part[k];
+            o += g * v[k];
+        }
+        m = next;
     }
     const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
     const int64_t i = row % a.Tq, bh = row / a.Tq;
@@ -287,25 +317,30 @@ struct FwdPlan {
 };
 
 // 128 queries a workgroup read each key tile once for four waves, so they are
-// taken where that leaves enough workgroups; else 32 queries, and where those
-// are few too, the keys are split until about two workgroups per compute unit
-// are there.  The plan goes by the sizes alone (lengths are on the device).
-static FwdPlan fwd_plan(const AttnShape& s) {
+// taken where they make workgroups enough; next 64, whose two pairs of waves
+// divide the keys; and with the fewest queries 32, the keys then being split
+// over workgroups until each compute unit has one.  The plan goes by the sizes
+// alone (lengths are on the device).
+static FwdPlan fwd_plan(const AttnShape& s, int elem_bytes) {
     constexpr int64_t kUnits = 256;
+    const int64_t wide = kUnits * (elem_bytes == 4 ? DW_ATTN_WIDE_F32 : DW_ATTN_WIDE_BF16);
     FwdPlan p;
-    const int64_t wide = (s.Tq + 127) / 128, narrow = (s.Tq + 31) / 32;
-    p.qw = s.Tq > 32 && s.B * s.H * wide >= kUnits * 3 / 4 ? 4 : 1;
-    p.nqb = p.qw == 4 ? wide : narrow;
-    const int64_t queries = p.qw == 4 ? 128 : 32, keys = p.qw == 4 ? 64 : 128;
-    int64_t span = s.Tk;
-    if (s.left < kNoLimit && s.right < kNoLimit) {
-        const int64_t window = s.left + s.right + queries;
-        span = window < 1 ? 1 : window < span ? window : span;
+    auto blocks_of = [&](int64_t queries) { return s.B * s.H * ((s.Tq + queries - 1) / queries); };
+    p.qw = s.Tq > 32 && blocks_of(128) >= wide ? 4 : s.Tq > 32 && blocks_of(64) >= kUnits ? 2 : 1;
+    const int64_t queries = 32 * p.qw;
+    p.nqb = (s.Tq + queries - 1) / queries;
+    p.splits = 1;
+    if (p.qw == 1) {
+        int64_t span = s.Tk;
+        if (s.left < kNoLimit && s.right < kNoLimit) {
+            const int64_t window = s.left + s.right + queries;
+            span = window < 1 ? 1 : window < span ? window : span;
+        }
+        const int64_t blocks = blocks_of(32), tiles = (span + 127) / 128;
+        int64_t n = kUnits / (blocks ? blocks : 1);
+        n = n < tiles ? n : tiles;
+        p.splits = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
     }
-    const int64_t blocks = s.B * s.H * p.nqb, tiles = (span + keys - 1) / keys;
-    int64_t n = 2 * kUnits / (blocks ? blocks : 1);
-    n = n < tiles ? n : tiles;
-    p.splits = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
     return p;
 }
 
@@ -313,7 +348,9 @@ static int64_t part_floats(const AttnShape& s, int splits) {
     return splits > 1 ? splits * s.B * s.H * s.Tq * ((s.D + 3) / 4 * 4 + 2) : 0;
 }
 
-size_t dwattn_fwd_workspace(const AttnShape& s) { return (size_t)part_floats(s, fwd_plan(s).splits) * sizeof(float); }
+size_t dwattn_fwd_workspace(const AttnShape& s, int elem_bytes) {
+    return (size_t)part_floats(s, fwd_plan(s, elem_bytes).splits) * sizeof(float);
+}
 
 bool dwattn_fits(const AttnShape& s) {
     // workgroups of the narrowest tiles times the most splits, and the threads of the join
@@ -335,9 +372,11 @@ template <typename S>
 static hipError_t fwd_of_type(const AttnFwd& a, int qw, hipStream_t stream) {
     const bool dma = dma_fits<S>(a.k, a.ks, a.D) && dma_fits<S>(a.v, a.vs, a.D);
     const hipError_t e = with_head_width(a.D, [&](auto dp) {
-        return qw != 4 ? launch_fwd<S, dp.value, 1, false>(a, stream)
-               : dma   ? launch_fwd<S, dp.value, 4, true>(a, stream)
-                       : launch_fwd<S, dp.value, 4, false>(a, stream);
+        return qw == 1 ? launch_fwd<S, dp.value, 1, false>(a, stream)
+               : qw == 2 && dma ? launch_fwd<S, dp.value, 2, true>(a, stream)
+               : qw == 2 ? launch_fwd<S, dp.value, 2, false>(a, stream)
+               : dma ? launch_fwd<S, dp.value, 4, true>(a, stream)
+                     : launch_fwd<S, dp.value, 4, false>(a, stream);
     });
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t threads = (int64_t)a.B * a.H * a.Tq * ((a.D + 3) / 4);
@@ -348,7 +387,7 @@ static hipError_t fwd_of_type(const AttnFwd& a, int qw, hipStream_t stream) {
 
 hipError_t launch_dwattn_fwd(const AttnPtrs& p, const AttnShape& s, void* out, float* lse, void* workspace, bool bf16,
                              hipStream_t stream) {
-    const FwdPlan plan = fwd_plan(s);
+    const FwdPlan plan = fwd_plan(s, bf16 ? 2 : 4);
     AttnFwd a;
     (AttnArgs&)a = attn_args(p, s);
     a.out = out;

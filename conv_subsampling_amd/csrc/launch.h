@@ -162,7 +162,7 @@ struct AttnShape {
 };
 
 bool dwattn_fits(const AttnShape& s);
-size_t dwattn_fwd_workspace(const AttnShape& s);
+size_t dwattn_fwd_workspace(const AttnShape& s, int elem_bytes);
 hipError_t launch_dwattn_fwd(const AttnPtrs& p, const AttnShape& s, void* out, float* lse, void* workspace, bool bf16,
                              hipStream_t stream);
 
