@@ -117,7 +117,7 @@ __device__ __forceinline__ Frag<S> to_frag(const RawGroup<S>& g) {
 template <typename S, int DP>
 struct Tile {
     static constexpr int kChunks = DP * (int)sizeof(S) / 16;
-    static constexpr int kSlots = kChunks + (kChunks == 16 && sizeof(S) == 2 ? 3 : 1);  // with the pad
+    static constexpr int kSlots = kChunks + 1;  // with the pad
     static constexpr int kStride = kSlots * 16 / (int)sizeof(S);
     static constexpr int kGroups = DP / kGroup;  // 8-element groups of a row
 
@@ -198,8 +198,8 @@ struct TileRegs {
 // to the wave's LDS address (m0) plus 16 times the lane.  A lane works out once
 // which row and chunk its place in the tile is; lanes on a pad sit out.  The
 // buffer ends at the last live row, so what lies past it arrives as zero.
-// start() returns with the loads in flight: wave_loads_done() and a barrier
-// come before the tile is read.  (Written as inline assembly, without a result
+// start() returns with the loads in flight: a wait for them and a barrier come
+// before the tile is read.  (Written as inline assembly, without a result
 // register, because the compiler would else wait for them before any LDS read.
 // Nothing else in these kernels takes its operand from m0.)
 template <typename S, int DP, int ROWS>
@@ -221,8 +221,8 @@ struct TileDma {
     }
 
     __device__ __forceinline__ void start(const S* base, int64_t frame, int live, int D, S* tile) {
-        if (live > ROWS) live = ROWS;
-        const uint32_t bytes = (uint32_t)(((live - 1) * frame + D) * (int)sizeof(S));
+        const uint32_t bytes =
+            live > 0 ? (uint32_t)((((live < ROWS ? live : ROWS) - 1) * frame + D) * (int)sizeof(S)) : 0;
         const uint64_t at = (uint64_t)base;
         const u32x4 rsrc = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, (uint32_t)kBufferFlags};
         const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)tile +
@@ -248,10 +248,61 @@ bool dma_fits(const void* base, const AttnStride& s, int64_t D) {
            s.head % chunk == 0 && s.frame >= D && s.frame <= ((int64_t)1 << 29) / 256;
 }
 
-template <typename S, int DP, int ROWS, bool DMA>
-using TileLoad = std::conditional_t<DMA, TileDma<S, DP, ROWS>, TileRegs<S, DP, ROWS>>;
-
 __device__ __forceinline__ void wave_loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// The tiles of two tensors (keys and values, or queries and output gradients),
+// with two buffers each (tile t + 1 on its way while tile t is used) or one (its
+// registers hold tile t + 1).  A third and fourth buffer, with counted waits, made
+// no kernel faster: loads are not what the tiles wait for.
+template <typename S, int DP, int ROWS, int BUFFERS, bool DMA>
+struct TilePair {
+    using Load = std::conditional_t<DMA, TileDma<S, DP, ROWS>, TileRegs<S, DP, ROWS>>;
+    static_assert(BUFFERS == 2 || !DMA, "direct loads write the tile while the one before is in use");
+    static constexpr int kBytes = Tile<S, DP>::bytes(ROWS), kAllBytes = 2 * BUFFERS * kBytes;
+    Load x, y;
+    char* at;
+    const S *xbase, *ybase;
+    int64_t xframe, yframe;
+    int D, total;  // head elements, frames
+
+    __device__ __forceinline__ TilePair(char* at, const S* xbase, int64_t xframe, const S* ybase, int64_t yframe, int D,
+                                        int total)
+        : at(at), xbase(xbase), ybase(ybase), xframe(xframe), yframe(yframe), D(D), total(total) {
+        x.setup(xframe, D);
+        y.setup(yframe, D);
+    }
+
+    __device__ __forceinline__ S* x_of(int t) const { return (S*)(at + (BUFFERS == 2 && (t & 1) ? 2 * kBytes : 0)); }
+    __device__ __forceinline__ S* y_of(int t) const { return (S*)((char*)x_of(t) + kBytes); }
+
+    __device__ __forceinline__ void start(int t) {
+        const int64_t from = (int64_t)t * ROWS;
+        x.start(xbase + from * xframe, xframe, total - (int)from, D, x_of(t));
+        y.start(ybase + from * yframe, yframe, total - (int)from, D, y_of(t));
+    }
+
+    __device__ __forceinline__ void finish(int t) const {
+        x.finish(x_of(t));
+        y.finish(y_of(t));
+    }
+
+    // Everything before tile t is used: its loads are in, and every wave is
+    // done with the buffer that the next tile's loads write, which start here.
+    __device__ __forceinline__ void enter(int t, bool more) {
+        if (BUFFERS == 1) {
+            __syncthreads();
+            finish(t);
+        }
+        wave_loads_done();
+        __syncthreads();
+        if (more) start(t + 1);
+    }
+
+    // After tile t was used.
+    __device__ __forceinline__ void leave(int t, bool more) const {
+        if (BUFFERS == 2 && more) finish(t + 1);
+    }
+};
 
 // ---------------------------------------------------------------------------
 // Arguments

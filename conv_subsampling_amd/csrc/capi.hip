@@ -561,7 +561,7 @@ dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const v
 size_t dwattn_bwd_workspace_bytes(const dw_attn* shape) {
     dw::AttnShape s;
     if (!shape || check_attn("dwattn_bwd_workspace_bytes", shape, shape->buckets > 0, &s) != DW_OK) return 0;
-    return dw::dwattn_bwd_workspace(s);
+    return dw::dwattn_bwd_workspace(s, shape->dtype == DW_BF16 ? 2 : 4);
 }
 
 dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const void* v, const void* table,
@@ -590,7 +590,7 @@ dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const v
             return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
     if ((dq && (dq == dk || dq == dv)) || (dk && dk == dv))
         return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
-    const size_t need = dw::dwattn_bwd_workspace(s);
+    const size_t need = dw::dwattn_bwd_workspace(s, shape->dtype == DW_BF16 ? 2 : 4);
     if (need && (!workspace || workspace_bytes < need))
         return fail(DW_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
                     workspace ? workspace_bytes : (size_t)0, need);

@@ -11,8 +11,10 @@
 //                    (for the other kernel), and the sums of dS by distance
 //   attn_dkv_kernel  a wave owns 32 keys and streams the queries of every
 //                    head that shares them: dk and dv
-// attn_dbias_rows and attn_dtable then add the sums by distance over the
-// workgroups and into buckets, in fp64.
+// As in the forward, a workgroup's four waves own 128 frames (OW = 4), or where
+// those make too few workgroups 64 or 32, the waves that share frames dividing
+// the streamed tiles and adding their sums in LDS.  attn_dtable then adds the
+// sums by distance over the workgroups and into buckets, in fp64.
 #include "attn.h"
 
 namespace dw {
@@ -20,14 +22,13 @@ namespace dw {
 struct AttnBwd : AttnArgs {
     const void *out, *dout;  // [B][Tq][H][D]
     const float* lse;        // [B][H][Tq]
-    float* delta;            // [B][H][Tq]
+    float* stat;             // [B][H][Tq][2]: lse in units of log2 (inf where there are no keys), and delta
     void *dq, *dk, *dv;
     AttnStride dqs, dks, dvs;
     float* dist;  // [H][B * nqb][2 R + 1] sums of dS by distance; NULL: not wanted
     int32_t nqb, nkb;
 };
 
-constexpr int kBwdOwned = 4 * kTile;  // queries or keys a workgroup owns
 constexpr int kDiag = 36;             // row stride of the square that the diagonals are read from
 
 // exp(S - lse) of a query that has keys; lse = -inf marks one that has none,
@@ -37,6 +38,18 @@ __device__ __forceinline__ float lse_or_inf(float lse) {
 }
 
 
+// One float a lane of this wave's part of `from` into LDS at `to` (both by the
+// thread's place in the workgroup); past `count` floats it is zero.
+__device__ __forceinline__ void load_lds_floats(const float* from, int count, float* to) {
+    const uint64_t at = (uint64_t)from;
+    const u32x4 rsrc = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, count > 0 ? (uint32_t)count * 4 : 0,
+                        (uint32_t)kBufferFlags};
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)to + wave_of_block() * 256;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(threadIdx.x * 4), "s"(rsrc)
+                 : "memory");
+}
+
 // Orders a wave's LDS accesses before and after it: lanes read what other
 // lanes of their wave wrote.
 __device__ __forceinline__ void wave_lds_fence() {
@@ -44,16 +57,68 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// Streamed frames of a tile (two tiles of each tensor are in LDS).
-template <typename S, int DP>
-constexpr int kBwdRows = sizeof(S) * DP <= 128 ? 64 : 32;
+// Streamed frames of a tile, its buffers, and whether direct loads fill them.
+// float rows over 64 wide leave room for one buffer beside the sums by distance.
+template <typename S, int DP, int OW>
+struct BwdShape {
+    static constexpr int ROWS = OW == 1 ? 128 : OW == 2 || sizeof(S) * DP <= 128 ? 64 : 32;
+    static constexpr int kBuffers = OW == 1 || (OW == 2 && sizeof(S) == 4 && DP > 64) ? 1 : 2;
+    template <bool DMA>
+    using Tiles = TilePair<S, DP, ROWS, kBuffers, DMA && kBuffers == 2>;
+};
 
-template <typename S, int DP, bool DMA>
+// Adds acc over the waves that share owned frames (wave = part * OW + owner);
+// run n of `out` is then the sum of run part + n * KW of 32 head elements.
+template <int OW, int ND>
+__device__ __forceinline__ void add_waves(char* smem, f32x16 (&acc)[ND], int lane, int wave) {
+    constexpr int KW = 4 / OW;
+    if constexpr (KW > 1) {
+        float* all = (float*)smem;  // [4][ND * 16][64]
+        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) all[((wave * ND + d) * 16 + r) * 64 + lane] = acc[d][r];
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < (ND + KW - 1) / KW; ++n) {
+            const int d = wave / OW + n * KW;
+            if (d >= ND) break;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < KW; ++w) v += all[(((w * OW + wave % OW) * ND + d) * 16 + r) * 64 + lane];
+                acc[n][r] = v;
+            }
+        }
+    }
+}
+
+// The runs of 32 head elements that this wave has after add_waves, times scale.
+template <typename S, int OW, int ND>
+__device__ __forceinline__ void store_runs(S* row, const f32x16 (&acc)[ND], int D, float scale, int half, int wave) {
+    constexpr int KW = 4 / OW;
+#pragma unroll
+    for (int n = 0; n < (ND + KW - 1) / KW; ++n) {
+        const int d = wave / OW + n * KW;
+        if (d >= ND) break;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            store4<S>(row, 32 * d + 8 * g + 4 * half, D, acc[n][4 * g] * scale, acc[n][4 * g + 1] * scale,
+                      acc[n][4 * g + 2] * scale, acc[n][4 * g + 3] * scale);
+    }
+}
+
+template <typename S, int DP, int OW, bool DMA>
 __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) ? 1 : 2)) void attn_dq_kernel(const AttnBwd a) {
-    constexpr int BN = kBwdRows<S, DP>, KT = BN / kTile, NC = DP / 16, ND = DP / 32;
+    typedef BwdShape<S, DP, OW> Shape;
+    typedef typename Shape::template Tiles<DMA> Tiles;
     typedef Tile<S, DP> T;
+    constexpr int KW = 4 / OW, BN = Shape::ROWS, KT = BN / kTile / KW, NC = DP / 16, ND = DP / 32;
+    static_assert(KW == 1 || 4 * ND * 16 * 64 * 4 <= Tiles::kAllBytes, "the tiles' room holds the waves' sums");
     extern __shared__ __align__(16) char smem[];
-    float* bias = (float*)(smem + 4 * T::bytes(BN));
+    float* bias = (float*)(smem + Tiles::kAllBytes);
     const int nbias = 2 * a.R + 1 + 2 * kBiasMargin;
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
     float* square = bias + (nbias + 3) / 4 * 4 + wave * kTile * kDiag;                      // a tile of dS
@@ -62,7 +127,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
     const AttnPlace place(blockIdx.x, a.nqb, a.B * a.H, a.left == kNoLimit && a.right != kNoLimit);
     const int qb = place.block, h = place.pair % a.H, b = item_of_rank(a, place.pair / a.H);
     const AttnItem item(a, b);
-    const int i0 = qb * kBwdOwned, iw = i0 + wave * kTile, i = iw + lane % 32;
+    const int wk = wave / OW, i0 = qb * OW * kTile, iw = i0 + wave % OW * kTile, i = iw + lane % 32;
     const bool live = i < item.nq;
     const BiasFill<S> filler(a);
     if (a.dist)
@@ -86,57 +151,43 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
         delta += swap_halves(delta);
         const int64_t stat = ((int64_t)b * a.H + h) * a.Tq + i;
         if (live) lse2 = lse_or_inf(a.lse[stat]);
-        if (half == 0 && i < a.Tq) a.delta[stat] = delta;
+        if (half == 0 && wk == 0 && i < a.Tq) {
+            a.stat[2 * stat] = lse2;
+            a.stat[2 * stat + 1] = delta;
+        }
     }
     if (!a.dq && !a.dist) return;
-    filler.fill(a, h, bias);
     const int mine0 = item.first_key(a, i), mine1 = item.last_key(a, i);
     const uint32_t mine = live && mine1 >= mine0 ? mine1 - mine0 + 1 : 0;
     int j0 = 0, j1 = 0;
     if (i0 < item.nq) {
         j0 = item.first_key(a, i0);
-        j1 = item.last_key(a, min(i0 + kBwdOwned, item.nq) - 1) + 1;
+        j1 = item.last_key(a, min(i0 + OW * kTile, item.nq) - 1) + 1;
     }
     const int iwl = min(iw + kTile, item.nq) - 1;
     const int some0 = item.first_key(a, iw), some1 = iw < item.nq ? item.last_key(a, iwl) : -1;
     const int all0 = item.first_key(a, iwl), all1 = iw + kTile <= item.nq ? item.last_key(a, iw) : -1;
 
-    const S* kbase = (const S*)a.k + b * a.ks.item + (int64_t)(h / (a.H / a.Hkv)) * a.ks.head;
-    const S* vbase = (const S*)a.v + b * a.vs.item + (int64_t)(h / (a.H / a.Hkv)) * a.vs.head;
-    TileLoad<S, DP, BN, DMA> kl, vl;
-    kl.setup(a.ks.frame, a.D);
-    vl.setup(a.vs.frame, a.D);
-    auto ktile_of = [&](int t) { return (S*)(smem + (t & 1) * 2 * T::bytes(BN)); };
-    auto vtile_of = [&](int t) { return (S*)((char*)ktile_of(t) + T::bytes(BN)); };
-    auto start = [&](int t) {
-        const int64_t j = j0 + t * BN;
-        kl.start(kbase + j * a.ks.frame, a.ks.frame, j1 - (int)j, a.D, ktile_of(t));
-        vl.start(vbase + j * a.vs.frame, a.vs.frame, j1 - (int)j, a.D, vtile_of(t));
-    };
-    auto finish = [&](int t) {
-        kl.finish(ktile_of(t));
-        vl.finish(vtile_of(t));
-    };
+    const int hk = h / (a.H / a.Hkv);
+    Tiles kv(smem, (const S*)a.k + b * a.ks.item + hk * a.ks.head + (int64_t)j0 * a.ks.frame, a.ks.frame,
+             (const S*)a.v + b * a.vs.item + hk * a.vs.head + (int64_t)j0 * a.vs.frame, a.vs.frame, a.D, j1 - j0);
     const int tiles = j1 > j0 ? (j1 - j0 + BN - 1) / BN : 0;
-    if (tiles) {
-        start(0);
-        finish(0);
-    }
+    if (tiles) kv.start(0);
+    filler.fill(a, h, bias);
+    if (tiles && Shape::kBuffers == 2) kv.finish(0);
 #pragma unroll
     for (int c = 0; c < NC; ++c) arrived(q[c]), arrived(g[c]);
     asm volatile("" : "+v"(lse2), "+v"(delta));
     f32x16 acc[ND] = {};
     float low = 0.0f, high = 0.0f;  // sums of dS past the map's reach
     for (int t = 0; t < tiles; ++t) {
-        wave_loads_done();
-        __syncthreads();
-        if (t + 1 < tiles) start(t + 1);
-        const S* ktile = ktile_of(t);
-        const S* vtile = vtile_of(t);
+        kv.enter(t, t + 1 < tiles);
+        const S* ktile = kv.x_of(t);
+        const S* vtile = kv.y_of(t);
         const int jt = j0 + t * BN;
 #pragma unroll
         for (int u = 0; u < KT; ++u) {
-            const int row0 = u * kTile, j = jt + row0;
+            const int row0 = (wk * KT + u) * kTile, j = jt + row0;
             if (j > some1 || j + kTile <= some0) continue;
             f32x16 s = {}, ds = {};
 #pragma unroll
@@ -204,17 +255,14 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
                 }
             }
         }
-        if (t + 1 < tiles) finish(t + 1);
+        kv.leave(t, t + 1 < tiles);
     }
     products_done<S>();
-    if (a.dq && i < a.Tq) {
-        S* row = (S*)a.dq + b * a.dqs.item + (int64_t)i * a.dqs.frame + h * a.dqs.head;
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-                store4<S>(row, 32 * d + 8 * n + 4 * half, a.D, acc[d][4 * n] * a.scale, acc[d][4 * n + 1] * a.scale,
-                          acc[d][4 * n + 2] * a.scale, acc[d][4 * n + 3] * a.scale);
+    if (a.dq) {
+        add_waves<OW, ND>(smem, acc, lane, wave);
+        if (i < a.Tq)
+            store_runs<S, OW, ND>((S*)a.dq + b * a.dqs.item + (int64_t)i * a.dqs.frame + h * a.dqs.head, acc, a.D, a.scale,
+                                  half, wave);
     }
     if (!a.dist) return;
     low = lane_sum<64>(low);
@@ -236,55 +284,61 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
     }
 }
 
-// Sums by distance of one head over all workgroups, [H][2 R + 1] doubles: 16
-// sub-rows x 64 distances, each sub-row every 16th workgroup, then in order.
-constexpr int kDistCols = 64, kDistRows = 16;
-
-__global__ __launch_bounds__(kDistCols* kDistRows) void attn_dbias_rows(const float* __restrict__ dist,
-                                                                      double* __restrict__ total, int32_t n,
-                                                                      int32_t parts) {
-    __shared__ double acc[kDistRows][kDistCols];
-    const int lane = threadIdx.x % kDistCols, sub = threadIdx.x / kDistCols, x = blockIdx.x * kDistCols + lane;
-    const float* from = dist + (int64_t)blockIdx.y * parts * n;
-    double s = 0.0;
-    if (x < n) {
-#pragma unroll 4
-        for (int32_t r = sub; r < parts; r += kDistRows) s += from[(int64_t)r * n + x];
-    }
-    acc[sub][lane] = s;
-    __syncthreads();
-    if (sub != 0 || x >= n) return;
-    double t = acc[0][lane];
-#pragma unroll
-    for (int q = 1; q < kDistRows; ++q) t += acc[q][lane];
-    total[(int64_t)blockIdx.y * n + x] = t;
-}
-
-// dtable[bucket][h]: each wave takes a bucket and adds the distances in it.
-__global__ __launch_bounds__(kAttnThreads) void attn_dtable(const double* __restrict__ total,
+// dtable[bucket][h]: a workgroup lists the distances of its bucket and adds
+// their sums over the parts (items and query blocks), in an order that the
+// sizes and the map fix: each thread every 256th, then lanes, then waves.
+__global__ __launch_bounds__(kAttnThreads) void attn_dtable(const float* __restrict__ dist,
                                                            const int32_t* __restrict__ map, float* __restrict__ dtable,
-                                                           int32_t n, int32_t NB, int32_t H) {
-    const int h = blockIdx.y, lane = threadIdx.x % 64;
-    const int bucket = blockIdx.x * (kAttnThreads / 64) + threadIdx.x / 64;
-    if (bucket >= NB) return;
+                                                           int32_t n, int32_t parts, int32_t NB, int32_t H) {
+    constexpr int kMost = 2 * kAttnMaxReach + 1, kSteps = (kMost + kAttnThreads - 1) / kAttnThreads;
+    __shared__ int16_t list[kMost];
+    __shared__ int found[kSteps][4];
+    __shared__ double waves[4];
+    const int bucket = blockIdx.x, h = blockIdx.y, lane = threadIdx.x % 64, wave = wave_of_block();
+    uint64_t mask[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+        const int x = threadIdx.x + k * kAttnThreads;
+        int m = x < n ? map[x] : -1;
+        m = x >= n ? -1 : m < 0 ? 0 : m >= NB ? NB - 1 : m;
+        mask[k] = __ballot(m == bucket);
+        if (lane == 0) found[k][wave] = __popcll(mask[k]);
+    }
+    __syncthreads();
+    int count = 0;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w == wave && mask[k] >> lane & 1)
+                list[count + __popcll(mask[k] & ((1ull << lane) - 1))] = (int16_t)(threadIdx.x + k * kAttnThreads);
+            count += found[k][w];
+        }
+    }
+    __syncthreads();
     double s = 0.0;
-    for (int x = lane; x < n; x += 64) {
-        int m = map[x];
-        m = m < 0 ? 0 : m >= NB ? NB - 1 : m;
-        s += m == bucket ? total[(int64_t)h * n + x] : 0.0;
+    const float* from = dist + (int64_t)h * parts * n;
+    const uint32_t each = count, all = each * (uint32_t)parts;
+#pragma unroll 8
+    for (uint32_t at = threadIdx.x; at < all; at += kAttnThreads) {
+        const uint32_t part = at / each;
+        s += from[(int64_t)part * n + list[at - part * each]];
     }
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) s += __shfl_xor(s, m);
-    if (lane == 0) dtable[(int64_t)bucket * H + h] = (float)s;
+    if (lane == 0) waves[wave] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) dtable[(int64_t)bucket * H + h] = (float)(waves[0] + waves[1] + waves[2] + waves[3]);
 }
 
-// ---------------------------------------------------------------------------
-template <typename S, int DP, bool DMA>
-__global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) void attn_dkv_kernel(const AttnBwd a) {
-    constexpr int BQ = kBwdRows<S, DP>, QT = BQ / kTile, NC = DP / 16, ND = DP / 32;
+template <typename S, int DP, int OW, bool DMA>
+__global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 || (!DMA && DP > 32) ? 1 : 2)) void attn_dkv_kernel(const AttnBwd a) {
+    typedef BwdShape<S, DP, OW> Shape;
+    typedef typename Shape::template Tiles<DMA> Tiles;
     typedef Tile<S, DP> T;
+    constexpr int KW = 4 / OW, BQ = Shape::ROWS, QT = BQ / kTile / KW, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) char smem[];
-    float* stats = (float*)(smem + 4 * T::bytes(BQ));  // of two tiles: [2][2][BQ], lse in units of log2, then delta
+    float* stats = (float*)(smem + Tiles::kAllBytes);  // of two tiles: [2][BQ][2], as a.stat
     float* bias = stats + 4 * BQ;
     const int nbias = 2 * a.R + 1 + 2 * kBiasMargin;
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
@@ -292,7 +346,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
     const AttnPlace place(blockIdx.x, a.nkb, a.B * a.Hkv, a.right == kNoLimit && a.left != kNoLimit);
     const int kb = place.block, hk = place.pair % a.Hkv, b = item_of_rank(a, place.pair / a.Hkv), group = a.H / a.Hkv;
     const AttnItem item(a, b);
-    const int j0 = kb * kBwdOwned, jw = j0 + wave * kTile, j = jw + lane % 32;
+    const int wk = wave / OW, j0 = kb * OW * kTile, jw = j0 + wave % OW * kTile, j = jw + lane % 32;
     const bool live = j < item.nk;
 
     Frag<S> k[NC], v[NC];
@@ -310,7 +364,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
     int i0 = 0, i1 = 0;
     if (j0 < item.nk) {
         i0 = item.first_query(a, j0);
-        i1 = item.last_query(a, min(j0 + kBwdOwned, item.nk) - 1) + 1;
+        i1 = item.last_query(a, min(j0 + OW * kTile, item.nk) - 1) + 1;
     }
     const int jwl = min(jw + kTile, item.nk) - 1;
     const int some0 = item.first_query(a, jw), some1 = jw < item.nk ? item.last_query(a, jwl) : -1;
@@ -321,48 +375,33 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
         const int h = hk * group + n;
         __syncthreads();  // the head before is done with the tiles and its bias
         const BiasFill<S> filler(a);
-        const S* qbase = (const S*)a.q + b * a.qs.item + h * a.qs.head;
-        const S* gbase = (const S*)a.dout + ((int64_t)b * a.Tq * a.H + h) * a.D;
-        const int64_t gstride = (int64_t)a.H * a.D, srow = ((int64_t)b * a.H + h) * a.Tq;
-        TileLoad<S, DP, BQ, DMA> ql, gl;
-        ql.setup(a.qs.frame, a.D);
-        gl.setup(gstride, a.D);
-        float row_lse = 0.0f, row_delta = 0.0f;
-        auto qtile_of = [&](int t) { return (S*)(smem + (t & 1) * 2 * T::bytes(BQ)); };
-        auto gtile_of = [&](int t) { return (S*)((char*)qtile_of(t) + T::bytes(BQ)); };
-        auto start = [&](int t) {
-            const int64_t i = i0 + t * BQ;
-            const bool mine = threadIdx.x < BQ && i + threadIdx.x < i1;
-            row_lse = mine ? a.lse[srow + i + threadIdx.x] : -__builtin_inff();
-            row_delta = mine ? a.delta[srow + i + threadIdx.x] : 0.0f;
-            ql.start(qbase + i * a.qs.frame, a.qs.frame, i1 - (int)i, a.D, qtile_of(t));
-            gl.start(gbase + i * gstride, gstride, i1 - (int)i, a.D, gtile_of(t));
-        };
-        auto finish = [&](int t) {
-            ql.finish(qtile_of(t));
-            gl.finish(gtile_of(t));
-            if (threadIdx.x < BQ) {
-                stats[(t & 1) * 2 * BQ + threadIdx.x] = lse_or_inf(row_lse);
-                stats[(t & 1) * 2 * BQ + BQ + threadIdx.x] = row_delta;
-            }
+        const int64_t gstride = (int64_t)a.H * a.D;
+        Tiles qg(smem, (const S*)a.q + b * a.qs.item + h * a.qs.head + (int64_t)i0 * a.qs.frame, a.qs.frame,
+                 (const S*)a.dout + (((int64_t)b * a.Tq + i0) * a.H + h) * a.D, gstride, a.D, i1 - i0);
+        const float* stat_rows = a.stat + 2 * (((int64_t)b * a.H + h) * a.Tq + i0);
+        // the tile's lse and delta, one float a lane of its first waves
+        auto start_stats = [&](int t) {
+            if (threadIdx.x < 2 * BQ) load_lds_floats(stat_rows + 2 * t * BQ, 2 * (i1 - i0 - t * BQ), stats + (t & 1) * 2 * BQ);
         };
         const int tiles = i1 > i0 ? (i1 - i0 + BQ - 1) / BQ : 0;
-        if (tiles) start(0);
+        if (tiles) {
+            qg.start(0);
+            start_stats(0);
+        }
         filler.fill(a, h, bias);
-        if (tiles) finish(0);
+        if (tiles && Shape::kBuffers == 2) qg.finish(0);
 #pragma unroll
         for (int c = 0; c < NC; ++c) arrived(k[c]), arrived(v[c]);
         for (int t = 0; t < tiles; ++t) {
-            wave_loads_done();
-            __syncthreads();
-            if (t + 1 < tiles) start(t + 1);
-            const S* qtile = qtile_of(t);
-            const S* gtile = gtile_of(t);
+            qg.enter(t, t + 1 < tiles);
+            if (t + 1 < tiles) start_stats(t + 1);
+            const S* qtile = qg.x_of(t);
+            const S* gtile = qg.y_of(t);
             const float* stat = stats + (t & 1) * 2 * BQ;
             const int it = i0 + t * BQ;
 #pragma unroll
             for (int u = 0; u < QT; ++u) {
-                const int row0 = u * kTile, i = it + row0;
+                const int row0 = (wk * QT + u) * kTile, i = it + row0;
                 if (i > some1 || i + kTile <= some0) continue;
                 f32x16 s = {}, ds = {};
 #pragma unroll
@@ -374,22 +413,24 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
                 // distance of the tile's first key and first query; along the registers it falls
                 const int base = jw - i - item.pos32;
                 const Span span = span_of(base, a.R);
-                f32x4 lse2[4], delta[4];
+                f32x4 both[4][2];  // lse2 and delta of rows in turn
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    lse2[r] = *reinterpret_cast<const f32x4*>(stat + row0 + 8 * r + 4 * half);
-                    delta[r] = *reinterpret_cast<const f32x4*>(stat + BQ + row0 + 8 * r + 4 * half);
+                    both[r][0] = *reinterpret_cast<const f32x4*>(stat + 2 * (row0 + 8 * r + 4 * half));
+                    both[r][1] = *reinterpret_cast<const f32x4*>(stat + 2 * (row0 + 8 * r + 4 * half) + 4);
                 }
+                auto lse2 = [&](int r) { return both[r / 4][r % 4 / 2][r % 2 * 2]; };
+                auto delta = [&](int r) { return both[r / 4][r % 4 / 2][r % 2 * 2 + 1]; };
                 if (a.table && span == Span::kNear) {
                     const float* p = bias + (base + a.R + kBiasMargin - 4 * half + lane % 32);
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        s[r] = exp2_fast(fmaf(s[r], a.scale2, p[-acc_row(r, 0)]) - lse2[r / 4][r % 4]);
+                        s[r] = exp2_fast(fmaf(s[r], a.scale2, p[-acc_row(r, 0)]) - lse2(r));
                 } else {
                     const float flat = a.table ? bias[span == Span::kLow ? 0 : nbias - 1] : 0.0f;
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        s[r] = exp2_fast(fmaf(s[r], a.scale2, flat) - lse2[r / 4][r % 4]);
+                        s[r] = exp2_fast(fmaf(s[r], a.scale2, flat) - lse2(r));
                 }
                 if (i < all0 || i + kTile - 1 > all1) {
                     const uint32_t at = i + 4 * half - mine0;
@@ -397,7 +438,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
                     for (int r = 0; r < 16; ++r) s[r] = at + acc_row(r, 0) < mine ? s[r] : 0.0f;
                 }
 #pragma unroll
-                for (int r = 0; r < 16; ++r) ds[r] = s[r] * (ds[r] - delta[r / 4][r % 4]);
+                for (int r = 0; r < 16; ++r) ds[r] = s[r] * (ds[r] - delta(r));
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const Frag<S> p = to_frag<S>(s, c), g = to_frag<S>(ds, c);
@@ -408,63 +449,96 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 ? 1 : 2)) 
                     }
                 }
             }
-            if (t + 1 < tiles) finish(t + 1);
+            qg.leave(t, t + 1 < tiles);
         }
     }
     products_done<S>();
-    if (j >= a.Tk) return;
-    S* kr = a.dk ? (S*)a.dk + b * a.dks.item + (int64_t)j * a.dks.frame + hk * a.dks.head : nullptr;
-    S* vr = a.dv ? (S*)a.dv + b * a.dvs.item + (int64_t)j * a.dvs.frame + hk * a.dvs.head : nullptr;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int at = 32 * d + 8 * n + 4 * half;
-            if (kr)
-                store4<S>(kr, at, a.D, dk[d][4 * n] * a.scale, dk[d][4 * n + 1] * a.scale, dk[d][4 * n + 2] * a.scale,
-                          dk[d][4 * n + 3] * a.scale);
-            if (vr) store4<S>(vr, at, a.D, dv[d][4 * n], dv[d][4 * n + 1], dv[d][4 * n + 2], dv[d][4 * n + 3]);
-        }
+    const bool out = j < a.Tk;
+    if (a.dk) {
+        add_waves<OW, ND>(smem, dk, lane, wave);
+        if (out)
+            store_runs<S, OW, ND>((S*)a.dk + b * a.dks.item + (int64_t)j * a.dks.frame + hk * a.dks.head, dk, a.D, a.scale,
+                                  half, wave);
+    }
+    if (a.dv) {
+        add_waves<OW, ND>(smem, dv, lane, wave);
+        if (out)
+            store_runs<S, OW, ND>((S*)a.dv + b * a.dvs.item + (int64_t)j * a.dvs.frame + hk * a.dvs.head, dv, a.D, 1.0f,
+                                  half, wave);
     }
 }
 
 // ---------------------------------------------------------------------------
-static int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+// Launch plan
+// ---------------------------------------------------------------------------
+constexpr int kLdsBytes = 160 * 1024;
 
-static int64_t query_blocks(const AttnShape& s) { return (s.Tq + kBwdOwned - 1) / kBwdOwned; }
+static int padded_bias(const AttnShape& s) { return s.reach ? (2 * (int)s.reach + 1 + 2 * kBiasMargin + 3) / 4 * 4 : 0; }
 
-// delta, then the sums by distance: of the workgroups, and in all.
-static int64_t delta_bytes(const AttnShape& s) { return round16(s.B * s.H * s.Tq * (int64_t)sizeof(float)); }
-static int64_t dist_bytes(const AttnShape& s) {
-    return round16(s.H * s.B * query_blocks(s) * (2 * s.reach + 1) * (int64_t)sizeof(float));
+// Bytes of LDS of a workgroup that owns 32 * ow queries or keys of heads of DP.
+static int bwd_lds(const AttnShape& s, int elem_bytes, int ow, bool queries) {
+    const int dp = (int)(s.D + 31) / 32 * 32 + (s.D == 0 ? 32 : 0);
+    const int rows = ow == 1 ? 128 : ow == 2 || elem_bytes * dp <= 128 ? 64 : 32;
+    const int buffers = ow == 1 || (ow == 2 && elem_bytes == 4 && dp > 64) ? 1 : 2;
+    const int tiles = 2 * buffers * rows * (dp * elem_bytes / 16 + 1) * 16, bias = padded_bias(s) * 4;
+    return tiles + bias + (queries ? 4 * kTile * kDiag * 4 + 4 * bias : 4 * rows * 4);
 }
 
-size_t dwattn_bwd_workspace(const AttnShape& s) {
-    const int64_t total = s.reach ? s.H * (2 * s.reach + 1) * (int64_t)sizeof(double) : 0;
-    return (size_t)(delta_bytes(s) + (s.reach ? dist_bytes(s) : 0) + total);
+// Frames a workgroup owns, in units of 32: as many as leave enough workgroups
+// (bf16: two for each compute unit; float, whose products take 16 times as
+// long: eight, so that the last ones are short), if its LDS holds them.
+static int owned(const AttnShape& s, int elem_bytes, bool queries) {
+    constexpr int64_t kUnits = 256;
+    const int64_t pairs = s.B * (queries ? s.H : s.Hkv), frames = queries ? s.Tq : s.Tk;
+    const int64_t wide = kUnits * (elem_bytes == 4 ? 8 : 2);
+    int ow = pairs * ((frames + 127) / 128) >= wide ? 4 : pairs * ((frames + 63) / 64) >= kUnits ? 2 : 1;
+    while (ow < 4 && bwd_lds(s, elem_bytes, ow, queries) > kLdsBytes) ow *= 2;
+    return ow;
+}
+
+static int64_t blocks_of(int64_t frames, int ow) { return (frames + ow * kTile - 1) / (ow * kTile); }
+
+static int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// lse and delta, then the workgroups' sums by distance.
+static int64_t stat_bytes(const AttnShape& s) { return round16(s.B * s.H * s.Tq * 2 * (int64_t)sizeof(float)); }
+
+size_t dwattn_bwd_workspace(const AttnShape& s, int elem_bytes) {
+    const int64_t parts = s.B * blocks_of(s.Tq, owned(s, elem_bytes, true));
+    return (size_t)(stat_bytes(s) + (s.reach ? s.H * parts * (2 * s.reach + 1) * (int64_t)sizeof(float) : 0));
+}
+
+template <typename S, int DP, int OW>
+static hipError_t launch_dq(const AttnBwd& a, int lds, hipStream_t stream) {
+    const bool dma = dma_fits<S>(a.k, a.ks, a.D) && dma_fits<S>(a.v, a.vs, a.D) && BwdShape<S, DP, OW>::kBuffers == 2;
+    hipLaunchKernelGGL((dma ? attn_dq_kernel<S, DP, OW, BwdShape<S, DP, OW>::kBuffers == 2> : attn_dq_kernel<S, DP, OW, false>),
+                       dim3((uint32_t)(a.B * a.H) * a.nqb), dim3(kAttnThreads), lds, stream, a);
+    return hipGetLastError();
+}
+
+template <typename S, int DP, int OW>
+static hipError_t launch_dkv(const AttnBwd& a, int lds, hipStream_t stream) {
+    const AttnStride rows = {(int64_t)a.Tq * a.H * a.D, (int64_t)a.H * a.D, a.D};
+    const bool dma = dma_fits<S>(a.q, a.qs, a.D) && dma_fits<S>(a.dout, rows, a.D) && BwdShape<S, DP, OW>::kBuffers == 2;
+    hipLaunchKernelGGL((dma ? attn_dkv_kernel<S, DP, OW, BwdShape<S, DP, OW>::kBuffers == 2> : attn_dkv_kernel<S, DP, OW, false>),
+                       dim3((uint32_t)(a.B * a.Hkv) * a.nkb), dim3(kAttnThreads), lds, stream, a);
+    return hipGetLastError();
 }
 
 template <typename S, int DP>
-static hipError_t launch_bwd(const AttnBwd& a, hipStream_t stream) {
-    constexpr int kRows = kBwdRows<S, DP>;
-    const int nbias = a.table ? 2 * a.R + 1 + 2 * kBiasMargin : 0;
+static hipError_t launch_bwd(const AttnBwd& a, const AttnShape& s, int oq, int ok, hipStream_t stream) {
     if (a.nqb > 0) {
-        const int lds = 4 * Tile<S, DP>::bytes(kRows) + (nbias + 3) / 4 * 16 +
-                        (a.dist ? 4 * kTile * kDiag * 4 + 4 * nbias * 4 : 0);
-        const bool dma = dma_fits<S>(a.k, a.ks, a.D) && dma_fits<S>(a.v, a.vs, a.D);
-        hipLaunchKernelGGL((dma ? attn_dq_kernel<S, DP, true> : attn_dq_kernel<S, DP, false>),
-                           dim3((uint32_t)(a.B * a.H) * a.nqb), dim3(kAttnThreads), lds, stream, a);
-        const hipError_t e = hipGetLastError();
+        const int lds = bwd_lds(s, sizeof(S), oq, true);
+        const hipError_t e = oq == 4   ? launch_dq<S, DP, 4>(a, lds, stream)
+                             : oq == 2 ? launch_dq<S, DP, 2>(a, lds, stream)
+                                       : launch_dq<S, DP, 1>(a, lds, stream);
         if (e != hipSuccess) return e;
     }
     if (a.nkb > 0 && (a.dk || a.dv)) {
-        const int lds = 4 * Tile<S, DP>::bytes(kRows) + 4 * kRows * 4 + nbias * 4;
-        const AttnStride rows = {(int64_t)a.Tq * a.H * a.D, (int64_t)a.H * a.D, a.D};
-        const bool dma = dma_fits<S>(a.q, a.qs, a.D) && dma_fits<S>(a.dout, rows, a.D);
-        hipLaunchKernelGGL((dma ? attn_dkv_kernel<S, DP, true> : attn_dkv_kernel<S, DP, false>),
-                           dim3((uint32_t)(a.B * a.Hkv) * a.nkb), dim3(kAttnThreads), lds, stream, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        const int lds = bwd_lds(s, sizeof(S), ok, false);
+        return ok == 4   ? launch_dkv<S, DP, 4>(a, lds, stream)
+               : ok == 2 ? launch_dkv<S, DP, 2>(a, lds, stream)
+                         : launch_dkv<S, DP, 1>(a, lds, stream);
     }
     return hipSuccess;
 }
@@ -477,27 +551,21 @@ hipError_t launch_dwattn_bwd(const AttnPtrs& p, const AttnShape& s, const void* 
     a.out = out, a.lse = lse, a.dout = dout;
     a.dq = dq, a.dk = dk, a.dv = dv;
     a.dqs = s.dq, a.dks = s.dk, a.dvs = s.dv;
-    a.nqb = (int32_t)query_blocks(s);
-    a.nkb = (int32_t)((s.Tk + kBwdOwned - 1) / kBwdOwned);
-    char* at = (char*)workspace;
-    a.delta = (float*)at;
-    at += delta_bytes(s);
-    a.dist = dtable ? (float*)at : nullptr;
-    double* total = (double*)(at + dist_bytes(s));
+    const int oq = owned(s, bf16 ? 2 : 4, true), ok = owned(s, bf16 ? 2 : 4, false);
+    a.nqb = (int32_t)blocks_of(s.Tq, oq);
+    a.nkb = (int32_t)blocks_of(s.Tk, ok);
+    a.stat = (float*)workspace;
+    a.dist = dtable ? (float*)((char*)workspace + stat_bytes(s)) : nullptr;
     if (s.B > 0) {
         const hipError_t e = with_head_width(s.D, [&](auto dp) {
-            return bf16 ? launch_bwd<uint16_t, dp.value>(a, stream) : launch_bwd<float, dp.value>(a, stream);
+            return bf16 ? launch_bwd<uint16_t, dp.value>(a, s, oq, ok, stream)
+                        : launch_bwd<float, dp.value>(a, s, oq, ok, stream);
         });
         if (e != hipSuccess) return e;
     }
     if (!dtable) return hipSuccess;
-    const int32_t n = 2 * a.R + 1;
-    hipLaunchKernelGGL(attn_dbias_rows, dim3((n + kDistCols - 1) / kDistCols, a.H), dim3(kDistCols * kDistRows), 0, stream,
-                       a.dist, total, n, (int32_t)(s.B * a.nqb));
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(attn_dtable, dim3((a.NB + 3) / 4, a.H), dim3(kAttnThreads), 0, stream, total, p.buckets, dtable, n,
-                       a.NB, a.H);
+    hipLaunchKernelGGL(attn_dtable, dim3(a.NB, a.H), dim3(kAttnThreads), 0, stream, a.dist, p.buckets, dtable, 2 * a.R + 1,
+                       (int32_t)(s.B * a.nqb), a.NB, a.H);
     return hipGetLastError();
 }
 

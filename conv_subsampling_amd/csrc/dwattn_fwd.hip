@@ -32,21 +32,23 @@ struct AttnFwd : AttnArgs {
 // below 2^kSlack, and most tiles need no rescaling of the accumulators.
 constexpr float kSlack = 8.0f;
 
-// Keys of a tile, and the waves per SIMD its registers are to allow.
+// Keys of a tile, its buffers, and the waves per SIMD that its registers are to
+// allow.
 template <typename S, int DP, int QW, bool DMA>
 struct FwdShape {
     static constexpr int BN = QW == 1 ? 128 : QW == 2 || sizeof(S) * DP <= 128 ? 64 : 32;
-    static constexpr int kBuffers = QW == 1 ? 1 : 2;  // of the tiles
+    static constexpr int kBuffers = QW == 1 ? 1 : 2;
     static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : QW == 4 && DMA && sizeof(S) == 2 ? 3 : 2;
+    using Tiles = TilePair<S, DP, BN, kBuffers, DMA>;
 };
 
 template <typename S, int DP, int QW, bool DMA>
 __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) void attn_fwd_kernel(const AttnFwd a) {
-    constexpr int KW = 4 / QW, BN = FwdShape<S, DP, QW, DMA>::BN, KT = BN / kTile / KW, NC = DP / 16, ND = DP / 32;
-    constexpr int kBuffers = FwdShape<S, DP, QW, DMA>::kBuffers;
+    using F = FwdShape<S, DP, QW, DMA>;
+    constexpr int KW = 4 / QW, BN = F::BN, KT = BN / kTile / KW, NC = DP / 16, ND = DP / 32;
     typedef Tile<S, DP> T;
     extern __shared__ __align__(16) char smem[];
-    float* bias = (float*)(smem + 2 * kBuffers * T::bytes(BN));
+    float* bias = (float*)(smem + F::Tiles::kAllBytes);
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
     const int wq = wave % QW, wk = wave / QW;
 
@@ -76,25 +78,14 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
     const int some0 = item.first_key(a, iw), some1 = iw < item.nq ? item.last_key(a, iwl) : -1;
     const int all0 = item.first_key(a, iwl), all1 = iw + kTile <= item.nq ? item.last_key(a, iw) : -1;
 
-    const S* kbase = (const S*)a.k + b * a.ks.item + (int64_t)(h / (a.H / a.Hkv)) * a.ks.head;
-    const S* vbase = (const S*)a.v + b * a.vs.item + (int64_t)(h / (a.H / a.Hkv)) * a.vs.head;
-    TileLoad<S, DP, BN, DMA> kl, vl;
-    kl.setup(a.ks.frame, a.D);
-    vl.setup(a.vs.frame, a.D);
-    auto ktile = [&](int t) { return (S*)(smem + (kBuffers == 2 && (t & 1) ? 2 * T::bytes(BN) : 0)); };
-    auto vtile = [&](int t) { return (S*)((char*)ktile(t) + T::bytes(BN)); };
-    auto start = [&](int t) {
-        const int64_t j = j0 + t * BN;
-        kl.start(kbase + j * a.ks.frame, a.ks.frame, j1 - (int)j, a.D, ktile(t));
-        vl.start(vbase + j * a.vs.frame, a.vs.frame, j1 - (int)j, a.D, vtile(t));
-    };
-    auto finish = [&](int t) {
-        kl.finish(ktile(t));
-        vl.finish(vtile(t));
-    };
+    const int hk = h / (a.H / a.Hkv);
+    const int64_t j00 = j0 + t0 * BN;
+    typename F::Tiles kv(smem, (const S*)a.k + b * a.ks.item + hk * a.ks.head + j00 * a.ks.frame, a.ks.frame,
+                         (const S*)a.v + b * a.vs.item + hk * a.vs.head + j00 * a.vs.frame, a.vs.frame, a.D,
+                         min(j1, j0 + t1 * BN) - (int)j00);
 
     const BiasFill<S> filler(a);
-    if (t0 < t1) start(t0);
+    if (t0 < t1) kv.start(0);
     Frag<S> q[NC];
     {
         const S* row = (const S*)a.q + b * a.qs.item + (int64_t)(live ? i : 0) * a.qs.frame + h * a.qs.head;
@@ -102,24 +93,18 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
         for (int c = 0; c < NC; ++c) q[c] = to_frag<S>(load_group<S, !DMA>(row, 16 * c + 8 * half, live ? a.D : 0));
     }
     filler.fill(a, h, bias);
-    if (kBuffers == 2 && t0 < t1) finish(t0);
+    if (F::kBuffers == 2 && t0 < t1) kv.finish(0);
 #pragma unroll
     for (int c = 0; c < NC; ++c) arrived(q[c]);
     f32x16 o[ND] = {};
     float top = -__builtin_inff(), sum = 0.0f;
-    for (int t = t0; t < t1; ++t) {
-        if (kBuffers == 1) {
-            __syncthreads();
-            finish(t);
-        }
-        wave_loads_done();
-        __syncthreads();
-        if (t + 1 < t1) start(t + 1);
-        const S* kt = ktile(t);
-        const S* vt = vtile(t);
+    for (int t = 0; t < t1 - t0; ++t) {
+        kv.enter(t, t + 1 < t1 - t0);
+        const S* kt = kv.x_of(t);
+        const S* vt = kv.y_of(t);
 #pragma unroll
         for (int u = 0; u < KT; ++u) {
-            const int row0 = (wk * KT + u) * kTile, j = j0 + t * BN + row0;
+            const int row0 = (wk * KT + u) * kTile, j = (int)j00 + t * BN + row0;
             if (j > some1 || j + kTile <= some0) continue;
             // The tile's operands are read ahead of their use: the keys before
             // the first product, the first half of the values before the softmax
@@ -186,7 +171,7 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
                 for (int d = 0; d < ND; ++d)
                     o[d] = mma(kAhead && c == 0 ? v[d] : T::columns(vt, row0 + 16 * c, d, lane), p[c], o[d]);
         }
-        if (kBuffers == 2 && t + 1 < t1) finish(t + 1);
+        kv.leave(t, t + 1 < t1 - t0);
     }
     products_done<S>();
     sum += swap_halves(sum);
@@ -197,7 +182,7 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
     if constexpr (KW > 1) {
         float* opart = (float*)smem;                          // [4][ND * 16][64]
         float* stat = (float*)(smem + 4 * ND * 16 * 64 * 4);  // [4][2][32]
-        static_assert(4 * ND * 16 * 64 * 4 + 4 * 2 * 32 * 4 <= 2 * kBuffers * T::bytes(BN), "the tiles' room holds the join");
+        static_assert(4 * ND * 16 * 64 * 4 + 4 * 2 * 32 * 4 <= F::Tiles::kAllBytes, "the tiles' room holds the join");
         __syncthreads();
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -361,8 +346,8 @@ bool dwattn_fits(const AttnShape& s) {
 
 template <typename S, int DP, int QW, bool DMA>
 static hipError_t launch_fwd(const AttnFwd& a, hipStream_t stream) {
-    typedef FwdShape<S, DP, QW, DMA> F;
-    const int lds = 2 * F::kBuffers * Tile<S, DP>::bytes(F::BN) + (a.table ? attn_bias_bytes(a.R) : 0);
+    using F = FwdShape<S, DP, QW, DMA>;
+    const int lds = F::Tiles::kAllBytes + (a.table ? attn_bias_bytes(a.R) : 0);
     hipLaunchKernelGGL((attn_fwd_kernel<S, DP, QW, DMA>), dim3((uint32_t)(a.B * a.H) * a.nqb * a.splits),
                        dim3(kAttnThreads), lds, stream, a);
     return hipGetLastError();
