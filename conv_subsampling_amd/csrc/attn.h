@@ -111,13 +111,15 @@ __device__ __forceinline__ Frag<S> to_frag(const RawGroup<S>& g) {
 // A tile of frames x DP head elements in LDS.  A row is a whole number of
 // 16-byte chunks and a pad that puts the rows that one instruction touches on
 // different banks: eight neighbouring rows for a 16-byte read, four for a
-// transposing one (measured, a 16-byte read from every lane: 8.5 cycles with
-// these strides as from linear addresses, 64 without the pad at 128 elements).
-// ---------------------------------------------------------------------------
+// transposing one.  Measured, sixteen waves reading: 16-byte reads take 2.7
+// cycles with these pads as from linear addresses (25 without one at 128 bf16
+// elements), transposing reads 3.2 (4.7 there with one chunk of pad).
+constexpr int tile_slots(int chunks, int elem_bytes) { return chunks + (chunks == 16 && elem_bytes == 2 ? 3 : 1); }
+
 template <typename S, int DP>
 struct Tile {
     static constexpr int kChunks = DP * (int)sizeof(S) / 16;
-    static constexpr int kSlots = kChunks + 1;  // with the pad
+    static constexpr int kSlots = tile_slots(kChunks, sizeof(S));
     static constexpr int kStride = kSlots * 16 / (int)sizeof(S);
     static constexpr int kGroups = DP / kGroup;  // 8-element groups of a row
 

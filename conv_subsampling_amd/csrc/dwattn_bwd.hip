@@ -480,7 +480,7 @@ static int bwd_lds(const AttnShape& s, int elem_bytes, int ow, bool queries) {
     const int dp = (int)(s.D + 31) / 32 * 32 + (s.D == 0 ? 32 : 0);
     const int rows = ow == 1 ? 128 : ow == 2 || elem_bytes * dp <= 128 ? 64 : 32;
     const int buffers = ow == 1 || (ow == 2 && elem_bytes == 4 && dp > 64) ? 1 : 2;
-    const int tiles = 2 * buffers * rows * (dp * elem_bytes / 16 + 1) * 16, bias = padded_bias(s) * 4;
+    const int tiles = 2 * buffers * rows * tile_slots(dp * elem_bytes / 16, elem_bytes) * 16, bias = padded_bias(s) * 4;
     return tiles + bias + (queries ? 4 * kTile * kDiag * 4 + 4 * bias : 4 * rows * 4);
 }
 
