@@ -22,7 +22,7 @@ namespace dw {
 struct AttnBwd : AttnArgs {
     const void *out, *dout;  // [B][Tq][H][D]
     const float* lse;        // [B][H][Tq]
-    float* stat;             // [B][H][Tq][2]: lse in units of log2 (inf where there are no keys), and delta
+    float* stat;             // [B][H][2][Tq]: lse in units of log2 (inf where there are no keys), then delta
     void *dq, *dk, *dv;
     AttnStride dqs, dks, dvs;
     float* dist;  // [H][B * nqb][2 R + 1] sums of dS by distance; NULL: not wanted
@@ -38,15 +38,16 @@ __device__ __forceinline__ float lse_or_inf(float lse) {
 }
 
 
-// One float a lane of this wave's part of `from` into LDS at `to` (both by the
-// thread's place in the workgroup); past `count` floats it is zero.
-__device__ __forceinline__ void load_lds_floats(const float* from, int count, float* to) {
-    const uint64_t at = (uint64_t)from;
-    const u32x4 rsrc = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, count > 0 ? (uint32_t)count * 4 : 0,
+// from[at] of every lane into LDS at to[at], zero for at >= count; the lanes of
+// a wave have 64 neighbouring `at`.
+__device__ __forceinline__ void load_lds_floats(const float* from, int count, int at, float* to) {
+    const uint64_t base = (uint64_t)from;
+    const u32x4 rsrc = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, count > 0 ? (uint32_t)count * 4 : 0,
                         (uint32_t)kBufferFlags};
-    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)to + wave_of_block() * 256;
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)to +
+                         __builtin_amdgcn_readfirstlane(at / 64) * 256;
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(threadIdx.x * 4), "s"(rsrc)
+                 :: "s"(lds), "v"(at * 4), "s"(rsrc)
                  : "memory");
 }
 
@@ -152,8 +153,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
         const int64_t stat = ((int64_t)b * a.H + h) * a.Tq + i;
         if (live) lse2 = lse_or_inf(a.lse[stat]);
         if (half == 0 && wk == 0 && i < a.Tq) {
-            a.stat[2 * stat] = lse2;
-            a.stat[2 * stat + 1] = delta;
+            const int64_t head = ((int64_t)b * a.H + h) * 2 * a.Tq;
+            a.stat[head + i] = lse2;
+            a.stat[head + a.Tq + i] = delta;
         }
     }
     if (!a.dq && !a.dist) return;
@@ -331,14 +333,23 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dtable(const float* __restr
     if (threadIdx.x == 0) dtable[(int64_t)bucket * H + h] = (float)(waves[0] + waves[1] + waves[2] + waves[3]);
 }
 
+// Wide bf16 heads leave no room for all of a wave's operands and sums in the
+// registers of two waves a SIMD: its values then wait in LDS, in the order in
+// which the lanes read them (16 bytes a lane).
+template <typename S, int DP>
+constexpr bool kValuesInLds = sizeof(S) == 2 && DP > 64;
+template <typename S, int DP>
+constexpr int kValuesBytes = kValuesInLds<S, DP> ? 4 * (DP / 16) * 64 * 16 : 0;
+
 template <typename S, int DP, int OW, bool DMA>
-__global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 || (!DMA && DP > 32) ? 1 : 2)) void attn_dkv_kernel(const AttnBwd a) {
+__global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) ? 1 : 2)) void attn_dkv_kernel(const AttnBwd a) {
     typedef BwdShape<S, DP, OW> Shape;
     typedef typename Shape::template Tiles<DMA> Tiles;
     typedef Tile<S, DP> T;
     constexpr int KW = 4 / OW, BQ = Shape::ROWS, QT = BQ / kTile / KW, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) char smem[];
-    float* stats = (float*)(smem + Tiles::kAllBytes);  // of two tiles: [2][BQ][2], as a.stat
+    u32x4* values = (u32x4*)(smem + Tiles::kAllBytes);
+    float* stats = (float*)(smem + Tiles::kAllBytes + kValuesBytes<S, DP>);  // of two tiles: [2][2][BQ], as a.stat
     float* bias = stats + 4 * BQ;
     const int nbias = 2 * a.R + 1 + 2 * kBiasMargin;
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
@@ -358,7 +369,17 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 || (!DMA &
             k[c] = to_frag<S>(load_group<S, !DMA>(kr, 16 * c + 8 * half, live ? a.D : 0));
             v[c] = to_frag<S>(load_group<S, !DMA>(vr, 16 * c + 8 * half, live ? a.D : 0));
         }
+        if constexpr (kValuesInLds<S, DP>) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) values[(wave * NC + c) * 64 + lane] = v[c].r;
+        }
     }
+    auto value = [&](int c) {
+        if constexpr (kValuesInLds<S, DP>)
+            return Frag<S>{values[(wave * NC + c) * 64 + lane]};
+        else
+            return v[c];
+    };
     const int mine0 = item.first_query(a, j), mine1 = item.last_query(a, j);
     const uint32_t mine = live && mine1 >= mine0 ? mine1 - mine0 + 1 : 0;
     int i0 = 0, i1 = 0;
@@ -378,10 +399,13 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 || (!DMA &
         const int64_t gstride = (int64_t)a.H * a.D;
         Tiles qg(smem, (const S*)a.q + b * a.qs.item + h * a.qs.head + (int64_t)i0 * a.qs.frame, a.qs.frame,
                  (const S*)a.dout + (((int64_t)b * a.Tq + i0) * a.H + h) * a.D, gstride, a.D, i1 - i0);
-        const float* stat_rows = a.stat + 2 * (((int64_t)b * a.H + h) * a.Tq + i0);
-        // the tile's lse and delta, one float a lane of its first waves
+        // the tile's lse and delta, one float a lane: the first waves take the one, the next the other
+        const float* stat_rows = a.stat + ((int64_t)b * a.H + h) * 2 * a.Tq + i0;
         auto start_stats = [&](int t) {
-            if (threadIdx.x < 2 * BQ) load_lds_floats(stat_rows + 2 * t * BQ, 2 * (i1 - i0 - t * BQ), stats + (t & 1) * 2 * BQ);
+            constexpr int kEach = BQ < 64 ? 64 : BQ;
+            const int which = __builtin_amdgcn_readfirstlane(threadIdx.x / kEach), at = threadIdx.x % kEach;
+            if (which < 2 && at < BQ)
+                load_lds_floats(stat_rows + which * a.Tq + t * BQ, i1 - i0 - t * BQ, at, stats + ((t & 1) * 2 + which) * BQ);
         };
         const int tiles = i1 > i0 ? (i1 - i0 + BQ - 1) / BQ : 0;
         if (tiles) {
@@ -391,7 +415,10 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 || (!DMA &
         filler.fill(a, h, bias);
         if (tiles && Shape::kBuffers == 2) qg.finish(0);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) arrived(k[c]), arrived(v[c]);
+        for (int c = 0; c < NC; ++c) {
+            arrived(k[c]);
+            if (!kValuesInLds<S, DP>) arrived(v[c]);
+        }
         for (int t = 0; t < tiles; ++t) {
             qg.enter(t, t + 1 < tiles);
             if (t + 1 < tiles) start_stats(t + 1);
@@ -407,20 +434,17 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 || (!DMA &
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
                     s = mma(T::rows(qtile, row0, c, lane), k[c], s);
-                    ds = mma(T::rows(gtile, row0, c, lane), v[c], ds);
+                    ds = mma(T::rows(gtile, row0, c, lane), value(c), ds);
+                    if (kValuesInLds<S, DP> && c % 2) __builtin_amdgcn_sched_barrier(0);
                 }
                 products_done<S>();
                 // distance of the tile's first key and first query; along the registers it falls
                 const int base = jw - i - item.pos32;
                 const Span span = span_of(base, a.R);
-                f32x4 both[4][2];  // lse2 and delta of rows in turn
+                f32x4 row[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    both[r][0] = *reinterpret_cast<const f32x4*>(stat + 2 * (row0 + 8 * r + 4 * half));
-                    both[r][1] = *reinterpret_cast<const f32x4*>(stat + 2 * (row0 + 8 * r + 4 * half) + 4);
-                }
-                auto lse2 = [&](int r) { return both[r / 4][r % 4 / 2][r % 2 * 2]; };
-                auto delta = [&](int r) { return both[r / 4][r % 4 / 2][r % 2 * 2 + 1]; };
+                for (int r = 0; r < 4; ++r) row[r] = *reinterpret_cast<const f32x4*>(stat + row0 + 8 * r + 4 * half);
+                auto lse2 = [&](int r) { return row[r / 4][r % 4]; };
                 if (a.table && span == Span::kNear) {
                     const float* p = bias + (base + a.R + kBiasMargin - 4 * half + lane % 32);
 #pragma unroll
@@ -438,7 +462,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 || (!DMA &
                     for (int r = 0; r < 16; ++r) s[r] = at + acc_row(r, 0) < mine ? s[r] : 0.0f;
                 }
 #pragma unroll
-                for (int r = 0; r < 16; ++r) ds[r] = s[r] * (ds[r] - delta(r));
+                for (int r = 0; r < 4; ++r) row[r] = *reinterpret_cast<const f32x4*>(stat + BQ + row0 + 8 * r + 4 * half);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) ds[r] = s[r] * (ds[r] - row[r / 4][r % 4]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const Frag<S> p = to_frag<S>(s, c), g = to_frag<S>(ds, c);
@@ -446,6 +472,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 || sizeof(S) == 4 || (!DMA &
                     for (int d = 0; d < ND; ++d) {
                         dv[d] = mma(T::columns(gtile, row0 + 16 * c, d, lane), p, dv[d]);
                         dk[d] = mma(T::columns(qtile, row0 + 16 * c, d, lane), g, dk[d]);
+                        if (kValuesInLds<S, DP> && d % 2) __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
@@ -481,7 +508,8 @@ static int bwd_lds(const AttnShape& s, int elem_bytes, int ow, bool queries) {
     const int rows = ow == 1 ? 128 : ow == 2 || elem_bytes * dp <= 128 ? 64 : 32;
     const int buffers = ow == 1 || (ow == 2 && elem_bytes == 4 && dp > 64) ? 1 : 2;
     const int tiles = 2 * buffers * rows * tile_slots(dp * elem_bytes / 16, elem_bytes) * 16, bias = padded_bias(s) * 4;
-    return tiles + bias + (queries ? 4 * kTile * kDiag * 4 + 4 * bias : 4 * rows * 4);
+    const int values = elem_bytes == 2 && dp > 64 ? 4 * (dp / 16) * 64 * 16 : 0;  // kValuesBytes
+    return tiles + bias + (queries ? 4 * kTile * kDiag * 4 + 4 * bias : values + 4 * rows * 4);
 }
 
 // Frames a workgroup owns, in units of 32: as many as leave enough workgroups
