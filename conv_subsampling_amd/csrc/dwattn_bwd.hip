@@ -29,7 +29,7 @@ struct AttnBwd : AttnArgs {
     int32_t nqb, nkb;
 };
 
-constexpr int kDiag = 36;             // row stride of the square that the diagonals are read from
+constexpr int kDiag = 64;  // row of the square in which the diagonals of a tile lie in columns
 
 // exp(S - lse) of a query that has keys; lse = -inf marks one that has none,
 // whose weights are zero.
@@ -131,8 +131,10 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
     const int wk = wave / OW, i0 = qb * OW * kTile, iw = i0 + wave % OW * kTile, i = iw + lane % 32;
     const bool live = i < item.nq;
     const BiasFill<S> filler(a);
-    if (a.dist)
+    if (a.dist) {
         for (int x = lane; x < nbias; x += 64) sums[x] = 0.0f;
+        for (int x = lane; x < kTile * kDiag; x += 64) square[x] = 0.0f;
+    }
 
     Frag<S> q[NC], g[NC];
     float delta = 0.0f, lse2 = __builtin_inff();
@@ -218,27 +220,18 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
             }
             if (a.dist) {
                 if (span == Span::kNear) {
-                    // The 63 diagonals of the tile: rows are queries in the
-                    // square, and lane x reads column (x + row) mod 32, which
-                    // is the diagonal x up to the wrap and x - 32 after it.
+                    // The 63 diagonals of the tile: query i writes its 32 keys
+                    // from place 31 - i of its row of the square, so that a
+                    // column holds one distance, and the places that no tile
+                    // writes stay zero.
+                    float* to = square + (lane % 32) * (kDiag - 1) + 31 + 4 * half;
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        *reinterpret_cast<f32x4*>(square + (lane % 32) * kDiag + 8 * n + 4 * half) =
-                            f32x4{ds[4 * n], ds[4 * n + 1], ds[4 * n + 2], ds[4 * n + 3]};
+                    for (int r = 0; r < 16; ++r) to[acc_row(r, 0)] = ds[r];
                     wave_lds_fence();
-                    float up = 0.0f, down = 0.0f;
+                    float t[4] = {};
 #pragma unroll
-                    for (int n = 0; n < 16; ++n) {
-                        const int row = 16 * half + n, col = lane % 32 + row;
-                        const float x = square[row * kDiag + col % 32];
-                        up += col < 32 ? x : 0.0f;
-                        down += col < 32 ? 0.0f : x;
-                    }
-                    up += swap_halves(up);
-                    down += swap_halves(down);
-                    float* p = sums + base + a.R + kBiasMargin + lane % 32;
-                    if (half == 0) *p += up;
-                    else p[-32] += down;
+                    for (int n = 0; n < kTile; ++n) t[n % 4] += square[n * kDiag + lane];
+                    if (lane < kDiag - 1) sums[base + a.R + kBiasMargin - 31 + lane] += (t[0] + t[1]) + (t[2] + t[3]);
                     wave_lds_fence();
                 } else {
                     float t = 0.0f;
