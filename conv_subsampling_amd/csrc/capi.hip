@@ -561,6 +561,7 @@ dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const v
 size_t dwattn_bwd_workspace_bytes(const dw_attn* shape) {
     dw::AttnShape s;
     if (!shape || check_attn("dwattn_bwd_workspace_bytes", shape, shape->buckets > 0, &s) != DW_OK) return 0;
+    if (!dw::dwattn_bwd_fits(s)) return 0;
     return dw::dwattn_bwd_workspace(s, shape->dtype == DW_BF16 ? 2 : 4);
 }
 
@@ -576,7 +577,7 @@ dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const v
     if (c != DW_OK) return c;
     if (!strides_ok(shape->dq) || !strides_ok(shape->dk) || !strides_ok(shape->dv))
         return fail(DW_ERR_INVALID_ARG, "%s: negative stride", fn);
-    if ((dq && !strides_fit(shape->dq, s.B, s.Tq, s.H)) || (dk && !strides_fit(shape->dk, s.B, s.Tk, s.Hkv)) ||
+    if (!dw::dwattn_bwd_fits(s) || (dq && !strides_fit(shape->dq, s.B, s.Tq, s.H)) || (dk && !strides_fit(shape->dk, s.B, s.Tk, s.Hkv)) ||
         (dv && !strides_fit(shape->dv, s.B, s.Tk, s.Hkv)))
         return too_large(fn);
     if ((!dq && !dk && !dv && !dtable) || s.H == 0) return ok();

@@ -524,6 +524,11 @@ static int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 // lse and delta, then the workgroups' sums by distance.
 static int64_t stat_bytes(const AttnShape& s) { return round16(s.B * s.H * s.Tq * 2 * (int64_t)sizeof(float)); }
 
+bool dwattn_bwd_fits(const AttnShape& s) {
+    // the workgroups' sums by distance of one head, counted in 31 bits
+    return s.reach == 0 || product_below(kMaxExtent, {s.B, (s.Tq + kTile - 1) / kTile, 2 * s.reach + 1});
+}
+
 size_t dwattn_bwd_workspace(const AttnShape& s, int elem_bytes) {
     const int64_t parts = s.B * blocks_of(s.Tq, owned(s, elem_bytes, true));
     return (size_t)(stat_bytes(s) + (s.reach ? s.H * parts * (2 * s.reach + 1) * (int64_t)sizeof(float) : 0));

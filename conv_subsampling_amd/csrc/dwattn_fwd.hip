@@ -11,13 +11,6 @@
 // results attn_join adds.
 #include "attn.h"
 
-#ifndef DW_ATTN_WIDE_BF16
-#define DW_ATTN_WIDE_BF16 3
-#endif
-#ifndef DW_ATTN_WIDE_F32
-#define DW_ATTN_WIDE_F32 8
-#endif
-
 namespace dw {
 
 struct AttnFwd : AttnArgs {
@@ -37,7 +30,7 @@ constexpr float kSlack = 8.0f;
 template <typename S, int DP, int QW, bool DMA>
 struct FwdShape {
     static constexpr int BN = QW == 1 ? 128 : QW == 2 || sizeof(S) * DP <= 128 ? 64 : 32;
-    static constexpr int kBuffers = QW == 1 ? 1 : 2;
+    static constexpr int kBuffers = QW == 1 && !(DMA && sizeof(S) * DP <= 128) ? 1 : 2;
     static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : QW == 4 && DMA && sizeof(S) == 2 ? 3 : 2;
     using Tiles = TilePair<S, DP, BN, kBuffers, DMA>;
 };
@@ -305,10 +298,15 @@ struct FwdPlan {
 // taken where they make workgroups enough; next 64, whose two pairs of waves
 // divide the keys; and with the fewest queries 32, the keys then being split
 // over workgroups until each compute unit has one.  The plan goes by the sizes
-// alone (lengths are on the device).
+// alone (lengths are on the device).  Enough is three a compute unit for bf16
+// (that many are resident: [16,750,8x128] takes 49 us so, 69 us with 64 queries)
+// and eight for float, whose tiles take 16 times as long in the matrix units, so
+// that short workgroups fill up behind long ones (causal [8,1500,8x64], three a
+// unit: 221 us with 128 queries, 171 us with 64).  Twice as many splits cost the
+// join more than they save (16 frames over 20000 keys, 8 heads: 18 and 21 us).
 static FwdPlan fwd_plan(const AttnShape& s, int elem_bytes) {
     constexpr int64_t kUnits = 256;
-    const int64_t wide = kUnits * (elem_bytes == 4 ? DW_ATTN_WIDE_F32 : DW_ATTN_WIDE_BF16);
+    const int64_t wide = kUnits * (elem_bytes == 4 ? 8 : 3);
     FwdPlan p;
     auto blocks_of = [&](int64_t queries) { return s.B * s.H * ((s.Tq + queries - 1) / queries); };
     p.qw = s.Tq > 32 && blocks_of(128) >= wide ? 4 : s.Tq > 32 && blocks_of(64) >= kUnits ? 2 : 1;
@@ -357,7 +355,9 @@ template <typename S>
 static hipError_t fwd_of_type(const AttnFwd& a, int qw, hipStream_t stream) {
     const bool dma = dma_fits<S>(a.k, a.ks, a.D) && dma_fits<S>(a.v, a.vs, a.D);
     const hipError_t e = with_head_width(a.D, [&](auto dp) {
-        return qw == 1 ? launch_fwd<S, dp.value, 1, false>(a, stream)
+        constexpr bool kNarrow = sizeof(S) * dp.value <= 128;  // two buffers of 128 keys leave room for two workgroups
+        return qw == 1 && dma && kNarrow ? launch_fwd<S, dp.value, 1, kNarrow>(a, stream)
+               : qw == 1 ? launch_fwd<S, dp.value, 1, false>(a, stream)
                : qw == 2 && dma ? launch_fwd<S, dp.value, 2, true>(a, stream)
                : qw == 2 ? launch_fwd<S, dp.value, 2, false>(a, stream)
                : dma ? launch_fwd<S, dp.value, 4, true>(a, stream)

@@ -166,6 +166,7 @@ size_t dwattn_fwd_workspace(const AttnShape& s, int elem_bytes);
 hipError_t launch_dwattn_fwd(const AttnPtrs& p, const AttnShape& s, void* out, float* lse, void* workspace, bool bf16,
                              hipStream_t stream);
 
+bool dwattn_bwd_fits(const AttnShape& s);  // beyond dwattn_fits
 size_t dwattn_bwd_workspace(const AttnShape& s, int elem_bytes);
 hipError_t launch_dwattn_bwd(const AttnPtrs& p, const AttnShape& s, const void* out, const float* lse, const void* dout,
                              void* dq, void* dk, void* dv, float* dtable, void* workspace, bool bf16,

@@ -157,7 +157,8 @@ def test_attention_backward_validation(alib):
     X = [ctypes.c_void_p(0x10000 * i) for i in range(1, 12)]
     # q, k, v, table, map, q_lengths, k_lengths, q_pos, out, lse, dout, dq, dk, dv, dtable, workspace
     a = [X[0], X[1], X[2], X[3], X[4], N, N, N, X[5], X[6], X[7], X[8], X[9], X[10], P, W]
-    for bad, status in BAD_SHAPES + [(dict(dq=Strides(-1, 1, 1)), INVALID), (dict(dk=Strides(1 << 60, 1, 1)), UNSUPPORTED)]:
+    for bad, status in BAD_SHAPES + [(dict(dq=Strides(-1, 1, 1)), INVALID), (dict(dk=Strides(1 << 60, 1, 1)), UNSUPPORTED),
+                                  (dict(B=1 << 16, Tq=1 << 11, H=1, Hkv=1, D=1, reach=1024), UNSUPPORTED)]:
         assert f(attn(**bad), *a, big, N) == status, bad
 
     def with_(**k):
