@@ -14,6 +14,7 @@ same device (or None for full length).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -609,6 +610,8 @@ def rel_buckets(num_buckets: int, reach: int, bidirectional: bool = True, device
 
 def _heads(name, t, st, device, shape):
     """A [B, frames, heads, D] tensor whose head elements lie next to each other."""
+    if type(t) is torch.Tensor and t.dtype is st and t.device == device and t.shape == shape and t.stride(3) == 1:
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -654,6 +657,12 @@ def _attn_shape(q, k, v, table, buckets, q_lengths, k_lengths, q_pos, left, righ
 _NO_STRIDES = (0,) * 9   # dq, dk, dv of a call that has none
 
 
+@functools.lru_cache(maxsize=1024)
+def _attn_workspace(backward: bool, shape: bytes) -> int:
+    """The library's answer for these sizes, which depends on nothing else."""
+    return int((_lib.dwattn_bwd_workspace_bytes if backward else _lib.dwattn_fwd_workspace_bytes)(shape))
+
+
 def _limit(n: int) -> int:
     return n if -1 <= n < 1 << 40 else (-1 if n < 0 else 1 << 40)
 
@@ -661,7 +670,7 @@ def _limit(n: int) -> int:
 def dwattn_fwd_workspace_bytes(q, k, v, left: int = -1, right: int = -1) -> int:
     """Bytes of workspace `dwattn_fwd` takes for tensors of these sizes."""
     _, sizes, rest = _attn_shape(q, k, v, None, None, None, None, None, left, right, None)
-    return int(_lib.dwattn_fwd_workspace_bytes(_attn_struct.pack(*sizes, *_NO_STRIDES, *rest)))
+    return _attn_workspace(False, _attn_struct.pack(*sizes, *_NO_STRIDES, *rest))
 
 
 def dwattn_fwd(q, k, v, table=None, buckets=None, q_lengths=None, k_lengths=None, q_pos=None, left: int = -1,
@@ -688,7 +697,7 @@ def dwattn_fwd(q, k, v, table=None, buckets=None, q_lengths=None, k_lengths=None
     if workspace is not None:
         _dev_tensor("workspace", workspace, torch.uint8, dev)
     else:
-        need_ws = _lib.dwattn_fwd_workspace_bytes(shape)
+        need_ws = _attn_workspace(False, shape)
         if need_ws:
             workspace = torch.empty((need_ws,), dtype=torch.uint8, device=dev)
     _check(_lib.dwattn_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(table), _ptr(buckets), _ptr(q_lengths),
@@ -700,7 +709,7 @@ def dwattn_fwd(q, k, v, table=None, buckets=None, q_lengths=None, k_lengths=None
 def dwattn_bwd_workspace_bytes(q, k, v, table=None, buckets=None) -> int:
     """Bytes of workspace `dwattn_bwd` takes for tensors of these sizes."""
     _, sizes, rest = _attn_shape(q, k, v, table, buckets, None, None, None, -1, -1, None)
-    return int(_lib.dwattn_bwd_workspace_bytes(_attn_struct.pack(*sizes, *_NO_STRIDES, *rest)))
+    return _attn_workspace(True, _attn_struct.pack(*sizes, *_NO_STRIDES, *rest))
 
 
 def dwattn_bwd(q, k, v, out, lse, dout, table=None, buckets=None, q_lengths=None, k_lengths=None, q_pos=None,
@@ -740,7 +749,7 @@ def dwattn_bwd(q, k, v, out, lse, dout, table=None, buckets=None, q_lengths=None
     if workspace is not None:
         _dev_tensor("workspace", workspace, torch.uint8, dev)
     else:
-        workspace = torch.empty((max(int(_lib.dwattn_bwd_workspace_bytes(shape)), 1),), dtype=torch.uint8, device=dev)
+        workspace = torch.empty((max(_attn_workspace(True, shape), 1),), dtype=torch.uint8, device=dev)
     _check(_lib.dwattn_bwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(table), _ptr(buckets), _ptr(q_lengths),
                            _ptr(k_lengths), _ptr(q_pos), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                            _ptr(dtable), _ptr(workspace), workspace.numel(), _stream(dev)))
