@@ -39,23 +39,47 @@ template <>
 struct Frag<uint16_t> {
     u32x4 r;
 };
+// float32 as three bf16 parts of 8 significant bits each, cut off one after the
+// other (so that nothing overflows): their sum is the value, exactly.
 template <>
 struct Frag<float> {
-    f32x4 r[2];
+    u32x4 part[3];
 };
 
-__device__ __forceinline__ f32x16 mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.r), __builtin_bit_cast(bf16x8, b.r),
-                                                   c, 0, 0, 0);
+__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// float32 keeps its 24 bits: eight 2-deep products, the e-th of which pairs
-// depths e and 8 + e.
+__device__ __forceinline__ f32x16 mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x16 c) {
+    return mma(a.r, b.r, c);
+}
+
+// float32 keeps its 24 bits: the six products of parts that reach 2^-24 of the
+// whole, smallest first (what is left out is below 2^-25).  Six bf16 products
+// take 192 cycles of the matrix units where eight float ones take 512.
 __device__ __forceinline__ f32x16 mma(const Frag<float>& a, const Frag<float>& b, f32x16 c) {
+    c = mma(a.part[2], b.part[0], c);
+    c = mma(a.part[0], b.part[2], c);
+    c = mma(a.part[1], b.part[1], c);
+    c = mma(a.part[1], b.part[0], c);
+    c = mma(a.part[0], b.part[1], c);
+    return mma(a.part[0], b.part[0], c);
+}
+
+__device__ __forceinline__ Frag<float> split(const float (&v)[8]) {
+    Frag<float> f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.r[e / 4][e % 4], b.r[e / 4][e % 4], c, 0, 0, 0);
-    return c;
+    for (int e = 0; e < 8; e += 2) {
+        uint32_t x[2] = {__float_as_uint(v[e]), __float_as_uint(v[e + 1])};
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            f.part[p][e / 2] = __builtin_amdgcn_perm(x[1], x[0], 0x07060302);  // the high halves of both
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                x[i] = __float_as_uint(__uint_as_float(x[i]) - __uint_as_float(x[i] & 0xffff0000u));
+        }
+    }
+    return f;
 }
 
 // Stands between a run of products and the first arithmetic on their sums: the
@@ -81,8 +105,10 @@ template <typename S>
 __device__ __forceinline__ Frag<S> to_frag(const f32x16& c, int k) {
     Frag<S> f;
     if constexpr (sizeof(S) == 4) {
+        float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f.r[e / 4][e % 4] = c[8 * k + e];
+        for (int e = 0; e < 8; ++e) v[e] = c[8 * k + e];
+        f = split(v);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) f.r[e] = pack_bf16x2(c[8 * k + 2 * e], c[8 * k + 2 * e + 1]);
@@ -93,14 +119,18 @@ __device__ __forceinline__ Frag<S> to_frag(const f32x16& c, int k) {
 // Waits here for an operand that was loaded from memory.  Left to its first use
 // inside the loop over tiles, the wait would hold up that loop's own loads.
 __device__ __forceinline__ void arrived(Frag<uint16_t>& f) { asm volatile("" : "+v"(f.r)); }
-__device__ __forceinline__ void arrived(Frag<float>& f) { asm volatile("" : "+v"(f.r[0]), "+v"(f.r[1])); }
+__device__ __forceinline__ void arrived(Frag<float>& f) {
+    asm volatile("" : "+v"(f.part[0]), "+v"(f.part[1]), "+v"(f.part[2]));
+}
 
 template <typename S>
 __device__ __forceinline__ Frag<S> to_frag(const RawGroup<S>& g) {
     Frag<S> f;
     if constexpr (sizeof(S) == 4) {
-        f.r[0] = __builtin_bit_cast(f32x4, g.r[0]);
-        f.r[1] = __builtin_bit_cast(f32x4, g.r[1]);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(g.r[e / 4][e % 4]);
+        f = split(v);
     } else {
         f.r = g.r[0];
     }
@@ -131,8 +161,9 @@ struct Tile {
         const S* p = t + (row0 + lane % 32) * kStride + 16 * c + 8 * (lane / 32);
         Frag<S> f;
         if constexpr (sizeof(S) == 4) {
-            f.r[0] = *reinterpret_cast<const f32x4*>(p);
-            f.r[1] = *reinterpret_cast<const f32x4*>(p + 4);
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
+            const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            f = split(v);
         } else {
             f.r = *reinterpret_cast<const u32x4*>(p);
         }
@@ -148,8 +179,10 @@ struct Tile {
         Frag<S> f;
         if constexpr (sizeof(S) == 4) {
             const S* p = t + (row0 + 4 * (lane / 32)) * kStride + 32 * d + lane % 32;
+            float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f.r[e / 4][e % 4] = p[((e / 4) * 8 + e % 4) * kStride];
+            for (int e = 0; e < 8; ++e) v[e] = p[((e / 4) * 8 + e % 4) * kStride];
+            f = split(v);
         } else {
             const S* p = t + (row0 + 4 * (lane / 32) + lane % 16 / 4) * kStride + 32 * d + 16 * (lane / 16 % 2) +
                          4 * (lane % 4);

@@ -505,13 +505,13 @@ static int bwd_lds(const AttnShape& s, int elem_bytes, int ow, bool queries) {
     return tiles + bias + (queries ? 4 * kTile * kDiag * 4 + 4 * bias : values + 4 * rows * 4);
 }
 
-// Frames a workgroup owns, in units of 32: as many as leave enough workgroups
-// (bf16: two for each compute unit; float, whose products take 16 times as
-// long: eight, so that the last ones are short), if its LDS holds them.
+// Frames a workgroup owns, in units of 32: as many as leave two workgroups for
+// each compute unit, if its LDS holds them (float [32,375,8x64], 750 workgroups
+// of 128: 252 us so, 377 us with 64; [3,333,4x50], 36 of 128: 148 us with 128
+// for both kernels, 82 us with 32).
 static int owned(const AttnShape& s, int elem_bytes, bool queries) {
     constexpr int64_t kUnits = 256;
-    const int64_t pairs = s.B * (queries ? s.H : s.Hkv), frames = queries ? s.Tq : s.Tk;
-    const int64_t wide = kUnits * (elem_bytes == 4 ? 8 : 2);
+    const int64_t pairs = s.B * (queries ? s.H : s.Hkv), frames = queries ? s.Tq : s.Tk, wide = 2 * kUnits;
     int ow = pairs * ((frames + 127) / 128) >= wide ? 4 : pairs * ((frames + 63) / 64) >= kUnits ? 2 : 1;
     while (ow < 4 && bwd_lds(s, elem_bytes, ow, queries) > kLdsBytes) ow *= 2;
     return ow;

@@ -31,7 +31,7 @@ template <typename S, int DP, int QW, bool DMA>
 struct FwdShape {
     static constexpr int BN = QW == 1 ? 128 : QW == 2 || sizeof(S) * DP <= 128 ? 64 : 32;
     static constexpr int kBuffers = QW == 1 && !(DMA && sizeof(S) * DP <= 128) ? 1 : 2;
-    static constexpr int kWaves = QW == 1 && DP > 64 ? 1 : QW == 4 && DMA && sizeof(S) == 2 ? 3 : 2;
+    static constexpr int kWaves = (QW == 1 && DP > 64) || (sizeof(S) == 4 && DP > 96) ? 1 : QW == 4 && DMA && sizeof(S) == 2 ? 3 : 2;
     using Tiles = TilePair<S, DP, BN, kBuffers, DMA>;
 };
 
@@ -298,15 +298,17 @@ struct FwdPlan {
 // taken where they make workgroups enough; next 64, whose two pairs of waves
 // divide the keys; and with the fewest queries 32, the keys then being split
 // over workgroups until each compute unit has one.  The plan goes by the sizes
-// alone (lengths are on the device).  Enough is three a compute unit for bf16
-// (that many are resident: [16,750,8x128] takes 49 us so, 69 us with 64 queries)
-// and eight for float, whose tiles take 16 times as long in the matrix units, so
-// that short workgroups fill up behind long ones (causal [8,1500,8x64], three a
-// unit: 221 us with 128 queries, 171 us with 64).  Twice as many splits cost the
-// join more than they save (16 frames over 20000 keys, 8 heads: 18 and 21 us).
+// alone (lengths are on the device).  Enough is three a compute unit, as many as
+// are resident (bf16 [16,750,8x128] takes 49 us so and 69 us with 64 queries,
+// float [32,750,8x64] 171 and 205 us); but eight for float under a causal mask,
+// whose last workgroups have the most keys and, with six products for one, set
+// the time (causal [8,1500,8x64], three a unit: 130 us with 128 queries, 124 us
+// with 64).  Twice as many splits cost the join more than they save (16 frames
+// over 20000 keys, 8 heads: 18 and 21 us).
 static FwdPlan fwd_plan(const AttnShape& s, int elem_bytes) {
     constexpr int64_t kUnits = 256;
-    const int64_t wide = kUnits * (elem_bytes == 4 ? 8 : 3);
+    const bool causal = s.left == kNoLimit && s.right != kNoLimit;
+    const int64_t wide = kUnits * (elem_bytes == 4 && causal ? 8 : 3);
     FwdPlan p;
     auto blocks_of = [&](int64_t queries) { return s.B * s.H * ((s.Tq + queries - 1) / queries); };
     p.qw = s.Tq > 32 && blocks_of(128) >= wide ? 4 : s.Tq > 32 && blocks_of(64) >= kUnits ? 2 : 1;
