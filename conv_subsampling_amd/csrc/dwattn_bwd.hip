@@ -112,7 +112,7 @@ __device__ __forceinline__ void store_runs(S* row, const f32x16 (&acc)[ND], int 
 }
 
 template <typename S, int DP, int OW, bool DMA>
-__global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) ? 1 : 2)) void attn_dq_kernel(const AttnBwd a) {
+__global__ __launch_bounds__(kAttnThreads, ((sizeof(S) == 4 && !DMA) || (DP > 64 && (sizeof(S) == 4 || !DMA)) ? 1 : 2)) void attn_dq_kernel(const AttnBwd a) {
     typedef BwdShape<S, DP, OW> Shape;
     typedef typename Shape::template Tiles<DMA> Tiles;
     typedef Tile<S, DP> T;
@@ -193,13 +193,17 @@ __global__ __launch_bounds__(kAttnThreads, (DP > 64 && (sizeof(S) == 4 || !DMA) 
         for (int u = 0; u < KT; ++u) {
             const int row0 = (wk * KT + u) * kTile, j = jt + row0;
             if (j > some1 || j + kTile <= some0) continue;
-            f32x16 s = {}, ds = {};
+            f32x16 s = {}, ds = {}, s_small = {}, ds_small = {};
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                s = mma(T::rows(ktile, row0, c, lane), q[c], s);
-                ds = mma(T::rows(vtile, row0, c, lane), g[c], ds);
+                mma_apart(T::rows(ktile, row0, c, lane), q[c], s, s_small);
+                mma_apart(T::rows(vtile, row0, c, lane), g[c], ds, ds_small);
             }
             products_done<S>();
+            if constexpr (sizeof(S) == 4) {
+                s += s_small;
+                ds += ds_small;
+            }
             const int base = j - iw - item.pos32;
             const Span span = span_of(base, a.R);
             if (a.table && span == Span::kNear) {
