@@ -35,8 +35,12 @@ struct FwdShape {
     using Tiles = TilePair<S, DP, BN, kBuffers, DMA>;
 };
 
-template <typename S, int DP, int QW, bool DMA>
+// PACKED: the query heads that share a key head lie side by side in the columns
+// (column c is query c % Tq of the group's head c / Tq), so that their keys are
+// read and multiplied once; the bias is then there for each of them.
+template <typename S, int DP, int QW, bool DMA, bool PACKED = false>
 __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) void attn_fwd_kernel(const AttnFwd a) {
+    static_assert(!PACKED || QW == 1, "the heads of a group share one tile of queries");
     using F = FwdShape<S, DP, QW, DMA>;
     constexpr int KW = 4 / QW, BN = F::BN, KT = BN / kTile / KW, NC = DP / 16, ND = DP / 32;
     typedef Tile<S, DP> T;
@@ -45,12 +49,16 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
     const int wq = wave % QW, wk = wave / QW;
 
-    const AttnPlace place(blockIdx.x, a.nqb * a.splits, a.B * a.H, a.left == kNoLimit && a.right != kNoLimit);
+    const int heads = PACKED ? a.Hkv : a.H, group = a.H / a.Hkv;
+    const AttnPlace place(blockIdx.x, a.nqb * a.splits, a.B * heads, a.left == kNoLimit && a.right != kNoLimit);
     const int split = place.block % a.splits, qb = place.block / a.splits;
-    const int h = place.pair % a.H, b = a.nqb > 1 ? item_of_rank(a, place.pair / a.H) : place.pair / a.H;
+    const int head = place.pair % heads, b = a.nqb > 1 ? item_of_rank(a, place.pair / heads) : place.pair / heads;
+    const int hk = PACKED ? head : head / group;
     const AttnItem item(a, b);
-    const int i0 = qb * (kTile * QW), iw = i0 + wq * kTile, i = iw + lane % 32;
-    const bool live = i < item.nq;
+    const int i0 = qb * (kTile * QW), iw = i0 + wq * kTile;
+    const int member = PACKED ? lane % 32 / a.Tq : 0;  // of the group
+    const int i = PACKED ? lane % 32 - member * a.Tq : iw + lane % 32, h = PACKED ? hk * group + member : head;
+    const bool mine_to_write = PACKED ? member < group : i < a.Tq, live = mine_to_write && i < item.nq;
 
     // this lane's keys: [mine0, mine0 + mine)
     const int mine0 = item.first_key(a, i);
@@ -67,11 +75,10 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
     const int tiles = j1 > j0 ? (j1 - j0 + BN - 1) / BN : 0, share = (tiles + a.splits - 1) / a.splits;
     const int t0 = min(split * share, tiles), t1 = min(t0 + share, tiles);
     // the wave's keys, for the tiles that it can pass over or take unmasked
-    const int iwl = min(iw + kTile, item.nq) - 1;
+    const int iwl = min(iw + (PACKED ? a.Tq : kTile), item.nq) - 1;
     const int some0 = item.first_key(a, iw), some1 = iw < item.nq ? item.last_key(a, iwl) : -1;
-    const int all0 = item.first_key(a, iwl), all1 = iw + kTile <= item.nq ? item.last_key(a, iw) : -1;
+    const int all0 = item.first_key(a, iwl), all1 = iw < item.nq ? item.last_key(a, iw) : -1;
 
-    const int hk = h / (a.H / a.Hkv);
     const int64_t j00 = j0 + t0 * BN;
     typename F::Tiles kv(smem, (const S*)a.k + b * a.ks.item + hk * a.ks.head + j00 * a.ks.frame, a.ks.frame,
                          (const S*)a.v + b * a.vs.item + hk * a.vs.head + j00 * a.vs.frame, a.vs.frame, a.D,
@@ -85,7 +92,15 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
 #pragma unroll
         for (int c = 0; c < NC; ++c) q[c] = to_frag<S>(load_group<S, !DMA>(row, 16 * c + 8 * half, live ? a.D : 0));
     }
-    filler.fill(a, h, bias);
+    const int nbias = 2 * a.R + 1 + 2 * kBiasMargin;
+    if constexpr (PACKED) {
+        for (int m = 0; m < group; ++m) filler.fill(a, hk * group + m, bias + m * nbias);
+    } else {
+        filler.fill(a, h, bias);
+    }
+    // this lane's head's bias, from the place of its query
+    const float* my_bias = bias + min(member, group - 1) * nbias;
+    const int column = PACKED ? i : lane % 32;
     if (F::kBuffers == 2 && t0 < t1) kv.finish(0);
 #pragma unroll
     for (int c = 0; c < NC; ++c) arrived(q[c]);
@@ -125,12 +140,12 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
             // product); a looked-up one is added first.
             float factor = a.scale2, flat = 0.0f;
             if (a.table && span == Span::kNear) {
-                const float* f = bias + (base + a.R + kBiasMargin + 4 * half - lane % 32);
+                const float* f = my_bias + (base + a.R + kBiasMargin + 4 * half - column);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale2, f[acc_row(r, 0)]);
                 factor = 1.0f;
             } else if (a.table) {
-                flat = bias[span == Span::kLow ? 0 : 2 * a.R + 2 * kBiasMargin];
+                flat = my_bias[span == Span::kLow ? 0 : nbias - 1];
             }
             if (edge) {
                 const uint32_t at = j + 4 * half - mine0;
@@ -210,7 +225,13 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
             }
         }
     }
-    if (i >= a.Tq) return;
+    if (!mine_to_write) return;
+    if (!live) {  // its columns went along with the others'
+        top = -__builtin_inff();
+        sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) o[n] = f32x16{};
+    }
     const int64_t row = ((int64_t)b * a.H + h) * a.Tq + i;
     const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // a row without keys is zero; NaN stays
 #pragma unroll
@@ -291,6 +312,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnFwd a) {
 // ---------------------------------------------------------------------------
 struct FwdPlan {
     int qw, splits;
+    bool packed;
     int64_t nqb;
 };
 
@@ -304,7 +326,10 @@ struct FwdPlan {
 // whose last workgroups have the most keys and, with six products for one, set
 // the time (causal [8,1500,8x64], three a unit: 130 us with 128 queries, 124 us
 // with 64).  Twice as many splits cost the join more than they save (16 frames
-// over 20000 keys, 8 heads: 18 and 21 us).
+// over 20000 keys, 8 heads: 18 and 21 us).  The splits, and the workspace with
+// them, do not depend on the bias.
+constexpr int64_t kPackedBias = 16 * 1024;  // bytes of LDS for a group's biases beside the widest tiles
+
 static FwdPlan fwd_plan(const AttnShape& s, int elem_bytes) {
     constexpr int64_t kUnits = 256;
     const bool causal = s.left == kNoLimit && s.right != kNoLimit;
@@ -315,13 +340,16 @@ static FwdPlan fwd_plan(const AttnShape& s, int elem_bytes) {
     const int64_t queries = 32 * p.qw;
     p.nqb = (s.Tq + queries - 1) / queries;
     p.splits = 1;
+    const int64_t group = s.Hkv ? s.H / s.Hkv : 1;
+    const bool could = p.qw == 1 && group > 1 && group * s.Tq <= kTile;
+    p.packed = could && group * (s.reach ? attn_bias_bytes((int)s.reach) : 0) <= kPackedBias;
     if (p.qw == 1) {
         int64_t span = s.Tk;
         if (s.left < kNoLimit && s.right < kNoLimit) {
             const int64_t window = s.left + s.right + queries;
             span = window < 1 ? 1 : window < span ? window : span;
         }
-        const int64_t blocks = blocks_of(32), tiles = (span + 127) / 128;
+        const int64_t blocks = could ? s.B * s.Hkv : blocks_of(32), tiles = (span + 127) / 128;
         int64_t n = kUnits / (blocks ? blocks : 1);
         n = n < tiles ? n : tiles;
         p.splits = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
@@ -344,21 +372,23 @@ bool dwattn_fits(const AttnShape& s) {
            product_below(kMaxExtent, {s.B, s.H, s.Tq}) && product_below(kMaxExtent, {s.B, s.H, s.Tq, (s.D + 3) / 4 + 1});
 }
 
-template <typename S, int DP, int QW, bool DMA>
+template <typename S, int DP, int QW, bool DMA, bool PACKED = false>
 static hipError_t launch_fwd(const AttnFwd& a, hipStream_t stream) {
     using F = FwdShape<S, DP, QW, DMA>;
-    const int lds = F::Tiles::kAllBytes + (a.table ? attn_bias_bytes(a.R) : 0);
-    hipLaunchKernelGGL((attn_fwd_kernel<S, DP, QW, DMA>), dim3((uint32_t)(a.B * a.H) * a.nqb * a.splits),
-                       dim3(kAttnThreads), lds, stream, a);
+    const int biases = PACKED ? a.H / a.Hkv : 1, lds = F::Tiles::kAllBytes + (a.table ? biases * attn_bias_bytes(a.R) : 0);
+    hipLaunchKernelGGL((attn_fwd_kernel<S, DP, QW, DMA, PACKED>),
+                       dim3((uint32_t)(a.B * (PACKED ? a.Hkv : a.H)) * a.nqb * a.splits), dim3(kAttnThreads), lds, stream, a);
     return hipGetLastError();
 }
 
 template <typename S>
-static hipError_t fwd_of_type(const AttnFwd& a, int qw, hipStream_t stream) {
+static hipError_t fwd_of_type(const AttnFwd& a, int qw, bool packed, hipStream_t stream) {
     const bool dma = dma_fits<S>(a.k, a.ks, a.D) && dma_fits<S>(a.v, a.vs, a.D);
     const hipError_t e = with_head_width(a.D, [&](auto dp) {
         constexpr bool kNarrow = sizeof(S) * dp.value <= 128;  // two buffers of 128 keys leave room for two workgroups
-        return qw == 1 && dma && kNarrow ? launch_fwd<S, dp.value, 1, kNarrow>(a, stream)
+        return packed && dma && kNarrow ? launch_fwd<S, dp.value, 1, kNarrow, true>(a, stream)
+               : packed ? launch_fwd<S, dp.value, 1, false, true>(a, stream)
+               : qw == 1 && dma && kNarrow ? launch_fwd<S, dp.value, 1, kNarrow>(a, stream)
                : qw == 1 ? launch_fwd<S, dp.value, 1, false>(a, stream)
                : qw == 2 && dma ? launch_fwd<S, dp.value, 2, true>(a, stream)
                : qw == 2 ? launch_fwd<S, dp.value, 2, false>(a, stream)
@@ -382,7 +412,8 @@ hipError_t launch_dwattn_fwd(const AttnPtrs& p, const AttnShape& s, void* out, f
     a.part = (float*)workspace;
     a.splits = plan.splits;
     a.nqb = (int32_t)plan.nqb;
-    return bf16 ? fwd_of_type<uint16_t>(a, plan.qw, stream) : fwd_of_type<float>(a, plan.qw, stream);
+    return bf16 ? fwd_of_type<uint16_t>(a, plan.qw, plan.packed, stream)
+                : fwd_of_type<float>(a, plan.qw, plan.packed, stream);
 }
 
 }  // namespace dw

@@ -96,6 +96,17 @@ def test_shared_key_heads(dt):
 
 
 @DT
+@pytest.mark.parametrize("Tq,H,Hkv,D,reach", [(1, 8, 1, 64, 40), (1, 32, 1, 32, 8), (4, 8, 1, 50, 40), (7, 8, 2, 128, 40),
+                                              (3, 4, 2, 96, 40), (16, 4, 2, 64, 40), (1, 32, 1, 64, 1024), (2, 6, 3, 16, 40)])
+def test_shared_key_heads_of_few_queries(Tq, H, Hkv, D, reach, dt):
+    """A group's heads side by side in one tile (and, at the largest reach, not): ragged queries, windows, splits."""
+    check(make(3, Tq, 300, H, Hkv, D, dt, reach=reach, NB=32 if reach > 8 else 16, k_len=[300, 5, 131],
+               q_len=[Tq, max(Tq - 1, 1), Tq], pos=[300 - Tq, 0, 100]))
+    check(make(2, Tq, 700, H, Hkv, D, dt, reach=reach, NB=16, k_len=[700, 333], pos=[650, 330], left=200, right=3))
+    check(make(2, Tq, 90, H, Hkv, D, dt, bias=False, q_len=[Tq, 0]))
+
+
+@DT
 @pytest.mark.parametrize("left,right", [(-1, 0), (0, 0), (5, -1), (30, 10), (0, 40), (1000000000000, 3)])
 def test_context_windows(left, right, dt):
     check(make(2, 150, 150, 2, 2, 64, dt, q_len=[150, 77], k_len=[150, 77], left=left, right=right))
