@@ -31,6 +31,34 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 
 __device__ __forceinline__ int wave_of_block() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
+// BYTES (16 or 4) a lane from the buffer's byte off into LDS at lds plus BYTES
+// times the lane, without a register between.  Inline assembly, without a result
+// register, because the compiler would else wait for the load before any LDS
+// read; nothing else in these kernels takes its operand from m0.  A build without
+// optimisation keeps uniform values in vector registers, which the assembly
+// cannot take: it has the compiler's own form, with its waits.
+template <int BYTES>
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t bytes, uint32_t off, uint32_t lds) {
+    static_assert(BYTES == 16 || BYTES == 4, "the widths that the kernels use");
+#ifdef __OPTIMIZE__
+    const uint64_t at = (uint64_t)base;
+    const u32x4 rsrc = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, (uint32_t)kBufferFlags};
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     :: "s"(lds), "v"(off), "s"(rsrc) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                     :: "s"(lds), "v"(off), "s"(rsrc) : "memory");
+#else
+    const rsrc_t from = make_rsrc(base, bytes);
+    auto* to = (__attribute__((address_space(3))) void*)(uintptr_t)lds;
+    if constexpr (BYTES == 16)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, to, 16, off, 0, 0, 0);
+    else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, to, 4, off, 0, 0, 0);
+#endif
+}
+
 // The 16-deep operand of one 32x32 product: 8 values a lane, of the streamed
 // depth 8 * (lane / 32) + e.
 template <typename S>
@@ -105,17 +133,12 @@ __device__ __forceinline__ Frag<float> split(const float (&v)[8]) {
 
 // Stands between a run of products and the first arithmetic on their sums: the
 // wait states that the last product's result asks for before a vector
-// instruction may read it (16 + 2 for a float product, 8 + 4 for a bf16 one).
-// The compiler inserts them too, but where the sums sat in accumulation
-// registers and the reads behind a branch it was found to leave 13 of a float
-// product's 18 before the last register, which then lacked the last product.
-template <typename S>
+// instruction may read it (8 passes + 4).  The compiler inserts them too, but
+// where the sums sat in accumulation registers and the reads behind a branch it
+// was found to leave too few, and the last register lacked the last product.
 __device__ __forceinline__ void products_done() {
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (sizeof(S) == 4)
-        asm volatile("s_nop 15\n\ts_nop 3");
-    else
-        asm volatile("s_nop 11");
+    asm volatile("s_nop 11");
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -255,9 +278,7 @@ struct TileRegs {
 // which row and chunk its place in the tile is; lanes on a pad sit out.  The
 // buffer ends at the last live row, so what lies past it arrives as zero.
 // start() returns with the loads in flight: a wait for them and a barrier come
-// before the tile is read.  (Written as inline assembly, without a result
-// register, because the compiler would else wait for them before any LDS read.
-// Nothing else in these kernels takes its operand from m0.)
+// before the tile is read.
 template <typename S, int DP, int ROWS>
 struct TileDma {
     static constexpr int kTotal = ROWS * Tile<S, DP>::kSlots;
@@ -279,16 +300,11 @@ struct TileDma {
     __device__ __forceinline__ void start(const S* base, int64_t frame, int live, int D, S* tile) {
         const uint32_t bytes =
             live > 0 ? (uint32_t)((((live < ROWS ? live : ROWS) - 1) * frame + D) * (int)sizeof(S)) : 0;
-        const uint64_t at = (uint64_t)base;
-        const u32x4 rsrc = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, (uint32_t)kBufferFlags};
         const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)tile +
                              wave_of_block() * 1024;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            if (off[n] != kSkip)
-                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                             :: "s"(lds + n * kAttnThreads * 16), "v"(off[n]), "s"(rsrc)
-                             : "memory");
+            if (off[n] != kSkip) load_to_lds<16>(base, bytes, off[n], lds + n * kAttnThreads * 16);
         }
     }
 

@@ -15,6 +15,16 @@
 // those make too few workgroups 64 or 32, the waves that share frames dividing
 // the streamed tiles and adding their sums in LDS.  attn_dtable then adds the
 // sums by distance over the workgroups and into buckets, in fp64.
+//
+// Seven products instead of the five that a pass with atomics would take: the
+// two done twice keep the sums' order the same in every call.
+// Measured, kernels alone, bf16 [16,750,8x128], lengths 750 to 398 (56 GFLOP as
+// five products): dq with the sums by distance 110 us, dk and dv 102 us, the
+// table 6.5 us.  In an earlier form of dk and dv that took 126 us, one tile of
+// queries alone took 42; leaving out three quarters of dv's product saved 43,
+// seven eighths of the scores' 17, the weights 15, the loads of the tiles 12.
+// float [3,333,4x50]: dq 27 us, dk and dv 41, the table 5, on so few workgroups
+// that most compute units have none.
 #include "attn.h"
 
 namespace dw {
@@ -41,14 +51,9 @@ __device__ __forceinline__ float lse_or_inf(float lse) {
 // from[at] of every lane into LDS at to[at], zero for at >= count; the lanes of
 // a wave have 64 neighbouring `at`.
 __device__ __forceinline__ void load_lds_floats(const float* from, int count, int at, float* to) {
-    const uint64_t base = (uint64_t)from;
-    const u32x4 rsrc = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, count > 0 ? (uint32_t)count * 4 : 0,
-                        (uint32_t)kBufferFlags};
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)to +
                          __builtin_amdgcn_readfirstlane(at / 64) * 256;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(at * 4), "s"(rsrc)
-                 : "memory");
+    load_to_lds<4>(from, count > 0 ? (uint32_t)count * 4 : 0, at * 4, lds);
 }
 
 // Orders a wave's LDS accesses before and after it: lanes read what other
@@ -199,7 +204,7 @@ __global__ __launch_bounds__(kAttnThreads, ((sizeof(S) == 4 && !DMA) || (DP > 64
                 mma_apart(T::rows(ktile, row0, c, lane), q[c], s, s_small);
                 mma_apart(T::rows(vtile, row0, c, lane), g[c], ds, ds_small);
             }
-            products_done<S>();
+            products_done();
             if constexpr (sizeof(S) == 4) {
                 s += s_small;
                 ds += ds_small;
@@ -256,7 +261,7 @@ __global__ __launch_bounds__(kAttnThreads, ((sizeof(S) == 4 && !DMA) || (DP > 64
         }
         kv.leave(t, t + 1 < tiles);
     }
-    products_done<S>();
+    products_done();
     if (a.dq) {
         add_waves<OW, ND>(smem, acc, lane, wave);
         if (i < a.Tq)
@@ -283,6 +288,7 @@ __global__ __launch_bounds__(kAttnThreads, ((sizeof(S) == 4 && !DMA) || (DP > 64
     }
 }
 
+// 5 to 6 us, two rounds of dependent loads and a launch.
 // dtable[bucket][h]: a workgroup lists the distances of its bucket and adds
 // their sums over the parts (items and query blocks), in an order that the
 // sizes and the map fix: each thread every 256th, then lanes, then waves.
@@ -434,7 +440,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) 
                     ds = mma(T::rows(gtile, row0, c, lane), value(c), ds);
                     if (kValuesInLds<S, DP> && c % 2) __builtin_amdgcn_sched_barrier(0);
                 }
-                products_done<S>();
+                products_done();
                 // distance of the tile's first key and first query; along the registers it falls
                 const int base = jw - i - item.pos32;
                 const Span span = span_of(base, a.R);
@@ -476,7 +482,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) 
             qg.leave(t, t + 1 < tiles);
         }
     }
-    products_done<S>();
+    products_done();
     const bool out = j < a.Tk;
     if (a.dk) {
         add_waves<OW, ND>(smem, dk, lane, wave);

@@ -9,6 +9,20 @@
 // tiles of 128 keys, and their results are joined in LDS.  Where even that
 // leaves compute units idle, the key axis is split over workgroups, whose
 // results attn_join adds.
+//
+// What bounds it, and what it measured (kernels alone):
+//   bf16 [16,750,8x128], lengths 750 to 398: 47 us, 22.4 GFLOP of valid pairs,
+//     477 TFLOP/s.  A run over one key tile takes 20 us of that; leaving out
+//     most of either product saves 6 to 7 us, the weights 3, the bias 4, the
+//     loads of the tiles 8: no one unit fills it.  At [4,3000,8x128], all
+//     frames valid, 184 us a call, 801 TFLOP/s.
+//   float, causal [8,1500,8x64]: 131 us, 11.6 GFLOP, 89 TFLOP/s in the six bf16
+//     products that stand for each; each wave splits its own operands.
+//   bf16, 8 frames of 64 streams over 391 keys: 12 us; one frame of 4 streams
+//     over 6000 keys: 14 us and 3.8 us for the join, several times what their
+//     bytes take: few tiles a workgroup, so latency.
+// For [16,750,8x128], when it took 51 us: all of a tile's operands read ahead,
+// two workgroups a compute unit, 62 us; tiles of 64 keys, 61 us.
 #include "attn.h"
 
 namespace dw {
@@ -130,7 +144,7 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
 #pragma unroll
                 for (int d = 0; d < ND; ++d) v[d] = T::columns(vt, row0, d, lane);
             }
-            products_done<S>();
+            products_done();
             const int base = j - iw - item.pos32;
             const Span span = span_of(base, a.R);
             const bool edge = j < all0 || j + kTile - 1 > all1;
@@ -181,7 +195,7 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
         }
         kv.leave(t, t + 1 < t1 - t0);
     }
-    products_done<S>();
+    products_done();
     sum += swap_halves(sum);
 
     // Join the waves that share queries: wave wk of them takes every KW-th run
@@ -263,7 +277,9 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
     }
 }
 
-// Joins the splits of the key axis: one thread takes 4 head elements of a row.
+// Joins the splits of the key axis: one thread takes 4 head elements of a row,
+// kJoin splits' loads in flight together (3.8 us for 8 splits, nearly all of it
+// latency; one after the other 10 us).
 constexpr int kJoin = 8;
 
 template <typename S>
