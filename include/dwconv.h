@@ -25,6 +25,14 @@
  *   dwsub_fused_fwd_ex, dwsub_fused_bwd_ex
  *                    the front with its causal mode (same section) and bf16
  *                    storage
+ * and, beside the convolutions, what the same encoder block needs around them:
+ *   dwnorm_fwd, dwnorm_bwd
+ *                    layer norm with the residual add and dropout before it
+ *   dwdrop_fwd, dwdrop_bwd
+ *                    dropout from a counter-based generator, no mask stored
+ *   dwattn_fwd, dwattn_bwd, dwattn_rel_buckets
+ *                    attention with a learned relative position bias by
+ *                    buckets, for whole utterances and for streams over a cache
  *
  * Conventions shared by every entry point
  *   - Tensors are dense, contiguous and channel-last (channel index fastest):
@@ -43,7 +51,7 @@
  *   - Sizes are int64_t.  A forward call with no output elements enqueues
  *     nothing and returns DW_OK without looking at its pointers; a tensor
  *     with no elements may be NULL.
- *   - The kernels address each batch item with 32-bit byte offsets: an item
+ *   - The convolution kernels address each batch item with 32-bit byte offsets: an item
  *     whose tensors (with a few frames of padding) would reach 2^31 bytes is
  *     refused with DW_ERR_UNSUPPORTED ("sizes too large for one launch"),
  *     and so is any extent (B, T, F, C, K) of 2^31 or more.  These limits
