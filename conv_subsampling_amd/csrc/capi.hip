@@ -158,24 +158,26 @@ dw_status check_attn(const char* fn, const dw_attn* a, bool bias, dw::AttnShape*
     return DW_OK;
 }
 
-// How often p divides n.
-int times_divides(int64_t p, int64_t n) {
+// How often p divides n, which is left without it.
+int take_out(int64_t p, int64_t* n) {
     int e = 0;
-    for (; n % p == 0; n /= p) ++e;
+    for (; *n % p == 0; *n /= p) ++e;
     return e;
 }
 
 // floor(m log(n/e) / log(reach/e)) for n >= e.  The quotient is a whole number
 // k exactly where n^m e^k = reach^k e^m, which the exponents of the primes
-// decide; elsewhere long double tells the floor.
+// decide (a divisor that is no prime finds its primes taken out before it);
+// elsewhere long double tells the floor.
 int64_t log_steps(int64_t n, int64_t e, int64_t reach, int64_t m) {
     const long double t = m * (logl((long double)n / e) / logl((long double)reach / e));
     const int64_t k = llroundl(t);
     if (fabsl(t - k) > 1e-6L) return (int64_t)floorl(t);
     bool equal = true;
-    for (int64_t p = 2; p <= reach; ++p)
-        equal = equal && m * times_divides(p, n) + k * times_divides(p, e) ==
-                             k * times_divides(p, reach) + m * times_divides(p, e);
+    for (int64_t p = 2, a = n, b = e, c = reach; p <= reach; ++p) {
+        const int64_t of_n = take_out(p, &a), of_e = take_out(p, &b), of_reach = take_out(p, &c);
+        equal = equal && m * of_n + k * of_e == k * of_reach + m * of_e;
+    }
     return equal ? k : (int64_t)floorl(t);
 }
 

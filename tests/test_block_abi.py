@@ -5,6 +5,8 @@ import os
 
 import pytest
 
+import block_ref as ref
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 LIB = os.path.join(ROOT, "conv_subsampling_amd", "libdwconv.so")
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, -1, -2, -3
@@ -190,3 +192,17 @@ def test_bucket_map_validation(alib):
     assert f(m, 32, 8, 1) == INVALID and f(m, 32, 16, 0) == INVALID and f(m, 32, 9, 1) == OK
     assert f(m, 1, 0, 0) == INVALID and f(m, 32, -5, 1) == INVALID
     assert f(m, 32, 1025, 1) == UNSUPPORTED and f(m, 1 << 40, 1 << 50, 1) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("bidirectional", [0, 1])
+def test_bucket_map_is_exact(alib, bidirectional):
+    """Distances at which the logarithms' quotient is a whole number, for reaches that are powers, products and primes
+    times the exact distances; and every small pair of sizes."""
+    m = (ctypes.c_int32 * 4096)()
+    sizes = [(n, r) for n in range(1, 41) for r in range(1, 101)]
+    sizes += [(5, 1024), (17, 729), (32, 128), (64, 512), (64, 1024), (33, 1024), (128, 1000), (512, 1024)]
+    for buckets, reach in sizes:
+        if alib.dwattn_rel_buckets(m, buckets, reach, bidirectional) != OK:
+            continue
+        want = [ref.bucket(r, buckets, reach, bool(bidirectional)) for r in range(-reach, reach + 1)]
+        assert list(m[:2 * reach + 1]) == want, (buckets, reach)
