@@ -481,8 +481,9 @@ struct AttnItem {
 
 // The head's bias for every distance -R .. R in units of log2, with the ends
 // repeated kBiasMargin times on both sides.  A table may hold its type's lowest
-// value: times log2(e) that must stay a number, so that rows which hold nothing
-// else still weigh their keys alike.  Bucket numbers are held to the table.
+// or largest value: times log2(e) that must stay a number, so that rows which
+// hold nothing else still weigh their keys alike.  Bucket numbers are held to
+// the table.
 // The constructor reads the map (the first entries of each thread), fill() the
 // table: what is read in between is in flight with the map.
 template <typename S>
@@ -499,8 +500,8 @@ struct BiasFill {
 
     static __device__ __forceinline__ float value(const AttnArgs& a, int h, int b) {
         const float t = to_f32(((const S*)a.table)[(int64_t)b * a.H + h]);
-        const float v = t * kLog2e, lowest = -3.0e38f;
-        return v < lowest && t > -__builtin_inff() ? lowest : v;
+        const float v = t * kLog2e, most = 3.0e38f;
+        return fabsf(t) < __builtin_inff() ? __builtin_amdgcn_fmed3f(v, -most, most) : v;
     }
 
     __device__ __forceinline__ explicit BiasFill(const AttnArgs& a) {

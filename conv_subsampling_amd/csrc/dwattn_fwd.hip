@@ -39,6 +39,13 @@ struct AttnFwd : AttnArgs {
 // below 2^kSlack, and most tiles need no rescaling of the accumulators.
 constexpr float kSlack = 8.0f;
 
+// A flat bias up to this rides on the multiply that scales the scores.  In the
+// sum of a larger one and a score, which the running maximum follows, the score
+// may vanish, and a weight taken from both apart would pass 2^kSlack by as much
+// as the score (here the sum still has 2^-8 of it); that bias is added to the
+// scores first, as a looked-up one is.
+constexpr float kRides = 65536.0f;
+
 // Keys of a tile, its buffers, and the waves per SIMD that its registers are to
 // allow.
 template <typename S, int DP, int QW, bool DMA>
@@ -151,15 +158,21 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
             // s becomes the weights exp2(scale2 * s + bias - top).  The flat
             // bias of a tile past the map's reach rides on the multiply
             // (scale2 > 0, so the largest score is that of the largest
-            // product); a looked-up one is added first.
+            // product); a looked-up or a huge one is added first, the latter
+            // from the map's repeated ends.
             float factor = a.scale2, flat = 0.0f;
-            if (a.table && span == Span::kNear) {
-                const float* f = my_bias + (base + a.R + kBiasMargin + 4 * half - column);
+            bool look = a.table && span == Span::kNear;
+            if (a.table && span != Span::kNear) {
+                flat = my_bias[span == Span::kLow ? 0 : nbias - 1];
+                look = __any(fabsf(flat) > kRides);
+            }
+            if (look) {
+                const int at = max(-a.R - kTile + 1, min(base, a.R + kTile - 1));
+                const float* f = my_bias + (at + a.R + kBiasMargin + 4 * half - column);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], a.scale2, f[acc_row(r, 0)]);
                 factor = 1.0f;
-            } else if (a.table) {
-                flat = my_bias[span == Span::kLow ? 0 : nbias - 1];
+                flat = 0.0f;
             }
             if (edge) {
                 const uint32_t at = j + 4 * half - mine0;

@@ -576,7 +576,10 @@ size_t dwattn_fwd_workspace_bytes(const dw_attn *shape);
  *
  * table: [buckets][H] in the storage type; map: [2 * reach + 1] int32 in device
  * memory, from dwattn_rel_buckets or any other (entries are held to the table);
- * both NULL: no bias.  A table entry of -inf forbids its bucket.  lengths and
+ * both NULL: no bias.  A table entry of -inf forbids its bucket; finite entries
+ * beyond +-2.07e38 count as that.  The score is the float32 sum, so a row whose
+ * keys all have a bias in which their products vanish weighs them alike.
+ * lengths and
  * positions: int32 [B] or NULL (full lengths, position 0); lengths are clamped
  * to the tensors.  lse may be NULL.
  * Scores, softmax and sums are float32.  DW_BF16 rounds the weights p to bf16

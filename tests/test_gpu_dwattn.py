@@ -298,3 +298,40 @@ def test_binding_refusals():
     for bad in ((32, 8), (0, 9), (32, 2000)):
         with pytest.raises(dw.DwconvError):
             dw.rel_buckets(*bad)
+
+
+def far_and_near(dt, far, T=200, seed=0):
+    """Rows whose tiles lie within and past the map's reach, the far buckets of one value, and one far pair with a
+    product of 1120 (a score of 198) that no other pair shares."""
+    s = make(1, T, T, 2, 1, 32, dt, NB=8, reach=20, seed=seed)
+    for r in (0, -1):
+        s["table"][int(s["buckets"][r])] = far
+    s["q"][..., 0], s["k"][..., 0] = 0, 0
+    s["q"][0, 130, :, 0], s["k"][0, 10, 0, 0] = 80, 14
+    return s
+
+
+@DT
+@pytest.mark.parametrize("far", ["lowest", -1e30, -1e10, -1e6])
+def test_far_buckets_of_a_huge_negative_value(far, dt):
+    """The forbidden pair's score vanishes in its bias: the row stays finite and goes by its near keys."""
+    check(far_and_near(dt, torch.finfo(dt).min if far == "lowest" else far), what=str(far))
+
+
+@DT
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_rows_of_nothing_but_the_lowest_or_largest_value(sign, dt):
+    """A table of the lowest value alone weighs near and far keys alike; far buckets at the largest, only the far ones."""
+    T = 200
+    s = far_and_near(dt, sign * torch.finfo(dt).max, T)
+    if sign < 0:
+        s["table"][:] = torch.finfo(dt).min
+    out, _ = call(s)
+    torch.cuda.synchronize()
+    place = np.asarray(s["buckets"].tolist())[np.clip(np.arange(T)[None, :] - np.arange(T)[:, None], -20, 20) + 20]
+    w = np.ones((T, T)) if sign < 0 else np.isin(place, [place[-1, 0], place[0, -1]]).astype(float)
+    v = host64(s["v"])[0, :, 0]
+    want = w @ v / w.sum(1, keepdims=True)
+    # equal weights: one float32 sum of at most 200 terms; bf16 rounds out
+    tol = 2e-5 + (ref.U16 * np.abs(v).max() if dt == BF16 else 0)
+    assert np.abs(host64(out)[0] - want[:, None]).max() <= tol
