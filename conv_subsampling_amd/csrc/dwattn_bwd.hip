@@ -32,7 +32,7 @@ namespace dw {
 struct AttnBwd : AttnArgs {
     const void *out, *dout;  // [B][Tq][H][D]
     const float* lse;        // [B][H][Tq]
-    float* stat;             // [B][H][2][Tq]: lse in units of log2 (inf where there are no keys), then delta
+    float* stat;             // [B][H][3][Tq]: lse in units of log2 (inf where there are no keys), delta, one over the sum where lse lacks it (else 0)
     void *dq, *dk, *dv;
     AttnStride dqs, dks, dvs;
     float* dist;  // [H][B * nqb][2 R + 1] sums of dS by distance; NULL: not wanted
@@ -44,7 +44,57 @@ constexpr int kDiag = 64;  // row of the square in which the diagonals of a tile
 // exp(S - lse) of a query that has keys; lse = -inf marks one that has none,
 // whose weights are zero.
 __device__ __forceinline__ float lse_or_inf(float lse) {
-    return lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
+    if (lse == -__builtin_inff()) return __builtin_inff();
+    const float most = 3.0e38f;  // as the biases are held
+    return fabsf(lse) < __builtin_inff() ? __builtin_amdgcn_fmed3f(lse * kLog2e, -most, most) : lse;
+}
+
+// lse = maximum + log(sum) holds the logarithm to 2^-24 of the whole.  Beyond
+// this magnitude (in units of log2; a weight is off by 1e-4 there, and a row of
+// nothing but masks of -1e9 or of the type's lowest value absorbs the logarithm
+// altogether) the maximum stands in its place, and one over the sum apart.
+constexpr float kHeavy = 1024.0f;
+__device__ __forceinline__ bool heavy(float lse2) { return fabsf(lse2) > kHeavy && fabsf(lse2) < __builtin_inff(); }
+
+// The maximum of a lane's row of scores (in units of log2, as the kernels
+// compute them) and one over the sum of its weights over it, by one wave from
+// memory: keys first to last are those that any of its 32 queries may see, from
+// mine0 on `mine` of them are the lane's own.  Rare, so short and not fast.
+template <typename S, int DP>
+__device__ __forceinline__ void heavy_row(const AttnArgs& a, const AttnItem& item, int b, int h, int i, const Frag<S> (&q)[DP / 16],
+                                        int first, int last, int mine0, uint32_t mine, float& top, float& weight) {
+    const int lane = threadIdx.x % 64, half = lane / 32, hk = h / (a.H / a.Hkv);
+    const S* keys = (const S*)a.k + b * a.ks.item + hk * a.ks.head;
+    float sum = 0.0f;
+    top = -__builtin_inff();
+    for (int j = first; j <= last; j += kTile) {
+        const int at = j + lane % 32;
+        f32x16 s = {}, s_small = {};
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c)
+            mma_apart(to_frag<S>(load_group<S, true>(keys + (int64_t)min(at, last) * a.ks.frame, 16 * c + 8 * half,
+                                                     at <= last ? a.D : 0)), q[c], s, s_small);
+        products_done();
+        if constexpr (sizeof(S) == 4) s += s_small;
+        float m = top;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int key = j + acc_row(r, half);
+            const int x = min(max(key - i - item.pos32, -a.R), a.R) + a.R + kBiasMargin;
+            const float bias = a.table ? BiasFill<S>::value(a, h, BiasFill<S>::map_at(a, x)) : 0.0f;
+            s[r] = (uint32_t)(key - mine0) < mine ? fmaf(s[r], a.scale2, bias) : -__builtin_inff();
+            m = fmaxf(m, s[r]);
+        }
+        m = fmaxf(m, swap_halves(m));
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
+        sum *= exp2_fast(top - ref);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum += exp2_fast(s[r] - ref);
+        top = m;
+    }
+    sum += swap_halves(sum);
+    weight = 1.0f / sum;
+    if (sum == 0.0f) top = __builtin_inff(), weight = 1.0f;  // no keys, whatever lse says
 }
 
 
@@ -142,7 +192,11 @@ __global__ __launch_bounds__(kAttnThreads, ((sizeof(S) == 4 && !DMA) || (DP > 64
     }
 
     Frag<S> q[NC], g[NC];
-    float delta = 0.0f, lse2 = __builtin_inff();
+    float delta = 0.0f, lse2 = __builtin_inff(), weight = 1.0f;
+    const int mine0 = item.first_key(a, i), mine1 = item.last_key(a, i);
+    const uint32_t mine = live && mine1 >= mine0 ? mine1 - mine0 + 1 : 0;
+    const int iwl = min(iw + kTile, item.nq) - 1;
+    const int some0 = item.first_key(a, iw), some1 = iw < item.nq ? item.last_key(a, iwl) : -1;
     {
         const S* row = (const S*)a.q + b * a.qs.item + (int64_t)(live ? i : 0) * a.qs.frame + h * a.qs.head;
         const int64_t at = (((int64_t)b * a.Tq + (live ? i : 0)) * a.H + h) * a.D;
@@ -159,22 +213,26 @@ __global__ __launch_bounds__(kAttnThreads, ((sizeof(S) == 4 && !DMA) || (DP > 64
         delta += swap_halves(delta);
         const int64_t stat = ((int64_t)b * a.H + h) * a.Tq + i;
         if (live) lse2 = lse_or_inf(a.lse[stat]);
+        float apart = 0.0f;
+        if (__any(heavy(lse2))) {
+            float top, w;
+            heavy_row<S, DP>(a, item, b, h, i, q, some0, some1, mine0, mine, top, w);
+            if (heavy(lse2)) lse2 = top, weight = apart = w;
+        }
         if (half == 0 && wk == 0 && i < a.Tq) {
-            const int64_t head = ((int64_t)b * a.H + h) * 2 * a.Tq;
+            const int64_t head = ((int64_t)b * a.H + h) * 3 * a.Tq;
             a.stat[head + i] = lse2;
             a.stat[head + a.Tq + i] = delta;
+            a.stat[head + 2 * (int64_t)a.Tq + i] = apart;
         }
+        delta *= weight;
     }
     if (!a.dq && !a.dist) return;
-    const int mine0 = item.first_key(a, i), mine1 = item.last_key(a, i);
-    const uint32_t mine = live && mine1 >= mine0 ? mine1 - mine0 + 1 : 0;
     int j0 = 0, j1 = 0;
     if (i0 < item.nq) {
         j0 = item.first_key(a, i0);
         j1 = item.last_key(a, min(i0 + OW * kTile, item.nq) - 1) + 1;
     }
-    const int iwl = min(iw + kTile, item.nq) - 1;
-    const int some0 = item.first_key(a, iw), some1 = iw < item.nq ? item.last_key(a, iwl) : -1;
     const int all0 = item.first_key(a, iwl), all1 = iw + kTile <= item.nq ? item.last_key(a, iw) : -1;
 
     const int hk = h / (a.H / a.Hkv);
@@ -221,7 +279,7 @@ __global__ __launch_bounds__(kAttnThreads, ((sizeof(S) == 4 && !DMA) || (DP > 64
                 for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], a.scale2, flat) - lse2);
             }
 #pragma unroll
-            for (int r = 0; r < 16; ++r) ds[r] = s[r] * (ds[r] - delta);
+            for (int r = 0; r < 16; ++r) ds[r] = s[r] * fmaf(ds[r], weight, -delta);
             if (j < all0 || j + kTile - 1 > all1) {
                 const uint32_t at = j + 4 * half - mine0;
 #pragma unroll
@@ -352,8 +410,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) 
     constexpr int KW = 4 / OW, BQ = Shape::ROWS, QT = BQ / kTile / KW, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) char smem[];
     u32x4* values = (u32x4*)(smem + Tiles::kAllBytes);
-    float* stats = (float*)(smem + Tiles::kAllBytes + kValuesBytes<S, DP>);  // of two tiles: [2][2][BQ], as a.stat
-    float* bias = stats + 4 * BQ;
+    float* stats = (float*)(smem + Tiles::kAllBytes + kValuesBytes<S, DP>);  // of two tiles: [2][3][BQ], as a.stat
+    float* bias = stats + 6 * BQ;
     const int nbias = 2 * a.R + 1 + 2 * kBiasMargin;
     const int lane = threadIdx.x % 64, wave = wave_of_block(), half = lane / 32;
 
@@ -402,13 +460,18 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) 
         const int64_t gstride = (int64_t)a.H * a.D;
         Tiles qg(smem, (const S*)a.q + b * a.qs.item + h * a.qs.head + (int64_t)i0 * a.qs.frame, a.qs.frame,
                  (const S*)a.dout + (((int64_t)b * a.Tq + i0) * a.H + h) * a.D, gstride, a.D, i1 - i0);
-        // the tile's lse and delta, one float a lane: the first waves take the one, the next the other
-        const float* stat_rows = a.stat + ((int64_t)b * a.H + h) * 2 * a.Tq + i0;
+        // the tile's statistics, one float a lane: the first waves take lse, the next delta and so on
+        const float* stat_rows = a.stat + ((int64_t)b * a.H + h) * 3 * a.Tq + i0;
         auto start_stats = [&](int t) {
             constexpr int kEach = BQ < 64 ? 64 : BQ;
-            const int which = __builtin_amdgcn_readfirstlane(threadIdx.x / kEach), at = threadIdx.x % kEach;
-            if (which < 2 && at < BQ)
-                load_lds_floats(stat_rows + which * a.Tq + t * BQ, i1 - i0 - t * BQ, at, stats + ((t & 1) * 2 + which) * BQ);
+            const int at = threadIdx.x % kEach;
+#pragma unroll
+            for (int row = 0; row < 3; row += kAttnThreads / kEach) {
+                const int which = row + __builtin_amdgcn_readfirstlane(threadIdx.x / kEach);
+                if (which < 3 && at < BQ)
+                    load_lds_floats(stat_rows + (int64_t)which * a.Tq + t * BQ, i1 - i0 - t * BQ, at,
+                                    stats + ((t & 1) * 3 + which) * BQ);
+            }
         };
         const int tiles = i1 > i0 ? (i1 - i0 + BQ - 1) / BQ : 0;
         if (tiles) {
@@ -427,7 +490,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) 
             if (t + 1 < tiles) start_stats(t + 1);
             const S* qtile = qg.x_of(t);
             const S* gtile = qg.y_of(t);
-            const float* stat = stats + (t & 1) * 2 * BQ;
+            const float* stat = stats + (t & 1) * 3 * BQ;
             const int it = i0 + t * BQ;
 #pragma unroll
             for (int u = 0; u < QT; ++u) {
@@ -458,6 +521,14 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) 
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         s[r] = exp2_fast(fmaf(s[r], a.scale2, flat) - lse2(r));
+                }
+                if (__any(stat[2 * BQ + row0 + lane % 32] != 0.0f)) {  // scores reach a maximum only up to their rounding
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        row[r] = *reinterpret_cast<const f32x4*>(stat + 2 * BQ + row0 + 8 * r + 4 * half);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s[r] = row[r / 4][r % 4] != 0.0f ? fminf(s[r], 1.0f) * row[r / 4][r % 4] : s[r];
                 }
                 if (i < all0 || i + kTile - 1 > all1) {
                     const uint32_t at = i + 4 * half - mine0;
@@ -512,7 +583,7 @@ static int bwd_lds(const AttnShape& s, int elem_bytes, int ow, bool queries) {
     const int buffers = ow == 1 || (ow == 2 && elem_bytes == 4 && dp > 64) ? 1 : 2;
     const int tiles = 2 * buffers * rows * tile_slots(dp * elem_bytes / 16, elem_bytes) * 16, bias = padded_bias(s) * 4;
     const int values = elem_bytes == 2 && dp > 64 ? 4 * (dp / 16) * 64 * 16 : 0;  // kValuesBytes
-    return tiles + bias + (queries ? 4 * kTile * kDiag * 4 + 4 * bias : values + 4 * rows * 4);
+    return tiles + bias + (queries ? 4 * kTile * kDiag * 4 + 4 * bias : values + 6 * rows * 4);
 }
 
 // Frames a workgroup owns, in units of 32: as many as leave two workgroups for
@@ -531,8 +602,8 @@ static int64_t blocks_of(int64_t frames, int ow) { return (frames + ow * kTile -
 
 static int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// lse and delta, then the workgroups' sums by distance.
-static int64_t stat_bytes(const AttnShape& s) { return round16(s.B * s.H * s.Tq * 2 * (int64_t)sizeof(float)); }
+// Three statistics of each query, then the workgroups' sums by distance.
+static int64_t stat_bytes(const AttnShape& s) { return round16(s.B * s.H * s.Tq * 3 * (int64_t)sizeof(float)); }
 
 bool dwattn_bwd_fits(const AttnShape& s) {
     // the workgroups' sums by distance of one head, counted in 31 bits

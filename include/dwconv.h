@@ -609,6 +609,9 @@ size_t dwattn_bwd_workspace_bytes(const dw_attn *shape);
  *   dtable[n, h] = sum of dS_ij of head h over the pairs in bucket n
  * Frames at or past the lengths get zero gradients, and q, k, v, out, lse and
  * dout are not read there.  The maps P and dS are recomputed, never stored.
+ * Where |lse_i| is over 710 and no longer tells P_i (a row whose keys all have a
+ * bias of -1e9 or the type's lowest value), the row's maximum and sum are taken
+ * again from q and k; such rows are slower.
  *
  * dq [B][Tq][H][D], dk, dv [B][Tk][Hkv][D] have the strides shape->dq, dk, dv
  * and must not overlap each other or an input; dtable [buckets][H] is float.

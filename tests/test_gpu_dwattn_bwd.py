@@ -16,7 +16,7 @@ import torch
 import block_ref as ref
 import datagen
 from gpu_util import Guarded, host64
-from test_gpu_dwattn import BF16, DEV, DT, F32, call, host, lib, make
+from test_gpu_dwattn import BF16, DEV, DT, F32, call, far_and_near, host, lib, make
 
 pytestmark = pytest.mark.gpu
 
@@ -266,3 +266,79 @@ def test_on_another_stream_and_in_a_graph():
         seen = [t.clone() for t in o]
         for a, b in zip(seen, grads(s, out, lse)):
             assert torch.equal(a, b)
+
+
+def check_by_weights(s, absorbed, rel=2e-5, what=""):
+    """The gradients and their terms' bounds from the softmax of the scores, instead of from lse: for rows whose lse
+    says nothing.  A bias of magnitude `absorbed` or more swallows the products it is added to."""
+    out, lse = call(s)
+    got = grads(s, out, lse)
+    torch.cuda.synchronize()
+    q, k, v, table, buckets, q_len, k_len, pos, left, right, scale = host(s)
+    do, o = host64(s["dout"]), host64(out)
+    B, Tq, H, D = q.shape
+    G, R = H // k.shape[2], len(buckets) // 2
+    w = [np.zeros_like(x) for x in (q, k, v, table)]
+    bound = [np.zeros_like(x) for x in w]
+    for b in range(B):
+        nq, nk = int(np.clip(q_len[b], 0, Tq)), int(np.clip(k_len[b], 0, k.shape[1]))
+        rel_ = np.arange(nk)[None, :] - np.arange(nq)[:, None] - int(pos[b])
+        seen = ((left < 0) | (rel_ >= -left)) & ((right < 0) | (rel_ <= right))
+        place = np.asarray(buckets)[np.clip(rel_, -R, R) + R]
+        for h in range(H):
+            kk, vv, bias = k[b, :nk, h // G], v[b, :nk, h // G], table[place, h]
+            S = np.where(np.abs(bias) >= absorbed, bias, scale * q[b, :nq, h] @ kk.T + bias)
+            S = np.where(seen, S, -np.inf)
+            P = np.exp(S - S.max(1, keepdims=True))
+            P /= P.sum(1, keepdims=True)
+            g, oo = do[b, :nq, h], o[b, :nq, h]
+            dS = P * (g @ vv.T - (g * oo).sum(1, keepdims=True))
+            aS = P * (np.abs(g) @ np.abs(vv).T + (np.abs(g) * np.abs(oo)).sum(1, keepdims=True))
+            for into, ds, p, f in ((w, dS, P, lambda x: x), (bound, aS, P, np.abs)):
+                into[0][b, :nq, h] = scale * ds @ f(kk)
+                into[1][b, :nk, h // G] += scale * ds.T @ f(q[b, :nq, h])
+                into[2][b, :nk, h // G] += p.T @ f(g)
+                np.add.at(into[3][:, h], place, ds)
+    for name, g, x, b in zip(("dq", "dk", "dv", "dtable"), got, w, bound):
+        g = host64(g)
+        assert np.isfinite(g).all(), f"{what} {name}"
+        tol = rel * (b + 1e-6) + (ref.U16 * b + ref.U16 * np.abs(x) if s["dt"] == BF16 and name != "dtable" else 0)
+        off = np.abs(g - x)
+        assert (off <= tol).all(), f"{what} {name}: {off.max():.3e} at {np.argwhere(off > tol)[0]}"
+
+
+@DT
+@pytest.mark.parametrize("low", ["lowest", -1e30, -1e9, 1e9])
+def test_rows_of_nothing_but_one_huge_bias(low, dt):
+    """Such rows weigh their keys alike in both passes: over near and far tiles, ragged items, windows down to one key,
+    shared key heads."""
+    low = torch.finfo(dt).min if low == "lowest" else low
+    for s in (make(2, 170, 170, 4, 2, 32, dt, NB=8, reach=20, q_len=[170, 101], k_len=[170, 101]),
+              make(1, 90, 90, 2, 2, 50, dt, NB=8, reach=20, left=7, right=0),
+              make(2, 5, 300, 2, 1, 128, dt, NB=8, reach=20, pos=[295, 7])):
+        s["table"][:] = low
+        check_by_weights(s, absorbed=1e8, what=str(s["Tq"]))
+
+
+@DT
+def test_rows_of_lowest_values_beside_ordinary_rows(dt):
+    """Near buckets at the lowest value: the rows that see only near keys are uniform, the others ordinary; and far
+    buckets at it, with a huge score among them."""
+    low = torch.finfo(dt).min
+    s = make(2, 170, 170, 2, 2, 64, dt, NB=8, reach=20, k_len=[170, 12])
+    ends = [int(s["buckets"][0]), int(s["buckets"][-1])]
+    for n in range(8):
+        if n not in ends:
+            s["table"][n] = low
+    check_by_weights(s, absorbed=1e8)
+    check_by_weights(far_and_near(dt, low), absorbed=1e8)
+    check(far_and_near(dt, low))
+
+
+@DT
+def test_rows_of_a_large_bias(dt):
+    """A whole table at -2000: scores near 2885 in units of log2 are rounded to 2^-13, twice, in both passes alike: a
+    weight is off by 2 * 2^-13 * ln 2 = 1.7e-4 of itself, and its row's sum by as much."""
+    s = make(2, 170, 170, 2, 2, 64, dt, NB=8, reach=20, q_len=[170, 99], k_len=[170, 99])
+    s["table"][:] = -2000.0
+    check_by_weights(s, absorbed=1e8, rel=4e-4)
