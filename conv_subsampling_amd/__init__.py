@@ -512,8 +512,8 @@ def dwnorm_fwd(x, gamma=None, beta=None, lengths=None, residual=None, rng=None, 
                eps: float = 1e-5, y=None, sum=None, mean=None, rstd=None, need=("y", "sum", "mean", "rstd")):
     """Layer norm of s = residual + alpha * dropout(x) over the channels; x
     [B,T,C].  Returns (y, s, mean, rstd): s in x's storage type (x itself where
-    there is neither a residual, a scale nor a dropout and no `sum` is given),
-    mean and rstd float32 [B,T].  s, mean and rstd not in `need` are skipped
+    there is neither a residual, a scale nor a dropout, no `sum` is given and y
+    is not written over x), mean and rstd float32 [B,T].  s, mean and rstd not in `need` are skipped
     (None)."""
     if x.dim() != 3:
         raise ValueError("x must be [B, T, C]")
@@ -526,8 +526,8 @@ def dwnorm_fwd(x, gamma=None, beta=None, lengths=None, residual=None, rng=None, 
     _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
     _dev_tensor("residual", residual, st, dev, (B, T, C), allow_none=True)
     _rng(rng, p, dev)
-    plain = residual is None and p == 0 and alpha == 1.0 and sum is None
     y = torch.empty_like(x) if y is None else _dev_tensor("y", y, st, dev, (B, T, C))
+    plain = residual is None and p == 0 and alpha == 1.0 and sum is None and y.data_ptr() != x.data_ptr()
     if sum is not None:
         _dev_tensor("sum", sum, st, dev, (B, T, C))
     elif "sum" in need and not plain:

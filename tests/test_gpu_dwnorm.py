@@ -399,3 +399,22 @@ def test_binding_refusals():
     with pytest.raises(dw.DwconvError, match="workspace"):
         m = torch.zeros((2, 3), device=DEV)
         dw.dwnorm_bwd(x, None, None, m, m, x, workspace=torch.zeros(8, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_plain_norm_in_place_keeps_its_input_for_the_gradients(dt):
+    """y over x without a residual: the sum that comes back is the input, not y, and the gradients are the same."""
+    dw = lib()
+    s = make(2, 11, 320, dt, residual=False, p=0.0, alpha=1.0, lengths=[11, 7])
+    args = (s["gamma"], s["beta"], s["lengths"])
+    y, total, mean, rstd = dw.dwnorm_fwd(s["x"], *args)
+    x = s["x"].clone()
+    y2, total2, mean2, rstd2 = dw.dwnorm_fwd(x, *args, y=x)
+    assert y2 is x and torch.equal(y, y2) and torch.equal(mean, mean2) and torch.equal(rstd, rstd2)
+    live = s["lengths"].tolist()
+    for b, n in enumerate(live):
+        assert torch.equal(total[b, :n], total2[b, :n])
+    for a, b in zip(check_bwd(s, total, mean, rstd), check_bwd(s, total2, mean2, rstd2)):
+        assert torch.equal(a, b)
+    assert dw.dwnorm_fwd(s["x"].clone(), *args, y=x, need=("y",))[1] is None
+    assert dw.dwnorm_fwd(s["x"], *args)[1] is s["x"]
