@@ -476,6 +476,7 @@ dw_status dwnorm_fwd(const void* x, const void* residual, const void* gamma, con
     if (s != DW_OK) return s;
     if (!(eps >= 0.0f)) return fail(DW_ERR_INVALID_ARG, "%s: eps must not be negative", fn);
     if (B == 0 || T == 0 || C == 0) return ok();
+    if (!dw::dwnorm_fwd_fits(B * T, C)) return too_large(fn);
     if (!x || !y) return fail(DW_ERR_INVALID_ARG, "%s: x and y must not be NULL", fn);
     if (y == sum) return fail(DW_ERR_INVALID_ARG, "%s: y must not alias sum", fn);
     return from_hip(dw::launch_dwnorm_fwd(x, residual, gamma, beta, lengths, p > 0.0 ? rng : nullptr, y, sum, mean,
@@ -537,7 +538,8 @@ dw_status dwattn_rel_buckets(int32_t* map, int64_t buckets, int64_t reach, int b
 size_t dwattn_fwd_workspace_bytes(const dw_attn* shape) {
     dw::AttnShape s;
     if (check_attn("dwattn_fwd_workspace_bytes", shape, false, &s) != DW_OK) return 0;
-    return dw::dwattn_fwd_workspace(s, shape->dtype == DW_BF16 ? 2 : 4);
+    const int elem = shape->dtype == DW_BF16 ? 2 : 4;
+    return dw::dwattn_fwd_fits(s, elem) ? dw::dwattn_fwd_workspace(s, elem) : 0;
 }
 
 dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const void* v, const void* table,
@@ -549,6 +551,7 @@ dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const v
     const dw_status c = check_attn(fn, shape, table != nullptr, &s);
     if (c != DW_OK) return c;
     if (!nonempty(s.B, s.Tq, s.H, s.D)) return ok();
+    if (!dw::dwattn_fwd_fits(s, shape->dtype == DW_BF16 ? 2 : 4)) return too_large(fn);
     if (!q || !out || (s.Tk > 0 && (!k || !v)))
         return fail(DW_ERR_INVALID_ARG, "%s: q, k, v and out must not be NULL (unless empty)", fn);
     if (out == q || out == k || out == v) return fail(DW_ERR_INVALID_ARG, "%s: out must not alias an input", fn);
@@ -563,8 +566,8 @@ dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const v
 size_t dwattn_bwd_workspace_bytes(const dw_attn* shape) {
     dw::AttnShape s;
     if (!shape || check_attn("dwattn_bwd_workspace_bytes", shape, shape->buckets > 0, &s) != DW_OK) return 0;
-    if (!dw::dwattn_bwd_fits(s)) return 0;
-    return dw::dwattn_bwd_workspace(s, shape->dtype == DW_BF16 ? 2 : 4);
+    const int elem = shape->dtype == DW_BF16 ? 2 : 4;
+    return dw::dwattn_bwd_fits(s, elem) ? dw::dwattn_bwd_workspace(s, elem) : 0;
 }
 
 dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const void* v, const void* table,
@@ -579,7 +582,7 @@ dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const v
     if (c != DW_OK) return c;
     if (!strides_ok(shape->dq) || !strides_ok(shape->dk) || !strides_ok(shape->dv))
         return fail(DW_ERR_INVALID_ARG, "%s: negative stride", fn);
-    if (!dw::dwattn_bwd_fits(s) || (dq && !strides_fit(shape->dq, s.B, s.Tq, s.H)) || (dk && !strides_fit(shape->dk, s.B, s.Tk, s.Hkv)) ||
+    if (!dw::dwattn_bwd_fits(s, shape->dtype == DW_BF16 ? 2 : 4) || (dq && !strides_fit(shape->dq, s.B, s.Tq, s.H)) || (dk && !strides_fit(shape->dk, s.B, s.Tk, s.Hkv)) ||
         (dv && !strides_fit(shape->dv, s.B, s.Tk, s.Hkv)))
         return too_large(fn);
     if ((!dq && !dk && !dv && !dtable) || s.H == 0) return ok();

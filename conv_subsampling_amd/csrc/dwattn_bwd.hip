@@ -357,7 +357,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dtable(const float* __restr
     __shared__ int16_t list[kMost];
     __shared__ int found[kSteps][4];
     __shared__ double waves[4];
-    const int bucket = blockIdx.x, h = blockIdx.y, lane = threadIdx.x % 64, wave = wave_of_block();
+    const int bucket = blockIdx.x / H, h = blockIdx.x % H, lane = threadIdx.x % 64, wave = wave_of_block();
     uint64_t mask[kSteps];
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
@@ -605,9 +605,12 @@ static int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 // Three statistics of each query, then the workgroups' sums by distance.
 static int64_t stat_bytes(const AttnShape& s) { return round16(s.B * s.H * s.Tq * 3 * (int64_t)sizeof(float)); }
 
-bool dwattn_bwd_fits(const AttnShape& s) {
-    // the workgroups' sums by distance of one head, counted in 31 bits
-    return s.reach == 0 || product_below(kMaxExtent, {s.B, (s.Tq + kTile - 1) / kTile, 2 * s.reach + 1});
+bool dwattn_bwd_fits(const AttnShape& s, int elem_bytes) {
+    const int64_t nqb = blocks_of(s.Tq, owned(s, elem_bytes, true)), nkb = blocks_of(s.Tk, owned(s, elem_bytes, false));
+    if (!grid_of_256_fits(s.B * s.H * nqb) || !grid_of_256_fits(s.B * s.Hkv * nkb)) return false;
+    // the workgroups' sums by distance of one head, counted in 31 bits, and a workgroup for each entry of the table
+    return s.reach == 0 || (product_below(kMaxExtent, {s.B, (s.Tq + kTile - 1) / kTile, 2 * s.reach + 1}) &&
+                            grid_of_256_fits(s.buckets * s.H));
 }
 
 size_t dwattn_bwd_workspace(const AttnShape& s, int elem_bytes) {
@@ -671,7 +674,7 @@ hipError_t launch_dwattn_bwd(const AttnPtrs& p, const AttnShape& s, const void* 
         if (e != hipSuccess) return e;
     }
     if (!dtable) return hipSuccess;
-    hipLaunchKernelGGL(attn_dtable, dim3(a.NB, a.H), dim3(kAttnThreads), 0, stream, a.dist, p.buckets, dtable, 2 * a.R + 1,
+    hipLaunchKernelGGL(attn_dtable, dim3(a.NB * a.H), dim3(kAttnThreads), 0, stream, a.dist, p.buckets, dtable, 2 * a.R + 1,
                        (int32_t)(s.B * a.nqb), a.NB, a.H);
     return hipGetLastError();
 }

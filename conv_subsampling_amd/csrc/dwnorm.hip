@@ -444,6 +444,11 @@ static int64_t norm_rows_per_block(int64_t C) {
     return C <= 64 ? 32 : C <= 128 ? 16 : C <= 256 ? 8 : C <= 2048 ? 4 : 1;
 }
 
+bool dwnorm_fwd_fits(int64_t rows, int64_t C) {
+    const int64_t per = norm_rows_per_block(C);
+    return grid_of_256_fits((rows + per - 1) / per);
+}
+
 hipError_t launch_dwnorm_fwd(const void* x, const void* residual, const void* gamma, const void* beta,
                              const int32_t* lengths, const uint64_t* rng, void* y, void* sum, float* mean,
                              float* rstd, int64_t B, int64_t T, int64_t C, float eps, float alpha, double p, bool bf16,
@@ -507,7 +512,7 @@ static int64_t drop_blocks(int64_t rows, int64_t C) {
 }
 
 bool dwdrop_fits(int64_t rows, int64_t C) {
-    return product_below((int64_t)1 << 60, {rows, C + kGroup}) && drop_blocks(rows, C) < kMaxExtent;
+    return product_below((int64_t)1 << 60, {rows, C + kGroup}) && grid_of_256_fits(drop_blocks(rows, C));
 }
 
 hipError_t launch_dwdrop(const void* x, const void* residual, void* y, const uint64_t* rng, int64_t rows, int64_t C,

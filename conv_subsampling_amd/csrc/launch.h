@@ -123,9 +123,14 @@ hipError_t launch_dwconv2d_bwd(const void* x, const void* w, const int32_t* leng
                                float* dw, float* db, void* workspace, int64_t B, const Conv2dGeom& g, bool bf16,
                                int vec, hipStream_t stream);
 
+// Whether one launch takes this many workgroups of 256 threads: its threads
+// are counted in 32 bits.
+inline bool grid_of_256_fits(int64_t blocks) { return blocks < (int64_t)1 << 24; }
+
 // Layer norm with the residual add and dropout in front of it, and dropout
 // alone.  rng is NULL where nothing is dropped.
 bool dwnorm_width_supported(int64_t C);
+bool dwnorm_fwd_fits(int64_t rows, int64_t C);
 hipError_t launch_dwnorm_fwd(const void* x, const void* residual, const void* gamma, const void* beta,
                              const int32_t* lengths, const uint64_t* rng, void* y, void* sum, float* mean,
                              float* rstd, int64_t B, int64_t T, int64_t C, float eps, float alpha, double p, bool bf16,
@@ -161,12 +166,13 @@ struct AttnShape {
     float scale;
 };
 
-bool dwattn_fits(const AttnShape& s);
+bool dwattn_fits(const AttnShape& s);  // of both directions
+bool dwattn_fwd_fits(const AttnShape& s, int elem_bytes);  // beyond dwattn_fits
 size_t dwattn_fwd_workspace(const AttnShape& s, int elem_bytes);
 hipError_t launch_dwattn_fwd(const AttnPtrs& p, const AttnShape& s, void* out, float* lse, void* workspace, bool bf16,
                              hipStream_t stream);
 
-bool dwattn_bwd_fits(const AttnShape& s);  // beyond dwattn_fits
+bool dwattn_bwd_fits(const AttnShape& s, int elem_bytes);  // beyond dwattn_fits
 size_t dwattn_bwd_workspace(const AttnShape& s, int elem_bytes);
 hipError_t launch_dwattn_bwd(const AttnPtrs& p, const AttnShape& s, const void* out, const float* lse, const void* dout,
                              void* dq, void* dk, void* dv, float* dtable, void* workspace, bool bf16,

@@ -448,7 +448,8 @@ dw_status dwconv2d_bwd_noalloc(const void *x, const void *w, const int32_t *leng
  * and the sum are float32, rounded once.  y may be x or residual (in place);
  * other overlaps race.
  * Errors: DW_ERR_INVALID_ARG for a null x or y, a negative size, a bad dtype,
- * p outside [0, 1) or a null rng with p > 0.
+ * p outside [0, 1) or a null rng with p > 0; DW_ERR_UNSUPPORTED for sizes too
+ * large for one launch.
  */
 dw_status dwdrop_fwd(const void *x, const void *residual, void *y, const uint64_t *rng, int64_t rows, int64_t C,
                      double p, float alpha, dw_dtype dtype, void *stream);
@@ -477,7 +478,8 @@ dw_status dwdrop_bwd(const void *dy, void *dx, const uint64_t *rng, int64_t rows
  * be NULL (not written).  Everything is carried in float32; the statistics and
  * y are those of the unrounded s, in two passes over registers.  In place:
  * each of y and sum may be x or residual; y must not be sum.
- * Errors: DW_ERR_UNSUPPORTED for C > 8192; DW_ERR_INVALID_ARG for a null x or
+ * Errors: DW_ERR_UNSUPPORTED for C > 8192 or sizes too large for one launch;
+ * DW_ERR_INVALID_ARG for a null x or
  * y, a negative size or eps, a bad dtype, p outside [0, 1), a null rng with
  * p > 0, or y == sum.
  */

@@ -206,3 +206,22 @@ def test_bucket_map_is_exact(alib, bidirectional):
             continue
         want = [ref.bucket(r, buckets, reach, bool(bidirectional)) for r in range(-reach, reach + 1)]
         assert list(m[:2 * reach + 1]) == want, (buckets, reach)
+
+
+def test_more_workgroups_than_a_launch_takes_are_refused(alib):
+    """A launch counts its threads in 32 bits: 2^24 workgroups of 256 are too many, and are refused before it."""
+    tail = (1e-5, 1.0, 0.0, 0, N)
+    for B, T, C in ((1 << 15, 1 << 14, 8), (1 << 12, 1 << 12, 4096), (1 << 13, 1 << 13, 2048)):
+        assert alib.dwnorm_fwd(P, N, N, N, N, N, Q, N, N, N, B, T, C, *tail) == UNSUPPORTED and "too large" in err(alib)
+    assert alib.dwdrop_fwd(P, N, Q, R, 1 << 34, 8, 0.1, 1.0, 0, N) == UNSUPPORTED and "too large" in err(alib)
+    assert alib.dwdrop_bwd(P, Q, R, 1 << 30, 1 << 7, 0.1, 1.0, 0, N) == UNSUPPORTED
+    X = [ctypes.c_void_p(0x10000 * i) for i in range(1, 12)]
+    for many in (dict(B=1 << 24, H=1, Hkv=1), dict(B=1 << 20, H=1 << 5, Hkv=1), dict(B=1 << 12, H=1 << 12, Hkv=1)):
+        for dtype in (0, 1):
+            shape = attn(Tq=1, Tk=1, D=1, dtype=dtype, **many)
+            assert alib.dwattn_fwd(shape, P, R, S, P, P, N, N, N, Q, N, W, 1 << 40, N) == UNSUPPORTED and "too large" in err(alib)
+            assert alib.dwattn_bwd(shape, X[0], X[1], X[2], X[3], X[4], N, N, N, X[5], X[6], X[7], X[8], X[9], X[10], P, W,
+                                   1 << 40, N) == UNSUPPORTED and "too large" in err(alib)
+            assert alib.dwattn_fwd_workspace_bytes(shape) == 0 and alib.dwattn_bwd_workspace_bytes(shape) == 0
+    assert alib.dwattn_bwd(attn(buckets=1 << 23), X[0], X[1], X[2], X[3], X[4], N, N, N, X[5], X[6], X[7], X[8], X[9], X[10],
+                           P, W, 1 << 40, N) == UNSUPPORTED
