@@ -395,14 +395,15 @@ size_t dwattn_fwd_workspace(const AttnShape& s, int elem_bytes) {
 }
 
 bool dwattn_fits(const AttnShape& s) {
-    // workgroups of the narrowest tiles, and the threads of the join
+    // workgroups of the narrowest tiles, and the rows
     const int64_t q32 = (s.Tq + 31) / 32, k32 = (s.Tk + 31) / 32;
     return product_below(kMaxExtent, {s.B, s.H, q32}) && product_below(kMaxExtent, {s.B, s.H, k32}) &&
-           product_below(kMaxExtent, {s.B, s.H, s.Tq}) && product_below(kMaxExtent, {s.B, s.H, s.Tq, (s.D + 3) / 4 + 1});
+           product_below(kMaxExtent, {s.B, s.H, s.Tq});
 }
 
 bool dwattn_fwd_fits(const AttnShape& s, int elem_bytes) {
     const FwdPlan p = fwd_plan(s, elem_bytes);
+    // splits are for a few hundred workgroups of at most 32 queries, so the join's threads are few
     return grid_of_256_fits(s.B * (p.packed ? s.Hkv : s.H) * p.nqb * p.splits);
 }
 

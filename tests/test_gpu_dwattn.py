@@ -335,3 +335,17 @@ def test_rows_of_nothing_but_the_lowest_or_largest_value(sign, dt):
     # equal weights: one float32 sum of at most 200 terms; bf16 rounds out
     tol = 2e-5 + (ref.U16 * np.abs(v).max() if dt == BF16 else 0)
     assert np.abs(host64(out)[0] - want[:, None]).max() <= tol
+
+
+def test_rows_whose_elements_pass_32_bits():
+    """2^26 rows of 128: outputs of 17 GB.  With one key its weight is 1, and every row is that item's value."""
+    B, T, D = 1 << 20, 64, 128
+    q = torch.ones((1, 1, 1, D), dtype=BF16, device=DEV).expand(B, T, 1, D)
+    k, v = (datagen.normal((B, 1, 1, D), 1.0, f"rows/{n}", device=DEV).to(BF16) for n in "kv")
+    out, lse = lib().dwattn_fwd(q, k, v)
+    torch.cuda.synchronize()
+    for b in (0, 1, B // 2 + 1, B - 1):
+        assert torch.equal(out[b], v[b].expand(T, 1, D))
+    assert torch.equal(out[::4097].float().sum((1, 2)), v[::4097].float().sum((1, 2)) * T)
+    want = k.float().sum(-1) * D ** -0.5          # [B, 1, 1]; sums of 128 terms in another order
+    assert float((lse - want.view(B, 1, 1)).abs().max()) <= 128 * ref.U32 * 100
