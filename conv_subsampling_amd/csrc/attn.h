@@ -25,8 +25,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAttnThreads = 256;
-constexpr int kTile = 32;          // owned and streamed frames of one matrix tile
-constexpr int kBiasMargin = 64;    // entries beyond the map's ends: a tile that touches it reads without a clamp
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ int wave_of_block() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
@@ -188,8 +186,6 @@ __device__ __forceinline__ Frag<S> to_frag(const RawGroup<S>& g) {
 // transposing one.  Measured, sixteen waves reading: 16-byte reads take 2.7
 // cycles with these pads as from linear addresses (25 without one at 128 bf16
 // elements), transposing reads 3.2 (4.7 there with one chunk of pad).
-constexpr int tile_slots(int chunks, int elem_bytes) { return chunks + (chunks == 16 && elem_bytes == 2 ? 3 : 1); }
-
 template <typename S, int DP>
 struct Tile {
     static constexpr int kChunks = DP * (int)sizeof(S) / 16;
@@ -311,15 +307,6 @@ struct TileDma {
     __device__ __forceinline__ void finish(S*) const {}
 };
 
-// What direct loads ask of a tensor: whole groups of 8 elements, aligned 16-byte
-// chunks, frames that do not overlap, and a tile's offsets in 31 bits.
-template <typename S>
-bool dma_fits(const void* base, const AttnStride& s, int64_t D) {
-    const int64_t chunk = 16 / (int64_t)sizeof(S);
-    return (uintptr_t)base % 16 == 0 && D % kGroup == 0 && s.item % chunk == 0 && s.frame % chunk == 0 &&
-           s.head % chunk == 0 && s.frame >= D && s.frame <= ((int64_t)1 << 29) / 256;
-}
-
 __device__ __forceinline__ void wave_loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // The tiles of two tensors (keys and values, or queries and output gradients),
@@ -405,10 +392,12 @@ inline AttnArgs attn_args(const AttnPtrs& p, const AttnShape& s) {
 // Calls f with the padded head width that holds D.
 template <typename F>
 hipError_t with_head_width(int64_t D, F&& f) {
-    if (D <= 32) return f(std::integral_constant<int, 32>());
-    if (D <= 64) return f(std::integral_constant<int, 64>());
-    if (D <= 96) return f(std::integral_constant<int, 96>());
-    return f(std::integral_constant<int, 128>());
+    switch (head_width(D)) {
+        case 32: return f(std::integral_constant<int, 32>());
+        case 64: return f(std::integral_constant<int, 64>());
+        case 96: return f(std::integral_constant<int, 96>());
+        default: return f(std::integral_constant<int, 128>());
+    }
 }
 
 // The workgroup's place: its block of owned frames and its (item, head) pair.
@@ -521,8 +510,6 @@ struct BiasFill {
         for (int x = threadIdx.x + kFirst * kAttnThreads; x < n; x += kAttnThreads) bias[x] = value(a, h, map_at(a, x));
     }
 };
-
-inline int attn_bias_bytes(int32_t R) { return (2 * R + 1 + 2 * kBiasMargin) * 4; }
 
 // The distance key - query of a tile's first key and first query says what the
 // tile's bias is: past the map's reach on either side one value, else looked up.

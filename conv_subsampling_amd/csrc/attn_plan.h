@@ -1,0 +1,153 @@
+// The attention's launch plan: sizes, and the form of each kernel that they and
+// the operands' alignment ask for.  Host code alone, so that a CPU test can ask
+// which forms a shape takes.
+#pragma once
+
+#include <stdint.h>
+
+namespace dw {
+
+struct AttnStride {
+    int64_t item, frame, head;  // in elements
+};
+
+constexpr int32_t kNoLimit = 1 << 30;        // a context without a limit
+constexpr int64_t kAttnMaxFrames = 1 << 28;  // sums of frames and positions stay in 32 bits
+constexpr int64_t kAttnMaxHead = 128;        // what a wave's accumulators hold
+constexpr int64_t kAttnMaxReach = 1024;      // of the bias map: what LDS holds beside the tiles
+
+struct AttnShape {
+    int64_t B, Tq, Tk, H, Hkv, D;
+    AttnStride q, k, v, dq, dk, dv;
+    int64_t buckets, reach, left, right;  // left, right: at most kNoLimit
+    float scale;
+};
+
+constexpr int kTile = 32;        // owned and streamed frames of one matrix tile
+constexpr int kBiasMargin = 64;  // entries beyond the map's ends: a tile that touches it reads without a clamp
+constexpr int kDiag = 64;        // row of the square in which the diagonals of a tile lie in columns
+constexpr int64_t kUnits = 256;  // compute units
+constexpr int kLdsBytes = 160 * 1024;
+
+inline int attn_bias_bytes(int32_t R) { return (2 * R + 1 + 2 * kBiasMargin) * 4; }
+
+// 16-byte chunks from one row of a tile to the next.
+constexpr int tile_slots(int chunks, int elem_bytes) { return chunks + (chunks == 16 && elem_bytes == 2 ? 3 : 1); }
+
+// The padded width that holds a head of D.
+inline int head_width(int64_t D) { return D <= 32 ? 32 : D <= 64 ? 64 : D <= 96 ? 96 : 128; }
+
+// What direct loads ask of a tensor: whole groups of 8 elements, aligned 16-byte
+// chunks, frames that do not overlap, and a tile's offsets in 31 bits.
+inline bool direct_fits(const void* base, const AttnStride& s, int64_t D, int elem_bytes) {
+    const int64_t chunk = 16 / elem_bytes;
+    return (uintptr_t)base % 16 == 0 && D % 8 == 0 && s.item % chunk == 0 && s.frame % chunk == 0 &&
+           s.head % chunk == 0 && s.frame >= D && s.frame <= ((int64_t)1 << 29) / 256;
+}
+
+// The instance of a kernel that a call takes.
+struct AttnForm {
+    int dp, own;          // padded head width; owned frames of a workgroup, in units of 32
+    bool direct, packed;  // loads straight into LDS; the heads of a group side by side
+};
+
+struct FwdPlan {
+    int qw, splits;
+    bool packed;
+    int64_t nqb;
+};
+
+// 128 queries a workgroup read each key tile once for four waves, so they are
+// taken where they make workgroups enough; next 64, whose two pairs of waves
+// divide the keys; and with the fewest queries 32, the keys then being split
+// over workgroups until each compute unit has one.  The plan goes by the sizes
+// alone (lengths are on the device).  Enough is three a compute unit, as many as
+// are resident (bf16 [16,750,8x128] takes 49 us so and 69 us with 64 queries,
+// float [32,750,8x64] 171 and 205 us); but eight for float under a causal mask,
+// whose last workgroups have the most keys and, with six products for one, set
+// the time (causal [8,1500,8x64], three a unit: 130 us with 128 queries, 124 us
+// with 64).  Twice as many splits cost the join more than they save (16 frames
+// over 20000 keys, 8 heads: 18 and 21 us).  The splits, and the workspace with
+// them, do not depend on the bias.
+constexpr int64_t kPackedBias = 16 * 1024;  // bytes of LDS for a group's biases beside the widest tiles
+
+inline FwdPlan fwd_plan(const AttnShape& s, int elem_bytes) {
+    const bool causal = s.left == kNoLimit && s.right != kNoLimit;
+    const int64_t wide = kUnits * (elem_bytes == 4 && causal ? 8 : 3);
+    FwdPlan p;
+    auto blocks_of = [&](int64_t queries) { return s.B * s.H * ((s.Tq + queries - 1) / queries); };
+    p.qw = s.Tq > 32 && blocks_of(128) >= wide ? 4 : s.Tq > 32 && blocks_of(64) >= kUnits ? 2 : 1;
+    const int64_t queries = 32 * p.qw;
+    p.nqb = (s.Tq + queries - 1) / queries;
+    p.splits = 1;
+    const int64_t group = s.Hkv ? s.H / s.Hkv : 1;
+    const bool could = p.qw == 1 && group > 1 && group * s.Tq <= kTile;
+    p.packed = could && group * (s.reach ? attn_bias_bytes((int)s.reach) : 0) <= kPackedBias;
+    if (p.qw == 1) {
+        int64_t span = s.Tk;
+        if (s.left < kNoLimit && s.right < kNoLimit) {
+            const int64_t window = s.left + s.right + queries;
+            span = window < 1 ? 1 : window < span ? window : span;
+        }
+        const int64_t blocks = could ? s.B * s.Hkv : blocks_of(32), tiles = (span + 127) / 128;
+        int64_t n = kUnits / (blocks ? blocks : 1);
+        n = n < tiles ? n : tiles;
+        p.splits = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+    }
+    return p;
+}
+
+// Two buffers of 128 keys leave room for two workgroups a compute unit.
+constexpr bool fwd_narrow(int dp, int elem_bytes) { return dp * elem_bytes <= 128; }
+
+inline AttnForm fwd_form(const FwdPlan& p, int64_t D, int elem_bytes, bool direct) {
+    const int dp = head_width(D);
+    return {dp, p.qw, direct && (p.qw > 1 || fwd_narrow(dp, elem_bytes)), p.packed};
+}
+
+// Streamed frames of a tile of the gradients' kernels and its buffers: float rows
+// over 64 wide leave room for one buffer beside the sums by distance.
+constexpr int bwd_rows(int dp, int elem_bytes, int own) {
+    return own == 1 ? 128 : own == 2 || elem_bytes * dp <= 128 ? 64 : 32;
+}
+constexpr int bwd_buffers(int dp, int elem_bytes, int own) {
+    return own == 1 || (own == 2 && elem_bytes == 4 && dp > 64) ? 1 : 2;
+}
+
+// Wide bf16 heads leave no room for all of a wave's operands and sums in the
+// registers of two waves a SIMD: its values then wait in LDS, in the order in
+// which the lanes read them (16 bytes a lane).
+constexpr bool bwd_values_in_lds(int dp, int elem_bytes) { return elem_bytes == 2 && dp > 64; }
+
+constexpr int bwd_tile_bytes(int dp, int elem_bytes, int own) {
+    return 2 * bwd_buffers(dp, elem_bytes, own) * bwd_rows(dp, elem_bytes, own) *
+           tile_slots(dp * elem_bytes / 16, elem_bytes) * 16;
+}
+constexpr int kSquareBytes = 4 * kTile * kDiag * 4;  // a tile of dS for each wave, beside the tiles of the dq kernel
+
+inline int padded_bias(const AttnShape& s) { return s.reach ? (2 * (int)s.reach + 1 + 2 * kBiasMargin + 3) / 4 * 4 : 0; }
+
+// Bytes of LDS of a workgroup that owns 32 * ow queries or keys of heads of DP.
+inline int bwd_lds(const AttnShape& s, int elem_bytes, int ow, bool queries) {
+    const int dp = head_width(s.D), tiles = bwd_tile_bytes(dp, elem_bytes, ow), bias = padded_bias(s) * 4;
+    const int values = bwd_values_in_lds(dp, elem_bytes) ? 4 * (dp / 16) * 64 * 16 : 0;
+    return tiles + bias + (queries ? kSquareBytes + 4 * bias : values + 6 * bwd_rows(dp, elem_bytes, ow) * 4);
+}
+
+// Frames a workgroup owns, in units of 32: as many as leave two workgroups for
+// each compute unit, if its LDS holds them (float [32,375,8x64], 750 workgroups
+// of 128: 252 us so, 377 us with 64; [3,333,4x50], 36 of 128: 148 us with 128
+// for both kernels, 82 us with 32).
+inline int owned(const AttnShape& s, int elem_bytes, bool queries) {
+    const int64_t pairs = s.B * (queries ? s.H : s.Hkv), frames = queries ? s.Tq : s.Tk, wide = 2 * kUnits;
+    int ow = pairs * ((frames + 127) / 128) >= wide ? 4 : pairs * ((frames + 63) / 64) >= kUnits ? 2 : 1;
+    while (ow < 4 && bwd_lds(s, elem_bytes, ow, queries) > kLdsBytes) ow *= 2;
+    return ow;
+}
+
+inline AttnForm bwd_form(int own, int64_t D, int elem_bytes, bool direct) {
+    const int dp = head_width(D);
+    return {dp, own, direct && bwd_buffers(dp, elem_bytes, own) == 2, false};
+}
+
+}  // namespace dw

@@ -39,8 +39,6 @@ struct AttnBwd : AttnArgs {
     int32_t nqb, nkb;
 };
 
-constexpr int kDiag = 64;  // row of the square in which the diagonals of a tile lie in columns
-
 // exp(S - lse) of a query that has keys; lse = -inf marks one that has none,
 // whose weights are zero.
 __device__ __forceinline__ float lse_or_inf(float lse) {
@@ -113,12 +111,9 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// Streamed frames of a tile, its buffers, and whether direct loads fill them.
-// float rows over 64 wide leave room for one buffer beside the sums by distance.
 template <typename S, int DP, int OW>
 struct BwdShape {
-    static constexpr int ROWS = OW == 1 ? 128 : OW == 2 || sizeof(S) * DP <= 128 ? 64 : 32;
-    static constexpr int kBuffers = OW == 1 || (OW == 2 && sizeof(S) == 4 && DP > 64) ? 1 : 2;
+    static constexpr int ROWS = bwd_rows(DP, sizeof(S), OW), kBuffers = bwd_buffers(DP, sizeof(S), OW);
     template <bool DMA>
     using Tiles = TilePair<S, DP, ROWS, kBuffers, DMA && kBuffers == 2>;
 };
@@ -394,11 +389,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_dtable(const float* __restr
     if (threadIdx.x == 0) dtable[(int64_t)bucket * H + h] = (float)(waves[0] + waves[1] + waves[2] + waves[3]);
 }
 
-// Wide bf16 heads leave no room for all of a wave's operands and sums in the
-// registers of two waves a SIMD: its values then wait in LDS, in the order in
-// which the lanes read them (16 bytes a lane).
 template <typename S, int DP>
-constexpr bool kValuesInLds = sizeof(S) == 2 && DP > 64;
+constexpr bool kValuesInLds = bwd_values_in_lds(DP, sizeof(S));
 template <typename S, int DP>
 constexpr int kValuesBytes = kValuesInLds<S, DP> ? 4 * (DP / 16) * 64 * 16 : 0;
 
@@ -572,32 +564,6 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) 
 // ---------------------------------------------------------------------------
 // Launch plan
 // ---------------------------------------------------------------------------
-constexpr int kLdsBytes = 160 * 1024;
-
-static int padded_bias(const AttnShape& s) { return s.reach ? (2 * (int)s.reach + 1 + 2 * kBiasMargin + 3) / 4 * 4 : 0; }
-
-// Bytes of LDS of a workgroup that owns 32 * ow queries or keys of heads of DP.
-static int bwd_lds(const AttnShape& s, int elem_bytes, int ow, bool queries) {
-    const int dp = (int)(s.D + 31) / 32 * 32 + (s.D == 0 ? 32 : 0);
-    const int rows = ow == 1 ? 128 : ow == 2 || elem_bytes * dp <= 128 ? 64 : 32;
-    const int buffers = ow == 1 || (ow == 2 && elem_bytes == 4 && dp > 64) ? 1 : 2;
-    const int tiles = 2 * buffers * rows * tile_slots(dp * elem_bytes / 16, elem_bytes) * 16, bias = padded_bias(s) * 4;
-    const int values = elem_bytes == 2 && dp > 64 ? 4 * (dp / 16) * 64 * 16 : 0;  // kValuesBytes
-    return tiles + bias + (queries ? 4 * kTile * kDiag * 4 + 4 * bias : values + 6 * rows * 4);
-}
-
-// Frames a workgroup owns, in units of 32: as many as leave two workgroups for
-// each compute unit, if its LDS holds them (float [32,375,8x64], 750 workgroups
-// of 128: 252 us so, 377 us with 64; [3,333,4x50], 36 of 128: 148 us with 128
-// for both kernels, 82 us with 32).
-static int owned(const AttnShape& s, int elem_bytes, bool queries) {
-    constexpr int64_t kUnits = 256;
-    const int64_t pairs = s.B * (queries ? s.H : s.Hkv), frames = queries ? s.Tq : s.Tk, wide = 2 * kUnits;
-    int ow = pairs * ((frames + 127) / 128) >= wide ? 4 : pairs * ((frames + 63) / 64) >= kUnits ? 2 : 1;
-    while (ow < 4 && bwd_lds(s, elem_bytes, ow, queries) > kLdsBytes) ow *= 2;
-    return ow;
-}
-
 static int64_t blocks_of(int64_t frames, int ow) { return (frames + ow * kTile - 1) / (ow * kTile); }
 
 static int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
@@ -620,17 +586,21 @@ size_t dwattn_bwd_workspace(const AttnShape& s, int elem_bytes) {
 
 template <typename S, int DP, int OW>
 static hipError_t launch_dq(const AttnBwd& a, int lds, hipStream_t stream) {
-    const bool dma = dma_fits<S>(a.k, a.ks, a.D) && dma_fits<S>(a.v, a.vs, a.D) && BwdShape<S, DP, OW>::kBuffers == 2;
-    hipLaunchKernelGGL((dma ? attn_dq_kernel<S, DP, OW, BwdShape<S, DP, OW>::kBuffers == 2> : attn_dq_kernel<S, DP, OW, false>),
+    constexpr bool kDirect = BwdShape<S, DP, OW>::kBuffers == 2;
+    const bool fits = direct_fits(a.k, a.ks, a.D, sizeof(S)) && direct_fits(a.v, a.vs, a.D, sizeof(S));
+    hipLaunchKernelGGL((bwd_form(OW, a.D, sizeof(S), fits).direct ? attn_dq_kernel<S, DP, OW, kDirect>
+                                                                  : attn_dq_kernel<S, DP, OW, false>),
                        dim3((uint32_t)(a.B * a.H) * a.nqb), dim3(kAttnThreads), lds, stream, a);
     return hipGetLastError();
 }
 
 template <typename S, int DP, int OW>
 static hipError_t launch_dkv(const AttnBwd& a, int lds, hipStream_t stream) {
+    constexpr bool kDirect = BwdShape<S, DP, OW>::kBuffers == 2;
     const AttnStride rows = {(int64_t)a.Tq * a.H * a.D, (int64_t)a.H * a.D, a.D};
-    const bool dma = dma_fits<S>(a.q, a.qs, a.D) && dma_fits<S>(a.dout, rows, a.D) && BwdShape<S, DP, OW>::kBuffers == 2;
-    hipLaunchKernelGGL((dma ? attn_dkv_kernel<S, DP, OW, BwdShape<S, DP, OW>::kBuffers == 2> : attn_dkv_kernel<S, DP, OW, false>),
+    const bool fits = direct_fits(a.q, a.qs, a.D, sizeof(S)) && direct_fits(a.dout, rows, a.D, sizeof(S));
+    hipLaunchKernelGGL((bwd_form(OW, a.D, sizeof(S), fits).direct ? attn_dkv_kernel<S, DP, OW, kDirect>
+                                                                  : attn_dkv_kernel<S, DP, OW, false>),
                        dim3((uint32_t)(a.B * a.Hkv) * a.nkb), dim3(kAttnThreads), lds, stream, a);
     return hipGetLastError();
 }
@@ -639,9 +609,11 @@ template <typename S, int DP>
 static hipError_t launch_bwd(const AttnBwd& a, const AttnShape& s, int oq, int ok, hipStream_t stream) {
     if (a.nqb > 0) {
         const int lds = bwd_lds(s, sizeof(S), oq, true);
+        // Tiles of 128 float keys of the widest heads leave no room for the square at all.
+        constexpr int kLeast = bwd_tile_bytes(DP, sizeof(S), 1) + kSquareBytes > kLdsBytes ? 2 : 1;
         const hipError_t e = oq == 4   ? launch_dq<S, DP, 4>(a, lds, stream)
                              : oq == 2 ? launch_dq<S, DP, 2>(a, lds, stream)
-                                       : launch_dq<S, DP, 1>(a, lds, stream);
+                                       : launch_dq<S, DP, kLeast>(a, lds, stream);
         if (e != hipSuccess) return e;
     }
     if (a.nkb > 0 && (a.dk || a.dv)) {

@@ -51,7 +51,7 @@ constexpr float kRides = 65536.0f;
 template <typename S, int DP, int QW, bool DMA>
 struct FwdShape {
     static constexpr int BN = QW == 1 ? 128 : QW == 2 || sizeof(S) * DP <= 128 ? 64 : 32;
-    static constexpr int kBuffers = QW == 1 && !(DMA && sizeof(S) * DP <= 128) ? 1 : 2;
+    static constexpr int kBuffers = QW == 1 && !DMA ? 1 : 2;
     static constexpr int kWaves = (QW == 1 && DP > 64) || (sizeof(S) == 4 && DP > 96) ? 1 : QW == 4 && DMA && sizeof(S) == 2 ? 3 : 2;
     using Tiles = TilePair<S, DP, BN, kBuffers, DMA>;
 };
@@ -339,53 +339,6 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnFwd a) {
 // ---------------------------------------------------------------------------
 // Launch plan
 // ---------------------------------------------------------------------------
-struct FwdPlan {
-    int qw, splits;
-    bool packed;
-    int64_t nqb;
-};
-
-// 128 queries a workgroup read each key tile once for four waves, so they are
-// taken where they make workgroups enough; next 64, whose two pairs of waves
-// divide the keys; and with the fewest queries 32, the keys then being split
-// over workgroups until each compute unit has one.  The plan goes by the sizes
-// alone (lengths are on the device).  Enough is three a compute unit, as many as
-// are resident (bf16 [16,750,8x128] takes 49 us so and 69 us with 64 queries,
-// float [32,750,8x64] 171 and 205 us); but eight for float under a causal mask,
-// whose last workgroups have the most keys and, with six products for one, set
-// the time (causal [8,1500,8x64], three a unit: 130 us with 128 queries, 124 us
-// with 64).  Twice as many splits cost the join more than they save (16 frames
-// over 20000 keys, 8 heads: 18 and 21 us).  The splits, and the workspace with
-// them, do not depend on the bias.
-constexpr int64_t kPackedBias = 16 * 1024;  // bytes of LDS for a group's biases beside the widest tiles
-
-static FwdPlan fwd_plan(const AttnShape& s, int elem_bytes) {
-    constexpr int64_t kUnits = 256;
-    const bool causal = s.left == kNoLimit && s.right != kNoLimit;
-    const int64_t wide = kUnits * (elem_bytes == 4 && causal ? 8 : 3);
-    FwdPlan p;
-    auto blocks_of = [&](int64_t queries) { return s.B * s.H * ((s.Tq + queries - 1) / queries); };
-    p.qw = s.Tq > 32 && blocks_of(128) >= wide ? 4 : s.Tq > 32 && blocks_of(64) >= kUnits ? 2 : 1;
-    const int64_t queries = 32 * p.qw;
-    p.nqb = (s.Tq + queries - 1) / queries;
-    p.splits = 1;
-    const int64_t group = s.Hkv ? s.H / s.Hkv : 1;
-    const bool could = p.qw == 1 && group > 1 && group * s.Tq <= kTile;
-    p.packed = could && group * (s.reach ? attn_bias_bytes((int)s.reach) : 0) <= kPackedBias;
-    if (p.qw == 1) {
-        int64_t span = s.Tk;
-        if (s.left < kNoLimit && s.right < kNoLimit) {
-            const int64_t window = s.left + s.right + queries;
-            span = window < 1 ? 1 : window < span ? window : span;
-        }
-        const int64_t blocks = could ? s.B * s.Hkv : blocks_of(32), tiles = (span + 127) / 128;
-        int64_t n = kUnits / (blocks ? blocks : 1);
-        n = n < tiles ? n : tiles;
-        p.splits = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
-    }
-    return p;
-}
-
 static int64_t part_floats(const AttnShape& s, int splits) {
     return splits > 1 ? splits * s.B * s.H * s.Tq * ((s.D + 3) / 4 * 4 + 2) : 0;
 }
@@ -417,18 +370,19 @@ static hipError_t launch_fwd(const AttnFwd& a, hipStream_t stream) {
 }
 
 template <typename S>
-static hipError_t fwd_of_type(const AttnFwd& a, int qw, bool packed, hipStream_t stream) {
-    const bool dma = dma_fits<S>(a.k, a.ks, a.D) && dma_fits<S>(a.v, a.vs, a.D);
+static hipError_t fwd_of_type(const AttnFwd& a, const FwdPlan& plan, hipStream_t stream) {
+    const bool direct = direct_fits(a.k, a.ks, a.D, sizeof(S)) && direct_fits(a.v, a.vs, a.D, sizeof(S));
+    const AttnForm f = fwd_form(plan, a.D, sizeof(S), direct);
     const hipError_t e = with_head_width(a.D, [&](auto dp) {
-        constexpr bool kNarrow = sizeof(S) * dp.value <= 128;  // two buffers of 128 keys leave room for two workgroups
-        return packed && dma && kNarrow ? launch_fwd<S, dp.value, 1, kNarrow, true>(a, stream)
-               : packed ? launch_fwd<S, dp.value, 1, false, true>(a, stream)
-               : qw == 1 && dma && kNarrow ? launch_fwd<S, dp.value, 1, kNarrow>(a, stream)
-               : qw == 1 ? launch_fwd<S, dp.value, 1, false>(a, stream)
-               : qw == 2 && dma ? launch_fwd<S, dp.value, 2, true>(a, stream)
-               : qw == 2 ? launch_fwd<S, dp.value, 2, false>(a, stream)
-               : dma ? launch_fwd<S, dp.value, 4, true>(a, stream)
-                     : launch_fwd<S, dp.value, 4, false>(a, stream);
+        constexpr bool kNarrow = fwd_narrow(dp.value, sizeof(S));
+        return f.packed && f.direct   ? launch_fwd<S, dp.value, 1, kNarrow, true>(a, stream)
+               : f.packed             ? launch_fwd<S, dp.value, 1, false, true>(a, stream)
+               : f.own == 1 && f.direct ? launch_fwd<S, dp.value, 1, kNarrow>(a, stream)
+               : f.own == 1           ? launch_fwd<S, dp.value, 1, false>(a, stream)
+               : f.own == 2 && f.direct ? launch_fwd<S, dp.value, 2, true>(a, stream)
+               : f.own == 2           ? launch_fwd<S, dp.value, 2, false>(a, stream)
+               : f.direct             ? launch_fwd<S, dp.value, 4, true>(a, stream)
+                                      : launch_fwd<S, dp.value, 4, false>(a, stream);
     });
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t threads = (int64_t)a.B * a.H * a.Tq * ((a.D + 3) / 4);
@@ -447,8 +401,7 @@ hipError_t launch_dwattn_fwd(const AttnPtrs& p, const AttnShape& s, void* out, f
     a.part = (float*)workspace;
     a.splits = plan.splits;
     a.nqb = (int32_t)plan.nqb;
-    return bf16 ? fwd_of_type<uint16_t>(a, plan.qw, plan.packed, stream)
-                : fwd_of_type<float>(a, plan.qw, plan.packed, stream);
+    return bf16 ? fwd_of_type<uint16_t>(a, plan, stream) : fwd_of_type<float>(a, plan, stream);
 }
 
 }  // namespace dw

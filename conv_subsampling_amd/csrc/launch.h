@@ -9,6 +9,8 @@
 
 #include <initializer_list>
 
+#include "attn_plan.h"
+
 namespace dw {
 
 // Every extent the C ABI passes to these launchers (B, T, F, C, K) is below
@@ -145,25 +147,9 @@ hipError_t launch_dwdrop(const void* x, const void* residual, void* y, const uin
                          double p, float alpha, bool bf16, hipStream_t stream);
 
 // Attention with a bucketed relative position bias.
-struct AttnStride {
-    int64_t item, frame, head;  // in elements
-};
-
-constexpr int32_t kNoLimit = 1 << 30;        // a context without a limit
-constexpr int64_t kAttnMaxFrames = 1 << 28;  // sums of frames and positions stay in 32 bits
-constexpr int64_t kAttnMaxHead = 128;        // what a wave's accumulators hold
-constexpr int64_t kAttnMaxReach = 1024;      // of the bias map: what LDS holds beside the tiles
-
 struct AttnPtrs {
     const void *q, *k, *v, *table;
     const int32_t *buckets, *q_lengths, *k_lengths, *q_pos;
-};
-
-struct AttnShape {
-    int64_t B, Tq, Tk, H, Hkv, D;
-    AttnStride q, k, v, dq, dk, dv;
-    int64_t buckets, reach, left, right;  // left, right: at most kNoLimit
-    float scale;
 };
 
 bool dwattn_fits(const AttnShape& s);  // of both directions
