@@ -130,14 +130,20 @@ __device__ __forceinline__ Frag<float> split(const float (&v)[8]) {
 }
 
 // Stands between a run of products and the first arithmetic on their sums: the
-// wait states that the last product's result asks for before a vector
-// instruction may read it (8 passes + 4).  The compiler inserts them too, but
-// where the sums sat in accumulation registers and the reads behind a branch it
-// was found to leave too few, and the last register lacked the last product.
-__device__ __forceinline__ void products_done() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_nop 11");
-    __builtin_amdgcn_sched_barrier(0);
+// wait states that a vector instruction has to keep from the product whose
+// result it reads (8 passes + 4).  The compiler counts them too, but where two
+// paths of different length lead from the products to a read it was seen to go by
+// the longer one (7 states on the other, gfx950 at -O3).  The sums pass through
+// the wait, because products, which have no other effect, else move past it.
+__device__ __forceinline__ void products_done(f32x16& a) { asm volatile("s_nop 11" : "+v"(a)); }
+__device__ __forceinline__ void products_done(f32x16& a, f32x16& b) { asm volatile("s_nop 11" : "+v"(a), "+v"(b)); }
+template <int N>
+__device__ __forceinline__ void products_done(f32x16 (&a)[N]) {
+    static_assert(N <= 4, "runs of 32 head elements");
+    if constexpr (N == 1) products_done(a[0]);
+    if constexpr (N == 2) products_done(a[0], a[1]);
+    if constexpr (N == 3) asm volatile("s_nop 11" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]));
+    if constexpr (N == 4) asm volatile("s_nop 11" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
 }
 
 // Accumulator registers 8k .. 8k + 7 as the operand of the next product,

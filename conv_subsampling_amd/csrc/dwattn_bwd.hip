@@ -72,8 +72,12 @@ __device__ __forceinline__ void heavy_row(const AttnArgs& a, const AttnItem& ite
         for (int c = 0; c < DP / 16; ++c)
             mma_apart(to_frag<S>(load_group<S, true>(keys + (int64_t)min(at, last) * a.ks.frame, 16 * c + 8 * half,
                                                      at <= last ? a.D : 0)), q[c], s, s_small);
-        products_done();
-        if constexpr (sizeof(S) == 4) s += s_small;
+        if constexpr (sizeof(S) == 4) {
+            products_done(s, s_small);
+            s += s_small;
+        } else {
+            products_done(s);
+        }
         float m = top;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
@@ -252,15 +256,25 @@ __global__ __launch_bounds__(kAttnThreads, ((sizeof(S) == 4 && !DMA) || (DP > 64
             const int row0 = (wk * KT + u) * kTile, j = jt + row0;
             if (j > some1 || j + kTile <= some0) continue;
             f32x16 s = {}, ds = {}, s_small = {}, ds_small = {};
+            // float's widest heads take one sum after the other: four at once leave no registers ([8,375,8x128] 124 us
+            // so and 137 us side by side, [16,375,8x64] 109 and 105)
+            constexpr bool kInTurn = sizeof(S) == 4 && DP > 64;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 mma_apart(T::rows(ktile, row0, c, lane), q[c], s, s_small);
-                mma_apart(T::rows(vtile, row0, c, lane), g[c], ds, ds_small);
+                if (!kInTurn) mma_apart(T::rows(vtile, row0, c, lane), g[c], ds, ds_small);
             }
-            products_done();
             if constexpr (sizeof(S) == 4) {
+                products_done(s, s_small);
                 s += s_small;
+                if constexpr (kInTurn) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) mma_apart(T::rows(vtile, row0, c, lane), g[c], ds, ds_small);
+                }
+                products_done(ds, ds_small);
                 ds += ds_small;
+            } else {
+                products_done(s, ds);
             }
             const int base = j - iw - item.pos32;
             const Span span = span_of(base, a.R);
@@ -314,7 +328,7 @@ __global__ __launch_bounds__(kAttnThreads, ((sizeof(S) == 4 && !DMA) || (DP > 64
         }
         kv.leave(t, t + 1 < tiles);
     }
-    products_done();
+    products_done(acc);
     if (a.dq) {
         add_waves<OW, ND>(smem, acc, lane, wave);
         if (i < a.Tq)
@@ -495,7 +509,7 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) 
                     ds = mma(T::rows(gtile, row0, c, lane), value(c), ds);
                     if (kValuesInLds<S, DP> && c % 2) __builtin_amdgcn_sched_barrier(0);
                 }
-                products_done();
+                products_done(s, ds);
                 // distance of the tile's first key and first query; along the registers it falls
                 const int base = jw - i - item.pos32;
                 const Span span = span_of(base, a.R);
@@ -545,7 +559,8 @@ __global__ __launch_bounds__(kAttnThreads, (sizeof(S) == 4 || (!DMA && DP > 32) 
             qg.leave(t, t + 1 < tiles);
         }
     }
-    products_done();
+    products_done(dk);
+    products_done(dv);
     const bool out = j < a.Tk;
     if (a.dk) {
         add_waves<OW, ND>(smem, dk, lane, wave);

@@ -151,7 +151,7 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
 #pragma unroll
                 for (int d = 0; d < ND; ++d) v[d] = T::columns(vt, row0, d, lane);
             }
-            products_done();
+            products_done(s);
             const int base = j - iw - item.pos32;
             const Span span = span_of(base, a.R);
             const bool edge = j < all0 || j + kTile - 1 > all1;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(kAttnThreads, (FwdShape<S, DP, QW, DMA>::kWaves)) v
         }
         kv.leave(t, t + 1 < t1 - t0);
     }
-    products_done();
+    products_done(o);
     sum += swap_halves(sum);
 
     // Join the waves that share queries: wave wk of them takes every KW-th run
