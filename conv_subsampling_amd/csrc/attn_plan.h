@@ -61,22 +61,35 @@ struct FwdPlan {
 // taken where they make workgroups enough; next 64, whose two pairs of waves
 // divide the keys; and with the fewest queries 32, the keys then being split
 // over workgroups until each compute unit has one.  The plan goes by the sizes
-// alone (lengths are on the device).  Enough is three a compute unit, as many as
-// are resident (bf16 [16,750,8x128] takes 49 us so and 69 us with 64 queries,
-// float [32,750,8x64] 171 and 205 us); but eight for float under a causal mask,
-// whose last workgroups have the most keys and, with six products for one, set
-// the time (causal [8,1500,8x64], three a unit: 130 us with 128 queries, 124 us
-// with 64).  Twice as many splits cost the join more than they save (16 frames
-// over 20000 keys, 8 heads: 18 and 21 us).  The splits, and the workspace with
-// them, do not depend on the bias.
+// alone (lengths are on the device).
+//
+// From 128 queries to 64, measured over the batch, lengths from the whole to
+// half: the times cross at 290 to 380 workgroups of 128 (bf16 [B,750,8x128],
+// 128 and 64 queries: B = 6 33 and 29 us, 8 36 and 41, 15 44 and 63), 380 to 430
+// ([B,375,8x64]: B = 16 16.8 and 16.3, 24 20 and 25) and 430 to 480
+// ([B,750,8x50]), for float at 290 to 380 ([B,750,8x64]: B = 6 62 and 45, 8 66 and
+// 67, 16 97 and 110), and for its widest heads they lie within 8% of each other from
+// 170 to 400; so from 1.5 a compute unit on.  Under a causal mask, whose last
+// workgroups have the most keys, they cross at 1000 (bf16 [B,1500,4x64]: B = 16
+// 37 and 35, 24 40 and 47), 1100 (float [B,1500,8x64]: B = 9 137 and 113, 12 134 and
+// 154) and, of three blocks an item, 580 and 700 ([B,300,8x64]): from 4 a unit on.
+//
+// From 64 queries to 32: of heads over 64, of which a unit takes one workgroup of
+// 32, at 100 to 150 workgroups of 64 (bf16 [B,750,8x128], 64 and 32 queries: B = 1
+// 19 and 19, 2 20 and 35; float [B,375,8x128]: B = 2 33 and 30, 3 33 and 33, 5 34 and
+// 63); of narrower ones at about 250 (bf16 [B,750,8x64]: B = 2 16 and 14, 3 16 and 16).
+//
+// Twice as many splits cost the join more than they save (16 frames over 20000
+// keys, 8 heads: 18 and 21 us).  The splits, and the workspace with them, do not
+// depend on the bias.
 constexpr int64_t kPackedBias = 16 * 1024;  // bytes of LDS for a group's biases beside the widest tiles
 
-inline FwdPlan fwd_plan(const AttnShape& s, int elem_bytes) {
+inline FwdPlan fwd_plan(const AttnShape& s) {
     const bool causal = s.left == kNoLimit && s.right != kNoLimit;
-    const int64_t wide = kUnits * (elem_bytes == 4 && causal ? 8 : 3);
+    const int64_t for4 = causal ? 4 * kUnits : kUnits * 3 / 2, for2 = s.D > 64 ? kUnits / 2 : kUnits;
     FwdPlan p;
     auto blocks_of = [&](int64_t queries) { return s.B * s.H * ((s.Tq + queries - 1) / queries); };
-    p.qw = s.Tq > 32 && blocks_of(128) >= wide ? 4 : s.Tq > 32 && blocks_of(64) >= kUnits ? 2 : 1;
+    p.qw = s.Tq > 32 && blocks_of(128) >= for4 ? 4 : s.Tq > 32 && blocks_of(64) >= for2 ? 2 : 1;
     const int64_t queries = 32 * p.qw;
     p.nqb = (s.Tq + queries - 1) / queries;
     p.splits = 1;

@@ -538,8 +538,7 @@ dw_status dwattn_rel_buckets(int32_t* map, int64_t buckets, int64_t reach, int b
 size_t dwattn_fwd_workspace_bytes(const dw_attn* shape) {
     dw::AttnShape s;
     if (check_attn("dwattn_fwd_workspace_bytes", shape, false, &s) != DW_OK) return 0;
-    const int elem = shape->dtype == DW_BF16 ? 2 : 4;
-    return dw::dwattn_fwd_fits(s, elem) ? dw::dwattn_fwd_workspace(s, elem) : 0;
+    return dw::dwattn_fwd_fits(s) ? dw::dwattn_fwd_workspace(s) : 0;
 }
 
 dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const void* v, const void* table,
@@ -551,11 +550,11 @@ dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const v
     const dw_status c = check_attn(fn, shape, table != nullptr, &s);
     if (c != DW_OK) return c;
     if (!nonempty(s.B, s.Tq, s.H, s.D)) return ok();
-    if (!dw::dwattn_fwd_fits(s, shape->dtype == DW_BF16 ? 2 : 4)) return too_large(fn);
+    if (!dw::dwattn_fwd_fits(s)) return too_large(fn);
     if (!q || !out || (s.Tk > 0 && (!k || !v)))
         return fail(DW_ERR_INVALID_ARG, "%s: q, k, v and out must not be NULL (unless empty)", fn);
     if (out == q || out == k || out == v) return fail(DW_ERR_INVALID_ARG, "%s: out must not alias an input", fn);
-    const size_t need = dw::dwattn_fwd_workspace(s, shape->dtype == DW_BF16 ? 2 : 4);
+    const size_t need = dw::dwattn_fwd_workspace(s);
     if (need && (!workspace || workspace_bytes < need))
         return fail(DW_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
                     workspace ? workspace_bytes : (size_t)0, need);

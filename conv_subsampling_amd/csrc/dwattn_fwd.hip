@@ -343,8 +343,8 @@ static int64_t part_floats(const AttnShape& s, int splits) {
     return splits > 1 ? splits * s.B * s.H * s.Tq * ((s.D + 3) / 4 * 4 + 2) : 0;
 }
 
-size_t dwattn_fwd_workspace(const AttnShape& s, int elem_bytes) {
-    return (size_t)part_floats(s, fwd_plan(s, elem_bytes).splits) * sizeof(float);
+size_t dwattn_fwd_workspace(const AttnShape& s) {
+    return (size_t)part_floats(s, fwd_plan(s).splits) * sizeof(float);
 }
 
 bool dwattn_fits(const AttnShape& s) {
@@ -354,8 +354,8 @@ bool dwattn_fits(const AttnShape& s) {
            product_below(kMaxExtent, {s.B, s.H, s.Tq});
 }
 
-bool dwattn_fwd_fits(const AttnShape& s, int elem_bytes) {
-    const FwdPlan p = fwd_plan(s, elem_bytes);
+bool dwattn_fwd_fits(const AttnShape& s) {
+    const FwdPlan p = fwd_plan(s);
     // splits are for a few hundred workgroups of at most 32 queries, so the join's threads are few
     return grid_of_256_fits(s.B * (p.packed ? s.Hkv : s.H) * p.nqb * p.splits);
 }
@@ -393,7 +393,7 @@ static hipError_t fwd_of_type(const AttnFwd& a, const FwdPlan& plan, hipStream_t
 
 hipError_t launch_dwattn_fwd(const AttnPtrs& p, const AttnShape& s, void* out, float* lse, void* workspace, bool bf16,
                              hipStream_t stream) {
-    const FwdPlan plan = fwd_plan(s, bf16 ? 2 : 4);
+    const FwdPlan plan = fwd_plan(s);
     AttnFwd a;
     (AttnArgs&)a = attn_args(p, s);
     a.out = out;

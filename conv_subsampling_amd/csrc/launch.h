@@ -153,8 +153,8 @@ struct AttnPtrs {
 };
 
 bool dwattn_fits(const AttnShape& s);  // of both directions
-bool dwattn_fwd_fits(const AttnShape& s, int elem_bytes);  // beyond dwattn_fits
-size_t dwattn_fwd_workspace(const AttnShape& s, int elem_bytes);
+bool dwattn_fwd_fits(const AttnShape& s);  // beyond dwattn_fits
+size_t dwattn_fwd_workspace(const AttnShape& s);
 hipError_t launch_dwattn_fwd(const AttnPtrs& p, const AttnShape& s, void* out, float* lse, void* workspace, bool bf16,
                              hipStream_t stream);
 

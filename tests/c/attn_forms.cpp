@@ -28,7 +28,7 @@ int main() {
         const int e = (int)elem;
         const bool keys = direct_fits(nullptr, stride(Tk, Hkv, pad), D, e);
         const bool queries = direct_fits(nullptr, stride(Tq, H, pad), D, e) && direct_fits(nullptr, stride(Tq, H, 0), D, e);
-        print("attn_fwd_kernel", e, fwd_form(fwd_plan(s, e), D, e, keys), true);
+        print("attn_fwd_kernel", e, fwd_form(fwd_plan(s), D, e, keys), true);
         print("attn_dq_kernel", e, bwd_form(owned(s, e, true), D, e, keys), false);
         print("attn_dkv_kernel", e, bwd_form(owned(s, e, false), D, e, queries), false);
         printf("\n");
