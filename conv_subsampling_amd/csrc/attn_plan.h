@@ -147,13 +147,24 @@ inline int bwd_lds(const AttnShape& s, int elem_bytes, int ow, bool queries) {
     return tiles + bias + (queries ? kSquareBytes + 4 * bias : values + 6 * bwd_rows(dp, elem_bytes, ow) * 4);
 }
 
-// Frames a workgroup owns, in units of 32: as many as leave two workgroups for
-// each compute unit, if its LDS holds them (float [32,375,8x64], 750 workgroups
-// of 128: 252 us so, 377 us with 64; [3,333,4x50], 36 of 128: 148 us with 128
-// for both kernels, 82 us with 32).
+// Frames a workgroup owns, in units of 32: fewer where more would leave compute
+// units without one, if LDS holds the tiles.  dq, then dk/dv, in us over the batch:
+//   128 and 64 frames  bf16 [B,750,8x128]    B = 2 51, 38; 55, 35    4 52, 63; 56, 55    8 58, 93; 60, 81
+//                      bf16 [B,375,8x64]     B = 8 30, 29; 20, 16   12 32, 44; 21, 25
+//                      float [B,375,8x64]    B = 6 56, 46; 57, 35    8 56, 67; 57, 58   16 65, 104; 86, 91
+//                      float [B,375,8x128]   B = 6 97, 75; 97, 82    8 97, 122; 97, 141
+//                      bf16 causal [B,1000,8x64]  B = 6 48, 48; 40, 32  8 50, 55; 40, 39  12 61, 78; 51, 55
+//   64 and 32 frames   bf16 [B,750,8x128]    B = 2 38, 67; 35, 52
+//                      bf16 [B,375,8x64]     B = 2 26, 23; 14, 14    4 25, 26; 14, 25
+//                      float [B,375,8x64]    B = 2 39, 35; 35, 26    4 39, 61; 35, 47
+// The first cross at 150 to 200 workgroups of 128, of bf16 heads up to 64, whose
+// workgroups of 64 a unit holds more of, at 270, and at up to twice that under a
+// causal mask; the second between 96 and 192 workgroups of 64.
 inline int owned(const AttnShape& s, int elem_bytes, bool queries) {
-    const int64_t pairs = s.B * (queries ? s.H : s.Hkv), frames = queries ? s.Tq : s.Tk, wide = 2 * kUnits;
-    int ow = pairs * ((frames + 127) / 128) >= wide ? 4 : pairs * ((frames + 63) / 64) >= kUnits ? 2 : 1;
+    const int64_t pairs = s.B * (queries ? s.H : s.Hkv), frames = queries ? s.Tq : s.Tk;
+    const bool narrow = elem_bytes == 2 && s.D <= 64, one_sided = (s.left == kNoLimit) != (s.right == kNoLimit);
+    const int64_t for4 = (narrow ? kUnits : kUnits * 3 / 4) * (one_sided ? 2 : 1), for2 = kUnits / 2;
+    int ow = pairs * ((frames + 127) / 128) >= for4 ? 4 : pairs * ((frames + 63) / 64) >= for2 ? 2 : 1;
     while (ow < 4 && bwd_lds(s, elem_bytes, ow, queries) > kLdsBytes) ow *= 2;
     return ow;
 }

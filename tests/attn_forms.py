@@ -5,7 +5,7 @@ groups of 8 elements and without; lengths, windows, positions, biases and shared
 key heads in turn."""
 
 # (owned frames in units of 32, B, H, Hkv, frames)
-SIZES = [(4, 50, 16, 8, 140), (2, 11, 16, 8, 140), (1, 3, 4, 2, 140)]
+SIZES = [(4, 50, 16, 8, 140), (2, 23, 4, 2, 140), (1, 3, 4, 2, 140)]
 HEADS = [32, 24, 20, 64, 40, 50, 96, 72, 90, 128, 104, 127]
 
 
