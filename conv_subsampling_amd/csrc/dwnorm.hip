@@ -169,9 +169,12 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormFwd a)
     }
 }
 
-// At most kNormBwdBlocks workgroups take the rows in turn: 256 leave memory
-// waiting (29 us for [16,750,1024] bf16), 768 take 22.8 and 1024 take 23.8 where
-// 512 take 23.2, and write more partial sums; a row loaded ahead, 23.2.
+// At most kNormBwdBlocks workgroups take the rows in turn.  256, 512, 768, 1024
+// and 2048 of them, with the sums of their partials, us from cold memory: bf16
+// [16,750,1024] 41 39 39 42 44, [32,1500,512] 92 68 65 68 74, [8,1500,256] 21 19 18 19
+// 23, [16,750,2048] 72 72 74 74 79, [16,750,4096] 117 120 123 135 149; float
+// [16,750,1024] 70 69 69 72 75, [4,1500,4096] 120 122 129 135 147.  Fewer leave memory
+// waiting, more write more partial sums.  A row loaded ahead gained nothing.
 // One workgroup takes rows first, first + stride, ...; each lane keeps the
 // weight gradients of its own columns in fp32 registers over them (a few tens
 // of rows), the workgroup adds its waves in order and writes one partial row,
