@@ -594,9 +594,17 @@ bool dwattn_bwd_fits(const AttnShape& s, int elem_bytes) {
                             grid_of_256_fits(s.buckets * s.H));
 }
 
+// Enough for any context: one limited on one side may own fewer queries a workgroup.
 size_t dwattn_bwd_workspace(const AttnShape& s, int elem_bytes) {
-    const int64_t parts = s.B * blocks_of(s.Tq, owned(s, elem_bytes, true));
-    return (size_t)(stat_bytes(s) + (s.reach ? s.H * parts * (2 * s.reach + 1) * (int64_t)sizeof(float) : 0));
+    AttnShape all = s, causal = s;
+    all.left = all.right = causal.left = kNoLimit;
+    causal.right = 0;
+    int64_t blocks = 0;
+    for (const AttnShape& c : {all, causal}) {
+        const int64_t n = blocks_of(s.Tq, owned(c, elem_bytes, true));
+        blocks = n > blocks ? n : blocks;
+    }
+    return (size_t)(stat_bytes(s) + (s.reach ? s.H * s.B * blocks * (2 * s.reach + 1) * (int64_t)sizeof(float) : 0));
 }
 
 template <typename S, int DP, int OW>

@@ -225,3 +225,12 @@ def test_more_workgroups_than_a_launch_takes_are_refused(alib):
             assert alib.dwattn_fwd_workspace_bytes(shape) == 0 and alib.dwattn_bwd_workspace_bytes(shape) == 0
     assert alib.dwattn_bwd(attn(buckets=1 << 23), X[0], X[1], X[2], X[3], X[4], N, N, N, X[5], X[6], X[7], X[8], X[9], X[10],
                            P, W, 1 << 40, N) == UNSUPPORTED
+
+
+def test_backward_workspace_holds_for_any_context(alib):
+    """The binding asks for it without the call's context limits."""
+    for B, H, T in ((4, 4, 1000), (10, 8, 375), (3, 4, 333), (24, 8, 750), (30, 8, 100)):
+        for D, dtype in ((64, 1), (128, 1), (64, 0), (128, 0)):
+            sizes = {alib.dwattn_bwd_workspace_bytes(attn(B=B, H=H, Hkv=H, Tq=T, Tk=T, D=D, dtype=dtype, left=left, right=right))
+                     for left, right in ((-1, -1), (-1, 0), (100, -1), (30, 30))}
+            assert len(sizes) == 1 and sizes.pop() > 0

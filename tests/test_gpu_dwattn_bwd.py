@@ -342,3 +342,15 @@ def test_rows_of_a_large_bias(dt):
     s = make(2, 170, 170, 2, 2, 64, dt, NB=8, reach=20, q_len=[170, 99], k_len=[170, 99])
     s["table"][:] = -2000.0
     check_by_weights(s, absorbed=1e8, rel=4e-4)
+
+
+def test_a_workspace_asked_for_without_the_context_serves_a_causal_call():
+    s = make(10, 375, 375, 4, 4, 32, BF16, left=-1, right=0)
+    out, lse = call(s)
+    n = lib().dwattn_bwd_workspace_bytes(s["q"], s["k"], s["v"], s["table"], s["buckets"])
+    ws = Guarded((n,), torch.uint8, DEV, G=4096)
+    got = grads(s, out, lse, workspace=ws.t)
+    torch.cuda.synchronize()
+    ws.check("workspace")
+    for a, b in zip(got, grads(s, out, lse)):
+        assert torch.equal(a, b)
