@@ -585,7 +585,10 @@ size_t dwattn_fwd_workspace_bytes(const dw_attn *shape);
  * positions: int32 [B] or NULL (full lengths, position 0); lengths are clamped
  * to the tensors.  lse may be NULL.
  * Scores, softmax and sums are float32.  DW_BF16 rounds the weights p to bf16
- * for their product with v (their sum is taken before), and out once.
+ * for their product with v (their sum is taken before), and out once.  DW_F32
+ * multiplies on bf16 matrix instructions too, each operand as three parts that
+ * add up to it: what is left out of a product is at most 2^-22 of it, and an
+ * infinite operand gives NaN.
  * Repeated calls agree bit for bit.
  * Errors: DW_ERR_INVALID_ARG for a null pointer that holds elements, a negative
  * size or stride, a scale that is not positive, H not a multiple of Hkv, a table without a map or the other
@@ -620,7 +623,7 @@ size_t dwattn_bwd_workspace_bytes(const dw_attn *shape);
  * Each may be NULL (not computed).  An empty batch still writes dtable = 0.
  * Scores, P, delta and all sums are float32 (dtable's across workgroups fp64);
  * DW_BF16 rounds P and dS to bf16 for their products with dout, q and k, but
- * not for dtable.  No atomics: repeated calls agree bit for bit.
+ * not for dtable; DW_F32 multiplies as in dwattn_fwd.  No atomics: repeated calls agree bit for bit.
  * Errors: as dwattn_fwd; DW_ERR_INVALID_ARG also for a dtable without a table,
  * a null lse or dout that holds elements, or an output aliasing an input.
  */
