@@ -123,6 +123,11 @@ bool strides_fit(const dw_strides& s, int64_t n, int64_t t, int64_t h) {
            dw::product_below(far, {h, s.head});
 }
 
+// A table without a map or the other way round; the table of no heads may be NULL.
+bool half_a_bias(const dw_attn* a, const void* table, const int32_t* map) {
+    return !table != !map && (table || !a || a->H != 0);
+}
+
 // The problem as the launchers take it.
 dw_status check_attn(const char* fn, const dw_attn* a, bool bias, dw::AttnShape* s) {
     if (!a) return fail(DW_ERR_INVALID_ARG, "%s: shape must not be NULL", fn);
@@ -545,7 +550,7 @@ dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const v
                      const int32_t* map, const int32_t* q_lengths, const int32_t* k_lengths, const int32_t* q_pos,
                      void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
     const char* fn = "dwattn_fwd";
-    if (!table != !map) return fail(DW_ERR_INVALID_ARG, "%s: a bias needs both its table and its map", fn);
+    if (half_a_bias(shape, table, map)) return fail(DW_ERR_INVALID_ARG, "%s: a bias needs both its table and its map", fn);
     dw::AttnShape s;
     const dw_status c = check_attn(fn, shape, table != nullptr, &s);
     if (c != DW_OK) return c;
@@ -574,7 +579,7 @@ dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const v
                      const void* out, const float* lse, const void* dout, void* dq, void* dk, void* dv, float* dtable,
                      void* workspace, size_t workspace_bytes, void* stream) {
     const char* fn = "dwattn_bwd";
-    if (!table != !map) return fail(DW_ERR_INVALID_ARG, "%s: a bias needs both its table and its map", fn);
+    if (half_a_bias(shape, table, map)) return fail(DW_ERR_INVALID_ARG, "%s: a bias needs both its table and its map", fn);
     if (dtable && !table) return fail(DW_ERR_INVALID_ARG, "%s: dtable needs a table", fn);
     dw::AttnShape s;
     const dw_status c = check_attn(fn, shape, table != nullptr, &s);
@@ -584,11 +589,11 @@ dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const v
     if (!dw::dwattn_bwd_fits(s, shape->dtype == DW_BF16 ? 2 : 4) || (dq && !strides_fit(shape->dq, s.B, s.Tq, s.H)) || (dk && !strides_fit(shape->dk, s.B, s.Tk, s.Hkv)) ||
         (dv && !strides_fit(shape->dv, s.B, s.Tk, s.Hkv)))
         return too_large(fn);
-    if ((!dq && !dk && !dv && !dtable) || s.H == 0) return ok();
+    if ((!dq && !dk && !dv && !dtable) || (s.H == 0 && (s.Hkv == 0 || (!dk && !dv)))) return ok();
     if (!dtable && (s.B == 0 || s.D == 0)) return ok();
-    if (nonempty(s.B, s.Tq) && (!lse || (s.D > 0 && (!q || !out || !dout))))
+    if (nonempty(s.B, s.Tq, s.H) && (!lse || (s.D > 0 && (!q || !out || !dout))))
         return fail(DW_ERR_INVALID_ARG, "%s: q, out, lse and dout must not be NULL (unless empty)", fn);
-    if (nonempty(s.B, s.Tk, s.D) && (!k || !v))
+    if (nonempty(s.B, s.Tk, s.Hkv, s.D) && (!k || !v))
         return fail(DW_ERR_INVALID_ARG, "%s: k and v must not be NULL (unless empty)", fn);
     for (const void* o : {(const void*)dq, (const void*)dk, (const void*)dv})
         if (o && (o == q || o == k || o == v || o == out || o == dout))

@@ -630,7 +630,7 @@ static hipError_t launch_dkv(const AttnBwd& a, int lds, hipStream_t stream) {
 
 template <typename S, int DP>
 static hipError_t launch_bwd(const AttnBwd& a, const AttnShape& s, int oq, int ok, hipStream_t stream) {
-    if (a.nqb > 0) {
+    if (a.nqb > 0 && a.H > 0) {
         const int lds = bwd_lds(s, sizeof(S), oq, true);
         // Tiles of 128 float keys of the widest heads leave no room for the square at all.
         constexpr int kLeast = bwd_tile_bytes(DP, sizeof(S), 1) + kSquareBytes > kLdsBytes ? 2 : 1;
@@ -668,7 +668,7 @@ hipError_t launch_dwattn_bwd(const AttnPtrs& p, const AttnShape& s, const void* 
         });
         if (e != hipSuccess) return e;
     }
-    if (!dtable) return hipSuccess;
+    if (!dtable || s.H == 0) return hipSuccess;
     hipLaunchKernelGGL(attn_dtable, dim3(a.NB * a.H), dim3(kAttnThreads), 0, stream, a.dist, p.buckets, dtable, 2 * a.R + 1,
                        (int32_t)(s.B * a.nqb), a.NB, a.H);
     return hipGetLastError();

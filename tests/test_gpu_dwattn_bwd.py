@@ -354,3 +354,15 @@ def test_a_workspace_asked_for_without_the_context_serves_a_causal_call():
     ws.check("workspace")
     for a, b in zip(got, grads(s, out, lse)):
         assert torch.equal(a, b)
+
+
+@DT
+def test_key_heads_that_no_query_head_reads_get_zero_gradients(dt):
+    k = datagen.normal((2, 40, 2, 32), 1.0, "lone/k", device=DEV).to(dt)
+    q = torch.empty((2, 30, 0, 32), dtype=dt, device=DEV)
+    table, buckets = torch.empty((16, 0), dtype=dt, device=DEV), lib().rel_buckets(16, 40, device=DEV)
+    out, lse = lib().dwattn_fwd(q, k, k, table, buckets)
+    dk, dv = (torch.full_like(k, float("nan")) for _ in range(2))
+    dq, dk, dv, dt_ = lib().dwattn_bwd(q, k, k, out, lse, out, table, buckets, dk=dk, dv=dv)
+    torch.cuda.synchronize()
+    assert dq.shape == q.shape and dt_.shape == (16, 0) and not dk.any() and not dv.any()
