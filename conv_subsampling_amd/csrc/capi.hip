@@ -91,6 +91,16 @@ dw_status check_dropout(const char* fn, double p, const uint64_t* rng) {
     return DW_OK;
 }
 
+// The block operators' workspaces: large enough, and aligned for their vector
+// and direct loads.
+dw_status check_workspace(const char* fn, const void* workspace, size_t bytes, size_t need) {
+    if (need && (!workspace || bytes < need))
+        return fail(DW_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn, workspace ? bytes : (size_t)0, need);
+    if (need && (uintptr_t)workspace % 16 != 0)
+        return fail(DW_ERR_INVALID_ARG, "%s: the workspace must start on a multiple of 16 bytes", fn);
+    return DW_OK;
+}
+
 dw_status check_norm_sizes(const char* fn, int64_t B, int64_t T, int64_t C) {
     if (B < 0 || T < 0 || C < 0) return fail(DW_ERR_INVALID_ARG, "%s: negative size", fn);
     if (!dw::dwnorm_width_supported(C))
@@ -509,10 +519,8 @@ dw_status dwnorm_bwd(const void* sum, const void* gamma, const int32_t* lengths,
         return fail(DW_ERR_INVALID_ARG, "%s: sum, mean, rstd and dy must not be NULL (unless empty)", fn);
     if (dx && dx == dres) return fail(DW_ERR_INVALID_ARG, "%s: dx must not alias dres", fn);
     if (params) {
-        const size_t need = dw::dwnorm_bwd_workspace(B, T, C);
-        if (need && (!workspace || workspace_bytes < need))
-            return fail(DW_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
-                        workspace ? workspace_bytes : (size_t)0, need);
+        const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwnorm_bwd_workspace(B, T, C));
+        if (w != DW_OK) return w;
     }
     return from_hip(dw::launch_dwnorm_bwd(sum, gamma, lengths, mean, rstd, dy, dsum, p > 0.0 ? rng : nullptr, dx, dres,
                                           dgamma, dbeta, workspace, B, T, C, alpha, p, dtype == DW_BF16,
@@ -559,10 +567,8 @@ dw_status dwattn_fwd(const dw_attn* shape, const void* q, const void* k, const v
     if (!q || !out || (s.Tk > 0 && (!k || !v)))
         return fail(DW_ERR_INVALID_ARG, "%s: q, k, v and out must not be NULL (unless empty)", fn);
     if (out == q || out == k || out == v) return fail(DW_ERR_INVALID_ARG, "%s: out must not alias an input", fn);
-    const size_t need = dw::dwattn_fwd_workspace(s);
-    if (need && (!workspace || workspace_bytes < need))
-        return fail(DW_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
-                    workspace ? workspace_bytes : (size_t)0, need);
+    const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwattn_fwd_workspace(s));
+    if (w != DW_OK) return w;
     const dw::AttnPtrs p = {q, k, v, table, map, q_lengths, k_lengths, q_pos};
     return from_hip(dw::launch_dwattn_fwd(p, s, out, lse, workspace, shape->dtype == DW_BF16, (hipStream_t)stream), fn);
 }
@@ -600,10 +606,9 @@ dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const v
             return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
     if ((dq && (dq == dk || dq == dv)) || (dk && dk == dv))
         return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
-    const size_t need = dw::dwattn_bwd_workspace(s, shape->dtype == DW_BF16 ? 2 : 4);
-    if (need && (!workspace || workspace_bytes < need))
-        return fail(DW_ERR_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", fn,
-                    workspace ? workspace_bytes : (size_t)0, need);
+    const dw_status w =
+        check_workspace(fn, workspace, workspace_bytes, dw::dwattn_bwd_workspace(s, shape->dtype == DW_BF16 ? 2 : 4));
+    if (w != DW_OK) return w;
     const dw::AttnPtrs p = {q, k, v, table, map, q_lengths, k_lengths, q_pos};
     return from_hip(dw::launch_dwattn_bwd(p, s, out, lse, dout, dq, dk, dv, dtable, workspace, shape->dtype == DW_BF16,
                                           (hipStream_t)stream), fn);

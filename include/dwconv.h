@@ -488,7 +488,9 @@ dw_status dwnorm_fwd(const void *x, const void *residual, const void *gamma, con
                      int64_t C, float eps, float alpha, double p, dw_dtype dtype, void *stream);
 
 /* Bytes of device workspace dwnorm_bwd needs when it computes dgamma or dbeta
- * (0 for an empty batch, and for sizes that the call refuses). */
+ * (0 for an empty batch, and for sizes that the call refuses).  This workspace
+ * and the attention's start on a multiple of 16 bytes, or the call fails with
+ * DW_ERR_INVALID_ARG. */
 size_t dwnorm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C);
 
 /*

@@ -234,3 +234,15 @@ def test_backward_workspace_holds_for_any_context(alib):
             sizes = {alib.dwattn_bwd_workspace_bytes(attn(B=B, H=H, Hkv=H, Tq=T, Tk=T, D=D, dtype=dtype, left=left, right=right))
                      for left, right in ((-1, -1), (-1, 0), (100, -1), (30, 30))}
             assert len(sizes) == 1 and sizes.pop() > 0
+
+
+def test_workspaces_off_16_bytes_are_refused(alib):
+    X = [ctypes.c_void_p(0x10000 * i) for i in range(1, 12)]
+    few, good = attn(B=1, Tq=1, Tk=5000), attn()
+    for off in (1, 4, 8):
+        w = ctypes.c_void_p(0x5000 + off)
+        assert alib.dwattn_fwd(few, P, P, P, P, P, N, N, N, Q, N, w, 1 << 40, N) == INVALID and "16 bytes" in err(alib)
+        assert alib.dwattn_bwd(good, X[0], X[1], X[2], X[3], X[4], N, N, N, X[5], X[6], X[7], X[8], X[9], X[10], P, w, 1 << 40,
+                               N) == INVALID and "16 bytes" in err(alib)
+        assert alib.dwnorm_bwd(P, N, N, P, P, P, N, N, Q, N, R, N, w, 1 << 40, 16, 750, 1024, 1.0, 0.0, 0,
+                               N) == INVALID and "16 bytes" in err(alib)
