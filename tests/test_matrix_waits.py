@@ -1,7 +1,9 @@
 """The attention kernels as built, in assembly: every path from a matrix
 instruction to the first other use of its result has the wait states that
 gfx950 asks for, and nothing but the direct loads takes its operand from m0
-(which their inline assembly writes without telling the compiler).
+(which their inline assembly writes without telling the compiler); and those
+loads, whose scalar operands the compiler does not count waits for, keep the 5
+wait states from a vector instruction that writes one.
 
 Wait states: an instruction counts one, `s_nop n` counts n + 1; a vector, LDS or
 memory instruction, and a matrix instruction by an operand other than the sum
@@ -31,6 +33,13 @@ def registers(text):
     found = {(k, int(n)) for k, n in re.findall(r"\b([va])(\d+)\b", text)}
     for k, first, last in re.findall(r"\b([va])\[(\d+):(\d+)\]", text):
         found |= {(k, n) for n in range(int(first), int(last) + 1)}
+    return found
+
+
+def scalars(text):
+    found = {int(n) for n in re.findall(r"\bs(\d+)\b", text)}
+    for first, last in re.findall(r"\bs\[(\d+):(\d+)\]", text):
+        found |= set(range(int(first), int(last) + 1))
     return found
 
 
@@ -90,6 +99,34 @@ def too_early(code):
     return bad
 
 
+def loads_too_early(code, need=5):
+    """Direct loads within `need` wait states of a vector instruction that writes one of their scalars."""
+    label = {op: at for at, (op, args) in enumerate(code) if args is None}
+    bad = []
+    for at, (op, args) in enumerate(code):
+        if args is None or not op.startswith("v_"):
+            continue
+        written, todo, seen = scalars(args.split(",")[0]), [(at + 1, 0)], {}
+        while written and todo:
+            i, waited = todo.pop()
+            while i < len(code) and waited < need and seen.get(i, need) > waited:
+                seen[i] = waited
+                name, more = code[i]
+                if more is not None:
+                    if name.startswith("buffer_load") and more.endswith(" lds") and scalars(more) & written:
+                        bad.append((f"{op} {args}", f"{name} {more}", waited))
+                    if name == "s_endpgm":
+                        break
+                    waited += int(more) + 1 if name == "s_nop" else 1
+                    if name == "s_branch":
+                        i = label[more.strip()]
+                        continue
+                    if name.startswith("s_cbranch"):
+                        todo.append((label[more.strip()], waited))
+                i += 1
+    return bad
+
+
 @pytest.fixture(scope="module")
 def assembly(tmp_path_factory):
     b, folder = builder(), tmp_path_factory.mktemp("asm")
@@ -130,3 +167,14 @@ def test_m0_is_the_direct_loads_own(assembly, which):
     others = [(op, args) for code in assembly[which].values() for op, args in code
               if args and re.search(r"\bm0\b", args) and not (op == "s_mov_b32" and args.startswith("m0"))]
     assert not others, others[:3]
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+def test_direct_loads_keep_clear_of_their_scalars(assembly, which):
+    early = [("v_readfirstlane_b32", "s4, v0"), ("s_mov_b32", "m0, s9"), ("s_nop", "0"),
+             ("buffer_load_dwordx4", "v1, s[4:7], 0 offen lds")]
+    assert len(loads_too_early(early)) == 1 and not loads_too_early(early[:1] + [("s_nop", "2")] + early[1:])
+    loads = [args for code in assembly[which].values() for op, args in code if op.startswith("buffer_load") and args.endswith(" lds")]
+    assert len(loads) > 100
+    found = {name: loads_too_early(code) for name, code in assembly[which].items()}
+    assert not any(found.values()), {n: b[:2] for n, b in found.items() if b}
