@@ -18,13 +18,14 @@
 //
 // Seven products instead of the five that a pass with atomics would take: the
 // two done twice keep the sums' order the same in every call.
-// Measured, kernels alone, bf16 [16,750,8x128], lengths 750 to 398 (56 GFLOP as
-// five products): dq with the sums by distance 110 us, dk and dv 102 us, the
-// table 6.5 us.  In an earlier form of dk and dv that took 126 us, one tile of
-// queries alone took 42; leaving out three quarters of dv's product saved 43,
-// seven eighths of the scores' 17, the weights 15, the loads of the tiles 12.
-// float [3,333,4x50]: dq 27 us, dk and dv 41, the table 5, on so few workgroups
-// that most compute units have none.
+// Measured, kernels in a row under the profiler, bf16 [16,750,8x128], lengths 750
+// to 398 (56 GFLOP as five products): dq with the sums by distance 110 us, dk
+// and dv 100 us, the table 6.6 us.  The matrix units are busy for a sixth of
+// that; the rest is a run over one tile, which nothing overlaps, and the
+// arithmetic between the products.  With a reach over 191 a compute unit holds
+// one of dq's workgroups and not two (200: 123 us).
+// float [3,333,4x50]: dq 27 to 31 us, dk and dv 41 to 45, the table 5, on so few
+// workgroups that most compute units have none.
 #include "attn.h"
 
 namespace dw {

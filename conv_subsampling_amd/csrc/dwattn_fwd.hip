@@ -10,15 +10,16 @@
 // leaves compute units idle, the key axis is split over workgroups, whose
 // results attn_join adds.
 //
-// What bounds it, and what it measured (kernels alone):
-//   bf16 [16,750,8x128], lengths 750 to 398: 47 us, 22.4 GFLOP of valid pairs,
-//     477 TFLOP/s.  A run over one key tile takes 20 us of that; leaving out
-//     most of either product saves 6 to 7 us, the weights 3, the bias 4, the
-//     loads of the tiles 8: no one unit fills it.  At [4,3000,8x128], all
-//     frames valid, 184 us a call, 801 TFLOP/s.
-//   float, causal [8,1500,8x64]: 131 us, 11.6 GFLOP, 89 TFLOP/s in the six bf16
-//     products that stand for each; each wave splits its own operands.
-//   bf16, 8 frames of 64 streams over 391 keys: 12 us; one frame of 4 streams
+// What bounds it, and what it measured (kernels in a row under the profiler;
+// among other work, at a higher clock, the calls take 43 and 110 us):
+//   bf16 [16,750,8x128], lengths 750 to 398: 46 to 49 us, 22.4 GFLOP of valid
+//     pairs, 470 TFLOP/s.  A run over one key tile takes 22 us of that; at 47 us
+//     in all, leaving out most of either product saved 6 to 7 us, the weights 3,
+//     the bias 4, the loads of the tiles 8: no one unit fills it.  At
+//     [4,3000,8x128], all frames valid, 188 us, 786 TFLOP/s.
+//   float, causal [8,1500,8x64]: 126 to 129 us, 11.6 GFLOP, 91 TFLOP/s in the six
+//     bf16 products that stand for each; each wave splits its own operands.
+//   bf16, 8 frames of 64 streams over 391 keys: 11 us; one frame of 4 streams
 //     over 6000 keys: 14 us and 3.8 us for the join, several times what their
 //     bytes take: few tiles a workgroup, so latency.
 // For [16,750,8x128], when it took 51 us: all of a tile's operands read ahead,

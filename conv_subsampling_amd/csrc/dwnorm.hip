@@ -10,9 +10,10 @@
 // variance are two passes over registers and memory sees each tensor once.
 //
 // All of it is bound by memory.  Measured against the 5.19 TB/s of a large copy,
-// kernels alone: forward of [16,750,1024] bf16 with residual and dropout (87 MB
-// over its valid frames) 16.5 us, 5.3 TB/s; backward with both residual
-// gradients (106 MB) 23.0 us, 4.6 TB/s, and 3.9 us for the weights' sums.
+// kernels in a row under the profiler: forward of [16,750,1024] bf16 with residual
+// and dropout (87 MB over its valid frames) 16.4 us, 5.3 TB/s; backward with both
+// residual gradients (106 MB) 24 to 26 us, 4.1 to 4.5 TB/s, and 3.9 us for the
+// weights' sums.
 #include "launch.h"
 #include "rowops.h"
 
@@ -344,8 +345,8 @@ __global__ __launch_bounds__(kParamCols* kParamRows) void norm_param_reduce(
 // ---------------------------------------------------------------------------
 // Dropout by itself: y = residual + alpha * drop(x).  Bound by memory: the
 // generator's 20 wide multiplies serve 8 elements and hide behind the loads.
-// [16,750,4096] bf16 (197 MB) takes 32.7 us, 6.0 TB/s; float [32,1500,512], the
-// same bytes, 34.0 us.
+// [16,750,4096] bf16 (197 MB) takes 33.2 us, 5.9 TB/s; float [32,1500,512], the
+// same bytes, 33.9 us.
 // ---------------------------------------------------------------------------
 struct Drop {
     const void *x, *residual;
