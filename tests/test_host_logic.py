@@ -177,3 +177,12 @@ def test_row_kernel_names_exist_in_the_library():
     for name, prefix in bench.ROW_KERNELS:
         assert "void " + prefix in syms, (name, prefix)
     assert bench.PROBE_KERNEL + "(" in syms
+
+
+def test_committed_kernel_times_are_of_the_current_sources():
+    """The bench line's kernel-only times come from the committed profile, which has to be of the sources as they are:
+    every row and every probe copy has one."""
+    import bench
+    got = bench.read_kernel_stats()
+    assert {n for n, _ in bench.ROW_KERNELS} | {"probe:" + n for n in bench.PROBE_ROWS} == set(got)
+    assert all(us > 0 for us in got.values())
