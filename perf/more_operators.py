@@ -19,7 +19,7 @@ own = False
 F32, BF16 = "float32", "bfloat16"
 SCALE = 8.0   # of the recurrence's decay
 EPS = 1e-6    # of the heads' norm
-GROUP = 32    # columns that share a scale
+GROUP = 32    # columns that share a scale, within each half of a GLU's input
 
 
 def listed():
@@ -149,7 +149,7 @@ def prepare(case, seed):
     if case["op"] == "scan_bwd":  # what the forward pass left
         s["y"] = _scan_fwd_plain(s)[0]
     if case["op"] == "act_bwd":
-        s["kept"] = _pack_plain(s["x"], s["lengths"])
+        s["kept"] = _pack_plain(s["x"], case["kind"], s["lengths"])
     return s
 
 
@@ -197,7 +197,7 @@ def work(case):
         return {"bytes": (5 * live + 3 * rows) * C * e + (3 * B * C * 4 if case["state"] else 0) + 8 * C, "flops": 45 * live * C}
     if op.startswith("act"):
         C, wide = case["C"], 2 if case["kind"] == "glu" else 1
-        kept = rows * (wide * C + -(-wide * C // GROUP))
+        kept = rows * wide * (C + -(-C // GROUP))
         fwd, bwd = live * wide * C * e + rows * C * e + kept, kept * live // rows + live * C * e + rows * wide * C * e
         if op == "act_pass":
             return {"bytes": fwd + bwd, "flops": 25 * live * C}
@@ -329,24 +329,28 @@ def _rope_bwd_plain(s):
     return dq, dk, dgq, dgk
 
 
-def _pack_plain(x, lengths):
-    """8-bit values [B,T,W] and codes of their scales [B,T,ceil(W/32)]: scale 2^(code-127), the smallest with which the group's
-    largest is at most 127; what lies past the lengths is zero, as is its code."""
+def _pack_plain(x, kind, lengths):
+    """8-bit values [B,T,W] and codes [B,T,parts*ceil(C/32)] of their scales, for each of the input's parts of C columns: scale
+    2^(code-127), the smallest with which the group's largest is at most 127; what lies past the lengths is zero, as is its code."""
     B, T, W = x.shape
-    n = -(-W // GROUP)
-    xg = torch.nn.functional.pad(x.float(), (0, n * GROUP - W)).view(B, T, n, GROUP)
+    parts = 2 if kind == "glu" else 1
+    C = W // parts
+    n = -(-C // GROUP)
+    xg = torch.nn.functional.pad(x.float().view(B, T, parts, C), (0, n * GROUP - C)).view(B, T, parts * n, GROUP)
     top = xg.abs().amax(-1).contiguous()
     code = ((top.view(torch.int32) + 0x1FFFF >> 23) - 6).clamp_min(1)
     q = torch.round(xg * torch.exp2((127 - code).float())[..., None])
     live = torch.arange(T, device=x.device)[None, :] < lengths[:, None]
-    q = torch.where(live[..., None, None], q, 0.0).view(B, T, n * GROUP)[..., :W]
-    return q.to(torch.int8).contiguous(), torch.where(live[..., None], code, 0).to(torch.uint8)
+    q = torch.where(live[..., None, None], q, 0.0).view(B, T, parts, n * GROUP)[..., :C].reshape(B, T, W)
+    return q.to(torch.int8), torch.where(live[..., None], code, 0).to(torch.uint8)
 
 
-def _unpack_plain(kept):
+def _unpack_plain(kept, kind):
     q, code = kept
-    scale = torch.exp2(code.float() - 127).repeat_interleave(GROUP, -1)[..., :q.shape[-1]]
-    return q.float() * scale
+    parts = 2 if kind == "glu" else 1
+    C = q.shape[-1] // parts
+    scale = torch.exp2(code.float() - 127).unflatten(-1, (parts, -1)).repeat_interleave(GROUP, -1)[..., :C]
+    return q.float() * scale.flatten(-2)
 
 
 def _act_plain(x, kind):
@@ -369,14 +373,14 @@ def _act_pass_plain(s):
     kind, dt = s["case"]["kind"], s["x"].dtype
     live = _valid(s, s["x"].shape[1])
     y = torch.where(live, _act_plain(s["x"].float(), kind), 0.0).to(dt)
-    kept = _unpack_plain(_pack_plain(s["x"], s["lengths"]))
+    kept = _unpack_plain(_pack_plain(s["x"], kind, s["lengths"]), kind)
     return y, torch.where(live, _act_grad_plain(kept, s["dy"].float(), kind), 0.0).to(dt)
 
 
 def _act_bwd_plain(s):
     kind, dt = s["case"]["kind"], s["x"].dtype
     live = _valid(s, s["x"].shape[1])
-    kept = _unpack_plain(s["kept"])
+    kept = _unpack_plain(s["kept"], kind)
     dx = torch.where(live, _act_grad_plain(kept, s["dy"].float(), kind), 0.0).to(dt)
     return dx, torch.where(live, _act_plain(kept, kind), 0.0).to(dt)
 
@@ -432,11 +436,11 @@ def _exact_act(s):
     B, T, W = s["x"].shape
     x = s["x"].double()
     live = (torch.arange(T, device=x.device) < s["lengths"][:, None]).unsqueeze(-1)
+    C = c["C"]
     if c["op"] == "act_pass":
-        n = (W + GROUP - 1) // GROUP
         scale = torch.ones((B, T, W), dtype=torch.float64, device=x.device)
-        for j in range(n):
-            part = slice(j * GROUP, min(W, (j + 1) * GROUP))
+        for j in [k for half in range(0, W, C) for k in range(half, half + C, GROUP)]:
+            part = slice(j, min(j + GROUP, C if j < C else W))
             top = x[..., part].abs().amax(-1, keepdim=True)
             e = torch.ceil(torch.log2(top / 127))
             e = torch.where(top > 127 * torch.exp2(e), e + 1, torch.where(top <= 127 * torch.exp2(e - 1), e - 1, e))
@@ -444,7 +448,8 @@ def _exact_act(s):
         kept = torch.round(x / scale) * scale
     else:
         q, code = s["kept"]
-        kept = q.double() * torch.exp2(code.double() - 127)[..., torch.arange(W, device=x.device) // GROUP]
+        column = torch.arange(W, device=x.device)
+        kept = q.double() * torch.exp2(code.double() - 127)[..., column // C * -(-C // GROUP) + column % C // GROUP]
     dy = s["dy"].double()
 
     def act(z):
