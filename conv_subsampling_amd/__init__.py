@@ -26,6 +26,8 @@ __all__ = [
     "dwconv2d_fwd", "dwconv2d_bwd", "dwconv2d_bwd_workspace_bytes", "dwconv2d_bwd_noalloc",
     "dwattn_fwd", "dwattn_fwd_workspace_bytes", "dwattn_bwd", "dwattn_bwd_workspace_bytes", "rel_buckets",
     "dwnorm_fwd", "dwnorm_bwd", "dwnorm_bwd_workspace_bytes", "dwdrop_fwd", "dwdrop_bwd",
+    "dwscan_fwd", "dwscan_fwd_workspace_bytes", "dwscan_bwd", "dwscan_bwd_workspace_bytes",
+    "dwrope_fwd", "dwrope_bwd", "dwrope_bwd_workspace_bytes", "rope_frequencies", "dwact_fwd", "dwact_bwd",
     "conv2d_out_shape", "CAUSAL_PADS_2D", "front_out_shape", "out_len",
 ]
 
@@ -56,6 +58,10 @@ _f32, _f64 = ctypes.c_float, ctypes.c_double
 # struct dw_attn: 6 sizes, the strides of q, k, v, dq, dk and dv, buckets, reach,
 # left, right; scale, dtype.
 _attn_struct = struct.Struct("=28qfi")
+# struct dw_scan: 3 sizes, the strides of x, r, g, y, dy, dx, dr and dg; scale, dtype.
+_scan_struct = struct.Struct("=19qfi")
+# struct dw_rope: 7 sizes, the strides of q, k, v, their outputs, dq and dk; eps, pairs, dtype.
+_rope_struct = struct.Struct("=31qfii4x")
 
 
 def _bind(path: str) -> ctypes.CDLL:
@@ -120,6 +126,25 @@ def _bind(path: str) -> ctypes.CDLL:
     lib.dwattn_bwd_workspace_bytes.argtypes = [attn]
     lib.dwattn_bwd.restype = _int
     lib.dwattn_bwd.argtypes = [attn] + [_vp] * 16 + [_sz, _vp]
+    scan = rope = ctypes.c_char_p  # a packed dw_scan, dw_rope
+    lib.dwscan_fwd_workspace_bytes.restype = _sz
+    lib.dwscan_fwd_workspace_bytes.argtypes = [scan]
+    lib.dwscan_fwd.restype = _int
+    lib.dwscan_fwd.argtypes = [scan] + [_vp] * 9 + [_sz, _vp]
+    lib.dwscan_bwd_workspace_bytes.restype = _sz
+    lib.dwscan_bwd_workspace_bytes.argtypes = [scan]
+    lib.dwscan_bwd.restype = _int
+    lib.dwscan_bwd.argtypes = [scan] + [_vp] * 15 + [_sz, _vp]
+    lib.dwrope_fwd.restype = _int
+    lib.dwrope_fwd.argtypes = [rope] + [_vp] * 13
+    lib.dwrope_bwd_workspace_bytes.restype = _sz
+    lib.dwrope_bwd_workspace_bytes.argtypes = [rope]
+    lib.dwrope_bwd.restype = _int
+    lib.dwrope_bwd.argtypes = [rope] + [_vp] * 14 + [_sz, _vp]
+    lib.dwact_fwd.restype = _int
+    lib.dwact_fwd.argtypes = [_int] + [_vp] * 5 + [_i64] * 3 + [_int, _vp]
+    lib.dwact_bwd.restype = _int
+    lib.dwact_bwd.argtypes = [_int] + [_vp] * 6 + [_i64] * 3 + [_int, _vp]
     return lib
 
 
@@ -754,3 +779,337 @@ def dwattn_bwd(q, k, v, out, lse, dout, table=None, buckets=None, q_lengths=None
                            _ptr(k_lengths), _ptr(q_pos), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                            _ptr(dtable), _ptr(workspace), workspace.numel(), _stream(dev)))
     return dq, dk, dv, dtable
+
+
+def _frames(name, t, st, device, shape):
+    """A [B, T, C] tensor whose channels lie next to each other."""
+    if type(t) is torch.Tensor and t.dtype is st and t.device == device and t.shape == shape and t.stride(2) == 1:
+        return t
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != st:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {st}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have the channels of a frame next to each other")
+    return t
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_workspace(backward: bool, shape: bytes) -> int:
+    """The library's answer for these sizes, which depends on nothing else."""
+    return int((_lib.dwscan_bwd_workspace_bytes if backward else _lib.dwscan_fwd_workspace_bytes)(shape))
+
+
+def _scan_check(x, r, g, decay, lengths, h0):
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    dev, shape = x.device, x.shape
+    st, code = _storage(x)
+    B, T, C = shape
+    _frames("x", x, st, dev, shape)
+    _frames("r", r, st, dev, shape)
+    _frames("g", g, st, dev, shape)
+    _dev_tensor("decay", decay, torch.float32, dev, (C,))
+    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
+    _dev_tensor("h0", h0, torch.float32, dev, (B, C), allow_none=True)
+    return dev, st, code, B, T, C
+
+
+def _scan_shape(B, T, C, tensors, scale, code):
+    strides = [n for t in tensors for n in ((0, 0) if t is None else t.stride()[:2])]
+    return _scan_struct.pack(B, T, C, *strides, scale, code)
+
+
+def dwscan_fwd_workspace_bytes(B, T, C) -> int:
+    """Bytes of workspace `dwscan_fwd` takes for tensors of these sizes."""
+    return _scan_workspace(False, _scan_struct.pack(B, T, C, *(0,) * 16, 1.0, DW_F32))
+
+
+def dwscan_fwd(x, r, g, decay, lengths=None, h0=None, scale: float = 8.0, y=None, h_last=None, workspace=None,
+               need=("y", "h_last")):
+    """Gated linear recurrence over the frames: h_t = a h_{t-1} + sqrt(1 - a^2)
+    sigmoid(g) x with a = exp(-scale * softplus(decay) * sigmoid(r)); x, r, g
+    [B,T,C] (float32 or bfloat16, any strides above the last), decay float32
+    [C], h0 float32 [B,C] or None (zero).  Returns (y [B,T,C], h_last float32
+    [B,C] or None if not in `need`): the states, and the one after the last
+    valid frame, with which a stream goes on (it may be h0, updated in place)."""
+    dev, st, code, B, T, C = _scan_check(x, r, g, decay, lengths, h0)
+    if y is None:
+        y = torch.empty((B, T, C), dtype=st, device=dev)
+    else:
+        _frames("y", y, st, dev, x.shape)
+    if h_last is not None:
+        _dev_tensor("h_last", h_last, torch.float32, dev, (B, C))
+    elif "h_last" in need:
+        h_last = torch.empty((B, C), dtype=torch.float32, device=dev)
+    shape = _scan_shape(B, T, C, (x, r, g, y, None, None, None, None), scale, code)
+    if workspace is not None:
+        _dev_tensor("workspace", workspace, torch.uint8, dev)
+    else:
+        need_ws = _scan_workspace(False, shape)
+        if need_ws:
+            workspace = torch.empty((need_ws,), dtype=torch.uint8, device=dev)
+    _check(_lib.dwscan_fwd(shape, _ptr(x), _ptr(r), _ptr(g), _ptr(decay), _ptr(lengths), _ptr(h0), _ptr(y),
+                           _ptr(h_last), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev)))
+    return y, h_last
+
+
+def dwscan_bwd_workspace_bytes(B, T, C) -> int:
+    """Bytes of workspace `dwscan_bwd` takes for tensors of these sizes."""
+    return _scan_workspace(True, _scan_struct.pack(B, T, C, *(0,) * 16, 1.0, DW_F32))
+
+
+def dwscan_bwd(x, r, g, decay, y, dy, lengths=None, h0=None, dh_last=None, scale: float = 8.0, dx=None, dr=None, dg=None,
+               ddecay=None, dh0=None, workspace=None, need=("dx", "dr", "dg", "ddecay", "dh0")):
+    """Gradients (dx, dr, dg, ddecay, dh0) of dwscan_fwd given its y, dy and, for
+    h_last, dh_last; the other arguments are the forward's.  dx, dr and dg are
+    in the storage type (given ones may have any strides above the last),
+    ddecay [C] and dh0 [B,C] float32; those not in `need` are skipped (None)."""
+    dev, st, code, B, T, C = _scan_check(x, r, g, decay, lengths, h0)
+    f32, full = torch.float32, x.shape
+    _frames("y", y, st, dev, full)
+    _frames("dy", dy, st, dev, full)
+    _dev_tensor("dh_last", dh_last, f32, dev, (B, C), allow_none=True)
+    if dx is not None:
+        _frames("dx", dx, st, dev, full)
+    elif "dx" in need:
+        dx = torch.empty((B, T, C), dtype=st, device=dev)
+    if dr is not None:
+        _frames("dr", dr, st, dev, full)
+    elif "dr" in need:
+        dr = torch.empty((B, T, C), dtype=st, device=dev)
+    if dg is not None:
+        _frames("dg", dg, st, dev, full)
+    elif "dg" in need:
+        dg = torch.empty((B, T, C), dtype=st, device=dev)
+    if ddecay is not None:
+        _dev_tensor("ddecay", ddecay, f32, dev, (C,))
+    elif "ddecay" in need:
+        ddecay = torch.empty((C,), dtype=f32, device=dev)
+    if dh0 is not None:
+        _dev_tensor("dh0", dh0, f32, dev, (B, C))
+    elif "dh0" in need:
+        dh0 = torch.empty((B, C), dtype=f32, device=dev)
+    shape = _scan_shape(B, T, C, (x, r, g, y, dy, dx, dr, dg), scale, code)
+    if workspace is not None:
+        _dev_tensor("workspace", workspace, torch.uint8, dev)
+    else:
+        workspace = torch.empty((max(_scan_workspace(True, shape), 1),), dtype=torch.uint8, device=dev)
+    _check(_lib.dwscan_bwd(shape, _ptr(x), _ptr(r), _ptr(g), _ptr(decay), _ptr(lengths), _ptr(h0), _ptr(y), _ptr(dy),
+                           _ptr(dh_last), _ptr(dx), _ptr(dr), _ptr(dg), _ptr(ddecay), _ptr(dh0), _ptr(workspace),
+                           workspace.numel(), _stream(dev)))
+    return dx, dr, dg, ddecay, dh0
+
+
+def rope_frequencies(R: int, base: float = 10000.0, device="cuda"):
+    """The usual frequencies of `dwrope_fwd`, in radians a frame: base^(-2j/R)
+    for pair j of the R rotated elements, float64 [R/2]."""
+    if R < 0 or R % 2:
+        raise ValueError("R must be even")
+    if not base > 0:
+        raise ValueError("base must be positive")
+    return torch.tensor([float(base) ** (-2.0 * j / R) for j in range(R // 2)], dtype=torch.float64).to(device)
+
+
+_PAIRS = {"halves": 0, "neighbours": 1}
+
+
+@functools.lru_cache(maxsize=1024)
+def _rope_workspace(shape: bytes) -> int:
+    """The library's answer for these sizes, which depends on nothing else."""
+    return int(_lib.dwrope_bwd_workspace_bytes(shape))
+
+
+def _rope_check(q, k, q_gamma, k_gamma, freq, lengths, pos, pairs):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, T, H, D] and k [B, T, Hkv, D]")
+    if pairs not in _PAIRS:
+        raise ValueError("pairs must be 'halves' or 'neighbours'")
+    dev = q.device
+    st, code = _storage(q)
+    B, T, H, D = q.shape
+    Hkv = k.shape[2]
+    _heads("q", q, st, dev, q.shape)
+    _heads("k", k, st, dev, (B, T, Hkv, D))
+    _dev_tensor("q_gamma", q_gamma, st, dev, (D,), allow_none=True)
+    _dev_tensor("k_gamma", k_gamma, st, dev, (D,), allow_none=True)
+    R = 0
+    if freq is not None:
+        if freq.dim() != 1:
+            raise ValueError("freq must be [R / 2]")
+        _dev_tensor("freq", freq, torch.float64, dev)
+        R = 2 * freq.shape[0]
+    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
+    _dev_tensor("pos", pos, torch.int32, dev, (B,), allow_none=True)
+    return dev, st, code, B, T, H, Hkv, D, R
+
+
+def _rope_shape(sizes, tensors, eps, pairs, code):
+    strides = [n for t in tensors for n in ((0, 0, 0) if t is None else t.stride()[:3])]
+    return _rope_struct.pack(*sizes, *strides, eps, _PAIRS[pairs], code)
+
+
+def dwrope_fwd(q, k, q_gamma=None, k_gamma=None, freq=None, lengths=None, pos=None, v=None, place=None,
+               pairs: str = "halves", eps: float = 1e-6, q_out=None, k_out=None, v_out=None):
+    """Root mean square norm of each head of q [B,T,H,D] and k [B,T,Hkv,D]
+    (float32 or bfloat16, any strides above the last) with weights q_gamma,
+    k_gamma [D], then the rotation of their first 2 * len(freq) elements by
+    (pos[b] + t) * freq (float64, radians a frame; see `rope_frequencies`).
+    pairs: element j turns with its neighbour ("neighbours") or with the one
+    half of them further ("halves").  With place int32 [B], k_out and v_out are
+    caches [B,S,Hkv,D] and item b's frames go to place[b], place[b] + 1, ...;
+    without, k_out is a tensor like k.  v, if given, is copied to v_out.
+    Returns (q_out, k_out, v_out)."""
+    dev, st, code, B, T, H, Hkv, D, R = _rope_check(q, k, q_gamma, k_gamma, freq, lengths, pos, pairs)
+    rows = T
+    if place is not None:
+        _dev_tensor("place", place, torch.int32, dev, (B,))
+        if k_out is None or (v is not None and v_out is None):
+            raise ValueError("with place, the caches k_out and v_out must be given")
+        if k_out.dim() != 4:
+            raise ValueError("k_out must be [B, S, Hkv, D]")
+        rows = k_out.shape[1]
+    if v is not None:
+        _heads("v", v, st, dev, k.shape)
+    elif v_out is not None:
+        raise ValueError("v_out needs v")
+    q_out = torch.empty((B, T, H, D), dtype=st, device=dev) if q_out is None else _heads("q_out", q_out, st, dev, q.shape)
+    to = (B, rows, Hkv, D)
+    k_out = torch.empty(to, dtype=st, device=dev) if k_out is None else _heads("k_out", k_out, st, dev, to)
+    if v is not None:
+        v_out = torch.empty(to, dtype=st, device=dev) if v_out is None else _heads("v_out", v_out, st, dev, to)
+    shape = _rope_shape((B, T, H, Hkv, D, R, rows), (q, k, v, q_out, k_out, v_out, None, None), eps, pairs, code)
+    _check(_lib.dwrope_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(q_gamma), _ptr(k_gamma), _ptr(freq), _ptr(lengths),
+                           _ptr(pos), _ptr(place), _ptr(q_out), _ptr(k_out), _ptr(v_out), _stream(dev)))
+    return q_out, k_out, v_out
+
+
+def dwrope_bwd_workspace_bytes(B, T, H, Hkv, D) -> int:
+    """Bytes of workspace `dwrope_bwd` takes for tensors of these sizes."""
+    return _rope_workspace(_rope_struct.pack(B, T, H, Hkv, D, 0, 0, *(0,) * 24, 0.0, 0, DW_F32))
+
+
+def dwrope_bwd(q, k, dq_out, dk_out, q_gamma=None, k_gamma=None, freq=None, lengths=None, pos=None,
+               pairs: str = "halves", eps: float = 1e-6, dq=None, dk=None, dq_gamma=None, dk_gamma=None, workspace=None,
+               need=("dq", "dk", "dq_gamma", "dk_gamma")):
+    """Gradients (dq, dk, dq_gamma, dk_gamma) of dwrope_fwd without caches, given
+    those of its outputs; the other arguments are the forward's.  dq and dk are
+    in the storage type (given ones may have any strides above the last), the
+    gammas' float32 [D]; those not in `need` are skipped (None)."""
+    dev, st, code, B, T, H, Hkv, D, R = _rope_check(q, k, q_gamma, k_gamma, freq, lengths, pos, pairs)
+    f32 = torch.float32
+    _heads("dq_out", dq_out, st, dev, q.shape)
+    _heads("dk_out", dk_out, st, dev, k.shape)
+    if dq is not None:
+        _heads("dq", dq, st, dev, q.shape)
+    elif "dq" in need:
+        dq = torch.empty((B, T, H, D), dtype=st, device=dev)
+    if dk is not None:
+        _heads("dk", dk, st, dev, k.shape)
+    elif "dk" in need:
+        dk = torch.empty((B, T, Hkv, D), dtype=st, device=dev)
+    if dq_gamma is not None:
+        _dev_tensor("dq_gamma", dq_gamma, f32, dev, (D,))
+    elif "dq_gamma" in need:
+        dq_gamma = torch.empty((D,), dtype=f32, device=dev)
+    if dk_gamma is not None:
+        _dev_tensor("dk_gamma", dk_gamma, f32, dev, (D,))
+    elif "dk_gamma" in need:
+        dk_gamma = torch.empty((D,), dtype=f32, device=dev)
+    shape = _rope_shape((B, T, H, Hkv, D, R, 0), (q, k, None, dq_out, dk_out, None, dq, dk), eps, pairs, code)
+    ws_bytes = 0
+    if dq_gamma is not None or dk_gamma is not None:
+        if workspace is None:
+            workspace = torch.empty((max(_rope_workspace(shape), 1),), dtype=torch.uint8, device=dev)
+        _dev_tensor("workspace", workspace, torch.uint8, dev)
+        ws_bytes = workspace.numel()
+    _check(_lib.dwrope_bwd(shape, _ptr(q), _ptr(k), _ptr(q_gamma), _ptr(k_gamma), _ptr(freq), _ptr(lengths), _ptr(pos),
+                           _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dq_gamma), _ptr(dk_gamma),
+                           _ptr(workspace), ws_bytes, _stream(dev)))
+    return dq, dk, dq_gamma, dk_gamma
+
+
+_ACTS = {"none": 0, "silu": 1, "glu": 2}
+
+
+def _act_parts(kind):
+    if kind not in _ACTS:
+        raise ValueError("kind must be 'none', 'silu' or 'glu'")
+    return 2 if kind == "glu" else 1
+
+
+def dwact_fwd(x, kind: str, lengths=None, y=None, kept=None, need=("y", "kept")):
+    """y = silu(x), or for kind "glu" the first half of x's channels times the
+    sigmoid of the second, or x itself ("none"); x [B,T,C or 2C] (float32 or
+    bfloat16).  Returns (y, kept): kept = (int8 like x, uint8 codes of the
+    scales [B,T,parts * ceil(C/32)]) is x in 8 bits, from which `dwact_bwd`
+    works.  Those not in `need` are skipped (None)."""
+    parts = _act_parts(kind)
+    if x.dim() != 3 or x.shape[2] % parts:
+        raise ValueError("x must be [B, T, C], or [B, T, 2 * C] for a GLU")
+    dev = x.device
+    st, code = _storage(x)
+    B, T, W = x.shape
+    C = W // parts
+    _dev_tensor("x", x, st, dev)
+    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
+    if y is not None:
+        _dev_tensor("y", y, st, dev, (B, T, C))
+    elif "y" in need:
+        y = torch.empty((B, T, C), dtype=st, device=dev)
+    if kept is not None:
+        q, codes = kept
+        _dev_tensor("kept[0]", q, torch.int8, dev, (B, T, W))
+        _dev_tensor("kept[1]", codes, torch.uint8, dev, (B, T, parts * -(-C // 32)))
+    elif "kept" in need:
+        q = torch.empty((B, T, W), dtype=torch.int8, device=dev)
+        codes = torch.empty((B, T, parts * -(-C // 32)), dtype=torch.uint8, device=dev)
+        kept = (q, codes)
+    else:
+        q = codes = None
+    _check(_lib.dwact_fwd(_ACTS[kind], _ptr(x), _ptr(lengths), _ptr(y), _ptr(q), _ptr(codes), B, T, C, code,
+                          _stream(dev)))
+    return y, kept
+
+
+def dwact_bwd(kept, dy, kind: str, lengths=None, dtype=None, dx=None, y=None, need=("dx",)):
+    """(dx, y) from the checkpoint of `dwact_fwd` alone: dx the gradient of its
+    input given dy, y the activation of the kept input (for kind "none" the
+    kept input itself).  Both are in dy's storage type; without dy, dtype gives
+    it.  Those not in `need` are skipped (None)."""
+    parts = _act_parts(kind)
+    q, codes = kept
+    if q.dim() != 3 or q.shape[2] % parts:
+        raise ValueError("kept[0] must be [B, T, C], or [B, T, 2 * C] for a GLU")
+    dev = q.device
+    B, T, W = q.shape
+    C = W // parts
+    if dy is not None:
+        st, code = _storage(dy)
+        if dtype is not None and dtype != st:
+            raise TypeError(f"dy has dtype {st}, expected {dtype}")
+        _dev_tensor("dy", dy, st, dev, (B, T, C))
+    else:
+        if dx is not None or "dx" in need:
+            raise ValueError("dx needs dy")
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("without dy, dtype must be float32 or bfloat16")
+        st, code = dtype, DW_BF16 if dtype == torch.bfloat16 else DW_F32
+    _dev_tensor("kept[0]", q, torch.int8, dev)
+    _dev_tensor("kept[1]", codes, torch.uint8, dev, (B, T, parts * -(-C // 32)))
+    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
+    if dx is not None:
+        _dev_tensor("dx", dx, st, dev, (B, T, W))
+    elif "dx" in need:
+        dx = torch.empty((B, T, W), dtype=st, device=dev)
+    if y is not None:
+        _dev_tensor("y", y, st, dev, (B, T, C))
+    elif "y" in need:
+        y = torch.empty((B, T, C), dtype=st, device=dev)
+    _check(_lib.dwact_bwd(_ACTS[kind], _ptr(q), _ptr(codes), _ptr(lengths), _ptr(dy), _ptr(dx), _ptr(y), B, T, C, code,
+                          _stream(dev)))
+    return dx, y

@@ -196,6 +196,81 @@ int64_t log_steps(int64_t n, int64_t e, int64_t reach, int64_t m) {
     return equal ? k : (int64_t)floorl(t);
 }
 
+bool frames_ok(const dw_frames& s) { return s.item >= 0 && s.frame >= 0; }
+
+// The distances of an axis of one are never taken.
+dw::FrameStride frames_of(const dw_frames& s, int64_t B, int64_t T) { return {B > 1 ? s.item : 0, T > 1 ? s.frame : 0}; }
+
+// Frames of one tile are addressed by 32-bit offsets, everything else by 64-bit ones.
+bool frames_fit(const dw::FrameStride& s, int64_t B, int64_t T) {
+    const int64_t far = (int64_t)1 << 58;
+    return s.frame < dw::kScanMaxFrameStride && dw::product_below(far, {B, s.item}) && dw::product_below(far, {T, s.frame});
+}
+
+// The recurrence's problem as the launchers take it.
+dw_status check_scan(const char* fn, const dw_scan* a, bool backward, dw::ScanShape* s) {
+    if (!a) return fail(DW_ERR_INVALID_ARG, "%s: shape must not be NULL", fn);
+    if (a->B < 0 || a->T < 0 || a->C < 0) return fail(DW_ERR_INVALID_ARG, "%s: negative size", fn);
+    const dw_frames* strides[] = {&a->x, &a->r, &a->g, &a->y, &a->dy, &a->dx, &a->dr, &a->dg};
+    const int n = backward ? 8 : 4;
+    for (int i = 0; i < n; ++i)
+        if (!frames_ok(*strides[i])) return fail(DW_ERR_INVALID_ARG, "%s: negative stride", fn);
+    const dw_status t = check_dtype(fn, a->dtype);
+    if (t != DW_OK) return t;
+    if (!(a->scale > 0.0f && a->scale <= 3.4e38f)) return fail(DW_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+    if (!extents_ok(a->B, a->T, a->C)) return too_large(fn);
+    dw::FrameStride f[8] = {};
+    for (int i = 0; i < n; ++i) {
+        f[i] = frames_of(*strides[i], a->B, a->T);
+        if (!frames_fit(f[i], a->B, a->T)) return too_large(fn);
+    }
+    *s = {a->B, a->T, a->C, f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7], a->scale};
+    return dw::dwscan_fits(*s) ? DW_OK : too_large(fn);
+}
+
+bool same_strides(const dw_strides& a, const dw_strides& b) {
+    return a.item == b.item && a.frame == b.frame && a.head == b.head;
+}
+
+// The heads' problem as the launchers take it.
+dw_status check_rope(const char* fn, const dw_rope* a, const double* freq, bool freq_given, bool backward, bool cache,
+                     dw::RopeShape* s) {
+    if (!a) return fail(DW_ERR_INVALID_ARG, "%s: shape must not be NULL", fn);
+    if (a->B < 0 || a->T < 0 || a->H < 0 || a->Hkv < 0 || a->D < 1 || a->R < 0 || (cache && a->S < 0))
+        return fail(DW_ERR_INVALID_ARG, "%s: negative size, or heads without elements", fn);
+    if (a->R % 2 != 0 || a->R > a->D)
+        return fail(DW_ERR_INVALID_ARG, "%s: R=%lld of D=%lld elements cannot be rotated in pairs", fn, (long long)a->R, (long long)a->D);
+    if (a->pairs != DW_PAIRS_HALVES && a->pairs != DW_PAIRS_NEIGHBOURS)
+        return fail(DW_ERR_INVALID_ARG, "%s: unknown pairs %d", fn, (int)a->pairs);
+    if (!(a->eps >= 0.0f)) return fail(DW_ERR_INVALID_ARG, "%s: eps must not be negative", fn);
+    const dw_status t = check_dtype(fn, a->dtype);
+    if (t != DW_OK) return t;
+    const dw_strides* strides[] = {&a->q, &a->k, &a->q_out, &a->k_out, backward ? &a->dq : &a->v, backward ? &a->dk : &a->v_out};
+    for (const dw_strides* x : strides)
+        if (!strides_ok(*x)) return fail(DW_ERR_INVALID_ARG, "%s: negative stride", fn);
+    if (a->D > 128) return fail(DW_ERR_UNSUPPORTED, "%s: heads of D=%lld have no kernel (at most 128)", fn, (long long)a->D);
+    if (freq_given && a->R > 0 && !freq) return fail(DW_ERR_INVALID_ARG, "%s: a rotation needs freq", fn);
+    if (!extents_ok(a->B, a->T, a->H, a->Hkv) || (cache && !extents_ok(a->S))) return too_large(fn);
+    const int64_t heads = a->H > a->Hkv ? a->H : a->Hkv, frames = cache && a->S > a->T ? a->S : a->T;
+    for (const dw_strides* x : strides)
+        if (!strides_fit(*x, a->B, frames, heads)) return too_large(fn);
+    *s = {a->B, a->T, a->H, a->Hkv, a->D, a->R, a->S, stride_of(a->q), stride_of(a->k), stride_of(a->v), stride_of(a->q_out),
+          stride_of(a->k_out), stride_of(a->v_out), stride_of(a->dq), stride_of(a->dk), a->eps, a->pairs == DW_PAIRS_HALVES};
+    return dw::dwrope_fits(*s) ? DW_OK : too_large(fn);
+}
+
+dw_status check_act(const char* fn, dw_act act, dw_dtype dtype, int64_t B, int64_t T, int64_t C) {
+    if (act != DW_ACT_NONE && act != DW_ACT_SILU && act != DW_ACT_GLU)
+        return fail(DW_ERR_INVALID_ARG, "%s: unknown act %d", fn, (int)act);
+    if (B < 0 || T < 0 || C < 0) return fail(DW_ERR_INVALID_ARG, "%s: negative size", fn);
+    const dw_status t = check_dtype(fn, dtype);
+    if (t != DW_OK) return t;
+    if (!extents_ok(B, T, C) || C >= dw::kMaxExtent - 64 || !dw::product_below((int64_t)1 << 58, {B, T}) ||
+        !dw::dwact_fits(B * T, C, (int)act))
+        return too_large(fn);
+    return DW_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -612,6 +687,151 @@ dw_status dwattn_bwd(const dw_attn* shape, const void* q, const void* k, const v
     const dw::AttnPtrs p = {q, k, v, table, map, q_lengths, k_lengths, q_pos};
     return from_hip(dw::launch_dwattn_bwd(p, s, out, lse, dout, dq, dk, dv, dtable, workspace, shape->dtype == DW_BF16,
                                           (hipStream_t)stream), fn);
+}
+
+size_t dwscan_fwd_workspace_bytes(const dw_scan* shape) {
+    dw::ScanShape s;
+    return check_scan("dwscan_fwd_workspace_bytes", shape, false, &s) == DW_OK ? dw::dwscan_fwd_workspace(s) : 0;
+}
+
+dw_status dwscan_fwd(const dw_scan* shape, const void* x, const void* r, const void* g, const float* decay,
+                     const int32_t* lengths, const float* h0, void* y, float* h_last, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    const char* fn = "dwscan_fwd";
+    dw::ScanShape s;
+    const dw_status c = check_scan(fn, shape, false, &s);
+    if (c != DW_OK) return c;
+    if (!nonempty(s.B, s.C) || (s.T == 0 && !h_last)) return ok();
+    if (!decay || (s.T > 0 && (!x || !r || !g || !y)))
+        return fail(DW_ERR_INVALID_ARG, "%s: x, r, g, decay and y must not be NULL (unless empty)", fn);
+    if (s.T > 0 && (y == x || y == r || y == g)) return fail(DW_ERR_INVALID_ARG, "%s: y must not alias an input", fn);
+    const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwscan_fwd_workspace(s));
+    if (w != DW_OK) return w;
+    const dw::ScanPtrs p = {x, r, g, decay, lengths, h0};
+    return from_hip(dw::launch_dwscan_fwd(p, s, y, h_last, workspace, shape->dtype == DW_BF16, (hipStream_t)stream), fn);
+}
+
+size_t dwscan_bwd_workspace_bytes(const dw_scan* shape) {
+    dw::ScanShape s;
+    return check_scan("dwscan_bwd_workspace_bytes", shape, true, &s) == DW_OK ? dw::dwscan_bwd_workspace(s) : 0;
+}
+
+dw_status dwscan_bwd(const dw_scan* shape, const void* x, const void* r, const void* g, const float* decay,
+                     const int32_t* lengths, const float* h0, const void* y, const void* dy, const float* dh_last,
+                     void* dx, void* dr, void* dg, float* ddecay, float* dh0, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+    const char* fn = "dwscan_bwd";
+    dw::ScanShape s;
+    const dw_status c = check_scan(fn, shape, true, &s);
+    if (c != DW_OK) return c;
+    if ((!dx && !dr && !dg && !ddecay && !dh0) || s.C == 0) return ok();
+    if (!ddecay && (s.B == 0 || (s.T == 0 && !dh0))) return ok();
+    if (s.B > 0 && !decay) return fail(DW_ERR_INVALID_ARG, "%s: decay must not be NULL (unless empty)", fn);
+    if (nonempty(s.B, s.T)) {
+        if (!x || !r || !g || !y || !dy)
+            return fail(DW_ERR_INVALID_ARG, "%s: x, r, g, y and dy must not be NULL (unless empty)", fn);
+        for (const void* o : {(const void*)dx, (const void*)dr, (const void*)dg})
+            if (o && (o == x || o == r || o == g || o == y || o == dy))
+                return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
+        if ((dx && (dx == dr || dx == dg)) || (dr && dr == dg))
+            return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
+        if ((ddecay && ddecay == decay) || (dh0 && dh0 == h0))
+            return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
+    }
+    const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwscan_bwd_workspace(s));
+    if (w != DW_OK) return w;
+    const dw::ScanPtrs p = {x, r, g, decay, lengths, h0};
+    return from_hip(dw::launch_dwscan_bwd(p, s, y, dy, dh_last, dx, dr, dg, ddecay, dh0, workspace,
+                                          shape->dtype == DW_BF16, (hipStream_t)stream), fn);
+}
+
+dw_status dwrope_fwd(const dw_rope* shape, const void* q, const void* k, const void* v, const void* q_gamma,
+                     const void* k_gamma, const double* freq, const int32_t* lengths, const int32_t* pos,
+                     const int32_t* place, void* q_out, void* k_out, void* v_out, void* stream) {
+    const char* fn = "dwrope_fwd";
+    dw::RopeShape s;
+    const dw_status c = check_rope(fn, shape, freq, true, false, place != nullptr, &s);
+    if (c != DW_OK) return c;
+    const bool any_q = nonempty(s.B, s.T, s.H), any_k = nonempty(s.B, s.T, s.Hkv) && (!place || s.S > 0);
+    if (any_k && !v != !v_out) return fail(DW_ERR_INVALID_ARG, "%s: v and v_out come together", fn);
+    if ((any_q && (!q || !q_out)) || (any_k && (!k || !k_out)))
+        return fail(DW_ERR_INVALID_ARG, "%s: q, k, q_out and k_out must not be NULL (unless empty)", fn);
+    if (any_q && ((q_out == q && !same_strides(shape->q, shape->q_out)) || (any_k && (q_out == k || q_out == v || q_out == k_out || q_out == v_out))))
+        return fail(DW_ERR_INVALID_ARG, "%s: q_out must not alias another tensor", fn);
+    if (any_k && ((k_out == k && (place || !same_strides(shape->k, shape->k_out))) || (any_q && k_out == q) || k_out == v || k_out == v_out))
+        return fail(DW_ERR_INVALID_ARG, "%s: k_out must not alias another tensor", fn);
+    if (any_k && v && (v_out == v || v_out == k || (any_q && v_out == q)))
+        return fail(DW_ERR_INVALID_ARG, "%s: v_out must not alias another tensor", fn);
+    if (!any_k) s.Hkv = 0;
+    if (!any_q) s.H = 0;
+    if (!any_q && !any_k) return ok();
+    const dw::RopePtrs p = {q, k, q_gamma, k_gamma, freq, lengths, pos};
+    return from_hip(dw::launch_dwrope_fwd(p, s, v, place, q_out, k_out, v_out, shape->dtype == DW_BF16,
+                                          (hipStream_t)stream), fn);
+}
+
+size_t dwrope_bwd_workspace_bytes(const dw_rope* shape) {
+    dw::RopeShape s;
+    return check_rope("dwrope_bwd_workspace_bytes", shape, nullptr, false, true, false, &s) == DW_OK ? dw::dwrope_bwd_workspace(s) : 0;
+}
+
+dw_status dwrope_bwd(const dw_rope* shape, const void* q, const void* k, const void* q_gamma, const void* k_gamma,
+                     const double* freq, const int32_t* lengths, const int32_t* pos, const void* dq_out,
+                     const void* dk_out, void* dq, void* dk, float* dq_gamma, float* dk_gamma, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    const char* fn = "dwrope_bwd";
+    dw::RopeShape s;
+    const dw_status c = check_rope(fn, shape, freq, true, true, false, &s);
+    if (c != DW_OK) return c;
+    const bool params = dq_gamma || dk_gamma;
+    if (!dq && !dk && !params) return ok();
+    const bool any_q = nonempty(s.B, s.T, s.H), any_k = nonempty(s.B, s.T, s.Hkv);
+    if (!any_q && !any_k && !params) return ok();
+    if ((any_q && (!q || !dq_out)) || (any_k && (!k || !dk_out)))
+        return fail(DW_ERR_INVALID_ARG, "%s: q, k, dq_out and dk_out must not be NULL (unless empty)", fn);
+    if (any_q && dq && ((dq == q && !same_strides(shape->q, shape->dq)) || (dq == dq_out && !same_strides(shape->q_out, shape->dq)) ||
+                        (any_k && (dq == k || dq == dk_out || dq == dk))))
+        return fail(DW_ERR_INVALID_ARG, "%s: dq must not alias another tensor", fn);
+    if (any_k && dk && ((dk == k && !same_strides(shape->k, shape->dk)) || (dk == dk_out && !same_strides(shape->k_out, shape->dk)) ||
+                        (any_q && (dk == q || dk == dq_out))))
+        return fail(DW_ERR_INVALID_ARG, "%s: dk must not alias another tensor", fn);
+    if (dq_gamma && dq_gamma == dk_gamma) return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
+    if (params) {
+        const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwrope_bwd_workspace(s));
+        if (w != DW_OK) return w;
+    }
+    const dw::RopePtrs p = {q, k, q_gamma, k_gamma, freq, lengths, pos};
+    return from_hip(dw::launch_dwrope_bwd(p, s, dq_out, dk_out, dq, dk, dq_gamma, dk_gamma, workspace,
+                                          shape->dtype == DW_BF16, (hipStream_t)stream), fn);
+}
+
+dw_status dwact_fwd(dw_act act, const void* x, const int32_t* lengths, void* y, int8_t* kept, uint8_t* codes,
+                    int64_t B, int64_t T, int64_t C, dw_dtype dtype, void* stream) {
+    const char* fn = "dwact_fwd";
+    const dw_status c = check_act(fn, act, dtype, B, T, C);
+    if (c != DW_OK) return c;
+    if (!kept != !codes) return fail(DW_ERR_INVALID_ARG, "%s: kept and codes come together", fn);
+    if (!nonempty(B, T, C) || (!y && !kept)) return ok();
+    if (!x) return fail(DW_ERR_INVALID_ARG, "%s: x must not be NULL", fn);
+    if (y == x && act == DW_ACT_GLU) return fail(DW_ERR_INVALID_ARG, "%s: y must not alias x", fn);
+    if (kept && ((const void*)kept == x || (const void*)codes == x || kept == y || codes == y || (const void*)kept == (const void*)codes))
+        return fail(DW_ERR_INVALID_ARG, "%s: kept and codes must not alias another tensor", fn);
+    return from_hip(dw::launch_dwact_fwd((int)act, x, lengths, y, kept, codes, B, T, C, dtype == DW_BF16, (hipStream_t)stream), fn);
+}
+
+dw_status dwact_bwd(dw_act act, const int8_t* kept, const uint8_t* codes, const int32_t* lengths, const void* dy,
+                    void* dx, void* y, int64_t B, int64_t T, int64_t C, dw_dtype dtype, void* stream) {
+    const char* fn = "dwact_bwd";
+    const dw_status c = check_act(fn, act, dtype, B, T, C);
+    if (c != DW_OK) return c;
+    if (!nonempty(B, T, C) || (!dx && !y)) return ok();
+    if (!kept || !codes || (dx && !dy)) return fail(DW_ERR_INVALID_ARG, "%s: kept, codes and dy must not be NULL", fn);
+    if (dx && ((dx == dy && act == DW_ACT_GLU) || dx == y))
+        return fail(DW_ERR_INVALID_ARG, "%s: dx must not alias y, nor dy with DW_ACT_GLU", fn);
+    for (const void* o : {(const void*)dx, (const void*)y})
+        if (o && (o == (const void*)kept || o == (const void*)codes || (o == dy && o != dx)))
+            return fail(DW_ERR_INVALID_ARG, "%s: an output must not alias an input", fn);
+    return from_hip(dw::launch_dwact_bwd((int)act, kept, codes, lengths, dy, dx, y, B, T, C, dtype == DW_BF16, (hipStream_t)stream), fn);
 }
 
 }  // extern "C"

@@ -164,4 +164,62 @@ hipError_t launch_dwattn_bwd(const AttnPtrs& p, const AttnShape& s, const void* 
                              void* dq, void* dk, void* dv, float* dtable, void* workspace, bool bf16,
                              hipStream_t stream);
 
+// Gated linear recurrence over the frames.
+struct FrameStride {
+    int64_t item, frame;  // in elements
+};
+
+struct ScanShape {
+    int64_t B, T, C;
+    FrameStride x, r, g, y, dy, dx, dr, dg;
+    float scale;
+};
+
+struct ScanPtrs {
+    const void *x, *r, *g;
+    const float* decay;
+    const int32_t* lengths;
+    const float* h0;
+};
+
+constexpr int64_t kScanMaxFrameStride = (int64_t)1 << 23;  // offsets inside a tile of frames stay in 32 bits
+
+bool dwscan_fits(const ScanShape& s);
+size_t dwscan_fwd_workspace(const ScanShape& s);
+hipError_t launch_dwscan_fwd(const ScanPtrs& p, const ScanShape& s, void* y, float* h_last, void* workspace, bool bf16,
+                             hipStream_t stream);
+size_t dwscan_bwd_workspace(const ScanShape& s);
+hipError_t launch_dwscan_bwd(const ScanPtrs& p, const ScanShape& s, const void* y, const void* dy, const float* dh_last,
+                             void* dx, void* dr, void* dg, float* ddecay, float* dh0, void* workspace, bool bf16,
+                             hipStream_t stream);
+
+// Norm of the heads and rotation by positions.
+struct RopeShape {
+    int64_t B, T, H, Hkv, D, R, S;
+    AttnStride q, k, v, q_out, k_out, v_out, dq, dk;
+    float eps;
+    bool halves;
+};
+
+struct RopePtrs {
+    const void *q, *k, *q_gamma, *k_gamma;
+    const double* freq;
+    const int32_t *lengths, *pos;
+};
+
+bool dwrope_fits(const RopeShape& s);
+hipError_t launch_dwrope_fwd(const RopePtrs& p, const RopeShape& s, const void* v, const int32_t* place, void* q_out,
+                             void* k_out, void* v_out, bool bf16, hipStream_t stream);
+size_t dwrope_bwd_workspace(const RopeShape& s);
+hipError_t launch_dwrope_bwd(const RopePtrs& p, const RopeShape& s, const void* dq_out, const void* dk_out, void* dq,
+                             void* dk, float* dq_gamma, float* dk_gamma, void* workspace, bool bf16,
+                             hipStream_t stream);
+
+// Activations with an 8-bit checkpoint of their input; act is the ABI's dw_act.
+bool dwact_fits(int64_t rows, int64_t C, int act);
+hipError_t launch_dwact_fwd(int act, const void* x, const int32_t* lengths, void* y, int8_t* kept, uint8_t* codes,
+                            int64_t B, int64_t T, int64_t C, bool bf16, hipStream_t stream);
+hipError_t launch_dwact_bwd(int act, const int8_t* kept, const uint8_t* codes, const int32_t* lengths, const void* dy,
+                            void* dx, void* y, int64_t B, int64_t T, int64_t C, bool bf16, hipStream_t stream);
+
 }  // namespace dw

@@ -33,6 +33,14 @@
  *   dwattn_fwd, dwattn_bwd, dwattn_rel_buckets
  *                    attention with a learned relative position bias by
  *                    buckets, for whole utterances and for streams over a cache
+ *   dwscan_fwd, dwscan_bwd
+ *                    a gated linear recurrence over the frames, channel by
+ *                    channel, for whole utterances and frame by frame
+ *   dwrope_fwd, dwrope_bwd
+ *                    the norm of each head of queries and keys and the rotation
+ *                    by their positions, with the append to a stream's cache
+ *   dwact_fwd, dwact_bwd
+ *                    SiLU and GLU whose input is kept in 8 bits for the gradients
  *
  * Conventions shared by every entry point
  *   - Tensors are dense, contiguous and channel-last (channel index fastest):
@@ -633,6 +641,213 @@ dw_status dwattn_bwd(const dw_attn *shape, const void *q, const void *k, const v
                      const int32_t *map, const int32_t *q_lengths, const int32_t *k_lengths, const int32_t *q_pos,
                      const void *out, const float *lse, const void *dout, void *dq, void *dk, void *dv, float *dtable,
                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated linear recurrence.
+ *
+ * Sizes and layout of one problem.  x, r, g, y and the gradients are [B][T][C]
+ * with the C channels of a frame next to each other and any distance between
+ * items and frames, given in elements (so the gates may be slices of one
+ * projection's output; an input's distance may be 0, its gradients are then
+ * those of each frame, not summed).
+ */
+typedef struct {
+    int64_t item, frame; /* elements from one to the next; a frame's below 2^23 */
+} dw_frames;
+
+typedef struct {
+    int64_t B, T, C;
+    dw_frames x, r, g, y;
+    dw_frames dy, dx, dr, dg; /* dwscan_bwd only */
+    float scale;              /* of the decay, positive */
+    dw_dtype dtype;           /* of x, r, g, y, dy, dx, dr, dg */
+} dw_scan;
+
+/* Bytes of device workspace dwscan_fwd needs: none where there are sequences
+ * enough to fill the GPU; where there are few, the frames are shared out, and
+ * the parts are joined from the workspace.  0 for sizes that the call refuses. */
+size_t dwscan_fwd_workspace_bytes(const dw_scan *shape);
+
+/*
+ * dwscan_fwd -- a linear recurrence over the frames of each channel, gated by
+ * two inputs:
+ *   a_t = exp(-scale * softplus(decay[c]) * sigmoid(r[b, t, c]))
+ *   h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * sigmoid(g[b, t, c]) * x[b, t, c]
+ *   y[b, t, c] = h_t                for t < len_b, else 0
+ * from h_{-1} = h0[b, c] (NULL: zero).  h_last[b, c] (may be NULL) receives the
+ * state after the last valid frame, h0 where there is none: the h0 of the
+ * stream's next call, which may be the same buffer.  Inputs at or past the
+ * length are not read.
+ *
+ * decay: [C] float; h0, h_last: [B][C] float, dense.  The state, the gates and
+ * 1 - a (taken without cancellation) are float32 whatever the storage type; y
+ * is rounded once.  Repeated calls agree bit for bit.
+ * Errors: DW_ERR_INVALID_ARG for a null pointer that holds elements, a negative
+ * size or stride, a scale that is not positive and finite, a bad dtype, or y
+ * aliasing an input; DW_ERR_UNSUPPORTED for sizes or strides too large for one
+ * launch; DW_ERR_WORKSPACE for a missing or short workspace (which starts on a
+ * multiple of 16 bytes, or the call fails with DW_ERR_INVALID_ARG).
+ */
+dw_status dwscan_fwd(const dw_scan *shape, const void *x, const void *r, const void *g, const float *decay,
+                     const int32_t *lengths, const float *h0, void *y, float *h_last, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace dwscan_bwd needs.  0 for sizes that the call refuses. */
+size_t dwscan_bwd_workspace_bytes(const dw_scan *shape);
+
+/*
+ * dwscan_bwd -- gradients of dwscan_fwd, given its y, the gradient dy of y and
+ * (or NULL: zero) dh_last of h_last.  With s = sigmoid(r), i = sigmoid(g),
+ * w = scale * softplus(decay) * s, m = sqrt(1 - a^2), h_{t-1} = y_{t-1} as
+ * stored (h0 before the first frame), and backwards from the last valid frame
+ *   G_t = dy_t + a_{t+1} * G_{t+1}          (dh_last in the last one's place)
+ *   dx  = G m i,   dg = G m x i (1 - i)
+ *   q   = w * (G i x a^2 / m - G a h_{t-1}),   dr = q * (1 - s)
+ *   ddecay[c] = sigmoid(decay) / softplus(decay) * sum_{b,t} q
+ *   dh0 = a_0 * G_0                          (dh_last where there is no frame)
+ * and dx = dr = dg = 0 at frames t >= len_b, whose inputs are not read.  Where
+ * the decay vanishes (w = 0) q is its limit, 0.  ddecay is float, added in a
+ * fixed order (float32 over each thread's frames, fp64 across workgroups), so
+ * repeated calls agree bit for bit.
+ *
+ * Each of dx, dr, dg, ddecay ([C] float) and dh0 ([B][C] float; may be dh_last)
+ * may be NULL (not computed).  An empty batch still writes ddecay = 0.
+ * Errors: as dwscan_fwd, and DW_ERR_INVALID_ARG for gradients that alias an
+ * input or each other.
+ */
+dw_status dwscan_bwd(const dw_scan *shape, const void *x, const void *r, const void *g, const float *decay,
+                     const int32_t *lengths, const float *h0, const void *y, const void *dy, const float *dh_last,
+                     void *dx, void *dr, void *dg, float *ddecay, float *dh0, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * Norm of the heads of queries and keys, and the rotation by their positions.
+ *
+ * q [B][T][H][D], k and v [B][T][Hkv][D] and their outputs and gradients, with
+ * the D elements of a head next to each other and any distance between items,
+ * frames and heads, given in elements (slices of one projection's output, or a
+ * cache; an input's distance may be 0, its gradients are then not summed).
+ */
+typedef enum {
+    DW_PAIRS_HALVES = 0,     /* element j of the first R turns with element j + R/2 */
+    DW_PAIRS_NEIGHBOURS = 1, /* element 2j with element 2j + 1 */
+    DW_PAIRS_INT32_LO_ = -2147483647 - 1,
+    DW_PAIRS_INT32_HI_ = 2147483647
+} dw_pairs;
+
+typedef struct {
+    int64_t B, T;
+    int64_t H, Hkv;   /* heads of q, and of k and v */
+    int64_t D, R;     /* elements of a head, 1 to 128; the first R of them are rotated (even, 0: none) */
+    int64_t S;        /* frames of k_out and v_out where they are caches (place given) */
+    dw_strides q, k, v;
+    dw_strides q_out, k_out, v_out; /* dwrope_bwd: of dq_out and dk_out */
+    dw_strides dq, dk;              /* dwrope_bwd only */
+    float eps;        /* of the norm, not negative */
+    dw_pairs pairs;
+    dw_dtype dtype;   /* of all tensors but freq */
+} dw_rope;
+
+/*
+ * dwrope_fwd -- for each head of q and k at frame t < len_b:
+ *   n[d] = x[d] / sqrt(sum_d x[d]^2 / D + eps) * gamma[d]
+ *   (out[i], out[j]) = (n[i] cos f - n[j] sin f, n[j] cos f + n[i] sin f)
+ * for the pairs (i, j) of the first R elements, f = (pos_b + t) * freq[p] for
+ * pair p; the other elements are n.  q_gamma, k_gamma: [D] in the storage type
+ * or NULL (ones); freq: [R/2] double, in radians a frame (NULL when R = 0);
+ * pos: [B] int32 or NULL (zeros).  The angle is formed and reduced in 64 bits,
+ * so far positions keep their digits; all else is float32, rounded once.
+ *
+ * place NULL: k_out is [B][T][Hkv][D]; rows at frames t >= len_b of every
+ * output are zeros, and their inputs are not read.  place [B] int32: k_out and
+ * v_out are caches of S frames, and frame t of item b goes to frame
+ * place_b + t of its cache; frames past the length, and those whose place is
+ * outside the cache, are not written there (q_out is as above).
+ * v, with v_out, is copied as it is (a stream's keys and values thus reach the
+ * cache in one call); both NULL: no values.
+ * H or Hkv may be 0 (q or k alone).  In place: q_out may be q, and k_out k
+ * (without place), with the same strides.
+ * Errors: DW_ERR_INVALID_ARG for a null pointer that holds elements, a negative
+ * size or stride, an odd R or R > D, R > 0 without freq, a negative or NaN eps, a bad
+ * dtype or pairs, v without v_out or the other way round, or an output that
+ * aliases another tensor; DW_ERR_UNSUPPORTED for D > 128 or sizes too large for
+ * one launch.
+ */
+dw_status dwrope_fwd(const dw_rope *shape, const void *q, const void *k, const void *v, const void *q_gamma,
+                     const void *k_gamma, const double *freq, const int32_t *lengths, const int32_t *pos,
+                     const int32_t *place, void *q_out, void *k_out, void *v_out, void *stream);
+
+/* Bytes of device workspace dwrope_bwd needs when it computes dq_gamma or
+ * dk_gamma.  0 for sizes that the call refuses. */
+size_t dwrope_bwd_workspace_bytes(const dw_rope *shape);
+
+/*
+ * dwrope_bwd -- gradients of dwrope_fwd without caches, given the gradients
+ * dq_out and dk_out of its outputs.  With u the gradient turned back by the
+ * angles, rstd = 1 / sqrt(sum x^2 / D + eps), xh = x * rstd, e = u * gamma:
+ *   dx[d]     = rstd * (e[d] - xh[d] * sum(e xh) / D)
+ *   dgamma[d] = sum over items, frames and heads of u[d] * xh[d]
+ * Rows at frames t >= len_b get zero gradients, and their inputs are not read.
+ * dq, dk (storage type), dq_gamma, dk_gamma ([D] float) may each be NULL (not
+ * computed).  The gammas' gradients are added in a fixed order (float32 within
+ * a workgroup, fp64 across them), so repeated calls agree bit for bit; an empty
+ * batch writes zeros.  In place: dq may be dq_out or q, dk dk_out or k, with the
+ * same strides.
+ * Errors: as dwrope_fwd, and DW_ERR_WORKSPACE for a missing or short workspace
+ * (which starts on a multiple of 16 bytes, or DW_ERR_INVALID_ARG).
+ */
+dw_status dwrope_bwd(const dw_rope *shape, const void *q, const void *k, const void *q_gamma, const void *k_gamma,
+                     const double *freq, const int32_t *lengths, const int32_t *pos, const void *dq_out,
+                     const void *dk_out, void *dq, void *dk, float *dq_gamma, float *dk_gamma, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Activations whose input is kept in 8 bits for the backward pass.
+ *
+ * An input row is one part of C columns, or two for DW_ACT_GLU (its rows are
+ * 2C wide).  Each group of 32 columns of a part (the last may be shorter) has a
+ * scale 2^(code - 127): the smallest power of two, not below 2^-126, with which
+ * the group's largest magnitude is at most 127.  kept holds x / scale rounded
+ * to nearest (ties to even) as int8, so kept * scale is within half a scale of
+ * x and is itself a bfloat16.  The largest scale is 2^121: magnitudes past 127
+ * times it (3.38e38) are kept as that.  A group with an infinity or a NaN has
+ * code 255 and stands for NaN.
+ */
+typedef enum {
+    DW_ACT_NONE = 0, /* the input itself: to keep any activation in 8 bits */
+    DW_ACT_SILU = 1, /* x * sigmoid(x) */
+    DW_ACT_GLU = 2,  /* the first C columns times the sigmoid of the last C */
+    DW_ACT_INT32_LO_ = -2147483647 - 1,
+    DW_ACT_INT32_HI_ = 2147483647
+} dw_act;
+
+/*
+ * dwact_fwd -- y = act(x), from the unrounded x, and the checkpoint of x.
+ * x: [B][T][parts * C], y: [B][T][C], in the storage type dtype; kept:
+ * [B][T][parts * C] int8; codes: [B][T][parts * ceil(C / 32)] uint8; all dense.
+ * y, or kept and codes together, may be NULL (not computed).  At frames
+ * t >= len_b all outputs are zero and x is not read.  y may be x (not for
+ * DW_ACT_GLU).
+ * Errors: DW_ERR_INVALID_ARG for a null x that holds elements, kept without
+ * codes or the other way round, a negative size, a bad act or dtype, or outputs
+ * that alias; DW_ERR_UNSUPPORTED for sizes too large for one launch.
+ */
+dw_status dwact_fwd(dw_act act, const void *x, const int32_t *lengths, void *y, int8_t *kept, uint8_t *codes,
+                    int64_t B, int64_t T, int64_t C, dw_dtype dtype, void *stream);
+
+/*
+ * dwact_bwd -- from the checkpoint alone: dx = dy * act'(x') and y = act(x')
+ * for x' = kept * scale (for a weight's gradient behind the activation, or, with
+ * DW_ACT_NONE, the kept activation itself for any other gradient).
+ *   SiLU: dx = dy * s (1 + x' (1 - s)), s = sigmoid(x')
+ *   GLU:  dx = (dy * sigmoid(b'), dy * a' * sigmoid(b') (1 - sigmoid(b')))
+ * dy, y: [B][T][C]; dx: [B][T][parts * C]; dtype their storage type.  dx or y
+ * may be NULL (not computed); dy is needed with dx only.  dx may be dy (not for
+ * DW_ACT_GLU).  At frames t >= len_b outputs are zero and nothing is read.
+ * Errors: as dwact_fwd.
+ */
+dw_status dwact_bwd(dw_act act, const int8_t *kept, const uint8_t *codes, const int32_t *lengths, const void *dy,
+                    void *dx, void *y, int64_t B, int64_t T, int64_t C, dw_dtype dtype, void *stream);
 
 #ifdef __cplusplus
 }
