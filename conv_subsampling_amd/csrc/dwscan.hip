@@ -10,25 +10,33 @@
 // products of decays are exponentials of sums of w.
 //
 // Frames in parallel: a run of frames maps the state h before it to P h + H
-// behind it, and runs compose.  A thread takes 4 channels of FR frames, in
-// registers; 4 threads along the frames share a wave and exchange (P, H) by
-// lane swaps, the 4 waves of a workgroup through LDS, so that a workgroup moves
-// through its frames in tiles of 16 * FR and memory sees each tensor once.
-// Where items and channels make too few workgroups, the frames are shared out
-// in chunks: a first kernel finds each chunk's (P, H), a second starts from
-// what those before it leave.
+// behind it, and runs compose.  A thread takes 2 channels of FR frames, in
+// registers; the 2 threads along the frames that share a wave exchange (P, H)
+// by a lane swap, the 4 waves of a workgroup through LDS, so a workgroup does a
+// tile of 8 * FR frames and memory sees each tensor once.
+//
+// Tiles of one item are joined in one of two ways.  Where items and channels
+// make workgroups enough, a workgroup goes through the tiles of its chain (an
+// item's 64 channels) in turn.  Elsewhere every tile has a workgroup of its
+// own, which publishes the (P, H) of its tile and composes those of the tiles
+// before it, in their order, so results repeat bit for bit.  Tiles are given
+// out by a counter for each chain: whoever waits for a tile waits for a
+// workgroup that has started, and that one waits for earlier ones alone.
 #include "launch.h"
 #include "rowops.h"
 #include "quad.h"
 
 namespace dw {
 
-constexpr int kScanThreads = 256;
-constexpr int kScanLanes = 16;                                // threads across the channels
+constexpr int kScanThreads = 256, kScanWaves = kScanThreads / 64;
+constexpr int kScanPair = 2;                                  // channels of a thread
+constexpr int kScanLanes = 32;                                // threads across the channels
 constexpr int kScanRows = kScanThreads / kScanLanes;          // and along frames, or items
-constexpr int kScanCols = kScanLanes * kQuad;                 // channels of a workgroup
-constexpr int kScanFwdRun = 8, kScanBwdRun = 4;               // frames of a thread in a tile
-constexpr int64_t kScanBlocks = 512;                          // workgroups that fill the GPU
+constexpr int kScanCols = kScanLanes * kScanPair;             // channels of a workgroup
+constexpr int kScanShortRun = 8;                              // frames of a thread where they are few
+constexpr int kScanFwdRun = 16, kScanBwdRun = 8;              // and in a tile
+constexpr int kScanGroup = 16;                                // tiles whose composition is published too
+constexpr int kScanPolls = 1 << 22;                           // of a word, before its wait is given up with a NaN
 
 struct ScanArgs {
     const void *x, *r, *g, *yin, *dy;
@@ -37,23 +45,75 @@ struct ScanArgs {
     const float* start;   // the state (backward: its gradient) that enters the first (last) frame, NULL: zero
     void *y, *dx, *dr, *dg;
     const float* h0;      // backward: the state before the first frame
-    float *end, *copy;    // what leaves the last (first) frame; a copy of `start` beside the summaries
-    float* summary;       // [2][B][chunks][C]: P, then H
+    float* end;           // what leaves the last (first) frame
+    uint32_t* tickets;    // [chains]: tiles given out
+    uint64_t* words;      // [chains][tiles + tiles / kScanGroup][kScanCols]: published (P, H)
     double* partial;      // backward: [row blocks][C], sums for ddecay
     FrameStride xs, rs, gs, ys, dys, dxs, drs, dgs;
-    int64_t B, T, chunk;  // frames of a chunk, whole tiles
-    int32_t C, col_blocks, chunks;
+    int64_t B, T;
+    int32_t C, col_blocks, tiles;
     float scale;
 };
 
-// What a phase of the work does: all frames of an item in one go; a chunk's
-// (P, H) alone; a chunk from the state that the summaries before it give.
-enum { kScanWhole = 0, kScanSummary = 1, kScanJoin = 2 };
-
-struct Decay {
-    float d, w;  // 1 - a, -log a
+// ---------------------------------------------------------------------------
+// Two neighbouring channels
+// ---------------------------------------------------------------------------
+template <typename S>
+struct PairRaw;
+template <>
+struct PairRaw<float> {
+    typedef u32x2 type;
+    typedef u32x2 access __attribute__((aligned(4)));
 };
+template <>
+struct PairRaw<uint16_t> {
+    typedef uint32_t type;
+    typedef uint32_t access __attribute__((aligned(2)));
+};
+template <typename S>
+using pair_raw = typename PairRaw<S>::type;
 
+// have: channels from p on; TAIL: it may be one.
+template <typename S, bool TAIL>
+__device__ __forceinline__ pair_raw<S> load_pair(const S* p, int have) {
+    if (!TAIL || have >= kScanPair) return *reinterpret_cast<const typename PairRaw<S>::access*>(p);
+    pair_raw<S> q = {};
+    if (have == 1) {
+        if constexpr (sizeof(S) == 4)
+            q[0] = __float_as_uint(p[0]);
+        else
+            q = p[0];
+    }
+    return q;
+}
+
+template <typename S>
+__device__ __forceinline__ float pair_at(const pair_raw<S>& q, int e) {
+    if constexpr (sizeof(S) == 4)
+        return __uint_as_float(q[e]);
+    else
+        return e ? bf16_hi(q) : bf16_lo(q);
+}
+
+template <typename S, bool TAIL>
+__device__ __forceinline__ void store_pair(S* p, int have, f32x2 v) {
+    if constexpr (sizeof(S) == 4) {
+        if (!TAIL || have >= kScanPair)
+            *reinterpret_cast<typename PairRaw<S>::access*>(p) = u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])};
+        else if (have == 1)
+            p[0] = v[0];
+    } else {
+        const uint32_t q = pack_bf16x2(v[0], v[1]);
+        if (!TAIL || have >= kScanPair)
+            *reinterpret_cast<typename PairRaw<S>::access*>(p) = q;
+        else if (have == 1)
+            p[0] = (uint16_t)q;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The step's functions
+// ---------------------------------------------------------------------------
 // 1 - exp(-w): a series where the difference would cancel (its first left out
 // term is 2^-24.4 of it at w = 1/8), the exponential beyond (off by 2^-21 at most).
 __device__ __forceinline__ float one_minus_exp(float w) {
@@ -75,162 +135,174 @@ __device__ __forceinline__ float softplus_slope(float v) {
     return v < -16.0f ? 1.0f : 1.0f / ((1.0f + expf(-v)) * softplus(v));
 }
 
+// ---------------------------------------------------------------------------
+// Runs and their composition
+// ---------------------------------------------------------------------------
 struct Run {
-    float p[kQuad], h[kQuad];  // state behind = p * state before + h
+    f32x2 p, h;  // state behind = p * state before + h
 };
 
-// The value of the wave's four rows of 16 lanes, in all lanes.
-__device__ __forceinline__ void wave_rows(float v, float out[4]) {
-    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    const auto e = __builtin_amdgcn_permlane32_swap(s[0], s[0], false, false);  // rows 0, 0, 2, 2
-    const auto o = __builtin_amdgcn_permlane32_swap(s[1], s[1], false, false);  // rows 1, 1, 3, 3
-    out[0] = __uint_as_float(e[0]);
-    out[1] = __uint_as_float(o[0]);
-    out[2] = __uint_as_float(e[1]);
-    out[3] = __uint_as_float(o[1]);
+__device__ __forceinline__ Run compose(const Run& first, const Run& then) {
+    return {first.p * then.p, then.p * first.h + then.h};
 }
 
-// From the threads' runs of one tile, in their order along it (REVERSE: last
-// first), and the state `carry` that enters the tile: the state that enters each
-// thread's run, and in `carry` the one that leaves the tile.  `total`, if given,
-// is composed with the tile's P.
+__device__ __forceinline__ f32x2 through(const Run& run, f32x2 state) { return run.p * state + run.h; }
+
+// The value of the wave's two rows of 32 lanes, in all lanes.
+__device__ __forceinline__ void wave_rows(float v, float& low, float& high) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    low = __uint_as_float(s[0]);
+    high = __uint_as_float(s[1]);
+}
+
+struct TileRuns {
+    Run before;  // this thread's part of the tile that comes before its run
+    Run all;     // the whole tile
+};
+
+// Composes the runs of the threads along the frames (REVERSE: last first).
 template <int SEGS, bool REVERSE>
-__device__ __forceinline__ void enter_runs(const Run& run, float carry[kQuad], float in[kQuad], float* total,
-                                           float (*lds)[2][kScanCols]) {
-    if constexpr (SEGS == 1) {
+__device__ __forceinline__ TileRuns tile_runs(const Run& run, float (*lds)[2][kScanCols]) {
+    const Run one = {f32x2(1.0f), f32x2(0.0f)};
+    if constexpr (SEGS == 1) return {one, run};
+    Run low, high;
 #pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-            in[e] = carry[e];
-            carry[e] = run.h[e] + run.p[e] * carry[e];
-            if (total) total[e] *= run.p[e];
-        }
-        return;
+    for (int e = 0; e < kScanPair; ++e) {
+        float l, h;
+        wave_rows(run.p[e], l, h);
+        low.p[e] = l, high.p[e] = h;
+        wave_rows(run.h[e], l, h);
+        low.h[e] = l, high.h[e] = h;
     }
-    const int row = threadIdx.x / kScanLanes % 4;
-    float p[kQuad][4], h[kQuad][4];
-#pragma unroll
-    for (int e = 0; e < kQuad; ++e) {
-        wave_rows(run.p[e], p[e]);
-        wave_rows(run.h[e], h[e]);
+    const Run &first = REVERSE ? high : low, &second = REVERSE ? low : high;
+    const bool upper = threadIdx.x % 64 >= kScanLanes, later = REVERSE ? !upper : upper;
+    Run before = {later ? first.p : one.p, later ? first.h : one.h};
+    const Run wave = compose(first, second);
+    if constexpr (SEGS == 2) return {before, wave};
+    const int at = threadIdx.x / 64, col = threadIdx.x % kScanLanes * kScanPair;
+    if (!upper) {
+        *(f32x2*)&lds[at][0][col] = wave.p;
+        *(f32x2*)&lds[at][1][col] = wave.h;
     }
-    if constexpr (SEGS > 4) {
-        const int wave = threadIdx.x / 64, col = threadIdx.x % kScanLanes * kQuad;
-        if (row == 0) {
+    __syncthreads();
+    Run all = one, mine = one;
 #pragma unroll
-            for (int e = 0; e < kQuad; ++e) {
-                float ph = p[e][0], hh = h[e][0];
-                if constexpr (REVERSE) {
-                    ph = p[e][3], hh = h[e][3];
-#pragma unroll
-                    for (int q = 2; q >= 0; --q) hh = h[e][q] + p[e][q] * hh, ph *= p[e][q];
-                } else {
-#pragma unroll
-                    for (int q = 1; q < 4; ++q) hh = h[e][q] + p[e][q] * hh, ph *= p[e][q];
-                }
-                lds[wave][0][col + e] = ph;
-                lds[wave][1][col + e] = hh;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-            float state = carry[e], mine = carry[e];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int at = REVERSE ? 3 - q : q;
-                if (at == wave) mine = state;
-                state = lds[at][1][col + e] + lds[at][0][col + e] * state;
-                if (total) total[e] *= lds[at][0][col + e];
-            }
-            carry[e] = state;
-            in[e] = mine;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) in[e] = carry[e];
+    for (int q = 0; q < kScanWaves; ++q) {
+        const int w = REVERSE ? kScanWaves - 1 - q : q;
+        const Run next = {*(const f32x2*)&lds[w][0][col], *(const f32x2*)&lds[w][1][col]};
+        if (w == at) mine = all;
+        all = q ? compose(all, next) : next;
     }
-#pragma unroll
-    for (int e = 0; e < kQuad; ++e) {
-        float state = in[e], mine = in[e];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int at = REVERSE ? 3 - q : q;
-            if (at == row) mine = state;
-            state = h[e][at] + p[e][at] * state;
-            if (SEGS <= 4 && total) total[e] *= p[e][at];
-        }
-        in[e] = mine;
-        if constexpr (SEGS <= 4) carry[e] = state;
-    }
+    return {compose(mine, before), all};
 }
 
-// Where a thread works.
+// A published (P, H): P is a product of decays, so its sign bit is free to say
+// that the word holds something (cleared words are 0).  One 64-bit access at
+// device scope, which passes the XCDs' own L2 caches, needs no order among words.
+__device__ __forceinline__ void publish(uint64_t* word, float p, float h) {
+    const uint64_t v = (uint64_t)__float_as_uint(h) << 32 | __float_as_uint(p) | 0x80000000u;
+    __hip_atomic_store(word, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ uint64_t peek(const uint64_t* word) {
+    return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// What `count` published words in a row compose to, for each thread's channels.
+// Each of the 4 waves takes a quarter of them, a lane for each channel; the
+// quarters are composed in order.  Every word read here belongs to a workgroup
+// that has started.
+__device__ __forceinline__ Run fold_words(const uint64_t* words, int count, float (*lds)[2][kScanCols]) {
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int each = (count + kScanWaves - 1) / kScanWaves;
+    const int first = wave * each, last = first + each < count ? first + each : count;
+    float p = 1.0f, h = 0.0f;
+    constexpr int kFly = 4;  // reads in flight together
+    for (int k = first; k < last; k += kFly) {
+        uint64_t v[kFly];
+#pragma unroll
+        for (int j = 0; j < kFly; ++j) v[j] = k + j < last ? peek(words + (int64_t)(k + j) * kScanCols + lane) : 0;
+#pragma unroll
+        for (int j = 0; j < kFly; ++j) {
+            if (k + j >= last) break;
+            for (int n = 0; (uint32_t)v[j] == 0 && n < kScanPolls; ++n) {
+                __builtin_amdgcn_s_sleep(1);
+                v[j] = peek(words + (int64_t)(k + j) * kScanCols + lane);
+            }
+            const bool there = (uint32_t)v[j] != 0;
+            const float wp = there ? __uint_as_float((uint32_t)v[j] & 0x7fffffffu) : __builtin_nanf("");
+            p *= wp;
+            h = wp * h + __uint_as_float((uint32_t)(v[j] >> 32));
+        }
+    }
+    lds[wave][0][lane] = p;
+    lds[wave][1][lane] = h;
+    __syncthreads();
+    const int col = threadIdx.x % kScanLanes * kScanPair;
+    Run all = {*(const f32x2*)&lds[0][0][col], *(const f32x2*)&lds[0][1][col]};
+#pragma unroll
+    for (int q = 1; q < kScanWaves; ++q)
+        all = compose(all, {*(const f32x2*)&lds[q][0][col], *(const f32x2*)&lds[q][1][col]});
+    return all;
+}
+
+// ---------------------------------------------------------------------------
+// Where a thread works, and its loads and stores
+// ---------------------------------------------------------------------------
 struct ScanPlace {
-    int64_t b, first, last;  // item, frames [first, last) of its workgroup's chunk
-    int64_t len;             // valid frames of the item
-    int chunk, seg, col, have;
+    int64_t b;      // item
+    int64_t len;    // its valid frames
+    uint32_t chain; // of the workgroup: item (or items) and column block
+    int seg, col, have;
 };
 
-template <int SEGS, int PHASE>
-__device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a) {
+template <int SEGS>
+__device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a, uint32_t chain) {
     ScanPlace p;
     const int row = threadIdx.x / kScanLanes;
-    const uint32_t rest = blockIdx.x / (uint32_t)a.col_blocks;
-    p.col = (int)(blockIdx.x - rest * a.col_blocks) * kScanCols + threadIdx.x % kScanLanes * kQuad;
+    const uint32_t rest = chain / (uint32_t)a.col_blocks;
+    p.chain = chain;
+    p.col = (int)(chain - rest * a.col_blocks) * kScanCols + threadIdx.x % kScanLanes * kScanPair;
     p.have = a.C - p.col;
     if (p.have <= 0) p.col = 0;  // past the last channel: loads what is there, stores nothing
     p.seg = row % SEGS;
-    if constexpr (PHASE == kScanWhole) {
-        p.chunk = 0;
-        p.b = (int64_t)rest * (kScanRows / SEGS);
-        if constexpr (SEGS == 4) p.b += __builtin_amdgcn_readfirstlane(row / SEGS);  // one item a wave
-        if constexpr (SEGS == 1) p.b += row;
-        p.first = 0, p.last = a.T;
-    } else {
-        const uint32_t b = rest / (uint32_t)a.chunks;
-        p.b = b;
-        p.chunk = (int)(rest - b * a.chunks);
-        p.first = p.chunk * a.chunk;
-        p.last = p.first + a.chunk < a.T ? p.first + a.chunk : a.T;
-    }
+    p.b = (int64_t)rest * (kScanRows / SEGS);
+    if constexpr (SEGS == 2) p.b += __builtin_amdgcn_readfirstlane(row / SEGS);  // one item a wave
+    if constexpr (SEGS == 1) p.b += row;
     p.len = p.b < a.B ? item_length(a.lengths, p.b, a.T) : 0;
     return p;
 }
 
-// One thread's FR frames of a tensor in the tile from frame t0 on; frames at or
-// past the length (`valid` of the tile's are below it, at least one) read the
-// last valid one and become `dead` (the bits of one stored value).
+// A thread's frames of a tensor in the tile from frame t0 on.  Frames at or past
+// the length (`valid` of the tile's are below it, at least one) read the last
+// valid one and become `dead` (the bits of two stored values).
 template <typename S, bool TAIL, int FR>
-__device__ __forceinline__ void load_run(quad_raw<S> out[FR], const void* base, const FrameStride& s,
+__device__ __forceinline__ void load_run(pair_raw<S> out[FR], const void* base, const FrameStride& s,
                                          const ScanPlace& p, int64_t t0, int valid, bool full, uint32_t dead) {
     const S* tile = (const S*)base + p.b * s.item + t0 * s.frame;
     const int at = p.seg * FR;
     const uint32_t fs = (uint32_t)s.frame;
     if (full) {
 #pragma unroll
-        for (int f = 0; f < FR; ++f) out[f] = load_quad<S, TAIL>(tile + (uint32_t)(f * fs) + (at * fs + p.col), p.have);
+        for (int f = 0; f < FR; ++f) out[f] = load_pair<S, TAIL>(tile + (uint32_t)(f * fs) + (at * fs + p.col), p.have);
         return;
     }
 #pragma unroll
     for (int f = 0; f < FR; ++f) {
         const int t = at + f < valid ? at + f : valid - 1;
-        out[f] = load_quad<S, TAIL>(tile + ((uint32_t)t * fs + p.col), p.have);
-        if (at + f >= valid) {
-#pragma unroll
-            for (int e = 0; e < (int)(sizeof(quad_raw<S>) / 4); ++e) out[f][e] = dead;
-        }
+        out[f] = load_pair<S, TAIL>(tile + ((uint32_t)t * fs + p.col), p.have);
+        if (at + f >= valid) out[f] = dead;
     }
 }
 
-// The frame's values, zeros past the length; frames at or past `rows` are not
-// the tile's.
+// A frame's values, zeros past the length; frames at or past `rows` are not the tile's.
 template <typename S, bool TAIL, int FR>
 __device__ __forceinline__ void store_frame(void* base, const FrameStride& s, const ScanPlace& p, int64_t t0, int f,
-                                            int valid, int rows, const Vf<kQuad>& v) {
+                                            int valid, int rows, f32x2 v) {
     const int t = p.seg * FR + f;
     if (t >= rows) return;
     S* tile = (S*)base + p.b * s.item + t0 * s.frame;
-    store_quad<S, TAIL>(tile + ((uint32_t)t * (uint32_t)s.frame + p.col), p.have, t < valid ? v : vzero<kQuad>());
+    store_pair<S, TAIL>(tile + ((uint32_t)t * (uint32_t)s.frame + p.col), p.have, t < valid ? v : f32x2(0.0f));
 }
 
 template <typename S>
@@ -238,272 +310,280 @@ constexpr uint32_t closed_gate() {  // -infinity, in each stored value
     return sizeof(S) == 4 ? 0xff800000u : 0xff80ff80u;
 }
 
-__device__ __forceinline__ Vf<kQuad> load_state(const float* base, int64_t row, int32_t C, const ScanPlace& p) {
-    return base ? widen_quad<float>(load_quad<float, true>(base + row * C + p.col, p.have)) : vzero<kQuad>();
+__device__ __forceinline__ f32x2 load_state(const float* base, int64_t row, int32_t C, const ScanPlace& p) {
+    f32x2 v = {0.0f, 0.0f};
+    if (base && p.have > 0) v[0] = base[row * C + p.col];
+    if (base && p.have > 1) v[1] = base[row * C + p.col + 1];
+    return v;
 }
 
-template <typename S, bool TAIL, int SEGS, int FR, int PHASE>
+__device__ __forceinline__ void store_state(float* base, int64_t row, int32_t C, const ScanPlace& p, f32x2 v) {
+    if (p.have > 0) base[row * C + p.col] = v[0];
+    if (p.have > 1) base[row * C + p.col + 1] = v[1];
+}
+
+// The tile that this workgroup takes of its chain, in the order of the chain.
+__device__ __forceinline__ int take_tile(uint32_t* ticket, int* lds) {
+    if (threadIdx.x == 0) *lds = (int)__hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*lds);
+}
+
+// The first row of threads publishes a run of the workgroup's 64 channels.
+__device__ __forceinline__ void publish_run(uint64_t* words, const Run& run) {
+    if (threadIdx.x >= kScanLanes) return;
+#pragma unroll
+    for (int e = 0; e < kScanPair; ++e) publish(words + threadIdx.x * kScanPair + e, run.p[e], run.h[e]);
+}
+
+// The state that enters a tile whose runs are known, and `carry`, the one that
+// leaves it (LINKED: both 0 unless `wanted`).  Where tiles are linked, the chain's first one takes up
+// the state that enters the chain and hands it on in its word, so nothing reads
+// that state after the last tile has written its own.  The last tile of 16
+// publishes what they compose to: tile `at` reads at / 16 such words and those
+// of its own group.
+template <bool LINKED>
+__device__ __forceinline__ f32x2 enter_tile(const ScanArgs& a, const ScanPlace& p, const Run& all, int at, bool wanted,
+                                            f32x2& carry, float (*lds)[kScanWaves][2][kScanCols]) {
+    const f32x2 zero = {0.0f, 0.0f};
+    if constexpr (!LINKED) {
+        const f32x2 in = carry;
+        carry = through(all, carry);
+        return in;
+    }
+    const int group = at / kScanGroup, of_group = at % kScanGroup;
+    uint64_t* words = a.words + (int64_t)p.chain * (a.tiles + a.tiles / kScanGroup) * kScanCols;
+    uint64_t* groups = words + (int64_t)a.tiles * kScanCols;
+    if (at == 0) {
+        const f32x2 in = carry;
+        carry = through(all, carry);
+        publish_run(words, {zero, carry});
+        return in;
+    }
+    publish_run(words + (int64_t)at * kScanCols, all);
+    const bool closes = of_group == kScanGroup - 1;
+    if (!wanted && !closes) return zero;
+    Run before = {f32x2(1.0f), zero};
+    if (of_group > 0) before = fold_words(words + (int64_t)group * kScanGroup * kScanCols, of_group, lds[0]);
+    if (closes) publish_run(groups + (int64_t)group * kScanCols, compose(before, all));
+    if (!wanted) return zero;
+    if (group > 0) before = compose(fold_words(groups, group, lds[1]), before);
+    carry = through(all, before.h);  // the first tile's word has P = 0: H is the state
+    return before.h;
+}
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+template <typename S, bool TAIL, int SEGS, int FR, bool LINKED>
 __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a) {
     constexpr int kTileFrames = SEGS * FR;
-    __shared__ float lds[2][4][2][kScanCols];
-    const ScanPlace p = scan_place<SEGS, PHASE>(a);
-    if (p.b >= a.B) return;  // SEGS < 16, where no thread waits for another wave
-    float rate[kQuad], carry[kQuad], total[kQuad];
-    {
-        const Vf<kQuad> decay = load_state(a.decay, 0, a.C, p), h0 = load_state(a.start, p.b, a.C, p);
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-            rate[e] = decay_rate(decay.v[e], a.scale);
-            carry[e] = PHASE == kScanSummary ? 0.0f : h0.v[e];
-            total[e] = 1.0f;
-        }
-        if (PHASE == kScanSummary && p.chunk == 0 && p.seg == 0 && p.have > 0)
-            store_quad<float, true>(a.copy + p.b * a.C + p.col, p.have, h0);
-    }
-    const int64_t plane = a.B * a.chunks * (int64_t)a.C;
-    if constexpr (PHASE == kScanJoin) {
-        for (int c = 0; c < p.chunk; ++c) {
-            const Vf<kQuad> P = load_state(a.summary, p.b * a.chunks + c, a.C, p);
-            const Vf<kQuad> H = load_state(a.summary + plane, p.b * a.chunks + c, a.C, p);
-#pragma unroll
-            for (int e = 0; e < kQuad; ++e) carry[e] = H.v[e] + P.v[e] * carry[e];
-        }
-    }
+    __shared__ float lds[LINKED ? 3 : 2][kScanWaves][2][kScanCols];
+    __shared__ int ticket;
+    const uint32_t chains = LINKED ? gridDim.x / (uint32_t)a.tiles : 0;
+    const ScanPlace p = scan_place<SEGS>(a, LINKED ? blockIdx.x % chains : blockIdx.x);
+    if (p.b >= a.B) return;  // SEGS < 8, where no thread waits for another wave
+    int tile = LINKED ? take_tile(a.tickets + p.chain, &ticket) : 0;
+    const int end = LINKED ? tile + 1 : a.tiles;
+    const f32x2 decay = load_state(a.decay, 0, a.C, p);
+    const f32x2 rate = {decay_rate(decay[0], a.scale), decay_rate(decay[1], a.scale)};
+    f32x2 carry = tile == 0 ? load_state(a.start, p.b, a.C, p) : f32x2(0.0f);
     int turn = 0;
-    for (int64_t t0 = p.first; t0 < p.last; t0 += kTileFrames) {
-        const int64_t left = p.len - t0, size = p.last - t0;
+    for (; tile < end; ++tile) {
+        const int64_t t0 = (int64_t)tile * kTileFrames, left = p.len - t0, size = a.T - t0;
         const int rows = size < kTileFrames ? (int)size : kTileFrames;
         const int valid = left < 0 ? 0 : left < rows ? (int)left : rows;
-        Vf<kQuad> y[FR] = {};
+        f32x2 d[FR], u[FR];
+        Run all = {f32x2(1.0f), f32x2(0.0f)}, before = all;
         if (valid > 0) {
-            quad_raw<S> xr[FR], rr[FR], gr[FR];
+            pair_raw<S> xr[FR], rr[FR], gr[FR];
             const bool full = valid == kTileFrames;
             load_run<S, TAIL, FR>(rr, a.r, a.rs, p, t0, valid, full, closed_gate<S>());
-            load_run<S, TAIL, FR>(xr, a.x, a.xs, p, t0, valid, full, 0);
             load_run<S, TAIL, FR>(gr, a.g, a.gs, p, t0, valid, full, 0);
-            float d[FR][kQuad], u[FR][kQuad];
+            load_run<S, TAIL, FR>(xr, a.x, a.xs, p, t0, valid, full, 0);
             Run run;
 #pragma unroll
-            for (int e = 0; e < kQuad; ++e) {
+            for (int e = 0; e < kScanPair; ++e) {
                 float w = 0.0f, h = 0.0f;
 #pragma unroll
                 for (int f = 0; f < FR; ++f) {
-                    const float wf = rate[e] * sigmoid_of<S>(quad_at<S>(rr[f], e));
+                    const float wf = rate[e] * sigmoid_of<S>(pair_at<S>(rr[f], e));
                     const float df = one_minus_exp(wf);
                     const float m = __builtin_amdgcn_sqrtf(df * (2.0f - df));
+                    const float uf = m * (sigmoid_of<S>(pair_at<S>(gr[f], e)) * pair_at<S>(xr[f], e));
                     d[f][e] = df;
-                    u[f][e] = m * (sigmoid_of<S>(quad_at<S>(gr[f], e)) * quad_at<S>(xr[f], e));
+                    u[f][e] = uf;
                     w += wf;
-                    h = __builtin_fmaf(-df, h, h) + u[f][e];
+                    h = __builtin_fmaf(-df, h, h) + uf;
                 }
                 run.p[e] = __builtin_amdgcn_exp2f(w * -1.44269504f);
                 run.h[e] = h;
             }
-            float in[kQuad];
-            enter_runs<SEGS, false>(run, carry, in, PHASE == kScanSummary ? total : nullptr, lds[turn]);
+            const TileRuns t = tile_runs<SEGS, false>(run, lds[turn]);
             turn ^= 1;
-            if constexpr (PHASE != kScanSummary) {
+            all = t.all;
+            before = t.before;
+        }
+        const bool wanted = valid > 0 || (a.end && tile == a.tiles - 1);
+        f32x2 h = through(before, enter_tile<LINKED>(a, p, all, tile, wanted, carry, lds + 1));
+        if (p.have > 0) {
 #pragma unroll
-                for (int e = 0; e < kQuad; ++e) {
-                    float h = in[e];
+            for (int f = 0; f < FR; ++f) {
+                if (valid > 0) {
 #pragma unroll
-                    for (int f = 0; f < FR; ++f) y[f].v[e] = h = __builtin_fmaf(-d[f][e], h, h) + u[f][e];
+                    for (int e = 0; e < kScanPair; ++e) h[e] = __builtin_fmaf(-d[f][e], h[e], h[e]) + u[f][e];
                 }
-            }
-        }
-        if constexpr (PHASE != kScanSummary) {
-            if (p.have > 0) {
-#pragma unroll
-                for (int f = 0; f < FR; ++f) store_frame<S, TAIL, FR>(a.y, a.ys, p, t0, f, valid, rows, y[f]);
+                store_frame<S, TAIL, FR>(a.y, a.ys, p, t0, f, valid, rows, h);
             }
         }
     }
-    if (p.seg != 0 || p.have <= 0) return;
-    Vf<kQuad> end, P;
-#pragma unroll
-    for (int e = 0; e < kQuad; ++e) end.v[e] = carry[e], P.v[e] = total[e];
-    if constexpr (PHASE == kScanSummary) {
-        const int64_t at = (p.b * a.chunks + p.chunk) * a.C + p.col;
-        store_quad<float, true>(a.summary + at, p.have, P);
-        store_quad<float, true>(a.summary + plane + at, p.have, end);
-    } else if (a.end && p.last == a.T) {
-        store_quad<float, true>(a.end + p.b * a.C + p.col, p.have, end);
-    }
+    if (a.end && end == a.tiles && p.seg == 0) store_state(a.end, p.b, a.C, p, carry);
 }
 
-// Backwards in time, G_t = dy_t + a_{t+1} G_{t+1}: the runs hand a_t G_t on to
+// ---------------------------------------------------------------------------
+// Backward in time, G_t = dy_t + a_{t+1} G_{t+1}: the runs hand a_t G_t on to
 // the frames before them.
-template <typename S, bool TAIL, int SEGS, int FR, int PHASE>
+// ---------------------------------------------------------------------------
+template <typename S, bool TAIL, int SEGS, int FR, bool LINKED>
 __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanArgs a) {
     constexpr int kTileFrames = SEGS * FR;
-    __shared__ float lds[2][4][2][kScanCols];
+    __shared__ float lds[LINKED ? 3 : 2][kScanWaves][2][kScanCols];
     __shared__ float column[kScanRows][kScanCols];
-    const ScanPlace p = scan_place<SEGS, PHASE>(a);
+    __shared__ int ticket;
+    const uint32_t chains = LINKED ? gridDim.x / (uint32_t)a.tiles : 0;
+    const ScanPlace p = scan_place<SEGS>(a, LINKED ? blockIdx.x % chains : blockIdx.x);
     const bool item = p.b < a.B;
-    float rate[kQuad], carry[kQuad], total[kQuad], sum[kQuad];
-    const Vf<kQuad> decay = load_state(a.decay, 0, a.C, p);
-    const Vf<kQuad> start = item ? load_state(a.start, p.b, a.C, p) : vzero<kQuad>();
-#pragma unroll
-    for (int e = 0; e < kQuad; ++e) {
-        rate[e] = decay_rate(decay.v[e], a.scale);
-        carry[e] = PHASE == kScanSummary ? 0.0f : start.v[e];
-        total[e] = 1.0f;
-        sum[e] = 0.0f;
-    }
-    if (PHASE == kScanSummary && p.chunk == 0 && p.seg == 0 && p.have > 0)
-        store_quad<float, true>(a.copy + p.b * a.C + p.col, p.have, start);
-    const int64_t plane = a.B * a.chunks * (int64_t)a.C;
-    if constexpr (PHASE == kScanJoin) {
-        for (int c = a.chunks - 1; c > p.chunk; --c) {
-            const Vf<kQuad> P = load_state(a.summary, p.b * a.chunks + c, a.C, p);
-            const Vf<kQuad> H = load_state(a.summary + plane, p.b * a.chunks + c, a.C, p);
-#pragma unroll
-            for (int e = 0; e < kQuad; ++e) carry[e] = H.v[e] + P.v[e] * carry[e];
-        }
-    }
+    int at = LINKED ? take_tile(a.tickets + p.chain, &ticket) : 0;  // in the order of the chain: the last tile is first
+    const int end = LINKED ? at + 1 : item ? a.tiles : 0;
+    const int row = LINKED ? (int)(p.chain / (uint32_t)a.col_blocks) * a.tiles + at : (int)(p.chain / (uint32_t)a.col_blocks);
+    const f32x2 decay = load_state(a.decay, 0, a.C, p);
+    const f32x2 rate = {decay_rate(decay[0], a.scale), decay_rate(decay[1], a.scale)};
+    f32x2 carry = item && at == 0 ? load_state(a.start, p.b, a.C, p) : f32x2(0.0f), sum = {0.0f, 0.0f};
     int turn = 0;
-    const int64_t tiles = item ? (p.last - p.first + kTileFrames - 1) / kTileFrames : 0;
-    for (int64_t i = tiles - 1; i >= 0; --i) {
-        const int64_t t0 = p.first + i * kTileFrames;
-        const int64_t left = p.len - t0, size = p.last - t0;
+    for (; at < end; ++at) {
+        const int64_t t0 = (int64_t)(a.tiles - 1 - at) * kTileFrames, left = p.len - t0, size = a.T - t0;
         const int rows = size < kTileFrames ? (int)size : kTileFrames;
         const int valid = left < 0 ? 0 : left < rows ? (int)left : rows;
-        Vf<kQuad> dx[FR] = {}, dr[FR] = {}, dg[FR] = {};
+        pair_raw<S> rr[FR], dyr[FR], xr[FR], gr[FR];
+        f32x2 prev[FR], d[FR], w[FR];
+        Run all = {f32x2(1.0f), f32x2(0.0f)}, before = all;
         if (valid > 0) {
-            quad_raw<S> rr[FR], dyr[FR], xr[FR], gr[FR];
-            Vf<kQuad> before[FR];
             const bool full = valid == kTileFrames;
             load_run<S, TAIL, FR>(rr, a.r, a.rs, p, t0, valid, full, closed_gate<S>());
             load_run<S, TAIL, FR>(dyr, a.dy, a.dys, p, t0, valid, full, 0);
-            if constexpr (PHASE != kScanSummary) {
-                load_run<S, TAIL, FR>(xr, a.x, a.xs, p, t0, valid, full, 0);
-                load_run<S, TAIL, FR>(gr, a.g, a.gs, p, t0, valid, full, 0);
-                // the state before each frame: what the forward stored for the one in front of it
-                const S* y = (const S*)a.yin + p.b * a.ys.item + t0 * a.ys.frame;
+            load_run<S, TAIL, FR>(xr, a.x, a.xs, p, t0, valid, full, 0);
+            load_run<S, TAIL, FR>(gr, a.g, a.gs, p, t0, valid, full, 0);
+            // the state before each frame: what the forward stored for the one in front of it
+            const S* y = (const S*)a.yin + p.b * a.ys.item + t0 * a.ys.frame;
 #pragma unroll
-                for (int f = 0; f < FR; ++f) {
-                    const int t = p.seg * FR + f;
-                    if (f == 0 && p.seg == 0 && t0 == 0) {
-                        before[f] = load_state(a.h0, p.b, a.C, p);
-                    } else {
-                        const int at = (t < valid ? t : valid) - 1;  // -1: the tile before
-                        before[f] = widen_quad<S>(load_quad<S, TAIL>(y + (at * (int64_t)a.ys.frame + p.col), p.have));
-                    }
+            for (int f = 0; f < FR; ++f) {
+                const int t = p.seg * FR + f;
+                if (f == 0 && p.seg == 0 && t0 == 0) {
+                    prev[f] = load_state(a.h0, p.b, a.C, p);
+                } else {
+                    const int from = (t < valid ? t : valid) - 1;  // -1: the tile before
+                    const pair_raw<S> q = load_pair<S, TAIL>(y + (from * (int64_t)a.ys.frame + p.col), p.have);
+                    prev[f] = f32x2{pair_at<S>(q, 0), pair_at<S>(q, 1)};
                 }
             }
-            float d[FR][kQuad], w[FR][kQuad];
             Run run;
 #pragma unroll
-            for (int e = 0; e < kQuad; ++e) {
+            for (int e = 0; e < kScanPair; ++e) {
                 float sw = 0.0f, c = 0.0f;
 #pragma unroll
                 for (int f = FR - 1; f >= 0; --f) {
-                    const float wf = rate[e] * sigmoid_of<S>(quad_at<S>(rr[f], e));
+                    const float wf = rate[e] * sigmoid_of<S>(pair_at<S>(rr[f], e));
                     const float df = one_minus_exp(wf);
                     w[f][e] = wf;
                     d[f][e] = df;
-                    const float G = quad_at<S>(dyr[f], e) + c;
+                    const float G = pair_at<S>(dyr[f], e) + c;
                     c = __builtin_fmaf(-df, G, G);
                     sw += wf;
                 }
                 run.p[e] = __builtin_amdgcn_exp2f(sw * -1.44269504f);
                 run.h[e] = c;
             }
-            float in[kQuad];
-            enter_runs<SEGS, true>(run, carry, in, PHASE == kScanSummary ? total : nullptr, lds[turn]);
+            const TileRuns t = tile_runs<SEGS, true>(run, lds[turn]);
             turn ^= 1;
-            if constexpr (PHASE != kScanSummary) {
+            all = t.all;
+            before = t.before;
+        }
+        const bool wanted = valid > 0 || (a.end && at == a.tiles - 1);
+        f32x2 c = through(before, enter_tile<LINKED>(a, p, all, at, wanted, carry, lds + 1));
 #pragma unroll
-                for (int e = 0; e < kQuad; ++e) {
-                    float c = in[e];
+        for (int f = FR - 1; f >= 0; --f) {
+            f32x2 dx = {0.0f, 0.0f}, dr = dx, dg = dx;
+            if (valid > 0) {
 #pragma unroll
-                    for (int f = FR - 1; f >= 0; --f) {
-                        const float G = quad_at<S>(dyr[f], e) + c;
-                        const float x = quad_at<S>(xr[f], e), s = sigmoid_of<S>(quad_at<S>(rr[f], e));
-                        const float gate = sigmoid_of<S>(quad_at<S>(gr[f], e));
-                        const float z = d[f][e] * (2.0f - d[f][e]);                       // 1 - a^2 = m^2
-                        const float rs = __builtin_amdgcn_rsqf(z > 1e-37f ? z : 1e-37f);  // w / m is 0 where w is
-                        const float ix = gate * x;
-                        const float open = G * (z * rs);
-                        const float q = G * w[f][e] * (ix * (1.0f - z) * rs - before[f].v[e] * (1.0f - d[f][e]));
-                        c = __builtin_fmaf(-d[f][e], G, G);
-                        dx[f].v[e] = open * gate;
-                        dg[f].v[e] = open * ix * (1.0f - gate);
-                        dr[f].v[e] = q * (1.0f - s);
-                        sum[e] += p.seg * FR + f < valid ? q : 0.0f;
-                    }
+                for (int e = 0; e < kScanPair; ++e) {
+                    const float G = pair_at<S>(dyr[f], e) + c[e];
+                    const float x = pair_at<S>(xr[f], e), s = sigmoid_of<S>(pair_at<S>(rr[f], e));
+                    const float gate = sigmoid_of<S>(pair_at<S>(gr[f], e));
+                    const float df = d[f][e], z = df * (2.0f - df);                   // 1 - a^2 = m^2
+                    const float rs = __builtin_amdgcn_rsqf(z > 1e-37f ? z : 1e-37f);  // w / m is 0 where w is
+                    const float ix = gate * x, open = G * (z * rs);
+                    const float q = G * w[f][e] * (ix * (1.0f - z) * rs - prev[f][e] * (1.0f - df));
+                    c[e] = __builtin_fmaf(-df, G, G);
+                    dx[e] = open * gate;
+                    dg[e] = open * ix * (1.0f - gate);
+                    dr[e] = q * (1.0f - s);
+                    sum[e] += p.seg * FR + f < valid ? q : 0.0f;
                 }
             }
-        }
-        if constexpr (PHASE != kScanSummary) {
             if (p.have > 0) {
-#pragma unroll
-                for (int f = 0; f < FR; ++f) {
-                    if (a.dx) store_frame<S, TAIL, FR>(a.dx, a.dxs, p, t0, f, valid, rows, dx[f]);
-                    if (a.dr) store_frame<S, TAIL, FR>(a.dr, a.drs, p, t0, f, valid, rows, dr[f]);
-                    if (a.dg) store_frame<S, TAIL, FR>(a.dg, a.dgs, p, t0, f, valid, rows, dg[f]);
-                }
+                if (a.dx) store_frame<S, TAIL, FR>(a.dx, a.dxs, p, t0, f, valid, rows, dx);
+                if (a.dr) store_frame<S, TAIL, FR>(a.dr, a.drs, p, t0, f, valid, rows, dr);
+                if (a.dg) store_frame<S, TAIL, FR>(a.dg, a.dgs, p, t0, f, valid, rows, dg);
             }
         }
     }
-    if (item && p.seg == 0 && p.have > 0) {
-        Vf<kQuad> end, P;
+    if (a.end && end == a.tiles && item && p.seg == 0) store_state(a.end, p.b, a.C, p, carry);
+    if (!a.partial) return;
+    const int mine = threadIdx.x / kScanLanes, lane = threadIdx.x % kScanLanes;
 #pragma unroll
-        for (int e = 0; e < kQuad; ++e) end.v[e] = carry[e], P.v[e] = total[e];
-        if constexpr (PHASE == kScanSummary) {
-            const int64_t at = (p.b * a.chunks + p.chunk) * a.C + p.col;
-            store_quad<float, true>(a.summary + at, p.have, P);
-            store_quad<float, true>(a.summary + plane + at, p.have, end);
-        } else if (a.end && p.first == 0) {
-            store_quad<float, true>(a.end + p.b * a.C + p.col, p.have, end);
-        }
+    for (int e = 0; e < kScanPair; ++e) column[mine][lane * kScanPair + e] = sum[e];
+    __syncthreads();
+    if (mine != 0) return;
+    double* out = a.partial + (int64_t)row * a.C + p.col;
+#pragma unroll
+    for (int e = 0; e < kScanPair; ++e) {
+        double t = 0.0;
+        for (int q = 0; q < kScanRows; ++q) t += column[q][lane * kScanPair + e];
+        if (e < p.have) out[e] = t * softplus_slope(decay[e]);
     }
-    if constexpr (PHASE != kScanSummary) {
-        if (!a.partial) return;
-        const int row = threadIdx.x / kScanLanes, lane = threadIdx.x % kScanLanes;
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) column[row][lane * kQuad + e] = sum[e];
-        __syncthreads();
-        if (row != 0) return;
-        double* out = a.partial + (int64_t)(blockIdx.x / (uint32_t)a.col_blocks) * a.C + p.col;
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-            double t = 0.0;
-            for (int q = 0; q < kScanRows; ++q) t += column[q][lane * kQuad + e];
-            if (e < p.have) out[e] = t * softplus_slope(decay.v[e]);
-        }
-    }
+}
+
+// Nothing taken, nothing published.
+__global__ __launch_bounds__(kScanThreads) void scan_clear_kernel(u32x4* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * kScanThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kScanThreads)
+        p[i] = u32x4(0u);
 }
 
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
 // segs: threads along the frames of an item in a workgroup; run: frames of each
-// in a tile.  chunks > 1: the frames are shared out.
+// in a tile; linked: a workgroup for each tile.
 struct ScanPlan {
     int segs, run;
-    int64_t chunks, chunk, row_blocks, col_blocks;
+    bool linked;
+    int64_t tiles, row_blocks, col_blocks;  // row_blocks: of one column block, tiles among them where linked
 };
 
 static ScanPlan scan_plan(const ScanShape& s, int run) {
     ScanPlan p = {};
-    p.run = s.T == 1 ? 1 : run;
-    p.segs = s.T <= run ? 1 : s.T <= 4 * run ? 4 : 16;
+    p.run = s.T == 1 ? 1 : s.T <= kScanRows * kScanShortRun ? kScanShortRun : run;
+    p.segs = s.T <= p.run ? 1 : s.T <= 2 * p.run ? 2 : kScanRows;
     p.col_blocks = (s.C + kScanCols - 1) / kScanCols;
-    p.chunks = 1;
-    p.chunk = s.T;
-    const int64_t tile = 16 * run, tiles = (s.T + tile - 1) / tile, per = kScanRows / p.segs;
+    p.tiles = (s.T + p.segs * p.run - 1) / (p.segs * p.run);
+    const int64_t per = kScanRows / p.segs;
     p.row_blocks = (s.B + per - 1) / per;
-    const int64_t blocks = p.row_blocks * p.col_blocks;
-    if (p.segs == 16 && blocks > 0 && blocks * 2 <= kScanBlocks && tiles >= 4) {
-        const int64_t most = tiles / 2, want = kScanBlocks / blocks;
-        const int64_t each = (tiles + (want < most ? want : most) - 1) / (want < most ? want : most);
-        p.chunk = each * tile;
-        p.chunks = (tiles + each - 1) / each;
-        p.row_blocks *= p.chunks;
-    }
+    p.linked = p.tiles > 1 && p.row_blocks * p.col_blocks < 1024;
+    if (p.linked) p.row_blocks *= p.tiles;
     return p;
 }
+
+static int64_t scan_chains(const ScanPlan& p) { return p.row_blocks / p.tiles * p.col_blocks; }
 
 bool dwscan_fits(const ScanShape& s) {
     if (!product_below((int64_t)1 << 58, {s.B, s.T, s.C})) return false;
@@ -514,10 +594,14 @@ bool dwscan_fits(const ScanShape& s) {
     return true;
 }
 
-static size_t scan_join_bytes(const ScanShape& s, const ScanPlan& p) {
-    if (p.chunks == 1) return 0;
-    const size_t bytes = (size_t)(s.B * (2 * p.chunks + 1) * s.C) * sizeof(float);
-    return (bytes + 15) / 16 * 16;
+// Tickets and words of a linked plan.
+static size_t scan_ticket_bytes(const ScanPlan& p) {
+    return p.linked ? ((size_t)scan_chains(p) * sizeof(uint32_t) + 15) / 16 * 16 : 0;
+}
+
+static size_t scan_link_bytes(const ScanPlan& p) {
+    if (!p.linked) return 0;
+    return scan_ticket_bytes(p) + (size_t)(scan_chains(p) * (p.tiles + p.tiles / kScanGroup) * kScanCols) * sizeof(uint64_t);
 }
 
 static int64_t scan_partial_rows(const ScanPlan& p) {
@@ -525,11 +609,11 @@ static int64_t scan_partial_rows(const ScanPlan& p) {
     return p.row_blocks + (chunks > 1 ? chunks : 1);
 }
 
-size_t dwscan_fwd_workspace(const ScanShape& s) { return scan_join_bytes(s, scan_plan(s, kScanFwdRun)); }
+size_t dwscan_fwd_workspace(const ScanShape& s) { return scan_link_bytes(scan_plan(s, kScanFwdRun)); }
 
 size_t dwscan_bwd_workspace(const ScanShape& s) {
     const ScanPlan p = scan_plan(s, kScanBwdRun);
-    return scan_join_bytes(s, p) + (size_t)(scan_partial_rows(p) * s.C) * sizeof(double);
+    return scan_link_bytes(p) + (size_t)(scan_partial_rows(p) * s.C) * sizeof(double);
 }
 
 static ScanArgs scan_args(const ScanPtrs& p, const ScanShape& s, const ScanPlan& plan, void* workspace) {
@@ -538,42 +622,46 @@ static ScanArgs scan_args(const ScanPtrs& p, const ScanShape& s, const ScanPlan&
     a.xs = s.x, a.rs = s.r, a.gs = s.g, a.ys = s.y;
     a.dys = s.dy, a.dxs = s.dx, a.drs = s.dr, a.dgs = s.dg;
     a.B = s.B, a.T = s.T, a.C = (int32_t)s.C, a.scale = s.scale;
-    a.chunk = plan.chunk, a.chunks = (int32_t)plan.chunks, a.col_blocks = (int32_t)plan.col_blocks;
-    if (plan.chunks > 1) {
-        a.summary = (float*)workspace;
-        a.copy = a.summary + 2 * s.B * plan.chunks * s.C;
+    a.col_blocks = (int32_t)plan.col_blocks, a.tiles = (int32_t)plan.tiles;
+    if (plan.linked) {
+        a.tickets = (uint32_t*)workspace;
+        a.words = (uint64_t*)((char*)workspace + scan_ticket_bytes(plan));
     }
     return a;
 }
 
-template <bool BACK, typename S, bool TAIL, int SEGS, int FR, int PHASE>
-static hipError_t launch_scan_phase(const ScanArgs& a, dim3 grid, hipStream_t stream) {
+template <bool BACK, typename S, bool TAIL, int SEGS, int FR, bool LINKED>
+static hipError_t launch_scan_kernel(const ScanPlan& plan, const ScanArgs& a, hipStream_t stream) {
+    const dim3 grid((uint32_t)(plan.row_blocks * plan.col_blocks));
     if constexpr (BACK)
-        hipLaunchKernelGGL((scan_bwd_kernel<S, TAIL, SEGS, FR, PHASE>), grid, dim3(kScanThreads), 0, stream, a);
+        hipLaunchKernelGGL((scan_bwd_kernel<S, TAIL, SEGS, FR, LINKED>), grid, dim3(kScanThreads), 0, stream, a);
     else
-        hipLaunchKernelGGL((scan_fwd_kernel<S, TAIL, SEGS, FR, PHASE>), grid, dim3(kScanThreads), 0, stream, a);
+        hipLaunchKernelGGL((scan_fwd_kernel<S, TAIL, SEGS, FR, LINKED>), grid, dim3(kScanThreads), 0, stream, a);
     return hipGetLastError();
 }
 
 template <bool BACK, typename S, bool TAIL>
-static hipError_t launch_scan_form(const ScanPlan& plan, ScanArgs a, hipStream_t stream) {
+static hipError_t launch_scan_form(const ScanPlan& plan, const ScanArgs& a, hipStream_t stream) {
     constexpr int kRun = BACK ? kScanBwdRun : kScanFwdRun;
-    const dim3 grid((uint32_t)(plan.row_blocks * plan.col_blocks));
-    if (plan.chunks > 1) {
-        const hipError_t e = launch_scan_phase<BACK, S, TAIL, 16, kRun, kScanSummary>(a, grid, stream);
+    if (plan.linked) {
+        const int64_t n = (int64_t)(scan_link_bytes(plan) / sizeof(u32x4)), blocks = (n + kScanThreads - 1) / kScanThreads;
+        hipLaunchKernelGGL(scan_clear_kernel, dim3((uint32_t)(blocks < 1024 ? blocks : 1024)), dim3(kScanThreads), 0,
+                           stream, (u32x4*)a.tickets, n);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        a.start = a.copy;  // what leaves may be written over what entered
-        return launch_scan_phase<BACK, S, TAIL, 16, kRun, kScanJoin>(a, grid, stream);
+        return launch_scan_kernel<BACK, S, TAIL, kScanRows, kRun, true>(plan, a, stream);
     }
-    if (plan.run == 1) return launch_scan_phase<BACK, S, TAIL, 1, 1, kScanWhole>(a, grid, stream);
-    if (plan.segs == 1) return launch_scan_phase<BACK, S, TAIL, 1, kRun, kScanWhole>(a, grid, stream);
-    if (plan.segs == 4) return launch_scan_phase<BACK, S, TAIL, 4, kRun, kScanWhole>(a, grid, stream);
-    return launch_scan_phase<BACK, S, TAIL, 16, kRun, kScanWhole>(a, grid, stream);
+    if (plan.run == 1) return launch_scan_kernel<BACK, S, TAIL, 1, 1, false>(plan, a, stream);
+    if (plan.segs == 1) return launch_scan_kernel<BACK, S, TAIL, 1, kScanShortRun, false>(plan, a, stream);
+    if (plan.segs == 2) return launch_scan_kernel<BACK, S, TAIL, 2, kScanShortRun, false>(plan, a, stream);
+    if (plan.run == kScanShortRun)
+        return launch_scan_kernel<BACK, S, TAIL, kScanRows, kScanShortRun, false>(plan, a, stream);
+    return launch_scan_kernel<BACK, S, TAIL, kScanRows, kRun, false>(plan, a, stream);
 }
 
 template <bool BACK>
 static hipError_t launch_scan(const ScanPlan& plan, const ScanArgs& a, bool bf16, hipStream_t stream) {
-    const bool tail = a.C % kQuad != 0;
+    const bool tail = a.C % kScanPair != 0;
     if (bf16 && tail) return launch_scan_form<BACK, uint16_t, true>(plan, a, stream);
     if (bf16) return launch_scan_form<BACK, uint16_t, false>(plan, a, stream);
     if (tail) return launch_scan_form<BACK, float, true>(plan, a, stream);
@@ -594,7 +682,7 @@ hipError_t launch_dwscan_bwd(const ScanPtrs& p, const ScanShape& s, const void* 
     const ScanPlan plan = scan_plan(s, kScanBwdRun);
     ScanArgs a = scan_args(p, s, plan, workspace);
     a.start = dh_last, a.h0 = p.h0, a.yin = y, a.dy = dy, a.dx = dx, a.dr = dr, a.dg = dg, a.end = dh0;
-    double* rows = (double*)((char*)workspace + scan_join_bytes(s, plan));
+    double* rows = (double*)((char*)workspace + scan_link_bytes(plan));
     a.partial = ddecay ? rows : nullptr;
     if (plan.row_blocks > 0) {
         const hipError_t e = launch_scan<true>(plan, a, bf16, stream);
