@@ -781,10 +781,14 @@ def dwattn_bwd(q, k, v, out, lse, dout, table=None, buckets=None, q_lengths=None
     return dq, dk, dv, dtable
 
 
+def _plain(t, st, index, shape) -> bool:
+    """Whether t is a contiguous tensor as expected, in the fewest steps: small calls are bound by the host."""
+    return (type(t) is torch.Tensor and t.dtype is st and t.shape == shape and t.get_device() == index
+            and t.is_contiguous())
+
+
 def _frames(name, t, st, device, shape):
     """A [B, T, C] tensor whose channels lie next to each other."""
-    if type(t) is torch.Tensor and t.dtype is st and t.device == device and t.shape == shape and t.stride(2) == 1:
-        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -804,29 +808,36 @@ def _scan_workspace(backward: bool, shape: bytes) -> int:
     return int((_lib.dwscan_bwd_workspace_bytes if backward else _lib.dwscan_fwd_workspace_bytes)(shape))
 
 
-def _scan_check(x, r, g, decay, lengths, h0):
-    if x.dim() != 3:
-        raise ValueError("x must be [B, T, C]")
-    dev, shape = x.device, x.shape
-    st, code = _storage(x)
-    B, T, C = shape
-    _frames("x", x, st, dev, shape)
-    _frames("r", r, st, dev, shape)
-    _frames("g", g, st, dev, shape)
-    _dev_tensor("decay", decay, torch.float32, dev, (C,))
-    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
-    _dev_tensor("h0", h0, torch.float32, dev, (B, C), allow_none=True)
-    return dev, st, code, B, T, C
+@functools.lru_cache(maxsize=1024)
+def _scan_dense(B, T, C, scale, code) -> bytes:
+    """The C ABI's dw_scan of contiguous tensors."""
+    return _scan_struct.pack(B, T, C, *(T * C, C) * 8, scale, code)
 
 
-def _scan_shape(B, T, C, tensors, scale, code):
-    strides = [n for t in tensors for n in ((0, 0) if t is None else t.stride()[:2])]
-    return _scan_struct.pack(B, T, C, *strides, scale, code)
+def _scan_shape(x, given, names, scale, code) -> bytes:
+    """The C ABI's dw_scan, of tensors like x or None; checks those that are not plain."""
+    B, T, C = x.shape
+    st, dev, index, shape = x.dtype, x.device, x.get_device(), x.shape
+    dense = True
+    for t in given:
+        if t is not None and not _plain(t, st, index, shape):
+            dense = False
+    if dense:
+        return _scan_dense(B, T, C, scale, code)
+    strides = []
+    for name, t in zip(names, given):
+        strides += (0, 0) if t is None else _frames(name, t, st, dev, shape).stride()[:2]
+    return _scan_struct.pack(B, T, C, *strides, *(0,) * (16 - len(strides)), scale, code)
+
+
+def _like(x):
+    """A contiguous tensor of x's sizes."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def dwscan_fwd_workspace_bytes(B, T, C) -> int:
     """Bytes of workspace `dwscan_fwd` takes for tensors of these sizes."""
-    return _scan_workspace(False, _scan_struct.pack(B, T, C, *(0,) * 16, 1.0, DW_F32))
+    return _scan_workspace(False, _scan_dense(B, T, C, 1.0, DW_F32))
 
 
 def dwscan_fwd(x, r, g, decay, lengths=None, h0=None, scale: float = 8.0, y=None, h_last=None, workspace=None,
@@ -837,16 +848,25 @@ def dwscan_fwd(x, r, g, decay, lengths=None, h0=None, scale: float = 8.0, y=None
     [C], h0 float32 [B,C] or None (zero).  Returns (y [B,T,C], h_last float32
     [B,C] or None if not in `need`): the states, and the one after the last
     valid frame, with which a stream goes on (it may be h0, updated in place)."""
-    dev, st, code, B, T, C = _scan_check(x, r, g, decay, lengths, h0)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    dev, f32 = x.device, torch.float32
+    st, code = _storage(x)
+    B, T, C = x.shape
     if y is None:
-        y = torch.empty((B, T, C), dtype=st, device=dev)
-    else:
-        _frames("y", y, st, dev, x.shape)
+        y = _like(x)
+    if r is None or g is None:
+        raise ValueError("r and g are required")
+    shape = _scan_shape(x, (x, r, g, y), ("x", "r", "g", "y"), scale, code)
+    _dev_tensor("decay", decay, f32, dev, (C,))
+    if lengths is not None:
+        _dev_tensor("lengths", lengths, torch.int32, dev, (B,))
+    if h0 is not None:
+        _dev_tensor("h0", h0, f32, dev, (B, C))
     if h_last is not None:
-        _dev_tensor("h_last", h_last, torch.float32, dev, (B, C))
+        _dev_tensor("h_last", h_last, f32, dev, (B, C))
     elif "h_last" in need:
-        h_last = torch.empty((B, C), dtype=torch.float32, device=dev)
-    shape = _scan_shape(B, T, C, (x, r, g, y, None, None, None, None), scale, code)
+        h_last = torch.empty((B, C), dtype=f32, device=dev) if h0 is None else torch.empty_like(h0)
     if workspace is not None:
         _dev_tensor("workspace", workspace, torch.uint8, dev)
     else:
@@ -860,7 +880,7 @@ def dwscan_fwd(x, r, g, decay, lengths=None, h0=None, scale: float = 8.0, y=None
 
 def dwscan_bwd_workspace_bytes(B, T, C) -> int:
     """Bytes of workspace `dwscan_bwd` takes for tensors of these sizes."""
-    return _scan_workspace(True, _scan_struct.pack(B, T, C, *(0,) * 16, 1.0, DW_F32))
+    return _scan_workspace(True, _scan_dense(B, T, C, 1.0, DW_F32))
 
 
 def dwscan_bwd(x, r, g, decay, y, dy, lengths=None, h0=None, dh_last=None, scale: float = 8.0, dx=None, dr=None, dg=None,
@@ -869,32 +889,35 @@ def dwscan_bwd(x, r, g, decay, y, dy, lengths=None, h0=None, dh_last=None, scale
     h_last, dh_last; the other arguments are the forward's.  dx, dr and dg are
     in the storage type (given ones may have any strides above the last),
     ddecay [C] and dh0 [B,C] float32; those not in `need` are skipped (None)."""
-    dev, st, code, B, T, C = _scan_check(x, r, g, decay, lengths, h0)
-    f32, full = torch.float32, x.shape
-    _frames("y", y, st, dev, full)
-    _frames("dy", dy, st, dev, full)
-    _dev_tensor("dh_last", dh_last, f32, dev, (B, C), allow_none=True)
-    if dx is not None:
-        _frames("dx", dx, st, dev, full)
-    elif "dx" in need:
-        dx = torch.empty((B, T, C), dtype=st, device=dev)
-    if dr is not None:
-        _frames("dr", dr, st, dev, full)
-    elif "dr" in need:
-        dr = torch.empty((B, T, C), dtype=st, device=dev)
-    if dg is not None:
-        _frames("dg", dg, st, dev, full)
-    elif "dg" in need:
-        dg = torch.empty((B, T, C), dtype=st, device=dev)
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    dev, f32 = x.device, torch.float32
+    st, code = _storage(x)
+    B, T, C = x.shape
+    if dx is None and "dx" in need:
+        dx = _like(x)
+    if dr is None and "dr" in need:
+        dr = _like(x)
+    if dg is None and "dg" in need:
+        dg = _like(x)
+    if r is None or g is None or y is None or dy is None:
+        raise ValueError("r, g, y and dy are required")
+    shape = _scan_shape(x, (x, r, g, y, dy, dx, dr, dg), ("x", "r", "g", "y", "dy", "dx", "dr", "dg"), scale, code)
+    _dev_tensor("decay", decay, f32, dev, (C,))
+    if lengths is not None:
+        _dev_tensor("lengths", lengths, torch.int32, dev, (B,))
+    if h0 is not None:
+        _dev_tensor("h0", h0, f32, dev, (B, C))
+    if dh_last is not None:
+        _dev_tensor("dh_last", dh_last, f32, dev, (B, C))
     if ddecay is not None:
         _dev_tensor("ddecay", ddecay, f32, dev, (C,))
     elif "ddecay" in need:
-        ddecay = torch.empty((C,), dtype=f32, device=dev)
+        ddecay = torch.empty_like(decay)
     if dh0 is not None:
         _dev_tensor("dh0", dh0, f32, dev, (B, C))
     elif "dh0" in need:
-        dh0 = torch.empty((B, C), dtype=f32, device=dev)
-    shape = _scan_shape(B, T, C, (x, r, g, y, dy, dx, dr, dg), scale, code)
+        dh0 = torch.empty((B, C), dtype=f32, device=dev) if h0 is None else torch.empty_like(h0)
     if workspace is not None:
         _dev_tensor("workspace", workspace, torch.uint8, dev)
     else:
@@ -948,9 +971,17 @@ def _rope_check(q, k, q_gamma, k_gamma, freq, lengths, pos, pairs):
     return dev, st, code, B, T, H, Hkv, D, R
 
 
-def _rope_shape(sizes, tensors, eps, pairs, code):
-    strides = [n for t in tensors for n in ((0, 0, 0) if t is None else t.stride()[:3])]
-    return _rope_struct.pack(*sizes, *strides, eps, _PAIRS[pairs], code)
+_NO_STRIDE = (0, 0, 0, 0)
+
+
+@functools.lru_cache(maxsize=1024)
+def _rope_pack(sizes, strides, eps, pairs, code) -> bytes:
+    return _rope_struct.pack(*sizes, *[n for s in strides for n in s[:3]], eps, _PAIRS[pairs], code)
+
+
+def _rope_shape(sizes, tensors, eps, pairs, code) -> bytes:
+    """The C ABI's dw_rope."""
+    return _rope_pack(sizes, tuple([_NO_STRIDE if t is None else t.stride() for t in tensors]), eps, pairs, code)
 
 
 def dwrope_fwd(q, k, q_gamma=None, k_gamma=None, freq=None, lengths=None, pos=None, v=None, place=None,

@@ -33,9 +33,9 @@ constexpr int kScanPair = 2;                                  // channels of a t
 constexpr int kScanLanes = 32;                                // threads across the channels
 constexpr int kScanRows = kScanThreads / kScanLanes;          // and along frames, or items
 constexpr int kScanCols = kScanLanes * kScanPair;             // channels of a workgroup
-constexpr int kScanShortRun = 8;                              // frames of a thread where they are few
-constexpr int kScanFwdRun = 16, kScanBwdRun = 8;              // and in a tile
+constexpr int kScanRun = 8, kScanLongRun = 16;                // frames of a thread in a tile
 constexpr int kScanGroup = 16;                                // tiles whose composition is published too
+constexpr int kScanTicket = 32;                               // words from one chain's counter to the next: a cache line
 constexpr int kScanPolls = 1 << 22;                           // of a word, before its wait is given up with a NaN
 
 struct ScanArgs {
@@ -46,7 +46,7 @@ struct ScanArgs {
     void *y, *dx, *dr, *dg;
     const float* h0;      // backward: the state before the first frame
     float* end;           // what leaves the last (first) frame
-    uint32_t* tickets;    // [chains]: tiles given out
+    uint32_t* tickets;    // [chains][kScanTicket]: tiles given out
     uint64_t* words;      // [chains][tiles + tiles / kScanGroup][kScanCols]: published (P, H)
     double* partial;      // backward: [row blocks][C], sums for ddecay
     FrameStride xs, rs, gs, ys, dys, dxs, drs, dgs;
@@ -95,18 +95,23 @@ __device__ __forceinline__ float pair_at(const pair_raw<S>& q, int e) {
         return e ? bf16_hi(q) : bf16_lo(q);
 }
 
+// Rounded to the storage type (nearest even).
+template <typename S>
+__device__ __forceinline__ pair_raw<S> pack_pair(f32x2 v) {
+    if constexpr (sizeof(S) == 4)
+        return u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])};
+    else
+        return pack_bf16x2(v[0], v[1]);
+}
+
 template <typename S, bool TAIL>
-__device__ __forceinline__ void store_pair(S* p, int have, f32x2 v) {
-    if constexpr (sizeof(S) == 4) {
-        if (!TAIL || have >= kScanPair)
-            *reinterpret_cast<typename PairRaw<S>::access*>(p) = u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])};
-        else if (have == 1)
-            p[0] = v[0];
-    } else {
-        const uint32_t q = pack_bf16x2(v[0], v[1]);
-        if (!TAIL || have >= kScanPair)
-            *reinterpret_cast<typename PairRaw<S>::access*>(p) = q;
-        else if (have == 1)
+__device__ __forceinline__ void store_pair(S* p, int have, pair_raw<S> q) {
+    if (!TAIL || have >= kScanPair) {
+        *reinterpret_cast<typename PairRaw<S>::access*>(p) = q;
+    } else if (have == 1) {
+        if constexpr (sizeof(S) == 4)
+            p[0] = __uint_as_float(q[0]);
+        else
             p[0] = (uint16_t)q;
     }
 }
@@ -114,19 +119,27 @@ __device__ __forceinline__ void store_pair(S* p, int have, f32x2 v) {
 // ---------------------------------------------------------------------------
 // The step's functions
 // ---------------------------------------------------------------------------
-// 1 - exp(-w): a series where the difference would cancel (its first left out
-// term is 2^-24.4 of it at w = 1/8), the exponential beyond (off by 2^-21 at most).
-__device__ __forceinline__ float one_minus_exp(float w) {
-    const float series = w * (1.0f + w * (-0.5f + w * (0.16666667f + w * (-0.041666668f + w * 0.0083333333f))));
-    const float direct = 1.0f - __builtin_amdgcn_exp2f(w * -1.44269504f);
-    return w < 0.125f ? series : direct;
+// 1 - 2^-v, v = w / log 2: a series in w where the difference would cancel (its
+// first left out term is 2^-24.4 of it at w = 1/8), the exponential beyond (off
+// by 2^-21 at most).
+__device__ __forceinline__ float one_minus_exp2(float v) {
+    const float series =
+        v * (0.69314718f + v * (-0.24022651f + v * (0.055504109f + v * (-0.0096181291f + v * 0.0013333558f))));
+    const float direct = 1.0f - __builtin_amdgcn_exp2f(-v);
+    return v < 0.18033688f ? series : direct;
 }
 
-__device__ __forceinline__ float softplus(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
+// log(1 + exp(v)): 2 atanh(e / (2 + e)) where e is small (left out: 2^-28 of it),
+// v itself where it is large.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = expf(v), z = e / (2.0f + e), z2 = z * z;
+    const float small = 2.0f * z * (1.0f + z2 * (0.33333333f + z2 * (0.2f + z2 * 0.14285714f)));
+    return v > 20.0f ? v : e < 0.25f ? small : logf(1.0f + e);
+}
 
-// scale * softplus(decay), finite so that a closed gate is a decay of 1.
+// scale * softplus(decay) / log 2, finite so that a closed gate is a decay of 1.
 __device__ __forceinline__ float decay_rate(float decay, float scale) {
-    const float k = scale * softplus(decay);
+    const float k = scale * softplus(decay) * 1.44269504f;
     return k > 1e30f ? 1e30f : k;
 }
 
@@ -250,10 +263,11 @@ __device__ __forceinline__ Run fold_words(const uint64_t* words, int count, floa
 // Where a thread works, and its loads and stores
 // ---------------------------------------------------------------------------
 struct ScanPlace {
-    int64_t b;      // item
-    int64_t len;    // its valid frames
-    uint32_t chain; // of the workgroup: item (or items) and column block
-    int seg, col, have;
+    int64_t b;       // item
+    int64_t len;     // its valid frames
+    uint32_t chain;  // of the workgroup: item (or items) and column block
+    uint32_t lane;   // the thread's first channel within the workgroup's 64
+    int seg, first, have;  // first: the workgroup's first channel
 };
 
 template <int SEGS>
@@ -262,9 +276,10 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a, uint32_t chai
     const int row = threadIdx.x / kScanLanes;
     const uint32_t rest = chain / (uint32_t)a.col_blocks;
     p.chain = chain;
-    p.col = (int)(chain - rest * a.col_blocks) * kScanCols + threadIdx.x % kScanLanes * kScanPair;
-    p.have = a.C - p.col;
-    if (p.have <= 0) p.col = 0;  // past the last channel: loads what is there, stores nothing
+    p.first = (int)(chain - rest * a.col_blocks) * kScanCols;
+    p.lane = threadIdx.x % kScanLanes * kScanPair;
+    p.have = a.C - p.first - (int)p.lane;
+    if (p.have <= 0) p.lane = 0;  // past the last channel: loads what is there, stores nothing
     p.seg = row % SEGS;
     p.b = (int64_t)rest * (kScanRows / SEGS);
     if constexpr (SEGS == 2) p.b += __builtin_amdgcn_readfirstlane(row / SEGS);  // one item a wave
@@ -273,36 +288,77 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a, uint32_t chai
     return p;
 }
 
-// A thread's frames of a tensor in the tile from frame t0 on.  Frames at or past
-// the length (`valid` of the tile's are below it, at least one) read the last
-// valid one and become `dead` (the bits of two stored values).
+// A thread's frames of a tensor in the tile that starts at `tile`: a uniform
+// base for each frame and one 32-bit offset (a frame's stride is below 2^23
+// elements).  Frames at or past the length (`valid` of the tile's are below it,
+// at least one) read the last valid one.
 template <typename S, bool TAIL, int FR>
 __device__ __forceinline__ void load_run(pair_raw<S> out[FR], const void* base, const FrameStride& s,
-                                         const ScanPlace& p, int64_t t0, int valid, bool full, uint32_t dead) {
-    const S* tile = (const S*)base + p.b * s.item + t0 * s.frame;
-    const int at = p.seg * FR;
-    const uint32_t fs = (uint32_t)s.frame;
+                                         const ScanPlace& p, int64_t t0, int valid, bool full) {
+    const char* tile = (const char*)((const S*)base + p.b * s.item + t0 * s.frame + p.first);
+    const uint32_t step = (uint32_t)s.frame * (uint32_t)sizeof(S), lane = p.lane * (uint32_t)sizeof(S);
+    const uint32_t at = p.seg * FR * step + lane;
     if (full) {
 #pragma unroll
-        for (int f = 0; f < FR; ++f) out[f] = load_pair<S, TAIL>(tile + (uint32_t)(f * fs) + (at * fs + p.col), p.have);
-        return;
-    }
+        for (int f = 0; f < FR; ++f) out[f] = load_pair<S, TAIL>((const S*)(tile + (uint32_t)f * step + at), p.have);
+    } else {
+        const uint32_t most = (uint32_t)(valid - 1) * step + lane;
 #pragma unroll
-    for (int f = 0; f < FR; ++f) {
-        const int t = at + f < valid ? at + f : valid - 1;
-        out[f] = load_pair<S, TAIL>(tile + ((uint32_t)t * fs + p.col), p.have);
-        if (at + f >= valid) out[f] = dead;
+        for (int f = 0; f < FR; ++f) out[f] = load_pair<S, TAIL>((const S*)(tile + min(at + f * step, most)), p.have);
     }
 }
 
-// A frame's values, zeros past the length; frames at or past `rows` are not the tile's.
+// The frames before those, one earlier each; frame 0 reads itself in place of the
+// one before it.
 template <typename S, bool TAIL, int FR>
-__device__ __forceinline__ void store_frame(void* base, const FrameStride& s, const ScanPlace& p, int64_t t0, int f,
-                                            int valid, int rows, f32x2 v) {
-    const int t = p.seg * FR + f;
-    if (t >= rows) return;
-    S* tile = (S*)base + p.b * s.item + t0 * s.frame;
-    store_pair<S, TAIL>(tile + ((uint32_t)t * (uint32_t)s.frame + p.col), p.have, t < valid ? v : f32x2(0.0f));
+__device__ __forceinline__ void load_before(pair_raw<S> out[FR], const void* base, const FrameStride& s,
+                                            const ScanPlace& p, int64_t t0, int valid, bool full) {
+    if (t0 > 0) return load_run<S, TAIL, FR>(out, base, s, p, t0 - 1, valid, full);
+    const char* tile = (const char*)((const S*)base + p.b * s.item + p.first);
+    const uint32_t step = (uint32_t)s.frame * (uint32_t)sizeof(S), lane = p.lane * (uint32_t)sizeof(S);
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+        const int t = min(p.seg * FR + f, valid);
+        out[f] = load_pair<S, TAIL>((const S*)(tile + ((t > 0 ? t - 1 : 0) * step + lane)), p.have);
+    }
+}
+
+// What the frames at or past the length become: the bits of two stored values.
+template <typename S, int FR>
+__device__ __forceinline__ void mask_run(pair_raw<S> out[FR], const ScanPlace& p, int valid, uint32_t dead) {
+#pragma unroll
+    for (int f = 0; f < FR; ++f)
+        if (p.seg * FR + f >= valid) out[f] = dead;
+}
+
+// Writes a thread's frames of the tile: zeros past the length, none at or past
+// `rows`.
+template <typename S, bool TAIL, int FR>
+__device__ __forceinline__ void store_run(void* base, const FrameStride& s, const ScanPlace& p, int64_t t0, int valid,
+                                          int rows, bool full, const pair_raw<S> v[FR]) {
+    if (p.have <= 0) return;
+    char* tile = (char*)((S*)base + p.b * s.item + t0 * s.frame + p.first);
+    const uint32_t step = (uint32_t)s.frame * (uint32_t)sizeof(S);
+    const uint32_t at = p.seg * FR * step + p.lane * (uint32_t)sizeof(S);
+    if (full) {
+#pragma unroll
+        for (int f = 0; f < FR; ++f) store_pair<S, TAIL>((S*)(tile + (uint32_t)f * step + at), p.have, v[f]);
+    } else {
+#pragma unroll
+        for (int f = 0; f < FR; ++f) {
+            const int t = p.seg * FR + f;
+            pair_raw<S> q = {};
+            if (t < valid) q = v[f];
+            if (t < rows) store_pair<S, TAIL>((S*)(tile + (uint32_t)f * step + at), p.have, q);
+        }
+    }
+}
+
+// Whether a workgroup goes through several tiles in turn: the other forms are for
+// sequences of one tile at most, and for linked tiles.
+template <int SEGS, int FR, bool LINKED>
+constexpr bool scan_loops() {
+    return !LINKED && SEGS == kScanRows && FR == kScanRun;
 }
 
 template <typename S>
@@ -311,22 +367,37 @@ constexpr uint32_t closed_gate() {  // -infinity, in each stored value
 }
 
 __device__ __forceinline__ f32x2 load_state(const float* base, int64_t row, int32_t C, const ScanPlace& p) {
+    const int64_t at = row * C + p.first + p.lane;
     f32x2 v = {0.0f, 0.0f};
-    if (base && p.have > 0) v[0] = base[row * C + p.col];
-    if (base && p.have > 1) v[1] = base[row * C + p.col + 1];
+    if (base && p.have > 0) v[0] = base[at];
+    if (base && p.have > 1) v[1] = base[at + 1];
     return v;
 }
 
 __device__ __forceinline__ void store_state(float* base, int64_t row, int32_t C, const ScanPlace& p, f32x2 v) {
-    if (p.have > 0) base[row * C + p.col] = v[0];
-    if (p.have > 1) base[row * C + p.col + 1] = v[1];
+    const int64_t at = row * C + p.first + p.lane;
+    if (p.have > 0) base[at] = v[0];
+    if (p.have > 1) base[at + 1] = v[1];
 }
 
-// The tile that this workgroup takes of its chain, in the order of the chain.
-__device__ __forceinline__ int take_tile(uint32_t* ticket, int* lds) {
-    if (threadIdx.x == 0) *lds = (int)__hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// What a workgroup finds out once for all its threads: the tile that it takes of
+// its chain, in the order of the chain, and the decays of its 64 channels.
+struct ScanShared {
+    float decay[kScanCols], rate[kScanCols];
+    int ticket;
+};
+
+template <bool LINKED>
+__device__ __forceinline__ void begin_scan(const ScanArgs& a, const ScanPlace& p, ScanShared& s) {
+    if (LINKED && threadIdx.x == 0)
+        s.ticket = (int)__hip_atomic_fetch_add(a.tickets + (int64_t)p.chain * kScanTicket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x / 64 == 1) {
+        const int lane = threadIdx.x % 64;
+        const float decay = p.first + lane < a.C ? a.decay[p.first + lane] : 0.0f;
+        s.decay[lane] = decay;
+        s.rate[lane] = decay_rate(decay, a.scale);
+    }
     __syncthreads();
-    return __builtin_amdgcn_readfirstlane(*lds);
 }
 
 // The first row of threads publishes a run of the workgroup's 64 channels.
@@ -379,46 +450,48 @@ template <typename S, bool TAIL, int SEGS, int FR, bool LINKED>
 __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a) {
     constexpr int kTileFrames = SEGS * FR;
     __shared__ float lds[LINKED ? 3 : 2][kScanWaves][2][kScanCols];
-    __shared__ int ticket;
+    __shared__ ScanShared shared;
     const uint32_t chains = LINKED ? gridDim.x / (uint32_t)a.tiles : 0;
     const ScanPlace p = scan_place<SEGS>(a, LINKED ? blockIdx.x % chains : blockIdx.x);
-    if (p.b >= a.B) return;  // SEGS < 8, where no thread waits for another wave
-    int tile = LINKED ? take_tile(a.tickets + p.chain, &ticket) : 0;
-    const int end = LINKED ? tile + 1 : a.tiles;
-    const f32x2 decay = load_state(a.decay, 0, a.C, p);
-    const f32x2 rate = {decay_rate(decay[0], a.scale), decay_rate(decay[1], a.scale)};
+    begin_scan<LINKED>(a, p, shared);
+    if (p.b >= a.B) return;  // SEGS < 8, where no thread waits for another wave from here on
+    int tile = LINKED ? __builtin_amdgcn_readfirstlane(shared.ticket) : 0;
+    const int end = scan_loops<SEGS, FR, LINKED>() ? a.tiles : tile + 1;
+    const f32x2 rate = *(const f32x2*)&shared.rate[p.lane];
     f32x2 carry = tile == 0 ? load_state(a.start, p.b, a.C, p) : f32x2(0.0f);
     int turn = 0;
     for (; tile < end; ++tile) {
         const int64_t t0 = (int64_t)tile * kTileFrames, left = p.len - t0, size = a.T - t0;
         const int rows = size < kTileFrames ? (int)size : kTileFrames;
         const int valid = left < 0 ? 0 : left < rows ? (int)left : rows;
+        const bool full = valid == kTileFrames;
         f32x2 d[FR], u[FR];
         Run all = {f32x2(1.0f), f32x2(0.0f)}, before = all;
         if (valid > 0) {
             pair_raw<S> xr[FR], rr[FR], gr[FR];
-            const bool full = valid == kTileFrames;
-            load_run<S, TAIL, FR>(rr, a.r, a.rs, p, t0, valid, full, closed_gate<S>());
-            load_run<S, TAIL, FR>(gr, a.g, a.gs, p, t0, valid, full, 0);
-            load_run<S, TAIL, FR>(xr, a.x, a.xs, p, t0, valid, full, 0);
-            Run run;
+            load_run<S, TAIL, FR>(rr, a.r, a.rs, p, t0, valid, full);
+            load_run<S, TAIL, FR>(gr, a.g, a.gs, p, t0, valid, full);
+            load_run<S, TAIL, FR>(xr, a.x, a.xs, p, t0, valid, full);
+            if (!full) {  // a decay of 1 and no input
+                mask_run<S, FR>(rr, p, valid, closed_gate<S>());
+                mask_run<S, FR>(xr, p, valid, 0);
+            }
+            f32x2 w = {0.0f, 0.0f}, h = w;
 #pragma unroll
-            for (int e = 0; e < kScanPair; ++e) {
-                float w = 0.0f, h = 0.0f;
+            for (int f = 0; f < FR; ++f) {
 #pragma unroll
-                for (int f = 0; f < FR; ++f) {
+                for (int e = 0; e < kScanPair; ++e) {
                     const float wf = rate[e] * sigmoid_of<S>(pair_at<S>(rr[f], e));
-                    const float df = one_minus_exp(wf);
+                    const float df = one_minus_exp2(wf);
                     const float m = __builtin_amdgcn_sqrtf(df * (2.0f - df));
                     const float uf = m * (sigmoid_of<S>(pair_at<S>(gr[f], e)) * pair_at<S>(xr[f], e));
                     d[f][e] = df;
                     u[f][e] = uf;
-                    w += wf;
-                    h = __builtin_fmaf(-df, h, h) + uf;
+                    w[e] += wf;
+                    h[e] = __builtin_fmaf(-df, h[e], h[e]) + uf;
                 }
-                run.p[e] = __builtin_amdgcn_exp2f(w * -1.44269504f);
-                run.h[e] = h;
             }
+            const Run run = {{__builtin_amdgcn_exp2f(-w[0]), __builtin_amdgcn_exp2f(-w[1])}, h};
             const TileRuns t = tile_runs<SEGS, false>(run, lds[turn]);
             turn ^= 1;
             all = t.all;
@@ -426,83 +499,85 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
         }
         const bool wanted = valid > 0 || (a.end && tile == a.tiles - 1);
         f32x2 h = through(before, enter_tile<LINKED>(a, p, all, tile, wanted, carry, lds + 1));
-        if (p.have > 0) {
+        pair_raw<S> y[FR] = {};
+        if (valid > 0) {
 #pragma unroll
             for (int f = 0; f < FR; ++f) {
-                if (valid > 0) {
 #pragma unroll
-                    for (int e = 0; e < kScanPair; ++e) h[e] = __builtin_fmaf(-d[f][e], h[e], h[e]) + u[f][e];
-                }
-                store_frame<S, TAIL, FR>(a.y, a.ys, p, t0, f, valid, rows, h);
+                for (int e = 0; e < kScanPair; ++e) h[e] = __builtin_fmaf(-d[f][e], h[e], h[e]) + u[f][e];
+                y[f] = pack_pair<S>(h);
             }
         }
+        store_run<S, TAIL, FR>(a.y, a.ys, p, t0, valid, rows, full, y);
     }
-    if (a.end && end == a.tiles && p.seg == 0) store_state(a.end, p.b, a.C, p, carry);
+    if (a.end && end >= a.tiles && p.seg == 0) store_state(a.end, p.b, a.C, p, carry);
 }
 
 // ---------------------------------------------------------------------------
 // Backward in time, G_t = dy_t + a_{t+1} G_{t+1}: the runs hand a_t G_t on to
 // the frames before them.
 // ---------------------------------------------------------------------------
+//
+// Waves that share a SIMD at least: linked bf16 tiles 4 (128 registers; [16,750,1024]
+// 52.9 us against 54.8 with the 131 that it would take), in turn 2.
+template <typename S, bool LINKED>
+constexpr int scan_bwd_waves() {
+    return LINKED ? (sizeof(S) == 2 ? 4 : 1) : 2;
+}
+
 template <typename S, bool TAIL, int SEGS, int FR, bool LINKED>
-__global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanArgs a) {
+__global__ __launch_bounds__(kScanThreads, (scan_bwd_waves<S, LINKED>())) void scan_bwd_kernel(const ScanArgs a) {
     constexpr int kTileFrames = SEGS * FR;
     __shared__ float lds[LINKED ? 3 : 2][kScanWaves][2][kScanCols];
     __shared__ float column[kScanRows][kScanCols];
-    __shared__ int ticket;
+    __shared__ ScanShared shared;
     const uint32_t chains = LINKED ? gridDim.x / (uint32_t)a.tiles : 0;
     const ScanPlace p = scan_place<SEGS>(a, LINKED ? blockIdx.x % chains : blockIdx.x);
     const bool item = p.b < a.B;
-    int at = LINKED ? take_tile(a.tickets + p.chain, &ticket) : 0;  // in the order of the chain: the last tile is first
-    const int end = LINKED ? at + 1 : item ? a.tiles : 0;
+    begin_scan<LINKED>(a, p, shared);
+    int at = LINKED ? __builtin_amdgcn_readfirstlane(shared.ticket) : 0;  // in the order of the chain: the last tile is first
+    const int end = LINKED ? at + 1 : !item ? 0 : scan_loops<SEGS, FR, LINKED>() ? a.tiles : 1;
     const int row = LINKED ? (int)(p.chain / (uint32_t)a.col_blocks) * a.tiles + at : (int)(p.chain / (uint32_t)a.col_blocks);
-    const f32x2 decay = load_state(a.decay, 0, a.C, p);
-    const f32x2 rate = {decay_rate(decay[0], a.scale), decay_rate(decay[1], a.scale)};
+    const f32x2 rate = *(const f32x2*)&shared.rate[p.lane];
+    f32x2 unrate;  // w * unrate is the gate; where the rate is 0 nothing comes of it
+#pragma unroll
+    for (int e = 0; e < kScanPair; ++e) unrate[e] = rate[e] > 1e-30f ? __builtin_amdgcn_rcpf(rate[e]) : 0.0f;
     f32x2 carry = item && at == 0 ? load_state(a.start, p.b, a.C, p) : f32x2(0.0f), sum = {0.0f, 0.0f};
     int turn = 0;
     for (; at < end; ++at) {
-        const int64_t t0 = (int64_t)(a.tiles - 1 - at) * kTileFrames, left = p.len - t0, size = a.T - t0;
+        const int64_t t0 = (int64_t)(scan_loops<SEGS, FR, LINKED>() || LINKED ? a.tiles - 1 - at : 0) * kTileFrames, left = p.len - t0, size = a.T - t0;
         const int rows = size < kTileFrames ? (int)size : kTileFrames;
         const int valid = left < 0 ? 0 : left < rows ? (int)left : rows;
-        pair_raw<S> rr[FR], dyr[FR], xr[FR], gr[FR];
-        f32x2 prev[FR], d[FR], w[FR];
+        const bool full = valid == kTileFrames;
+        pair_raw<S> rr[FR] = {}, dyr[FR], xr[FR] = {}, gr[FR] = {}, prev[FR];
+        f32x2 d[FR], w[FR];
         Run all = {f32x2(1.0f), f32x2(0.0f)}, before = all;
         if (valid > 0) {
-            const bool full = valid == kTileFrames;
-            load_run<S, TAIL, FR>(rr, a.r, a.rs, p, t0, valid, full, closed_gate<S>());
-            load_run<S, TAIL, FR>(dyr, a.dy, a.dys, p, t0, valid, full, 0);
-            load_run<S, TAIL, FR>(xr, a.x, a.xs, p, t0, valid, full, 0);
-            load_run<S, TAIL, FR>(gr, a.g, a.gs, p, t0, valid, full, 0);
+            load_run<S, TAIL, FR>(rr, a.r, a.rs, p, t0, valid, full);
+            load_run<S, TAIL, FR>(dyr, a.dy, a.dys, p, t0, valid, full);
+            load_run<S, TAIL, FR>(xr, a.x, a.xs, p, t0, valid, full);
+            load_run<S, TAIL, FR>(gr, a.g, a.gs, p, t0, valid, full);
             // the state before each frame: what the forward stored for the one in front of it
-            const S* y = (const S*)a.yin + p.b * a.ys.item + t0 * a.ys.frame;
-#pragma unroll
-            for (int f = 0; f < FR; ++f) {
-                const int t = p.seg * FR + f;
-                if (f == 0 && p.seg == 0 && t0 == 0) {
-                    prev[f] = load_state(a.h0, p.b, a.C, p);
-                } else {
-                    const int from = (t < valid ? t : valid) - 1;  // -1: the tile before
-                    const pair_raw<S> q = load_pair<S, TAIL>(y + (from * (int64_t)a.ys.frame + p.col), p.have);
-                    prev[f] = f32x2{pair_at<S>(q, 0), pair_at<S>(q, 1)};
-                }
+            load_before<S, TAIL, FR>(prev, a.yin, a.ys, p, t0, valid, full);
+            if (!full) {  // a decay of 1 and no gradient
+                mask_run<S, FR>(rr, p, valid, closed_gate<S>());
+                mask_run<S, FR>(dyr, p, valid, 0);
             }
-            Run run;
+            f32x2 sw = {0.0f, 0.0f}, c = sw;
 #pragma unroll
-            for (int e = 0; e < kScanPair; ++e) {
-                float sw = 0.0f, c = 0.0f;
+            for (int f = FR - 1; f >= 0; --f) {
 #pragma unroll
-                for (int f = FR - 1; f >= 0; --f) {
+                for (int e = 0; e < kScanPair; ++e) {
                     const float wf = rate[e] * sigmoid_of<S>(pair_at<S>(rr[f], e));
-                    const float df = one_minus_exp(wf);
+                    const float df = one_minus_exp2(wf);
                     w[f][e] = wf;
                     d[f][e] = df;
-                    const float G = pair_at<S>(dyr[f], e) + c;
-                    c = __builtin_fmaf(-df, G, G);
-                    sw += wf;
+                    const float G = pair_at<S>(dyr[f], e) + c[e];
+                    c[e] = __builtin_fmaf(-df, G, G);
+                    sw[e] += wf;
                 }
-                run.p[e] = __builtin_amdgcn_exp2f(sw * -1.44269504f);
-                run.h[e] = c;
             }
+            const Run run = {{__builtin_amdgcn_exp2f(-sw[0]), __builtin_amdgcn_exp2f(-sw[1])}, c};
             const TileRuns t = tile_runs<SEGS, true>(run, lds[turn]);
             turn ^= 1;
             all = t.all;
@@ -510,46 +585,52 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanArgs a
         }
         const bool wanted = valid > 0 || (a.end && at == a.tiles - 1);
         f32x2 c = through(before, enter_tile<LINKED>(a, p, all, at, wanted, carry, lds + 1));
+        if (valid > 0) {
+            const bool start = t0 == 0 && p.seg == 0;
+            const f32x2 h0 = start ? load_state(a.h0, p.b, a.C, p) : f32x2(0.0f);
 #pragma unroll
-        for (int f = FR - 1; f >= 0; --f) {
-            f32x2 dx = {0.0f, 0.0f}, dr = dx, dg = dx;
-            if (valid > 0) {
+            for (int f = FR - 1; f >= 0; --f) {
+                f32x2 dx, dr, dg;
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
                     const float G = pair_at<S>(dyr[f], e) + c[e];
-                    const float x = pair_at<S>(xr[f], e), s = sigmoid_of<S>(pair_at<S>(rr[f], e));
                     const float gate = sigmoid_of<S>(pair_at<S>(gr[f], e));
+                    const float h = f == 0 && start ? h0[e] : pair_at<S>(prev[f], e);
                     const float df = d[f][e], z = df * (2.0f - df);                   // 1 - a^2 = m^2
-                    const float rs = __builtin_amdgcn_rsqf(z > 1e-37f ? z : 1e-37f);  // w / m is 0 where w is
-                    const float ix = gate * x, open = G * (z * rs);
-                    const float q = G * w[f][e] * (ix * (1.0f - z) * rs - prev[f][e] * (1.0f - df));
+                    const float rs = __builtin_amdgcn_rsqf(z > 1e-37f ? z : 1e-37f);  // m = z rs, 0 where z is
+                    const float v = rs * rs;
+                    dx[e] = G * (z * rs) * gate;
+                    const float t = dx[e] * pair_at<S>(xr[f], e);
+                    dg[e] = t - t * gate;
                     c[e] = __builtin_fmaf(-df, G, G);
-                    dx[e] = open * gate;
-                    dg[e] = open * ix * (1.0f - gate);
-                    dr[e] = q * (1.0f - s);
-                    sum[e] += p.seg * FR + f < valid ? q : 0.0f;
+                    // G i x a^2 / m = t a^2 / m^2
+                    const float q = w[f][e] * (t * (v - z * v) - c[e] * h);
+                    const float s = w[f][e] * unrate[e];
+                    dr[e] = q * (0.69314718f - 0.69314718f * s);
+                    sum[e] += full || p.seg * FR + f < valid ? q : 0.0f;
                 }
-            }
-            if (p.have > 0) {
-                if (a.dx) store_frame<S, TAIL, FR>(a.dx, a.dxs, p, t0, f, valid, rows, dx);
-                if (a.dr) store_frame<S, TAIL, FR>(a.dr, a.drs, p, t0, f, valid, rows, dr);
-                if (a.dg) store_frame<S, TAIL, FR>(a.dg, a.dgs, p, t0, f, valid, rows, dg);
+                xr[f] = pack_pair<S>(dx);  // the gradients take their inputs' places
+                rr[f] = pack_pair<S>(dr);
+                gr[f] = pack_pair<S>(dg);
             }
         }
+        if (a.dx) store_run<S, TAIL, FR>(a.dx, a.dxs, p, t0, valid, rows, full, xr);
+        if (a.dr) store_run<S, TAIL, FR>(a.dr, a.drs, p, t0, valid, rows, full, rr);
+        if (a.dg) store_run<S, TAIL, FR>(a.dg, a.dgs, p, t0, valid, rows, full, gr);
     }
-    if (a.end && end == a.tiles && item && p.seg == 0) store_state(a.end, p.b, a.C, p, carry);
+    if (a.end && end >= a.tiles && item && p.seg == 0) store_state(a.end, p.b, a.C, p, carry);
     if (!a.partial) return;
     const int mine = threadIdx.x / kScanLanes, lane = threadIdx.x % kScanLanes;
 #pragma unroll
-    for (int e = 0; e < kScanPair; ++e) column[mine][lane * kScanPair + e] = sum[e];
+    for (int e = 0; e < kScanPair; ++e) column[mine][lane * kScanPair + e] = 0.69314718f * sum[e];
     __syncthreads();
     if (mine != 0) return;
-    double* out = a.partial + (int64_t)row * a.C + p.col;
+    double* out = a.partial + (int64_t)row * a.C + p.first + p.lane;
 #pragma unroll
     for (int e = 0; e < kScanPair; ++e) {
         double t = 0.0;
         for (int q = 0; q < kScanRows; ++q) t += column[q][lane * kScanPair + e];
-        if (e < p.have) out[e] = t * softplus_slope(decay[e]);
+        if (e < p.have) out[e] = t * softplus_slope(shared.decay[p.lane + e]);
     }
 }
 
@@ -570,15 +651,28 @@ struct ScanPlan {
     int64_t tiles, row_blocks, col_blocks;  // row_blocks: of one column block, tiles among them where linked
 };
 
-static ScanPlan scan_plan(const ScanShape& s, int run) {
+// Runs of 16 frames (forward only: the gradients' would not leave registers for
+// two waves a SIMD) make one tile of up to 128 frames, and in longer sequences
+// halve the words that a tile reads of those before it; with 8, sequences waste
+// less where they end.  us for 16 and 8: bf16 [16,750,1024] with lengths of half
+// to all 27.9 and 25.4, [64,750,256] 29.6 and 28.4, [32,1500,512] 52.5 and 54.8,
+// [2,6001,512] 19.7 and 20.3, float 24.7 and 26.8.
+//
+// Linked or in turn, us: 256 chains, bf16 [16,750,1024] 30 and 32 (gradients 59
+// and 77), float 45 and 58 (98 and 98); 512 chains, [16,1500,2048] bf16 101 and
+// 96 (204 and 215), float 165 and 159 (355 and 332), [32,130,1024] bf16 17 and 15.
+static ScanPlan scan_plan(const ScanShape& s, bool backward) {
     ScanPlan p = {};
-    p.run = s.T == 1 ? 1 : s.T <= kScanRows * kScanShortRun ? kScanShortRun : run;
-    p.segs = s.T <= p.run ? 1 : s.T <= 2 * p.run ? 2 : kScanRows;
+    const int64_t one = kScanRows * kScanRun;
     p.col_blocks = (s.C + kScanCols - 1) / kScanCols;
+    const bool many = s.B * p.col_blocks >= 512;
+    p.run = s.T == 1 ? 1 : kScanRun;
+    if (!backward && s.T > one && (s.T <= 2 * one || (!many && s.T > 1024))) p.run = kScanLongRun;
+    p.segs = s.T <= p.run ? 1 : s.T <= 2 * p.run ? 2 : kScanRows;
     p.tiles = (s.T + p.segs * p.run - 1) / (p.segs * p.run);
     const int64_t per = kScanRows / p.segs;
     p.row_blocks = (s.B + per - 1) / per;
-    p.linked = p.tiles > 1 && p.row_blocks * p.col_blocks < 1024;
+    p.linked = p.tiles > 1 && !many;
     if (p.linked) p.row_blocks *= p.tiles;
     return p;
 }
@@ -587,8 +681,8 @@ static int64_t scan_chains(const ScanPlan& p) { return p.row_blocks / p.tiles * 
 
 bool dwscan_fits(const ScanShape& s) {
     if (!product_below((int64_t)1 << 58, {s.B, s.T, s.C})) return false;
-    for (const int run : {kScanFwdRun, kScanBwdRun}) {
-        const ScanPlan p = scan_plan(s, run);
+    for (const bool backward : {false, true}) {
+        const ScanPlan p = scan_plan(s, backward);
         if (!product_below((int64_t)1 << 24, {p.row_blocks, p.col_blocks})) return false;
     }
     return true;
@@ -596,7 +690,7 @@ bool dwscan_fits(const ScanShape& s) {
 
 // Tickets and words of a linked plan.
 static size_t scan_ticket_bytes(const ScanPlan& p) {
-    return p.linked ? ((size_t)scan_chains(p) * sizeof(uint32_t) + 15) / 16 * 16 : 0;
+    return p.linked ? (size_t)(scan_chains(p) * kScanTicket) * sizeof(uint32_t) : 0;
 }
 
 static size_t scan_link_bytes(const ScanPlan& p) {
@@ -609,10 +703,10 @@ static int64_t scan_partial_rows(const ScanPlan& p) {
     return p.row_blocks + (chunks > 1 ? chunks : 1);
 }
 
-size_t dwscan_fwd_workspace(const ScanShape& s) { return scan_link_bytes(scan_plan(s, kScanFwdRun)); }
+size_t dwscan_fwd_workspace(const ScanShape& s) { return scan_link_bytes(scan_plan(s, false)); }
 
 size_t dwscan_bwd_workspace(const ScanShape& s) {
-    const ScanPlan p = scan_plan(s, kScanBwdRun);
+    const ScanPlan p = scan_plan(s, true);
     return scan_link_bytes(p) + (size_t)(scan_partial_rows(p) * s.C) * sizeof(double);
 }
 
@@ -642,21 +736,26 @@ static hipError_t launch_scan_kernel(const ScanPlan& plan, const ScanArgs& a, hi
 
 template <bool BACK, typename S, bool TAIL>
 static hipError_t launch_scan_form(const ScanPlan& plan, const ScanArgs& a, hipStream_t stream) {
-    constexpr int kRun = BACK ? kScanBwdRun : kScanFwdRun;
     if (plan.linked) {
         const int64_t n = (int64_t)(scan_link_bytes(plan) / sizeof(u32x4)), blocks = (n + kScanThreads - 1) / kScanThreads;
         hipLaunchKernelGGL(scan_clear_kernel, dim3((uint32_t)(blocks < 1024 ? blocks : 1024)), dim3(kScanThreads), 0,
                            stream, (u32x4*)a.tickets, n);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        return launch_scan_kernel<BACK, S, TAIL, kScanRows, kRun, true>(plan, a, stream);
+        if constexpr (!BACK) {
+            if (plan.run == kScanLongRun)
+                return launch_scan_kernel<BACK, S, TAIL, kScanRows, kScanLongRun, true>(plan, a, stream);
+        }
+        return launch_scan_kernel<BACK, S, TAIL, kScanRows, kScanRun, true>(plan, a, stream);
     }
     if (plan.run == 1) return launch_scan_kernel<BACK, S, TAIL, 1, 1, false>(plan, a, stream);
-    if (plan.segs == 1) return launch_scan_kernel<BACK, S, TAIL, 1, kScanShortRun, false>(plan, a, stream);
-    if (plan.segs == 2) return launch_scan_kernel<BACK, S, TAIL, 2, kScanShortRun, false>(plan, a, stream);
-    if (plan.run == kScanShortRun)
-        return launch_scan_kernel<BACK, S, TAIL, kScanRows, kScanShortRun, false>(plan, a, stream);
-    return launch_scan_kernel<BACK, S, TAIL, kScanRows, kRun, false>(plan, a, stream);
+    if (plan.segs == 1) return launch_scan_kernel<BACK, S, TAIL, 1, kScanRun, false>(plan, a, stream);
+    if (plan.segs == 2) return launch_scan_kernel<BACK, S, TAIL, 2, kScanRun, false>(plan, a, stream);
+    if constexpr (!BACK) {
+        if (plan.run == kScanLongRun)
+            return launch_scan_kernel<BACK, S, TAIL, kScanRows, kScanLongRun, false>(plan, a, stream);
+    }
+    return launch_scan_kernel<BACK, S, TAIL, kScanRows, kScanRun, false>(plan, a, stream);
 }
 
 template <bool BACK>
@@ -670,7 +769,7 @@ static hipError_t launch_scan(const ScanPlan& plan, const ScanArgs& a, bool bf16
 
 hipError_t launch_dwscan_fwd(const ScanPtrs& p, const ScanShape& s, void* y, float* h_last, void* workspace, bool bf16,
                              hipStream_t stream) {
-    const ScanPlan plan = scan_plan(s, kScanFwdRun);
+    const ScanPlan plan = scan_plan(s, false);
     ScanArgs a = scan_args(p, s, plan, workspace);
     a.start = p.h0, a.y = y, a.end = h_last;
     return launch_scan<false>(plan, a, bf16, stream);
@@ -679,7 +778,7 @@ hipError_t launch_dwscan_fwd(const ScanPtrs& p, const ScanShape& s, void* y, flo
 hipError_t launch_dwscan_bwd(const ScanPtrs& p, const ScanShape& s, const void* y, const void* dy, const float* dh_last,
                              void* dx, void* dr, void* dg, float* ddecay, float* dh0, void* workspace, bool bf16,
                              hipStream_t stream) {
-    const ScanPlan plan = scan_plan(s, kScanBwdRun);
+    const ScanPlan plan = scan_plan(s, true);
     ScanArgs a = scan_args(p, s, plan, workspace);
     a.start = dh_last, a.h0 = p.h0, a.yin = y, a.dy = dy, a.dx = dx, a.dr = dr, a.dg = dg, a.end = dh0;
     double* rows = (double*)((char*)workspace + scan_link_bytes(plan));
