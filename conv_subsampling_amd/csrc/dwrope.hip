@@ -30,7 +30,7 @@ struct RopeArgs {
     const double* freq;
     const int32_t *lengths, *pos, *place;
     void *q_out, *k_out, *v_out;  // backward: dq, dk
-    double* partial;              // backward: [gridDim.x][2][D], NULL: not wanted
+    float* partial;               // backward: [gridDim.x][2][D], NULL: not wanted
     RopeStride qs, ks, vs, qos, kos, vos, dqs, dks;
     int64_t S;
     uint64_t frames;  // B * T
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_bwd_kernel(const RopeArgs a
     __syncthreads();
     if (threadIdx.x >= 2 * LANES) return;
     const int n = threadIdx.x / LANES;
-    double* out = a.partial + ((int64_t)blockIdx.x * 2 + n) * D;
+    float* out = a.partial + ((int64_t)blockIdx.x * 2 + n) * D;
     Head total = {};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
@@ -368,29 +368,65 @@ __global__ __launch_bounds__(kRopeThreads) void rope_bwd_kernel(const RopeArgs a
     }
 }
 
+// Column sums of the [P][2][D] partials in fp64: 64 sub-rows x 16 columns a
+// workgroup, sub-row q adding partials q, q + 64, ..., then the sub-rows in
+// order, 16 at a time.
+constexpr int kGammaCols = 16, kGammaRows = 64, kGammaParts = 4;
+
+__global__ __launch_bounds__(kGammaCols* kGammaRows) void rope_gamma_reduce(const float* __restrict__ partial,
+                                                                           float* __restrict__ dq_gamma,
+                                                                           float* __restrict__ dk_gamma, int32_t D,
+                                                                           int32_t P) {
+    __shared__ double acc[kGammaRows][kGammaCols];
+    const int lane = threadIdx.x % kGammaCols, sub = threadIdx.x / kGammaCols, ncol = 2 * D;
+    const int col = blockIdx.x * kGammaCols + lane;
+    double s = 0.0;
+    if (col < ncol) {
+#pragma unroll 8
+        for (int32_t r = sub; r < P; r += kGammaRows) s += partial[(int64_t)r * ncol + col];
+    }
+    acc[sub][lane] = s;
+    __syncthreads();
+    constexpr int kEach = kGammaRows / kGammaParts;
+    if (sub < kGammaParts) {
+        s = 0.0;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) s += acc[sub * kEach + q][lane];
+    }
+    __syncthreads();
+    if (sub < kGammaParts) acc[sub][lane] = s;
+    __syncthreads();
+    if (sub != 0 || col >= ncol) return;
+#pragma unroll
+    for (int q = 1; q < kGammaParts; ++q) s += acc[q][lane];
+    float* out = col < D ? dq_gamma : dk_gamma;
+    if (out) out[col < D ? col : col - D] = (float)s;
+}
+
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
 static int rope_lanes(int64_t D) { return D <= 32 ? 4 : D <= 64 ? 8 : 16; }
 
 // Teams that share a frame's heads: one where the frames alone fill the GPU
-// (its cosines then serve all heads), else as many as there are heads.
-static int64_t rope_split(const RopeShape& s) {
+// (its cosines then serve all heads), else as many as there are heads.  12000
+// frames of 8 + 8 heads of 128 (192000 lanes), 1 and 2 teams a frame, us:
+// forward 20.5 and 19.2, gradients 29.4 and 32.2.
+static int64_t rope_split(const RopeShape& s, bool backward) {
     const int64_t heads = s.H > s.Hkv ? s.H : s.Hkv, lanes = s.B * s.T * rope_lanes(s.D);
+    const int64_t enough = backward ? 128 * 1024 : 256 * 1024;
     int64_t n = 1;
-    while (n < heads && n < 64 && lanes * n < 256 * 1024) n *= 2;
+    while (n < heads && n < 64 && lanes * n < enough) n *= 2;
     return n;
 }
 
-static int64_t rope_teams(const RopeShape& s) { return s.B * s.T * rope_split(s); }
-
-static int64_t rope_blocks(const RopeShape& s) {
-    const int64_t per = kRopeThreads / rope_lanes(s.D);
-    return (rope_teams(s) + per - 1) / per;
+static int64_t rope_blocks(const RopeShape& s, bool backward) {
+    const int64_t per = kRopeThreads / rope_lanes(s.D), teams = s.B * s.T * rope_split(s, backward);
+    return (teams + per - 1) / per;
 }
 
 bool dwrope_fits(const RopeShape& s) {
-    return product_below((int64_t)1 << 40, {s.B, s.T}) && grid_of_256_fits(rope_blocks(s));
+    return product_below((int64_t)1 << 40, {s.B, s.T}) && grid_of_256_fits(rope_blocks(s, false));
 }
 
 template <bool P, bool H, int L>
@@ -417,14 +453,14 @@ static hipError_t with_rope_form(const RopeShape& s, F&& f) {
 
 static RopeStride rope_stride(const AttnStride& s) { return {s.item, s.frame, s.head}; }
 
-static RopeArgs rope_args(const RopePtrs& p, const RopeShape& s) {
+static RopeArgs rope_args(const RopePtrs& p, const RopeShape& s, bool backward) {
     RopeArgs a = {};
     a.q = p.q, a.k = p.k, a.q_gamma = p.q_gamma, a.k_gamma = p.k_gamma;
     a.freq = p.freq, a.lengths = p.lengths, a.pos = p.pos;
     a.qs = rope_stride(s.q), a.ks = rope_stride(s.k), a.vs = rope_stride(s.v);
     a.qos = rope_stride(s.q_out), a.kos = rope_stride(s.k_out), a.vos = rope_stride(s.v_out);
     a.dqs = rope_stride(s.dq), a.dks = rope_stride(s.dk);
-    a.S = s.S, a.frames = (uint64_t)(s.B * s.T), a.T = (uint32_t)s.T, a.split = (uint32_t)rope_split(s);
+    a.S = s.S, a.frames = (uint64_t)(s.B * s.T), a.T = (uint32_t)s.T, a.split = (uint32_t)rope_split(s, backward);
     a.H = (int32_t)s.H, a.Hkv = (int32_t)s.Hkv, a.D = (int32_t)s.D, a.R = (int32_t)s.R;
     a.eps = s.eps;
     return a;
@@ -432,9 +468,9 @@ static RopeArgs rope_args(const RopePtrs& p, const RopeShape& s) {
 
 hipError_t launch_dwrope_fwd(const RopePtrs& p, const RopeShape& s, const void* v, const int32_t* place, void* q_out,
                              void* k_out, void* v_out, bool bf16, hipStream_t stream) {
-    RopeArgs a = rope_args(p, s);
+    RopeArgs a = rope_args(p, s, false);
     a.v = v, a.place = place, a.q_out = q_out, a.k_out = k_out, a.v_out = v_out;
-    const dim3 grid((uint32_t)rope_blocks(s));
+    const dim3 grid((uint32_t)rope_blocks(s, false));
     return with_rope_form(s, [&](auto form) {
         using N = decltype(form);
         if (bf16)
@@ -447,23 +483,23 @@ hipError_t launch_dwrope_fwd(const RopePtrs& p, const RopeShape& s, const void* 
     });
 }
 
+// As many as take equal turns.
 static int64_t rope_bwd_blocks(const RopeShape& s) {
-    const int64_t blocks = rope_blocks(s);
-    return blocks < kRopeBwdBlocks ? blocks : kRopeBwdBlocks;
+    const int64_t blocks = rope_blocks(s, true), turns = (blocks + kRopeBwdBlocks - 1) / kRopeBwdBlocks;
+    return turns > 1 ? (blocks + turns - 1) / turns : blocks;
 }
 
 size_t dwrope_bwd_workspace(const RopeShape& s) {
-    const int64_t rows = rope_bwd_blocks(s);
-    return (size_t)(rows + partial_reduce_chunks(rows) + 1) * 2 * (size_t)s.D * sizeof(double);
+    return (size_t)rope_bwd_blocks(s) * 2 * (size_t)s.D * sizeof(float);
 }
 
 hipError_t launch_dwrope_bwd(const RopePtrs& p, const RopeShape& s, const void* dq_out, const void* dk_out, void* dq,
                              void* dk, float* dq_gamma, float* dk_gamma, void* workspace, bool bf16,
                              hipStream_t stream) {
-    RopeArgs a = rope_args(p, s);
+    RopeArgs a = rope_args(p, s, true);
     a.dq_out = dq_out, a.dk_out = dk_out, a.q_out = dq, a.k_out = dk;
     const bool params = dq_gamma || dk_gamma;
-    a.partial = params ? (double*)workspace : nullptr;
+    a.partial = params ? (float*)workspace : nullptr;
     const int64_t blocks = rope_bwd_blocks(s);
     if (blocks > 0) {
         const hipError_t e = with_rope_form(s, [&](auto form) {
@@ -479,12 +515,10 @@ hipError_t launch_dwrope_bwd(const RopePtrs& p, const RopeShape& s, const void* 
         if (e != hipSuccess) return e;
     }
     if (!params) return hipSuccess;
-    RowOutputs out = {};
-    out.n = 2;
-    out.p[0] = dq_gamma, out.first[0] = 0, out.count[0] = 1;
-    out.p[1] = dk_gamma, out.first[1] = 1, out.count[1] = 1;
-    double* rows = (double*)workspace;
-    return launch_partial_reduce(rows, blocks, 2, s.D, rows + blocks * 2 * s.D, out, stream);
+    hipLaunchKernelGGL(rope_gamma_reduce, dim3((uint32_t)((2 * s.D + kGammaCols - 1) / kGammaCols)),
+                       dim3(kGammaCols * kGammaRows), 0, stream, (const float*)workspace, dq_gamma, dk_gamma,
+                       (int32_t)s.D, (int32_t)blocks);
+    return hipGetLastError();
 }
 
 }  // namespace dw
