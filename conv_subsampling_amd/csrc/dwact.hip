@@ -10,7 +10,6 @@
 // Bound by memory: about 20 vector operations an element beside 2 to 5 bytes.
 #include "launch.h"
 #include "rowops.h"
-#include "quad.h"
 
 namespace dw {
 
@@ -30,9 +29,10 @@ struct ActArgs {
     int32_t C;
 };
 
-// sigmoid_of that keeps its tail below 2^-126, which the activation's input lifts
-// back into the range: float by exp(-|v|), which does not overflow; bf16 by a
-// reciprocal taken 2^24 higher.
+// 1 / (1 + exp(-v)), kept below 2^-126 too, from where the activation's input lifts
+// it back into the range.  float: exp(-|v|), within a few units in the last place,
+// does not overflow.  bf16: the exponent is one rounded product (off by |v| 2^-24
+// of the result), the reciprocal is taken 2^24 higher.
 template <typename S>
 __device__ __forceinline__ float tail_sigmoid(float v) {
     if constexpr (sizeof(S) == 4) {

@@ -24,7 +24,6 @@
 // workgroup that has started, and that one waits for earlier ones alone.
 #include "launch.h"
 #include "rowops.h"
-#include "quad.h"
 
 namespace dw {
 
@@ -119,6 +118,13 @@ __device__ __forceinline__ void store_pair(S* p, int have, pair_raw<S> q) {
 // ---------------------------------------------------------------------------
 // The step's functions
 // ---------------------------------------------------------------------------
+// 1 / (1 + exp(-v)).  The exponent is one rounded product, so the result is off by
+// up to |v| 2^-24 of itself for negative v; an exponential that reduces its
+// argument cost 2 us of 25 ([2,6001,512] float).  Results below 2^-126 are zero.
+__device__ __forceinline__ float sigmoid(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+}
+
 // 1 - 2^-v, v = w / log 2: a series in w where the difference would cancel (its
 // first left out term is 2^-24.4 of it at w = 1/8), the exponential beyond (off
 // by 2^-21 at most).
@@ -481,10 +487,10 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
             for (int f = 0; f < FR; ++f) {
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
-                    const float wf = rate[e] * sigmoid_of<S>(pair_at<S>(rr[f], e));
+                    const float wf = rate[e] * sigmoid(pair_at<S>(rr[f], e));
                     const float df = one_minus_exp2(wf);
                     const float m = __builtin_amdgcn_sqrtf(df * (2.0f - df));
-                    const float uf = m * (sigmoid_of<S>(pair_at<S>(gr[f], e)) * pair_at<S>(xr[f], e));
+                    const float uf = m * (sigmoid(pair_at<S>(gr[f], e)) * pair_at<S>(xr[f], e));
                     d[f][e] = df;
                     u[f][e] = uf;
                     w[e] += wf;
@@ -518,11 +524,12 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
 // the frames before them.
 // ---------------------------------------------------------------------------
 //
-// Waves that share a SIMD at least: linked bf16 tiles 4 (128 registers; [16,750,1024]
-// 52.9 us against 54.8 with the 131 that it would take), in turn 2.
+// Waves that share a SIMD at least.  Linked bf16 tiles 4 (128 registers; [16,750,1024]
+// 52.9 us against 54.8 with the 131 that it would take), float 3 (168; 96 against
+// 98, [8,375,1024] 25.5 against 28.9); in turn 2.
 template <typename S, bool LINKED>
 constexpr int scan_bwd_waves() {
-    return LINKED ? (sizeof(S) == 2 ? 4 : 1) : 2;
+    return LINKED ? (sizeof(S) == 2 ? 4 : 3) : 2;
 }
 
 template <typename S, bool TAIL, int SEGS, int FR, bool LINKED>
@@ -568,7 +575,7 @@ __global__ __launch_bounds__(kScanThreads, (scan_bwd_waves<S, LINKED>())) void s
             for (int f = FR - 1; f >= 0; --f) {
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
-                    const float wf = rate[e] * sigmoid_of<S>(pair_at<S>(rr[f], e));
+                    const float wf = rate[e] * sigmoid(pair_at<S>(rr[f], e));
                     const float df = one_minus_exp2(wf);
                     w[f][e] = wf;
                     d[f][e] = df;
@@ -594,7 +601,7 @@ __global__ __launch_bounds__(kScanThreads, (scan_bwd_waves<S, LINKED>())) void s
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
                     const float G = pair_at<S>(dyr[f], e) + c[e];
-                    const float gate = sigmoid_of<S>(pair_at<S>(gr[f], e));
+                    const float gate = sigmoid(pair_at<S>(gr[f], e));
                     const float h = f == 0 && start ? h0[e] : pair_at<S>(prev[f], e);
                     const float df = d[f][e], z = df * (2.0f - df);                   // 1 - a^2 = m^2
                     const float rs = __builtin_amdgcn_rsqf(z > 1e-37f ? z : 1e-37f);  // m = z rs, 0 where z is

@@ -1,5 +1,5 @@
-// Four neighbouring columns of a row, as the operators over frames and heads
-// load and store them (8 bytes of bf16, 16 of float), and the sigmoid.
+// Four neighbouring columns of a row, as the operator over heads loads and stores
+// them (8 bytes of bf16, 16 of float).
 #pragma once
 
 #include "rowops.h"
@@ -86,20 +86,6 @@ __device__ __forceinline__ void store_quad(S* p, int have, const Vf<kQuad>& v) {
             }
         }
     }
-}
-
-// 1 / (1 + exp(-v)).  For bf16 the exponent is one rounded product, off by up to
-// |v| 2^-24 of the result; float takes the library's expf, whose argument
-// reduction keeps it within a few units in the last place.  Results below 2^-126
-// are zero.
-template <typename S>
-__device__ __forceinline__ float sigmoid_of(float v) {
-    float e;
-    if constexpr (sizeof(S) == 4)
-        e = expf(-v);
-    else
-        e = __builtin_amdgcn_exp2f(v * -1.44269504f);
-    return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 }  // namespace dw

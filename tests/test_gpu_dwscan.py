@@ -3,9 +3,10 @@ bits.
 
 Tolerances count roundings of 2^-24 (U).  A step's -log of the decay (w), 1 - a
 and sqrt(1 - a^2) each pass through two functions of a few units, the products
-and a series or difference of 8 U at most: 40 U together, 16 more where bf16
-takes the exponential of one rounded product of up to 4 octaves.  An error of
-40 U in w changes a product of decays by 40 U times its -log: the sum "bent",
+and a series or difference of 8 U at most: 40 U together, and the exponential of
+a gate is that of one rounded product, off by |r| U: 16 more for what
+is at most 16 of a gate that is not closed.  An error of
+56 U in w changes a product of decays by 56 U times its -log: the sum "bent",
 the absolute terms weighted by that.  The state itself is rounded twice a frame
 of a thread's run (8), twice a run of a tile on the way (8), and once more a
 tile; each such rounding is at most U of the sum of absolute terms, which
@@ -35,7 +36,7 @@ def h(t):
 
 
 def rel(dt):
-    return 40 if dt == F32 else 56
+    return 56
 
 
 def within(got, want, tol, dt, what):
