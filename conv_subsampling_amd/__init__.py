@@ -873,8 +873,11 @@ def dwscan_fwd(x, r, g, decay, lengths=None, h0=None, scale: float = 8.0, y=None
         need_ws = _scan_workspace(False, shape)
         if need_ws:
             workspace = torch.empty((need_ws,), dtype=torch.uint8, device=dev)
-    _check(_lib.dwscan_fwd(shape, _ptr(x), _ptr(r), _ptr(g), _ptr(decay), _ptr(lengths), _ptr(h0), _ptr(y),
-                           _ptr(h_last), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(dev)))
+    status = _lib.dwscan_fwd(shape, x.data_ptr(), r.data_ptr(), g.data_ptr(), decay.data_ptr(), _ptr(lengths), _ptr(h0),
+                             y.data_ptr(), _ptr(h_last), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                             _stream(dev))
+    if status:
+        _check(status)
     return y, h_last
 
 
@@ -922,9 +925,11 @@ def dwscan_bwd(x, r, g, decay, y, dy, lengths=None, h0=None, dh_last=None, scale
         _dev_tensor("workspace", workspace, torch.uint8, dev)
     else:
         workspace = torch.empty((max(_scan_workspace(True, shape), 1),), dtype=torch.uint8, device=dev)
-    _check(_lib.dwscan_bwd(shape, _ptr(x), _ptr(r), _ptr(g), _ptr(decay), _ptr(lengths), _ptr(h0), _ptr(y), _ptr(dy),
-                           _ptr(dh_last), _ptr(dx), _ptr(dr), _ptr(dg), _ptr(ddecay), _ptr(dh0), _ptr(workspace),
-                           workspace.numel(), _stream(dev)))
+    status = _lib.dwscan_bwd(shape, x.data_ptr(), r.data_ptr(), g.data_ptr(), decay.data_ptr(), _ptr(lengths), _ptr(h0),
+                             y.data_ptr(), dy.data_ptr(), _ptr(dh_last), _ptr(dx), _ptr(dr), _ptr(dg), _ptr(ddecay),
+                             _ptr(dh0), workspace.data_ptr(), workspace.numel(), _stream(dev))
+    if status:
+        _check(status)
     return dx, dr, dg, ddecay, dh0
 
 
@@ -956,18 +961,23 @@ def _rope_check(q, k, q_gamma, k_gamma, freq, lengths, pos, pairs):
     st, code = _storage(q)
     B, T, H, D = q.shape
     Hkv = k.shape[2]
-    _heads("q", q, st, dev, q.shape)
+    if q.stride(3) != 1:
+        _heads("q", q, st, dev, q.shape)
     _heads("k", k, st, dev, (B, T, Hkv, D))
-    _dev_tensor("q_gamma", q_gamma, st, dev, (D,), allow_none=True)
-    _dev_tensor("k_gamma", k_gamma, st, dev, (D,), allow_none=True)
+    if q_gamma is not None:
+        _dev_tensor("q_gamma", q_gamma, st, dev, (D,))
+    if k_gamma is not None:
+        _dev_tensor("k_gamma", k_gamma, st, dev, (D,))
     R = 0
     if freq is not None:
         if freq.dim() != 1:
             raise ValueError("freq must be [R / 2]")
         _dev_tensor("freq", freq, torch.float64, dev)
         R = 2 * freq.shape[0]
-    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
-    _dev_tensor("pos", pos, torch.int32, dev, (B,), allow_none=True)
+    if lengths is not None:
+        _dev_tensor("lengths", lengths, torch.int32, dev, (B,))
+    if pos is not None:
+        _dev_tensor("pos", pos, torch.int32, dev, (B,))
     return dev, st, code, B, T, H, Hkv, D, R
 
 
@@ -1008,14 +1018,17 @@ def dwrope_fwd(q, k, q_gamma=None, k_gamma=None, freq=None, lengths=None, pos=No
         _heads("v", v, st, dev, k.shape)
     elif v_out is not None:
         raise ValueError("v_out needs v")
-    q_out = torch.empty((B, T, H, D), dtype=st, device=dev) if q_out is None else _heads("q_out", q_out, st, dev, q.shape)
+    q_out = _like(q) if q_out is None else _heads("q_out", q_out, st, dev, q.shape)
     to = (B, rows, Hkv, D)
-    k_out = torch.empty(to, dtype=st, device=dev) if k_out is None else _heads("k_out", k_out, st, dev, to)
+    k_out = _like(k) if k_out is None else _heads("k_out", k_out, st, dev, to)
     if v is not None:
-        v_out = torch.empty(to, dtype=st, device=dev) if v_out is None else _heads("v_out", v_out, st, dev, to)
+        v_out = _like(v) if v_out is None else _heads("v_out", v_out, st, dev, to)
     shape = _rope_shape((B, T, H, Hkv, D, R, rows), (q, k, v, q_out, k_out, v_out, None, None), eps, pairs, code)
-    _check(_lib.dwrope_fwd(shape, _ptr(q), _ptr(k), _ptr(v), _ptr(q_gamma), _ptr(k_gamma), _ptr(freq), _ptr(lengths),
-                           _ptr(pos), _ptr(place), _ptr(q_out), _ptr(k_out), _ptr(v_out), _stream(dev)))
+    status = _lib.dwrope_fwd(shape, q.data_ptr(), k.data_ptr(), _ptr(v), _ptr(q_gamma), _ptr(k_gamma), _ptr(freq),
+                             _ptr(lengths), _ptr(pos), _ptr(place), q_out.data_ptr(), k_out.data_ptr(), _ptr(v_out),
+                             _stream(dev))
+    if status:
+        _check(status)
     return q_out, k_out, v_out
 
 
@@ -1038,11 +1051,11 @@ def dwrope_bwd(q, k, dq_out, dk_out, q_gamma=None, k_gamma=None, freq=None, leng
     if dq is not None:
         _heads("dq", dq, st, dev, q.shape)
     elif "dq" in need:
-        dq = torch.empty((B, T, H, D), dtype=st, device=dev)
+        dq = _like(dq_out)
     if dk is not None:
         _heads("dk", dk, st, dev, k.shape)
     elif "dk" in need:
-        dk = torch.empty((B, T, Hkv, D), dtype=st, device=dev)
+        dk = _like(dk_out)
     if dq_gamma is not None:
         _dev_tensor("dq_gamma", dq_gamma, f32, dev, (D,))
     elif "dq_gamma" in need:
@@ -1050,7 +1063,7 @@ def dwrope_bwd(q, k, dq_out, dk_out, q_gamma=None, k_gamma=None, freq=None, leng
     if dk_gamma is not None:
         _dev_tensor("dk_gamma", dk_gamma, f32, dev, (D,))
     elif "dk_gamma" in need:
-        dk_gamma = torch.empty((D,), dtype=f32, device=dev)
+        dk_gamma = torch.empty((D,), dtype=f32, device=dev) if dq_gamma is None else torch.empty_like(dq_gamma)
     shape = _rope_shape((B, T, H, Hkv, D, R, 0), (q, k, None, dq_out, dk_out, None, dq, dk), eps, pairs, code)
     ws_bytes = 0
     if dq_gamma is not None or dk_gamma is not None:
@@ -1058,9 +1071,11 @@ def dwrope_bwd(q, k, dq_out, dk_out, q_gamma=None, k_gamma=None, freq=None, leng
             workspace = torch.empty((max(_rope_workspace(shape), 1),), dtype=torch.uint8, device=dev)
         _dev_tensor("workspace", workspace, torch.uint8, dev)
         ws_bytes = workspace.numel()
-    _check(_lib.dwrope_bwd(shape, _ptr(q), _ptr(k), _ptr(q_gamma), _ptr(k_gamma), _ptr(freq), _ptr(lengths), _ptr(pos),
-                           _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dq_gamma), _ptr(dk_gamma),
-                           _ptr(workspace), ws_bytes, _stream(dev)))
+    status = _lib.dwrope_bwd(shape, q.data_ptr(), k.data_ptr(), _ptr(q_gamma), _ptr(k_gamma), _ptr(freq), _ptr(lengths),
+                             _ptr(pos), dq_out.data_ptr(), dk_out.data_ptr(), _ptr(dq), _ptr(dk), _ptr(dq_gamma),
+                             _ptr(dk_gamma), _ptr(workspace), ws_bytes, _stream(dev))
+    if status:
+        _check(status)
     return dq, dk, dq_gamma, dk_gamma
 
 
@@ -1086,24 +1101,28 @@ def dwact_fwd(x, kind: str, lengths=None, y=None, kept=None, need=("y", "kept"))
     st, code = _storage(x)
     B, T, W = x.shape
     C = W // parts
-    _dev_tensor("x", x, st, dev)
-    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if lengths is not None:
+        _dev_tensor("lengths", lengths, torch.int32, dev, (B,))
     if y is not None:
         _dev_tensor("y", y, st, dev, (B, T, C))
     elif "y" in need:
-        y = torch.empty((B, T, C), dtype=st, device=dev)
+        y = torch.empty_like(x) if parts == 1 else torch.empty((B, T, C), dtype=st, device=dev)
     if kept is not None:
         q, codes = kept
         _dev_tensor("kept[0]", q, torch.int8, dev, (B, T, W))
         _dev_tensor("kept[1]", codes, torch.uint8, dev, (B, T, parts * -(-C // 32)))
     elif "kept" in need:
-        q = torch.empty((B, T, W), dtype=torch.int8, device=dev)
+        q = torch.empty_like(x, dtype=torch.int8)
         codes = torch.empty((B, T, parts * -(-C // 32)), dtype=torch.uint8, device=dev)
         kept = (q, codes)
     else:
         q = codes = None
-    _check(_lib.dwact_fwd(_ACTS[kind], _ptr(x), _ptr(lengths), _ptr(y), _ptr(q), _ptr(codes), B, T, C, code,
-                          _stream(dev)))
+    status = _lib.dwact_fwd(_ACTS[kind], x.data_ptr(), _ptr(lengths), _ptr(y), _ptr(q), _ptr(codes), B, T, C, code,
+                            _stream(dev))
+    if status:
+        _check(status)
     return y, kept
 
 
@@ -1132,15 +1151,18 @@ def dwact_bwd(kept, dy, kind: str, lengths=None, dtype=None, dx=None, y=None, ne
         st, code = dtype, DW_BF16 if dtype == torch.bfloat16 else DW_F32
     _dev_tensor("kept[0]", q, torch.int8, dev)
     _dev_tensor("kept[1]", codes, torch.uint8, dev, (B, T, parts * -(-C // 32)))
-    _dev_tensor("lengths", lengths, torch.int32, dev, (B,), allow_none=True)
+    if lengths is not None:
+        _dev_tensor("lengths", lengths, torch.int32, dev, (B,))
     if dx is not None:
         _dev_tensor("dx", dx, st, dev, (B, T, W))
     elif "dx" in need:
-        dx = torch.empty((B, T, W), dtype=st, device=dev)
+        dx = torch.empty_like(dy) if parts == 1 else torch.empty((B, T, W), dtype=st, device=dev)
     if y is not None:
         _dev_tensor("y", y, st, dev, (B, T, C))
     elif "y" in need:
         y = torch.empty((B, T, C), dtype=st, device=dev)
-    _check(_lib.dwact_bwd(_ACTS[kind], _ptr(q), _ptr(codes), _ptr(lengths), _ptr(dy), _ptr(dx), _ptr(y), B, T, C, code,
-                          _stream(dev)))
+    status = _lib.dwact_bwd(_ACTS[kind], q.data_ptr(), codes.data_ptr(), _ptr(lengths), _ptr(dy), _ptr(dx), _ptr(y), B, T,
+                            C, code, _stream(dev))
+    if status:
+        _check(status)
     return dx, y

@@ -35,7 +35,11 @@ constexpr int kScanCols = kScanLanes * kScanPair;             // channels of a w
 constexpr int kScanRun = 8, kScanLongRun = 16;                // frames of a thread in a tile
 constexpr int kScanGroup = 16;                                // tiles whose composition is published too
 constexpr int kScanTicket = 32;                               // words from one chain's counter to the next: a cache line
-constexpr int kScanPolls = 1 << 22;                           // of a word, before its wait is given up with a NaN
+// Polls of a word, about a microsecond each.  A word that is read belongs to a
+// workgroup that has started and waits for nothing before it publishes, so it
+// comes within microseconds; only where the workspace is overwritten meanwhile
+// (two calls at once on one) does it not, and then the wait ends with a NaN.
+constexpr int kScanPolls = 1 << 16;
 
 struct ScanArgs {
     const void *x, *r, *g, *yin, *dy;
@@ -236,6 +240,7 @@ __device__ __forceinline__ Run fold_words(const uint64_t* words, int count, floa
     const int each = (count + kScanWaves - 1) / kScanWaves;
     const int first = wave * each, last = first + each < count ? first + each : count;
     float p = 1.0f, h = 0.0f;
+    int polls = kScanPolls;  // in all
     constexpr int kFly = 4;  // reads in flight together
     for (int k = first; k < last; k += kFly) {
         uint64_t v[kFly];
@@ -244,7 +249,7 @@ __device__ __forceinline__ Run fold_words(const uint64_t* words, int count, floa
 #pragma unroll
         for (int j = 0; j < kFly; ++j) {
             if (k + j >= last) break;
-            for (int n = 0; (uint32_t)v[j] == 0 && n < kScanPolls; ++n) {
+            for (; (uint32_t)v[j] == 0 && polls > 0; --polls) {
                 __builtin_amdgcn_s_sleep(1);
                 v[j] = peek(words + (int64_t)(k + j) * kScanCols + lane);
             }

@@ -292,3 +292,12 @@ def test_binding_refusals():
     with pytest.raises(dw.DwconvError, match="alias"):
         wide = torch.zeros((2, 3, 32), device=DEV)
         dw.dwact_fwd(wide, "glu", y=wide.view(-1)[:96].view(2, 3, 16))
+
+
+def test_tensors_of_the_host_are_refused():
+    dw = lib()
+    x = torch.zeros((2, 3, 16))
+    with pytest.raises(ValueError):
+        dw.dwact_fwd(x, "silu")
+    with pytest.raises(ValueError):
+        dw.dwact_bwd((x.to(torch.int8), torch.zeros((2, 3, 1), dtype=torch.uint8)), x, "silu")

@@ -397,3 +397,12 @@ def test_binding_refusals():
         dw.rope_frequencies(3)
     with pytest.raises(dw.DwconvError, match="workspace"):
         dw.dwrope_bwd(q, k, q, k, freq=f, workspace=torch.zeros(8, dtype=torch.uint8, device=DEV))
+
+
+def test_tensors_of_the_host_are_refused():
+    dw = lib()
+    x = torch.zeros((2, 3, 4, 16))
+    with pytest.raises(ValueError):
+        dw.dwrope_fwd(x, x)
+    with pytest.raises(ValueError):
+        dw.dwrope_bwd(x, x, x, x)

@@ -430,3 +430,12 @@ def test_binding_refusals():
         dw.dwscan_bwd(x, x, x, d, x, x, dx=x)
     with pytest.raises(dw.DwconvError, match="workspace"):
         dw.dwscan_bwd(x, x, x, d, x, x, workspace=torch.zeros(8, dtype=torch.uint8, device=DEV))
+
+
+def test_tensors_of_the_host_are_refused():
+    dw = lib()
+    x, d = torch.zeros((2, 3, 16)), torch.zeros(16)
+    with pytest.raises(ValueError):
+        dw.dwscan_fwd(x, x, x, d)
+    with pytest.raises(ValueError):
+        dw.dwscan_bwd(x, x, x, d, x, x)
