@@ -673,6 +673,9 @@ struct ScanPlan {
 // Linked or in turn, us: 256 chains, bf16 [16,750,1024] 30 and 32 (gradients 59
 // and 77), float 45 and 58 (98 and 98); 512 chains, [16,1500,2048] bf16 101 and
 // 96 (204 and 215), float 165 and 159 (355 and 332), [32,130,1024] bf16 17 and 15.
+// Up to 4 tiles in turn save the launch that clears the words: calls of [8,256,512]
+// bf16 15.8 and 10.8, [1,200,64] 15.1 and 10.4 (gradients 23.4 and 20.8), where 5 to
+// 8 tiles cost more than it: [4,500,1024] bf16 14.3 and 20.6.
 static ScanPlan scan_plan(const ScanShape& s, bool backward) {
     ScanPlan p = {};
     const int64_t one = kScanRows * kScanRun;
@@ -684,7 +687,7 @@ static ScanPlan scan_plan(const ScanShape& s, bool backward) {
     p.tiles = (s.T + p.segs * p.run - 1) / (p.segs * p.run);
     const int64_t per = kScanRows / p.segs;
     p.row_blocks = (s.B + per - 1) / per;
-    p.linked = p.tiles > 1 && !many;
+    p.linked = p.tiles > 4 && !many;
     if (p.linked) p.row_blocks *= p.tiles;
     return p;
 }
