@@ -17,15 +17,29 @@ constexpr int kActThreads = 256;
 constexpr int kActGroup = 32;                    // columns that share a scale
 constexpr int kActLanes = kActGroup / kGroup;    // lanes that hold them
 
+// n / d for n < 2^31 by one multiplication: (mulhi(n, m) + n) >> l with
+// 2^(l-1) < d <= 2^l and m = floor(2^32 (2^l - d) / d) + 1.
+struct Divisor {
+    uint32_t d, m, l;
+};
+
+static Divisor divisor(uint32_t d) {
+    uint32_t l = 0;
+    while (((uint64_t)1 << l) < d) ++l;
+    return {d, (uint32_t)(((((uint64_t)1 << l) - d) << 32) / d + 1), l};
+}
+
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& by) { return (__umulhi(n, by.m) + n) >> by.l; }
+
 struct ActArgs {
     const void *x, *dy;
     const int32_t* lengths;
     void *y, *dx;
     int8_t* kept;
     uint8_t* codes;
-    uint64_t units;    // lanes' pieces in all
-    uint32_t per_row;  // of a row, a multiple of 4
-    uint32_t T;
+    uint64_t units;   // lanes' pieces in all
+    Divisor per_row;  // of a row, a multiple of 4
+    Divisor T;
     int32_t C;
 };
 
@@ -127,12 +141,18 @@ struct ActPiece {
 __device__ __forceinline__ ActPiece act_piece(const ActArgs& a, uint64_t unit) {
     ActPiece p = {0, a.C, false};
     if (unit >= a.units) return p;
-    p.row = a.units >> 32 ? unit / a.per_row : (uint32_t)unit / a.per_row;
-    p.col = (int)(unit - p.row * a.per_row) * kGroup;
+    if (a.units >> 31) {
+        p.row = unit / a.per_row.d;
+        p.col = (int)(unit - p.row * a.per_row.d) * kGroup;
+    } else {
+        const uint32_t row = divide((uint32_t)unit, a.per_row);
+        p.row = row;
+        p.col = (int)((uint32_t)unit - row * a.per_row.d) * kGroup;
+    }
     p.live = true;
     if (a.lengths) {
-        const uint64_t b = p.row >> 32 ? p.row / a.T : (uint32_t)p.row / a.T;
-        p.live = (int64_t)(p.row - b * a.T) < a.lengths[b];
+        const uint64_t b = p.row >> 31 ? p.row / a.T.d : divide((uint32_t)p.row, a.T);
+        p.live = (int64_t)(p.row - b * a.T.d) < a.lengths[b];
     }
     return p;
 }
@@ -262,9 +282,9 @@ static void launch_act_kind(int act, bool backward, const ActArgs& a, dim3 grid,
 }
 
 static hipError_t launch_act(int act, bool backward, ActArgs a, int64_t B, bool bf16, hipStream_t stream) {
-    const int64_t rows = B * a.T;
-    a.per_row = (uint32_t)act_per_row(a.C);
-    a.units = (uint64_t)rows * a.per_row;
+    const int64_t rows = B * a.T.d;
+    a.per_row = divisor((uint32_t)act_per_row(a.C));
+    a.units = (uint64_t)rows * a.per_row.d;
     const dim3 grid((uint32_t)act_blocks(rows, a.C, act));
     if (bf16)
         launch_act_kind<uint16_t>(act, backward, a, grid, stream);
@@ -275,14 +295,14 @@ static hipError_t launch_act(int act, bool backward, ActArgs a, int64_t B, bool 
 
 hipError_t launch_dwact_fwd(int act, const void* x, const int32_t* lengths, void* y, int8_t* kept, uint8_t* codes,
                             int64_t B, int64_t T, int64_t C, bool bf16, hipStream_t stream) {
-    const ActArgs a = {x, nullptr, lengths, y, nullptr, kept, codes, 0, 0, (uint32_t)T, (int32_t)C};
+    const ActArgs a = {x, nullptr, lengths, y, nullptr, kept, codes, 0, {}, divisor((uint32_t)T), (int32_t)C};
     return launch_act(act, false, a, B, bf16, stream);
 }
 
 hipError_t launch_dwact_bwd(int act, const int8_t* kept, const uint8_t* codes, const int32_t* lengths, const void* dy,
                             void* dx, void* y, int64_t B, int64_t T, int64_t C, bool bf16, hipStream_t stream) {
-    const ActArgs a = {nullptr, dy, lengths, y, dx, const_cast<int8_t*>(kept), const_cast<uint8_t*>(codes), 0, 0,
-                       (uint32_t)T, (int32_t)C};
+    const ActArgs a = {nullptr, dy, lengths, y, dx, const_cast<int8_t*>(kept), const_cast<uint8_t*>(codes), 0, {},
+                       divisor((uint32_t)T), (int32_t)C};
     return launch_act(act, true, a, B, bf16, stream);
 }
 

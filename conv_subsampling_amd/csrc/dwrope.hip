@@ -40,31 +40,36 @@ struct RopeArgs {
 };
 
 // Where a lane's 4 pairs lie in a head.  PACKED: each of its two quads is 4
-// neighbouring elements (halves: the pairs' firsts and their seconds; neighbours
-// and unrotated pairs: 8 elements in a row), so vector accesses serve it.
-// Elsewhere each element has a place of its own, D standing for none.
+// neighbouring elements, so vector accesses serve it: halves, the pairs' firsts
+// and their seconds (a lane that is not rotated pairs the two quads of its 8
+// elements in a row); neighbours, 8 elements in a row.  Elsewhere each element has
+// a place of its own, D standing for none.
 template <bool PACKED, bool HALVES>
 struct PairMap {
-    int at[2][kQuad];  // PACKED: [.][0] alone
-    int first;         // the lane's first pair
-    bool in_halves;    // PACKED && HALVES: its quads are firsts and seconds
+    int at[2][kQuad];
+    int first;  // the lane's first pair
 
     __device__ __forceinline__ PairMap(int lane, int D, int R) {
         first = lane * kQuad;
-        in_halves = HALVES && first < R / 2;
-        if constexpr (PACKED) {
-            at[0][0] = in_halves ? first : 2 * first;
-            at[1][0] = in_halves ? R / 2 + first : 2 * first + kQuad;
-        } else {
+        const bool apart = HALVES && first < R / 2;
 #pragma unroll
-            for (int e = 0; e < kQuad; ++e) {
-                const int p = first + e;
-                const bool apart = HALVES && p < R / 2;
-                at[0][e] = min(D, apart ? p : 2 * p);
-                at[1][e] = min(D, apart ? p + R / 2 : 2 * p + 1);
+        for (int e = 0; e < kQuad; ++e) {
+            const int p = first + e;
+            if constexpr (PACKED && HALVES) {
+                at[0][e] = apart ? p : 2 * first + e;
+                at[1][e] = apart ? p + R / 2 : 2 * first + kQuad + e;
+            } else {
+                const bool halves = HALVES && p < R / 2;
+                at[0][e] = halves ? p : 2 * p;
+                at[1][e] = halves ? p + R / 2 : 2 * p + 1;
             }
+            at[0][e] = min(D, at[0][e]);
+            at[1][e] = min(D, at[1][e]);
         }
     }
+
+    // PACKED: the first elements of the two quads as they lie in memory
+    __device__ __forceinline__ int quad(int h) const { return HALVES ? at[h][0] : 2 * first + h * kQuad; }
 };
 
 template <typename S>
@@ -82,8 +87,8 @@ __device__ __forceinline__ HeadRaw<S> load_head(const S* head, const PairMap<PAC
     HeadRaw<S> r = {};
     if constexpr (PACKED) {
         if (on && 2 * m.first < D) {
-            r.q[0] = load_quad<S, false>(head + m.at[0][0], kQuad);
-            r.q[1] = load_quad<S, false>(head + m.at[1][0], kQuad);
+            r.q[0] = load_quad<S, false>(head + m.quad(0), kQuad);
+            r.q[1] = load_quad<S, false>(head + m.quad(1), kQuad);
         }
     } else {
 #pragma unroll
@@ -106,21 +111,21 @@ template <typename S, bool PACKED, bool HALVES>
 __device__ __forceinline__ Head widen_head(const HeadRaw<S>& r, const PairMap<PACKED, HALVES>& m) {
     const Vf<kQuad> xv = widen_quad<S>(r.q[0]), yv = widen_quad<S>(r.q[1]);
     const f32x4 x = {xv.v[0], xv.v[1], xv.v[2], xv.v[3]}, y = {yv.v[0], yv.v[1], yv.v[2], yv.v[3]};
-    if constexpr (!PACKED) return {x, y};
-    const bool apart = HALVES && m.in_halves;
-    return {{x[0], apart ? x[1] : x[2], apart ? x[2] : y[0], apart ? x[3] : y[2]},
-            {apart ? y[0] : x[1], apart ? y[1] : x[3], apart ? y[2] : y[1], y[3]}};
+    if constexpr (PACKED && !HALVES) return {{x[0], x[2], y[0], y[2]}, {x[1], x[3], y[1], y[3]}};
+    return {x, y};
 }
 
 template <typename S, bool PACKED, bool HALVES>
 __device__ __forceinline__ void store_head(S* head, const PairMap<PACKED, HALVES>& m, int D, Head h) {
     if constexpr (PACKED) {
         if (2 * m.first >= D) return;
-        const bool apart = HALVES && m.in_halves;
-        const Vf<kQuad> x = {{h.a[0], apart ? h.a[1] : h.b[0], apart ? h.a[2] : h.a[1], apart ? h.a[3] : h.b[1]}};
-        const Vf<kQuad> y = {{apart ? h.b[0] : h.a[2], apart ? h.b[1] : h.b[2], apart ? h.b[2] : h.a[3], h.b[3]}};
-        store_quad<S, false>(head + m.at[0][0], kQuad, x);
-        store_quad<S, false>(head + m.at[1][0], kQuad, y);
+        Vf<kQuad> x = {{h.a[0], h.a[1], h.a[2], h.a[3]}}, y = {{h.b[0], h.b[1], h.b[2], h.b[3]}};
+        if constexpr (!HALVES) {
+            x = {{h.a[0], h.b[0], h.a[1], h.b[1]}};
+            y = {{h.a[2], h.b[2], h.a[3], h.b[3]}};
+        }
+        store_quad<S, false>(head + m.quad(0), kQuad, x);
+        store_quad<S, false>(head + m.quad(1), kQuad, y);
     } else {
 #pragma unroll
         for (int e = 0; e < kQuad; ++e) {
@@ -180,19 +185,27 @@ __device__ __forceinline__ RopeTeam rope_frame(const RopeArgs& a, uint64_t frame
     return f;
 }
 
-// x: the heads of one frame; out: where they go, NULL for none.
+// Zeros for the heads of a frame past its length.
+template <typename S, bool PACKED, bool HALVES>
+__device__ __forceinline__ void zero_heads(S* out, int64_t os, int32_t heads, uint32_t from, uint32_t step,
+                                           const PairMap<PACKED, HALVES>& m, int D) {
+    for (uint32_t h = from; h < (uint32_t)heads; h += step) store_head<S>(out + (int64_t)h * os, m, D, Head{});
+}
+
+// x: the heads of one frame; out: where they go.
 template <typename S, bool PACKED, bool HALVES, int LANES>
 __device__ __forceinline__ void rope_heads(const S* x, int64_t xs, S* out, int64_t os, int32_t heads, uint32_t from,
                                            uint32_t step, const PairMap<PACKED, HALVES>& m, Head gamma,
-                                           const Turns& turn, int D, float eps, bool live) {
+                                           const Turns& turn, int D, float eps) {
     const float inv_d = 1.0f / (float)D;
-    for (uint32_t h0 = from; h0 < (uint32_t)heads; h0 += kRopeFly * step) {
+    const int64_t x_step = step * xs, o_step = step * os;  // one head of the team's to the next
+    x += from * xs;
+    out += from * os;
+    for (uint32_t h0 = from; h0 < (uint32_t)heads; h0 += kRopeFly * step, x += kRopeFly * x_step, out += kRopeFly * o_step) {
         HeadRaw<S> raw[kRopeFly];
 #pragma unroll
-        for (int j = 0; j < kRopeFly; ++j) {
-            const uint32_t h = h0 + j * step;
-            raw[j] = load_head<S>(x + (int64_t)h * xs, m, D, live && h < (uint32_t)heads);
-        }
+        for (int j = 0; j < kRopeFly; ++j)
+            raw[j] = load_head<S>(x + j * x_step, m, D, h0 + j * step < (uint32_t)heads);
 #pragma unroll
         for (int j = 0; j < kRopeFly; ++j) {
             const uint32_t h = h0 + j * step;
@@ -205,10 +218,10 @@ __device__ __forceinline__ void rope_heads(const S* x, int64_t xs, S* out, int64
 #pragma unroll
             for (int e = 0; e < kQuad; ++e) {
                 const float p = v.a[e] * rstd * gamma.a[e], q = v.b[e] * rstd * gamma.b[e];
-                o.a[e] = live ? p * turn.c[e] - q * turn.s[e] : 0.0f;  // (eps = 0 and zeros have no norm)
-                o.b[e] = live ? q * turn.c[e] + p * turn.s[e] : 0.0f;
+                o.a[e] = p * turn.c[e] - q * turn.s[e];
+                o.b[e] = q * turn.c[e] + p * turn.s[e];
             }
-            if (h < (uint32_t)heads) store_head<S>(out + (int64_t)h * os, m, D, o);
+            if (h < (uint32_t)heads) store_head<S>(out + j * o_step, m, D, o);
         }
     }
 }
@@ -223,28 +236,39 @@ __global__ __launch_bounds__(kRopeThreads) void rope_fwd_kernel(const RopeArgs a
     const uint32_t part = (uint32_t)(team - frame * a.split);
     const RopeTeam f = rope_frame(a, frame);
     const PairMap<PACKED, HALVES> m(lane, D, a.R);
-    const Turns turn = turns_of(a.freq, f.position, m.first, a.R);
-    if (a.H > 0)
-        rope_heads<S, PACKED, HALVES, LANES>((const S*)a.q + f.b * a.qs.item + f.t * a.qs.frame, a.qs.head,
-                                             (S*)a.q_out + f.b * a.qos.item + f.t * a.qos.frame, a.qos.head, a.H, part,
-                                             a.split, m, load_gamma<S>(a.q_gamma, m, D), turn, D, a.eps, f.live);
-    if (a.Hkv == 0) return;
-    int64_t to = f.t;
-    if (a.place) {  // a cache: only valid frames that fall into it
-        to += a.place[f.b];
-        if (!f.live || to < 0 || to >= a.S) return;
-    }
+    const S* q = (const S*)a.q + f.b * a.qs.item + f.t * a.qs.frame;
+    S* q_out = (S*)a.q_out + f.b * a.qos.item + f.t * a.qos.frame;
     // the first heads of k and v go to the teams behind those that hold the last of q
     const uint32_t from = (part + a.split - (uint32_t)a.H % a.split) % a.split;
-    rope_heads<S, PACKED, HALVES, LANES>((const S*)a.k + f.b * a.ks.item + f.t * a.ks.frame, a.ks.head,
-                                         (S*)a.k_out + f.b * a.kos.item + to * a.kos.frame, a.kos.head, a.Hkv, from,
-                                         a.split, m, load_gamma<S>(a.k_gamma, m, D), turn, D, a.eps, f.live);
+    const uint32_t v_from = (from + a.split - (uint32_t)a.Hkv % a.split) % a.split;
+    int64_t to = f.t;
+    bool keys = a.Hkv > 0;
+    if (a.place && keys) {  // a cache: only valid frames that fall into it
+        to += a.place[f.b];
+        keys = f.live && to >= 0 && to < a.S;
+    }
+    S* k_out = (S*)a.k_out + f.b * a.kos.item + to * a.kos.frame;
+    S* v_out = (S*)a.v_out + f.b * a.vos.item + to * a.vos.frame;
+    if (!f.live) {
+        zero_heads<S>(q_out, a.qos.head, a.H, part, a.split, m, D);
+        if (!keys) return;
+        zero_heads<S>(k_out, a.kos.head, a.Hkv, from, a.split, m, D);
+        if (a.v) zero_heads<S>(v_out, a.vos.head, a.Hkv, v_from, a.split, m, D);
+        return;
+    }
+    const Turns turn = turns_of(a.freq, f.position, m.first, a.R);
+    if (a.H > 0)
+        rope_heads<S, PACKED, HALVES, LANES>(q, a.qs.head, q_out, a.qos.head, a.H, part, a.split, m,
+                                             load_gamma<S>(a.q_gamma, m, D), turn, D, a.eps);
+    if (!keys) return;
+    rope_heads<S, PACKED, HALVES, LANES>((const S*)a.k + f.b * a.ks.item + f.t * a.ks.frame, a.ks.head, k_out,
+                                         a.kos.head, a.Hkv, from, a.split, m, load_gamma<S>(a.k_gamma, m, D), turn, D,
+                                         a.eps);
     if (!a.v) return;
     const S* v = (const S*)a.v + f.b * a.vs.item + f.t * a.vs.frame;
-    S* v_out = (S*)a.v_out + f.b * a.vos.item + to * a.vos.frame;
-    for (uint32_t h = (from + a.split - (uint32_t)a.Hkv % a.split) % a.split; h < (uint32_t)a.Hkv; h += a.split)
+    for (uint32_t h = v_from; h < (uint32_t)a.Hkv; h += a.split)
         store_head<S>(v_out + (int64_t)h * a.vos.head, m, D,
-                      widen_head<S>(load_head<S>(v + (int64_t)h * a.vs.head, m, D, f.live), m));
+                      widen_head<S>(load_head<S>(v + (int64_t)h * a.vs.head, m, D, true), m));
 }
 
 // Gradients of one frame's heads; dg takes the sums of u * xh.
@@ -252,17 +276,21 @@ template <typename S, bool PACKED, bool HALVES, int LANES>
 __device__ __forceinline__ void rope_grads(const S* x, int64_t xs, const S* dout, int64_t ds, S* dx, int64_t os,
                                            int32_t heads, uint32_t from, uint32_t step,
                                            const PairMap<PACKED, HALVES>& m, Head gamma, const Turns& turn,
-                                           int D, float eps, bool live, Head& dg) {
+                                           int D, float eps, Head& dg) {
     constexpr int kFly = kRopeFly / 2;  // two tensors each
     const float inv_d = 1.0f / (float)D;
+    const int64_t x_step = step * xs, d_step = step * ds, o_step = step * os;
+    x += from * xs;
+    dout += from * ds;
+    if (dx) dx += from * os;
     for (uint32_t h0 = from; h0 < (uint32_t)heads; h0 += kFly * step) {
         HeadRaw<S> xr[kFly], dr[kFly];
 #pragma unroll
         for (int j = 0; j < kFly; ++j) {
             const uint32_t h = h0 + j * step;
-            const bool on = live && h < (uint32_t)heads;
-            xr[j] = load_head<S>(x + (int64_t)h * xs, m, D, on);
-            dr[j] = load_head<S>(dout + (int64_t)h * ds, m, D, on);
+            const bool on = h < (uint32_t)heads;
+            xr[j] = load_head<S>(x + j * x_step, m, D, on);
+            dr[j] = load_head<S>(dout + j * d_step, m, D, on);
         }
 #pragma unroll
         for (int j = 0; j < kFly; ++j) {
@@ -273,7 +301,7 @@ __device__ __forceinline__ void rope_grads(const S* x, int64_t xs, const S* dout
             for (int e = 0; e < kQuad; ++e) sum += v.a[e] * v.a[e] + v.b[e] * v.b[e];
             // 0 where no head was loaded: with eps = 0 its zeros would have no norm
             const float mean = lane_sum<LANES>(sum) * inv_d;
-            const float rstd = live && h < (uint32_t)heads ? __builtin_amdgcn_rsqf(mean + eps) : 0.0f;
+            const float rstd = h < (uint32_t)heads ? __builtin_amdgcn_rsqf(mean + eps) : 0.0f;
             Head g;
             float dot = 0.0f;
 #pragma unroll
@@ -291,11 +319,14 @@ __device__ __forceinline__ void rope_grads(const S* x, int64_t xs, const S* dout
             dot = lane_sum<LANES>(dot) * inv_d;
 #pragma unroll
             for (int e = 0; e < kQuad; ++e) {
-                g.a[e] = live ? rstd * (g.a[e] - v.a[e] * dot) : 0.0f;
-                g.b[e] = live ? rstd * (g.b[e] - v.b[e] * dot) : 0.0f;
+                g.a[e] = rstd * (g.a[e] - v.a[e] * dot);
+                g.b[e] = rstd * (g.b[e] - v.b[e] * dot);
             }
-            if (dx && h < (uint32_t)heads) store_head<S>(dx + (int64_t)h * os, m, D, g);
+            if (dx && h < (uint32_t)heads) store_head<S>(dx + j * o_step, m, D, g);
         }
+        x += kFly * x_step;
+        dout += kFly * d_step;
+        if (dx) dx += kFly * o_step;
     }
 }
 
@@ -315,20 +346,23 @@ __global__ __launch_bounds__(kRopeThreads) void rope_bwd_kernel(const RopeArgs a
         const uint64_t frame = team >> 32 ? team / a.split : (uint32_t)team / a.split;
         const uint32_t part = (uint32_t)(team - frame * a.split);
         const RopeTeam f = rope_frame(a, frame);
+        const uint32_t from = (part + a.split - (uint32_t)a.H % a.split) % a.split;
+        S* dq = a.q_out ? (S*)a.q_out + f.b * a.dqs.item + f.t * a.dqs.frame : nullptr;
+        S* dk = a.k_out ? (S*)a.k_out + f.b * a.dks.item + f.t * a.dks.frame : nullptr;
+        if (!f.live) {
+            if (dq) zero_heads<S>(dq, a.dqs.head, a.H, part, a.split, m, D);
+            if (dk) zero_heads<S>(dk, a.dks.head, a.Hkv, from, a.split, m, D);
+            continue;
+        }
         const Turns turn = turns_of(a.freq, f.position, m.first, a.R);
         if (a.H > 0)
-            rope_grads<S, PACKED, HALVES, LANES>(
-                (const S*)a.q + f.b * a.qs.item + f.t * a.qs.frame, a.qs.head,
-                (const S*)a.dq_out + f.b * a.qos.item + f.t * a.qos.frame, a.qos.head,
-                a.q_out ? (S*)a.q_out + f.b * a.dqs.item + f.t * a.dqs.frame : nullptr, a.dqs.head, a.H, part, a.split,
-                m, q_gamma, turn, D, a.eps, f.live, dg[0]);
+            rope_grads<S, PACKED, HALVES, LANES>((const S*)a.q + f.b * a.qs.item + f.t * a.qs.frame, a.qs.head,
+                                                 (const S*)a.dq_out + f.b * a.qos.item + f.t * a.qos.frame, a.qos.head,
+                                                 dq, a.dqs.head, a.H, part, a.split, m, q_gamma, turn, D, a.eps, dg[0]);
         if (a.Hkv > 0)
-            rope_grads<S, PACKED, HALVES, LANES>(
-                (const S*)a.k + f.b * a.ks.item + f.t * a.ks.frame, a.ks.head,
-                (const S*)a.dk_out + f.b * a.kos.item + f.t * a.kos.frame, a.kos.head,
-                a.k_out ? (S*)a.k_out + f.b * a.dks.item + f.t * a.dks.frame : nullptr, a.dks.head, a.Hkv,
-                (part + a.split - (uint32_t)a.H % a.split) % a.split, a.split, m, k_gamma, turn, D, a.eps, f.live,
-                dg[1]);
+            rope_grads<S, PACKED, HALVES, LANES>((const S*)a.k + f.b * a.ks.item + f.t * a.ks.frame, a.ks.head,
+                                                 (const S*)a.dk_out + f.b * a.kos.item + f.t * a.kos.frame, a.kos.head,
+                                                 dk, a.dks.head, a.Hkv, from, a.split, m, k_gamma, turn, D, a.eps, dg[1]);
     }
     if (!a.partial) return;
 #pragma unroll
@@ -360,11 +394,10 @@ __global__ __launch_bounds__(kRopeThreads) void rope_bwd_kernel(const RopeArgs a
             total.b[e] += column[w][n][lane * 2 * kQuad + kQuad + e];
         }
     }
-    const PairMap<false, HALVES> place(lane, D, a.R);
 #pragma unroll
     for (int e = 0; e < kQuad; ++e) {
-        if (place.at[0][e] < D) out[place.at[0][e]] = total.a[e];
-        if (place.at[1][e] < D) out[place.at[1][e]] = total.b[e];
+        if (m.at[0][e] < D) out[m.at[0][e]] = total.a[e];
+        if (m.at[1][e] < D) out[m.at[1][e]] = total.b[e];
     }
 }
 
