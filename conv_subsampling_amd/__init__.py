@@ -857,6 +857,7 @@ def dwscan_fwd(x, r, g, decay, lengths=None, h0=None, scale: float = 8.0, y=None
         y = _like(x)
     if r is None or g is None:
         raise ValueError("r and g are required")
+    scale = float(scale)
     shape = _scan_shape(x, (x, r, g, y), ("x", "r", "g", "y"), scale, code)
     _dev_tensor("decay", decay, f32, dev, (C,))
     if lengths is not None:
@@ -905,6 +906,7 @@ def dwscan_bwd(x, r, g, decay, y, dy, lengths=None, h0=None, dh_last=None, scale
         dg = _like(x)
     if r is None or g is None or y is None or dy is None:
         raise ValueError("r, g, y and dy are required")
+    scale = float(scale)
     shape = _scan_shape(x, (x, r, g, y, dy, dx, dr, dg), ("x", "r", "g", "y", "dy", "dx", "dr", "dg"), scale, code)
     _dev_tensor("decay", decay, f32, dev, (C,))
     if lengths is not None:
@@ -991,7 +993,7 @@ def _rope_pack(sizes, strides, eps, pairs, code) -> bytes:
 
 def _rope_shape(sizes, tensors, eps, pairs, code) -> bytes:
     """The C ABI's dw_rope."""
-    return _rope_pack(sizes, tuple([_NO_STRIDE if t is None else t.stride() for t in tensors]), eps, pairs, code)
+    return _rope_pack(sizes, tuple([_NO_STRIDE if t is None else t.stride() for t in tensors]), float(eps), pairs, code)
 
 
 def dwrope_fwd(q, k, q_gamma=None, k_gamma=None, freq=None, lengths=None, pos=None, v=None, place=None,

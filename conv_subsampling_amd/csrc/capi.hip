@@ -207,6 +207,15 @@ bool frames_fit(const dw::FrameStride& s, int64_t B, int64_t T) {
     return s.frame < dw::kScanMaxFrameStride && dw::product_below(far, {B, s.item}) && dw::product_below(far, {T, s.frame});
 }
 
+// Whether what is written at these distances cannot overlap: each at least as long as a piece.
+bool apart(int64_t piece, int64_t n, int64_t step) { return n <= 1 || step >= piece; }
+
+bool frames_apart(const dw::FrameStride& s, int64_t B, int64_t T, int64_t C) { return apart(C, B, s.item) && apart(C, T, s.frame); }
+
+bool heads_apart(const dw_strides& s, int64_t B, int64_t T, int64_t H, int64_t D) {
+    return apart(D, B, s.item) && apart(D, T, s.frame) && apart(D, H, s.head);
+}
+
 // The recurrence's problem as the launchers take it.
 dw_status check_scan(const char* fn, const dw_scan* a, bool backward, dw::ScanShape* s) {
     if (!a) return fail(DW_ERR_INVALID_ARG, "%s: shape must not be NULL", fn);
@@ -705,6 +714,7 @@ dw_status dwscan_fwd(const dw_scan* shape, const void* x, const void* r, const v
     if (!decay || (s.T > 0 && (!x || !r || !g || !y)))
         return fail(DW_ERR_INVALID_ARG, "%s: x, r, g, decay and y must not be NULL (unless empty)", fn);
     if (s.T > 0 && (y == x || y == r || y == g)) return fail(DW_ERR_INVALID_ARG, "%s: y must not alias an input", fn);
+    if (s.T > 0 && !frames_apart(s.y, s.B, s.T, s.C)) return fail(DW_ERR_INVALID_ARG, "%s: frames of y overlap", fn);
     const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwscan_fwd_workspace(s));
     if (w != DW_OK) return w;
     const dw::ScanPtrs p = {x, r, g, decay, lengths, h0};
@@ -735,6 +745,9 @@ dw_status dwscan_bwd(const dw_scan* shape, const void* x, const void* r, const v
                 return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
         if ((dx && (dx == dr || dx == dg)) || (dr && dr == dg))
             return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
+        if ((dx && !frames_apart(s.dx, s.B, s.T, s.C)) || (dr && !frames_apart(s.dr, s.B, s.T, s.C)) ||
+            (dg && !frames_apart(s.dg, s.B, s.T, s.C)))
+            return fail(DW_ERR_INVALID_ARG, "%s: frames of a gradient overlap", fn);
         if ((ddecay && ddecay == decay) || (dh0 && dh0 == h0))
             return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
     }
@@ -762,6 +775,10 @@ dw_status dwrope_fwd(const dw_rope* shape, const void* q, const void* k, const v
         return fail(DW_ERR_INVALID_ARG, "%s: k_out must not alias another tensor", fn);
     if (any_k && v && (v_out == v || v_out == k || (any_q && v_out == q)))
         return fail(DW_ERR_INVALID_ARG, "%s: v_out must not alias another tensor", fn);
+    const int64_t rows = place ? s.S : s.T;
+    if ((any_q && !heads_apart(shape->q_out, s.B, s.T, s.H, s.D)) || (any_k && !heads_apart(shape->k_out, s.B, rows, s.Hkv, s.D)) ||
+        (any_k && v && !heads_apart(shape->v_out, s.B, rows, s.Hkv, s.D)))
+        return fail(DW_ERR_INVALID_ARG, "%s: heads of an output overlap", fn);
     if (!any_k) s.Hkv = 0;
     if (!any_q) s.H = 0;
     if (!any_q && !any_k) return ok();
@@ -795,6 +812,8 @@ dw_status dwrope_bwd(const dw_rope* shape, const void* q, const void* k, const v
     if (any_k && dk && ((dk == k && !same_strides(shape->k, shape->dk)) || (dk == dk_out && !same_strides(shape->k_out, shape->dk)) ||
                         (any_q && (dk == q || dk == dq_out))))
         return fail(DW_ERR_INVALID_ARG, "%s: dk must not alias another tensor", fn);
+    if ((any_q && dq && !heads_apart(shape->dq, s.B, s.T, s.H, s.D)) || (any_k && dk && !heads_apart(shape->dk, s.B, s.T, s.Hkv, s.D)))
+        return fail(DW_ERR_INVALID_ARG, "%s: heads of a gradient overlap", fn);
     if (dq_gamma && dq_gamma == dk_gamma) return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
     if (params) {
         const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwrope_bwd_workspace(s));

@@ -39,6 +39,8 @@ constexpr int kScanTicket = 32;                               // words from one 
 // workgroup that has started and waits for nothing before it publishes, so it
 // comes within microseconds; only where the workspace is overwritten meanwhile
 // (two calls at once on one) does it not, and then the wait ends with a NaN.
+// Nothing is written outside the call's tensors then: tickets past the last tile
+// end their workgroups.
 constexpr int kScanPolls = 1 << 16;
 
 struct ScanArgs {
@@ -481,6 +483,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
     begin_scan<LINKED>(a, p, shared);
     if (p.b >= a.B) return;  // SEGS < 8, where no thread waits for another wave from here on
     int tile = LINKED ? __builtin_amdgcn_readfirstlane(shared.ticket) : 0;
+    if (LINKED && tile >= a.tiles) return;  // given out by another call on this workspace
     const int end = scan_loops<SEGS, FR, LINKED>() ? a.tiles : tile + 1;
     const f32x2 rate = *(const f32x2*)&shared.rate[p.lane];
     f32x2 carry = tile == 0 ? load_state(a.start, p.b, a.C, p) : f32x2(0.0f);
@@ -562,6 +565,7 @@ __global__ __launch_bounds__(kScanThreads, (scan_bwd_waves<S, LINKED>())) void s
     const bool item = p.b < a.B;
     begin_scan<LINKED>(a, p, shared);
     int at = LINKED ? __builtin_amdgcn_readfirstlane(shared.ticket) : 0;  // in the order of the chain: the last tile is first
+    if (LINKED && at >= a.tiles) return;  // given out by another call on this workspace
     const int end = LINKED ? at + 1 : !item ? 0 : scan_loops<SEGS, FR, LINKED>() ? a.tiles : 1;
     const int row = LINKED ? (int)(p.chain / (uint32_t)a.col_blocks) * a.tiles + at : (int)(p.chain / (uint32_t)a.col_blocks);
     const f32x2 rate = *(const f32x2*)&shared.rate[p.lane];

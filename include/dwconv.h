@@ -649,7 +649,7 @@ dw_status dwattn_bwd(const dw_attn *shape, const void *q, const void *k, const v
  * with the C channels of a frame next to each other and any distance between
  * items and frames, given in elements (so the gates may be slices of one
  * projection's output; an input's distance may be 0, its gradients are then
- * those of each frame, not summed).
+ * those of each frame, not summed; an output's are at least C).
  */
 typedef struct {
     int64_t item, frame; /* elements from one to the next; a frame's below 2^23 */
@@ -681,10 +681,12 @@ size_t dwscan_fwd_workspace_bytes(const dw_scan *shape);
  *
  * decay: [C] float; h0, h_last: [B][C] float, dense.  The state, the gates and
  * 1 - a (taken without cancellation) are float32 whatever the storage type; y
- * is rounded once.  Repeated calls agree bit for bit.
+ * is rounded once.  Repeated calls agree bit for bit.  The workspace serves one
+ * call at a time: calls that may overlap (on two streams, or captured into graphs
+ * that may) take one each.
  * Errors: DW_ERR_INVALID_ARG for a null pointer that holds elements, a negative
- * size or stride, a scale that is not positive and finite, a bad dtype, or y
- * aliasing an input; DW_ERR_UNSUPPORTED for sizes or strides too large for one
+ * size or stride, a scale that is not positive and finite, a bad dtype, y
+ * aliasing an input, or frames of y that overlap; DW_ERR_UNSUPPORTED for sizes or strides too large for one
  * launch; DW_ERR_WORKSPACE for a missing or short workspace (which starts on a
  * multiple of 16 bytes, or the call fails with DW_ERR_INVALID_ARG).
  */
@@ -726,7 +728,8 @@ dw_status dwscan_bwd(const dw_scan *shape, const void *x, const void *r, const v
  * q [B][T][H][D], k and v [B][T][Hkv][D] and their outputs and gradients, with
  * the D elements of a head next to each other and any distance between items,
  * frames and heads, given in elements (slices of one projection's output, or a
- * cache; an input's distance may be 0, its gradients are then not summed).
+ * cache; an input's distance may be 0, its gradients are then not summed; an
+ * output's are at least D).
  */
 typedef enum {
     DW_PAIRS_HALVES = 0,     /* element j of the first R turns with element j + R/2 */

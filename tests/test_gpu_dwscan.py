@@ -403,6 +403,52 @@ def test_captured(T):
             assert torch.equal(a, b)
 
 
+def test_two_graphs_of_one_workspace():
+    """Linked tiles in two captured graphs that share their workspace, replayed in turn with eager calls between."""
+    dw = lib()
+    sizes = ((2, 700), (1, 1500))
+    n = max(f(B, T, 72) for B, T in sizes for f in (dw.dwscan_fwd_workspace_bytes, dw.dwscan_bwd_workspace_bytes))
+    ws = torch.empty((n,), dtype=torch.uint8, device=DEV)
+    problems, graphs, want = [], [], []
+    for B, T in sizes:
+        s = make(B, T, 72, BF16, [T] * B)
+        o = {k: torch.empty_like(s["x"]) for k in ("y", "dx", "dr", "dg")}
+        o |= {"ddecay": torch.empty((72,), device=DEV), "dh0": torch.empty_like(s["h0"])}
+
+        def step(s=s, o=o):
+            dw.dwscan_fwd(s["x"], s["r"], s["g"], s["decay"], s["lengths"], h0=s["h0"], y=o["y"], workspace=ws, need=("y",))
+            grads(s, o["y"], workspace=ws, **{k: t for k, t in o.items() if k != "y"})
+        step()
+        torch.cuda.synchronize()
+        want.append({k: t.clone() for k, t in o.items()})
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        problems.append((step, o))
+        graphs.append(g)
+    for k in range(4):
+        for (step, o), g, w in zip(problems, graphs, want):
+            for t in o.values():
+                t.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            for name, t in o.items():
+                assert torch.equal(t, w[name]), (k, name)
+            step()
+
+
+def test_a_scale_that_changes():
+    """The scale is the value given, not the object that gave it."""
+    dw = lib()
+    s = make(2, 9, 16, F32, [9, 9])
+    scale, out = torch.tensor(8.0), []
+    for v in (8.0, 2.0, 8.0):
+        scale.fill_(v)
+        out.append(dw.dwscan_fwd(s["x"], s["r"], s["g"], s["decay"], scale=scale)[0])
+        assert torch.equal(out[-1], dw.dwscan_fwd(s["x"], s["r"], s["g"], s["decay"], scale=v)[0])
+    assert torch.equal(out[0], out[2]) and not torch.equal(out[0], out[1])
+
+
 def test_binding_refusals():
     dw = lib()
     x, d, m = torch.zeros((2, 3, 16), device=DEV), torch.zeros(16, device=DEV), torch.zeros((2, 16), device=DEV)

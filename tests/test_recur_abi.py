@@ -150,6 +150,38 @@ def test_rope_validation(lib):
     assert lib.dwrope_bwd_workspace_bytes(rope(D=200)) == 0 and lib.dwrope_bwd_workspace_bytes(N) == 0
 
 
+def test_outputs_that_overlap_are_refused(lib):
+    """Distances of an output shorter than what is written there; an input may have them, and an axis of one has none."""
+    def fwd(strides, **kw):
+        return lib.dwscan_fwd(scan(strides=strides, **kw), A[0], A[1], A[2], A[3], N, N, A[4], N, N, 0, N)
+
+    def bwd(strides, **out):
+        o = [out.get(k, A[9 + j]) for j, k in enumerate(("dx", "dr", "dg"))]
+        return lib.dwscan_bwd(scan(strides=strides), A[0], A[1], A[2], A[3], N, N, A[6], A[7], N, *o, N, N, N, 0, N)
+    for bad in ([0, 8], [40, 0], [7, 8], [40, 7]):
+        assert fwd([40, 8] * 3 + bad + [40, 8] * 4) == INVALID and "overlap" in err(lib)
+        for j, k in enumerate(("dx", "dr", "dg")):
+            s = [40, 8] * 5 + [40, 8] * j + bad + [40, 8] * (2 - j)
+            assert bwd(s) == INVALID and "overlap" in err(lib)
+            assert bwd(s, **{k: N}) == WORKSPACE  # not written, so the next check answers
+    long = scan(B=1, T=6000, C=64, strides=[0, 64] * 8)
+    assert lib.dwscan_fwd(long, A[0], A[1], A[2], A[3], N, N, A[4], N, N, 0, N) == WORKSPACE
+    assert bwd([0, 0] * 5 + [40, 8] * 3) == WORKSPACE
+
+    def rope_fwd(j, bad):
+        return lib.dwrope_fwd(rope(strides=[320, 64, 16] * (3 + j) + bad + [320, 64, 16] * (4 - j)), A[0], A[1], A[2], A[3], A[4],
+                              A[5], N, N, N, A[6], A[7], A[8], N)
+
+    def rope_bwd(j, bad):
+        return lib.dwrope_bwd(rope(strides=[320, 64, 16] * (6 + j) + bad + [320, 64, 16] * (1 - j)), A[0], A[1], A[2], A[3], A[4],
+                              N, N, A[5], A[6], A[7], A[8], N, N, N, 0, N)
+    for bad in ([15, 64, 16], [0, 64, 16], [320, 0, 16], [320, 64, 15], [320, 64, 0]):
+        for j in range(3):
+            assert rope_fwd(j, bad) == INVALID and "overlap" in err(lib)
+        for j in range(2):
+            assert rope_bwd(j, bad) == INVALID and "overlap" in err(lib)
+
+
 def test_act_validation(lib):
     def f(act=1, x=A[0], y=A[1], kept=A[2], codes=A[3], B=2, T=3, C=8, dtype=0):
         return lib.dwact_fwd(act, x, N, y, kept, codes, B, T, C, dtype, N)
