@@ -561,16 +561,13 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
 // the frames before them.
 // ---------------------------------------------------------------------------
 //
-// Waves that share a SIMD at least.  Linked bf16 tiles 4 (128 registers; [16,750,1024]
-// 52.9 us against 54.8 with the 131 that it would take), float 3 (168; 96 against
-// 98, [8,375,1024] 25.5 against 28.9); in turn 2.
-template <typename S, bool LINKED>
-constexpr int scan_bwd_waves() {
-    return LINKED ? (sizeof(S) == 2 ? 4 : 3) : 2;
-}
+// Waves that share a SIMD at least: linked tiles 3 (168 registers; bf16
+// [16,750,1024] 57.4 us against 59.3 with 4, [2,6001,512] 37.4 and 39.3, float 85.1
+// against 86.6 with 2, [8,375,1024] 26.7 and 32.2), in turn 2.
+constexpr int scan_bwd_waves(bool linked) { return linked ? 3 : 2; }
 
 template <typename S, bool TAIL, int SEGS, int FR, bool LINKED>
-__global__ __launch_bounds__(kScanThreads, (scan_bwd_waves<S, LINKED>())) void scan_bwd_kernel(const ScanArgs a) {
+__global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd_kernel(const ScanArgs a) {
     constexpr int kTileFrames = SEGS * FR;
     __shared__ float lds[LINKED ? 3 : 2][kScanWaves][2][kScanCols];
     __shared__ float column[kScanRows][kScanCols];
@@ -705,15 +702,19 @@ struct ScanPlan {
 // two waves a SIMD) make one tile of up to 128 frames, and in longer sequences
 // halve the words that a tile reads of those before it; with 8, sequences waste
 // less where they end.  us for 16 and 8: bf16 [16,750,1024] with lengths of half
-// to all 27.9 and 25.4, [64,750,256] 29.6 and 28.4, [32,1500,512] 52.5 and 54.8,
-// [2,6001,512] 19.7 and 20.3, float 24.7 and 26.8.
+// to all 28.8 and 26.8, [64,750,256] 29.6 and 28.2, [2,6001,512] 19.9 and 20.2,
+// float 23.0 and 25.6, [1,20000,512] bf16 31.2 and 29.5, float 42.0 and 44.4.
 //
-// Linked or in turn, us: 256 chains, bf16 [16,750,1024] 30 and 32 (gradients 59
-// and 77), float 45 and 58 (98 and 98); 512 chains, [16,1500,2048] bf16 101 and
-// 96 (204 and 215), float 165 and 159 (355 and 332), [32,130,1024] bf16 17 and 15.
+// Linked or in turn, us: 256 chains, [16,750,1024] bf16 30 and 32, float 42 and 53;
+// 512 chains, [16,1500,2048] bf16 100 and 95, float 163 and 155, [32,130,1024] 17
+// and 15.  Gradients: [16,1500,2048] bf16 191 and 170, float 334 and 325,
+// [32,130,1024] 31 and 27.  One chain a CU, all of one length, does better in turn
+// (bf16 [16,750,1024] 59 and 56, float 85 and 80), but not with lengths of half to
+// all (51 and 53), nor do a few more chains (320, [20,750,1024], 70 and 83, float
+// 102 and 119) or fewer (192, [24,1500,512], 85 and 99).
 // Up to 4 tiles in turn save the launch that clears the words: calls of [8,256,512]
-// bf16 15.8 and 10.8, [1,200,64] 15.1 and 10.4 (gradients 23.4 and 20.8), where 5 to
-// 8 tiles cost more than it: [4,500,1024] bf16 14.3 and 20.6.
+// bf16 15.6 and 11.1, [1,200,64] 15.1 and 10.7 (gradients 23.3 and 20.5), where 5 to
+// 8 tiles cost more than it: [4,500,1024] bf16 15.6 and 20.9.
 static ScanPlan scan_plan(const ScanShape& s, bool backward) {
     ScanPlan p = {};
     const int64_t one = kScanRows * kScanRun;
