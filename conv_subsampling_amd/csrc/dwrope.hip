@@ -11,12 +11,12 @@
 // turns, reduced in 64 bits, then a float polynomial on [-1, 1].
 //
 // Bound by memory.  12000 frames of 8 + 8 heads of 128 in bf16: forward 86.8 MB in
-// 18.7 us (4.6 TB/s; a large copy reaches 5.1), about 14 vector operations an element,
+// 18.7 us (4.6 TB/s; a large copy reaches 5.1), about 19 vector operations an element,
 // which take 9 us of issue slots; gradients 124.5 MB in 29 us and 4 us for the
 // sum of the gammas' partial rows, 32 together.  Two heads of both tensors in
 // flight (134 registers, three waves a SIMD, so all workgroups at once); with four
-// 40 us, with one 33, with the next two read ahead 33.  One frame of 16 items
-// takes 11 us, which is the host's call and launch: the kernel is 6, a chain of
+// 40 us, with one 33, with the next two read ahead 33.  One frame of 64 items
+// takes 11.6 us, which is the host's call and launch: the kernel is 6, a chain of
 // loads, the angle's 64-bit reduction and two sums across a team.
 #include "launch.h"
 #include "rowops.h"
