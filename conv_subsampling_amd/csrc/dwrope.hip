@@ -46,12 +46,16 @@ struct RopeArgs {
     float eps;
 };
 
-// Where a lane's 4 pairs lie in a head.  PACKED: each of its two quads is 4
+// How a lane's 4 pairs lie in a head.  kWhole and kTail: each of its two quads is 4
 // neighbouring elements, so vector accesses serve it: halves, the pairs' firsts
 // and their seconds (a lane that is not rotated pairs the two quads of its 8
-// elements in a row); neighbours, 8 elements in a row.  Elsewhere each element has
-// a place of its own, D standing for none.
-template <bool PACKED, bool HALVES>
+// elements in a row); neighbours, 8 elements in a row.  kTail: the head may end
+// inside a quad (gradients of [9,1197,32+8 heads of 50] bf16, neighbours, 58 us;
+// 144 element by element).  kLoose: each element has a place of its own, D standing
+// for none.
+constexpr int kLoose = 0, kWhole = 1, kTail = 2;
+
+template <int PACKED, bool HALVES>
 struct PairMap {
     int at[2][kQuad];
     int first;  // the lane's first pair
@@ -62,7 +66,7 @@ struct PairMap {
 #pragma unroll
         for (int e = 0; e < kQuad; ++e) {
             const int p = first + e;
-            if constexpr (PACKED && HALVES) {
+            if constexpr (PACKED != kLoose && HALVES) {
                 at[0][e] = apart ? p : 2 * first + e;
                 at[1][e] = apart ? p + R / 2 : 2 * first + kQuad + e;
             } else {
@@ -75,7 +79,7 @@ struct PairMap {
         }
     }
 
-    // PACKED: the first elements of the two quads as they lie in memory
+    // not kLoose: the first elements of the two quads as they lie in memory
     __device__ __forceinline__ int quad(int h) const { return HALVES ? at[h][0] : 2 * first + h * kQuad; }
 };
 
@@ -89,13 +93,13 @@ struct Head {
 };
 
 // A head from its first element on; `on` is false for a head past the last.
-template <typename S, bool PACKED, bool HALVES>
+template <typename S, int PACKED, bool HALVES>
 __device__ __forceinline__ HeadRaw<S> load_head(const S* head, const PairMap<PACKED, HALVES>& m, int D, bool on) {
     HeadRaw<S> r = {};
-    if constexpr (PACKED) {
+    if constexpr (PACKED != kLoose) {
         if (on && 2 * m.first < D) {
-            r.q[0] = load_quad<S, false>(head + m.quad(0), kQuad);
-            r.q[1] = load_quad<S, false>(head + m.quad(1), kQuad);
+            r.q[0] = load_quad<S, PACKED == kTail>(head + m.quad(0), D - m.quad(0));
+            r.q[1] = load_quad<S, PACKED == kTail>(head + m.quad(1), D - m.quad(1));
         }
     } else {
 #pragma unroll
@@ -114,25 +118,25 @@ __device__ __forceinline__ HeadRaw<S> load_head(const S* head, const PairMap<PAC
     return r;
 }
 
-template <typename S, bool PACKED, bool HALVES>
+template <typename S, int PACKED, bool HALVES>
 __device__ __forceinline__ Head widen_head(const HeadRaw<S>& r, const PairMap<PACKED, HALVES>& m) {
     const Vf<kQuad> xv = widen_quad<S>(r.q[0]), yv = widen_quad<S>(r.q[1]);
     const f32x4 x = {xv.v[0], xv.v[1], xv.v[2], xv.v[3]}, y = {yv.v[0], yv.v[1], yv.v[2], yv.v[3]};
-    if constexpr (PACKED && !HALVES) return {{x[0], x[2], y[0], y[2]}, {x[1], x[3], y[1], y[3]}};
+    if constexpr (PACKED != kLoose && !HALVES) return {{x[0], x[2], y[0], y[2]}, {x[1], x[3], y[1], y[3]}};
     return {x, y};
 }
 
-template <typename S, bool PACKED, bool HALVES>
+template <typename S, int PACKED, bool HALVES>
 __device__ __forceinline__ void store_head(S* head, const PairMap<PACKED, HALVES>& m, int D, Head h) {
-    if constexpr (PACKED) {
+    if constexpr (PACKED != kLoose) {
         if (2 * m.first >= D) return;
         Vf<kQuad> x = {{h.a[0], h.a[1], h.a[2], h.a[3]}}, y = {{h.b[0], h.b[1], h.b[2], h.b[3]}};
         if constexpr (!HALVES) {
             x = {{h.a[0], h.b[0], h.a[1], h.b[1]}};
             y = {{h.a[2], h.b[2], h.a[3], h.b[3]}};
         }
-        store_quad<S, false>(head + m.quad(0), kQuad, x);
-        store_quad<S, false>(head + m.quad(1), kQuad, y);
+        store_quad<S, PACKED == kTail>(head + m.quad(0), D - m.quad(0), x);
+        store_quad<S, PACKED == kTail>(head + m.quad(1), D - m.quad(1), y);
     } else {
 #pragma unroll
         for (int e = 0; e < kQuad; ++e) {
@@ -149,7 +153,7 @@ __device__ __forceinline__ void store_head(S* head, const PairMap<PACKED, HALVES
 }
 
 // The weights of the lane's elements; ones where there is no gamma, 0 past the head.
-template <typename S, bool PACKED, bool HALVES>
+template <typename S, int PACKED, bool HALVES>
 __device__ __forceinline__ Head load_gamma(const void* gamma, const PairMap<PACKED, HALVES>& m, int D) {
     if (gamma) return widen_head<S>(load_head<S>((const S*)gamma, m, D, true), m);
     return {f32x4(1.0f), f32x4(1.0f)};
@@ -193,14 +197,14 @@ __device__ __forceinline__ RopeTeam rope_frame(const RopeArgs& a, uint64_t frame
 }
 
 // Zeros for the heads of a frame past its length.
-template <typename S, bool PACKED, bool HALVES>
+template <typename S, int PACKED, bool HALVES>
 __device__ __forceinline__ void zero_heads(S* out, int64_t os, int32_t heads, uint32_t from, uint32_t step,
                                            const PairMap<PACKED, HALVES>& m, int D) {
     for (uint32_t h = from; h < (uint32_t)heads; h += step) store_head<S>(out + (int64_t)h * os, m, D, Head{});
 }
 
 // x: the heads of one frame; out: where they go.
-template <typename S, bool PACKED, bool HALVES, int LANES>
+template <typename S, int PACKED, bool HALVES, int LANES>
 __device__ __forceinline__ void rope_heads(const S* x, int64_t xs, S* out, int64_t os, int32_t heads, uint32_t from,
                                            uint32_t step, const PairMap<PACKED, HALVES>& m, Head gamma,
                                            const Turns& turn, int D, float eps) {
@@ -233,7 +237,7 @@ __device__ __forceinline__ void rope_heads(const S* x, int64_t xs, S* out, int64
     }
 }
 
-template <typename S, bool PACKED, bool HALVES, int LANES>
+template <typename S, int PACKED, bool HALVES, int LANES>
 __global__ __launch_bounds__(kRopeThreads) void rope_fwd_kernel(const RopeArgs a) {
     constexpr int kTeams = kRopeThreads / LANES;
     const int lane = threadIdx.x % LANES, D = a.D;
@@ -279,7 +283,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_fwd_kernel(const RopeArgs a
 }
 
 // Gradients of one frame's heads; dg takes the sums of u * xh.
-template <typename S, bool PACKED, bool HALVES, int LANES>
+template <typename S, int PACKED, bool HALVES, int LANES>
 __device__ __forceinline__ void rope_grads(const S* x, int64_t xs, const S* dout, int64_t ds, S* dx, int64_t os,
                                            int32_t heads, uint32_t from, uint32_t step,
                                            const PairMap<PACKED, HALVES>& m, Head gamma, const Turns& turn,
@@ -340,7 +344,7 @@ __device__ __forceinline__ void rope_grads(const S* x, int64_t xs, const S* dout
 // Teams take frames (and parts of their heads) in turn and keep the gammas'
 // gradients of their own elements in registers; a workgroup adds its teams in a
 // fixed order and writes one partial row.
-template <typename S, bool PACKED, bool HALVES, int LANES>
+template <typename S, int PACKED, bool HALVES, int LANES>
 __global__ __launch_bounds__(kRopeThreads) void rope_bwd_kernel(const RopeArgs a) {
     constexpr int kTeams = kRopeThreads / LANES, kWaves = kRopeThreads / 64;
     __shared__ float column[kWaves][2][2 * kQuad * LANES];
@@ -470,13 +474,13 @@ bool dwrope_fits(const RopeShape& s) {
     return product_below((int64_t)1 << 40, {s.B, s.T}) && grid_of_256_fits(rope_blocks(s, false));
 }
 
-template <bool P, bool H, int L>
+template <int P, bool H, int L>
 struct RopeForm {
-    static constexpr bool PACKED = P, HALVES = H;
-    static constexpr int LANES = L;
+    static constexpr bool HALVES = H;
+    static constexpr int PACKED = P, LANES = L;
 };
 
-template <bool P, bool H, typename F>
+template <int P, bool H, typename F>
 static hipError_t with_rope_lanes(int64_t D, F&& f) {
     if (D <= 32) return f(RopeForm<P, H, 4>());
     if (D <= 64) return f(RopeForm<P, H, 8>());
@@ -484,12 +488,12 @@ static hipError_t with_rope_lanes(int64_t D, F&& f) {
 }
 
 // Quads of neighbouring elements serve a lane where its 4 pairs all are rotated
-// or none is (halves), and where the head holds whole lanes of 8 elements.
+// or none is: always with neighbours, with halves where R is a multiple of 8.
 template <typename F>
 static hipError_t with_rope_form(const RopeShape& s, F&& f) {
-    const bool packed = s.D % 8 == 0 && (!s.halves || s.R % 8 == 0);
-    if (packed) return s.halves ? with_rope_lanes<true, true>(s.D, f) : with_rope_lanes<true, false>(s.D, f);
-    return s.halves ? with_rope_lanes<false, true>(s.D, f) : with_rope_lanes<false, false>(s.D, f);
+    if (s.halves && s.R % 8 != 0) return with_rope_lanes<kLoose, true>(s.D, f);
+    if (s.D % 8 == 0) return s.halves ? with_rope_lanes<kWhole, true>(s.D, f) : with_rope_lanes<kWhole, false>(s.D, f);
+    return s.halves ? with_rope_lanes<kTail, true>(s.D, f) : with_rope_lanes<kTail, false>(s.D, f);
 }
 
 static RopeStride rope_stride(const AttnStride& s) { return {s.item, s.frame, s.head}; }
