@@ -6,6 +6,9 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+#include <initializer_list>
+
 #include "../../include/dwconv.h"
 #include "launch.h"
 #include "scratch.h"
@@ -207,13 +210,35 @@ bool frames_fit(const dw::FrameStride& s, int64_t B, int64_t T) {
     return s.frame < dw::kScanMaxFrameStride && dw::product_below(far, {B, s.item}) && dw::product_below(far, {T, s.frame});
 }
 
-// Whether what is written at these distances cannot overlap: each at least as long as a piece.
-bool apart(int64_t piece, int64_t n, int64_t step) { return n <= 1 || step >= piece; }
+// An axis of a tensor: its length, and the elements from one place to the next.
+struct Axis {
+    int64_t n, step;
+};
 
-bool frames_apart(const dw::FrameStride& s, int64_t B, int64_t T, int64_t C) { return apart(C, B, s.item) && apart(C, T, s.frame); }
+// Whether pieces written along these axes stay apart: from the shortest distance on,
+// each is at least as long as all that the shorter ones reach.
+template <size_t N>
+bool apart(int64_t piece, Axis (&&axes)[N]) {
+    for (const Axis& a : axes)
+        if (a.n == 0) return true;
+    std::sort(axes, axes + N, [](const Axis& a, const Axis& b) { return a.step < b.step; });
+    int64_t reach = piece;
+    for (const Axis& a : axes) {
+        if (a.n == 1) continue;
+        if (a.step < reach) return false;
+        reach += (a.n - 1) * a.step;
+    }
+    return true;
+}
+
+bool frames_apart(const dw::FrameStride& s, int64_t B, int64_t T, int64_t C) { return apart(C, {{B, s.item}, {T, s.frame}}); }
 
 bool heads_apart(const dw_strides& s, int64_t B, int64_t T, int64_t H, int64_t D) {
-    return apart(D, B, s.item) && apart(D, T, s.frame) && apart(D, H, s.head);
+    return apart(D, {{B, s.item}, {T, s.frame}, {H, s.head}});
+}
+
+bool among(const void* p, std::initializer_list<const void*> others) {
+    return p && std::find(others.begin(), others.end(), p) != others.end();
 }
 
 // The recurrence's problem as the launchers take it.
@@ -714,6 +739,8 @@ dw_status dwscan_fwd(const dw_scan* shape, const void* x, const void* r, const v
     if (!decay || (s.T > 0 && (!x || !r || !g || !y)))
         return fail(DW_ERR_INVALID_ARG, "%s: x, r, g, decay and y must not be NULL (unless empty)", fn);
     if (s.T > 0 && (y == x || y == r || y == g)) return fail(DW_ERR_INVALID_ARG, "%s: y must not alias an input", fn);
+    if (among(h_last, {decay}) || (s.T > 0 && among(h_last, {x, r, g, y})))
+        return fail(DW_ERR_INVALID_ARG, "%s: h_last must not alias y, nor an input but h0", fn);
     if (s.T > 0 && !frames_apart(s.y, s.B, s.T, s.C)) return fail(DW_ERR_INVALID_ARG, "%s: frames of y overlap", fn);
     const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwscan_fwd_workspace(s));
     if (w != DW_OK) return w;
@@ -748,8 +775,13 @@ dw_status dwscan_bwd(const dw_scan* shape, const void* x, const void* r, const v
         if ((dx && !frames_apart(s.dx, s.B, s.T, s.C)) || (dr && !frames_apart(s.dr, s.B, s.T, s.C)) ||
             (dg && !frames_apart(s.dg, s.B, s.T, s.C)))
             return fail(DW_ERR_INVALID_ARG, "%s: frames of a gradient overlap", fn);
-        if ((ddecay && ddecay == decay) || (dh0 && dh0 == h0))
+    }
+    if (s.B > 0) {
+        if (among(ddecay, {decay, h0, dh_last}) || among(dh0, {decay, h0}) ||
+            (s.T > 0 && (among(ddecay, {x, r, g, y, dy}) || among(dh0, {x, r, g, y, dy}))))
             return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
+        if (among(ddecay, {dh0}) || (s.T > 0 && (among(ddecay, {dx, dr, dg}) || among(dh0, {dx, dr, dg}))))
+            return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
     }
     const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwscan_bwd_workspace(s));
     if (w != DW_OK) return w;
@@ -814,7 +846,9 @@ dw_status dwrope_bwd(const dw_rope* shape, const void* q, const void* k, const v
         return fail(DW_ERR_INVALID_ARG, "%s: dk must not alias another tensor", fn);
     if ((any_q && dq && !heads_apart(shape->dq, s.B, s.T, s.H, s.D)) || (any_k && dk && !heads_apart(shape->dk, s.B, s.T, s.Hkv, s.D)))
         return fail(DW_ERR_INVALID_ARG, "%s: heads of a gradient overlap", fn);
-    if (dq_gamma && dq_gamma == dk_gamma) return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
+    if (among(dq_gamma, {dk_gamma}) || (any_q && (among(dq_gamma, {dq}) || among(dk_gamma, {dq}))) ||
+        (any_k && (among(dq_gamma, {dk}) || among(dk_gamma, {dk}))))
+        return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
     if (params) {
         const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwrope_bwd_workspace(s));
         if (w != DW_OK) return w;

@@ -649,7 +649,9 @@ dw_status dwattn_bwd(const dw_attn *shape, const void *q, const void *k, const v
  * with the C channels of a frame next to each other and any distance between
  * items and frames, given in elements (so the gates may be slices of one
  * projection's output; an input's distance may be 0, its gradients are then
- * those of each frame, not summed; an output's are at least C).
+ * those of each frame, not summed; an output's frames must not overlap: of the
+ * distances of its axes longer than one the shorter is at least C, the longer at
+ * least what the frames along the other axis reach).
  */
 typedef struct {
     int64_t item, frame; /* elements from one to the next; a frame's below 2^23 */
@@ -686,8 +688,8 @@ size_t dwscan_fwd_workspace_bytes(const dw_scan *shape);
  * that may) take one each.
  * Errors: DW_ERR_INVALID_ARG for a null pointer that holds elements, a negative
  * size or stride, a scale that is not positive and finite, a bad dtype, y
- * aliasing an input, or frames of y that overlap; DW_ERR_UNSUPPORTED for sizes or strides too large for one
- * launch; DW_ERR_WORKSPACE for a missing or short workspace (which starts on a
+ * aliasing an input, h_last aliasing y or an input but h0, or frames of y that
+ * overlap; DW_ERR_UNSUPPORTED for sizes or strides too large for one launch; DW_ERR_WORKSPACE for a missing or short workspace (which starts on a
  * multiple of 16 bytes, or the call fails with DW_ERR_INVALID_ARG).
  */
 dw_status dwscan_fwd(const dw_scan *shape, const void *x, const void *r, const void *g, const float *decay,
@@ -715,7 +717,7 @@ size_t dwscan_bwd_workspace_bytes(const dw_scan *shape);
  * Each of dx, dr, dg, ddecay ([C] float) and dh0 ([B][C] float; may be dh_last)
  * may be NULL (not computed).  An empty batch still writes ddecay = 0.
  * Errors: as dwscan_fwd, and DW_ERR_INVALID_ARG for gradients that alias an
- * input or each other.
+ * input (but dh0 dh_last) or each other, or whose frames overlap.
  */
 dw_status dwscan_bwd(const dw_scan *shape, const void *x, const void *r, const void *g, const float *decay,
                      const int32_t *lengths, const float *h0, const void *y, const void *dy, const float *dh_last,
@@ -729,7 +731,8 @@ dw_status dwscan_bwd(const dw_scan *shape, const void *x, const void *r, const v
  * the D elements of a head next to each other and any distance between items,
  * frames and heads, given in elements (slices of one projection's output, or a
  * cache; an input's distance may be 0, its gradients are then not summed; an
- * output's are at least D).
+ * output's heads must not overlap: from its shortest distance on, each is at least
+ * what the pieces along the axes with shorter ones reach, D to begin with).
  */
 typedef enum {
     DW_PAIRS_HALVES = 0,     /* element j of the first R turns with element j + R/2 */
@@ -772,8 +775,8 @@ typedef struct {
  * (without place), with the same strides.
  * Errors: DW_ERR_INVALID_ARG for a null pointer that holds elements, a negative
  * size or stride, an odd R or R > D, R > 0 without freq, a negative or NaN eps, a bad
- * dtype or pairs, v without v_out or the other way round, or an output that
- * aliases another tensor; DW_ERR_UNSUPPORTED for D > 128 or sizes too large for
+ * dtype or pairs, v without v_out or the other way round, an output that
+ * aliases another tensor, or heads of an output that overlap; DW_ERR_UNSUPPORTED for D > 128 or sizes too large for
  * one launch.
  */
 dw_status dwrope_fwd(const dw_rope *shape, const void *q, const void *k, const void *v, const void *q_gamma,
