@@ -4,10 +4,11 @@
 //   w = scale * softplus(decay) * sigmoid(r),  a = exp(-w)
 //   h_t = a h_{t-1} + sqrt(1 - a^2) sigmoid(g) x
 //
-// The state moves by d = 1 - a = -expm1(-w), taken without cancellation:
-// h <- (h - d h) + u, u = sqrt(d (2 - d)) sigmoid(g) x, the bracket one fused
-// operation.  A decay near 1 thus keeps its digits, as does one near 0, and
-// products of decays are exponentials of sums of w.
+// Where a > 1/2 the state moves by d = 1 - a = -expm1(-w), taken without
+// cancellation: h <- (h - d h) + u, u = sqrt(d (2 - d)) sigmoid(g) x, the bracket
+// one fused operation; elsewhere h <- a h + u.  A decay near 1 thus keeps its
+// digits, as does one near 0, down to 2^-126, and products of decays are
+// exponentials of sums of w.
 //
 // Frames in parallel: a run of frames maps the state h before it to P h + H
 // behind it, and runs compose.  A thread takes 2 channels of FR frames, in
@@ -155,15 +156,21 @@ __device__ __forceinline__ float sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
 }
 
-// 1 - 2^-v, v = w / log 2: a series in w where the difference would cancel (its
-// first left out term is 2^-24.4 of it at w = 1/8), the exponential beyond (off
-// by 2^-21 at most).
-__device__ __forceinline__ float one_minus_exp2(float v) {
-    const float series =
-        v * (0.69314718f + v * (-0.24022651f + v * (0.055504109f + v * (-0.0096181291f + v * 0.0013333558f))));
-    const float direct = 1.0f - __builtin_amdgcn_exp2f(-v);
-    return v < 0.18033688f ? series : direct;
+// What the decay a = 2^-v (v = w / log 2) does to a state, as the one of 1 - a and a
+// that a float holds without loss of digits: d = 1 - a where a > 1/2, a polynomial in
+// v (off by 2.2 2^-24 of d with its roundings), and -a elsewhere (-0: a decay of 0).
+__device__ __forceinline__ float decay_factor(float v) {
+    const float d = v * (0.69314718f + v * (-0.24022606f + v * (0.055498954f + v * (-0.0095962733f + v * (0.0012907785f + v * -0.00011458035f)))));
+    return v < 1.0f ? d : -__builtin_amdgcn_exp2f(-v);
 }
+
+__device__ __forceinline__ bool is_decay(float k) { return (int32_t)__float_as_uint(k) < 0; }
+
+// a h
+__device__ __forceinline__ float decayed(float k, float h) { return __builtin_fmaf(-k, h, is_decay(k) ? 0.0f : h); }
+
+// 1 - a^2
+__device__ __forceinline__ float lost_power(float k) { return __builtin_fmaf(-k, k, is_decay(k) ? 1.0f : 2.0f * k); }
 
 // log(1 + exp(v)): 2 atanh(e / (2 + e)) where e is small (left out: 2^-28 of it),
 // v itself where it is large.
@@ -518,7 +525,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
     for (; tile < end; ++tile) {
         const TileSpan span = tile_span(a, p, tile, kTileFrames);
         const int valid = span.valid;
-        f32x2 d[FR], u[FR];
+        f32x2 k[FR], u[FR];
         Run all = {f32x2(1.0f), f32x2(0.0f)}, before = all;
         if (valid > 0) {
             pair_raw<S> xr[FR], rr[FR], gr[FR];
@@ -535,13 +542,13 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
                     const float wf = rate[e] * sigmoid(pair_at<S>(rr[f], e));
-                    const float df = one_minus_exp2(wf);
-                    const float m = __builtin_amdgcn_sqrtf(df * (2.0f - df));
+                    const float kf = decay_factor(wf);
+                    const float m = __builtin_amdgcn_sqrtf(lost_power(kf));
                     const float uf = m * (sigmoid(pair_at<S>(gr[f], e)) * pair_at<S>(xr[f], e));
-                    d[f][e] = df;
+                    k[f][e] = kf;
                     u[f][e] = uf;
                     w[e] += wf;
-                    h[e] = __builtin_fmaf(-df, h[e], h[e]) + uf;
+                    h[e] = decayed(kf, h[e]) + uf;
                 }
             }
             const Run run = {{__builtin_amdgcn_exp2f(-w[0]), __builtin_amdgcn_exp2f(-w[1])}, h};
@@ -557,7 +564,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
 #pragma unroll
             for (int f = 0; f < FR; ++f) {
 #pragma unroll
-                for (int e = 0; e < kScanPair; ++e) h[e] = __builtin_fmaf(-d[f][e], h[e], h[e]) + u[f][e];
+                for (int e = 0; e < kScanPair; ++e) h[e] = decayed(k[f][e], h[e]) + u[f][e];
                 y[f] = pack_pair<S>(h);
             }
         }
@@ -613,7 +620,7 @@ __global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd
         const TileSpan span = tile_span(a, p, kSeveral ? a.tiles - 1 - at : 0, kTileFrames);
         const int valid = span.valid;
         load(span);
-        f32x2 d[FR], w[FR];
+        f32x2 k[FR], w[FR];
         Run all = {f32x2(1.0f), f32x2(0.0f)}, before = all;
         if (valid > 0) {
             if (!span.full) {  // a decay of 1 and no gradient
@@ -626,11 +633,9 @@ __global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
                     const float wf = rate[e] * sigmoid(pair_at<S>(rr[f], e));
-                    const float df = one_minus_exp2(wf);
                     w[f][e] = wf;
-                    d[f][e] = df;
-                    const float G = pair_at<S>(dyr[f], e) + c[e];
-                    c[e] = __builtin_fmaf(-df, G, G);
+                    k[f][e] = decay_factor(wf);
+                    c[e] = decayed(k[f][e], pair_at<S>(dyr[f], e) + c[e]);
                     sw[e] += wf;
                 }
             }
@@ -653,15 +658,15 @@ __global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd
                     const float G = pair_at<S>(dyr[f], e) + c[e];
                     const float gate = sigmoid(pair_at<S>(gr[f], e));
                     const float h = f == 0 && start ? h0[e] : pair_at<S>(prev[f], e);
-                    const float df = d[f][e], z = df * (2.0f - df);                   // 1 - a^2 = m^2
-                    const float rs = __builtin_amdgcn_rsqf(z > 1e-37f ? z : 1e-37f);  // m = z rs, 0 where z is
-                    const float v = rs * rs;
+                    const float kf = k[f][e], z = lost_power(kf);                           // 1 - a^2 = m^2
+                    const float rs = __builtin_amdgcn_rsqf(z > 0x1p-126f ? z : 0x1p-126f);  // m = z rs, 0 where z is
+                    const float a2 = is_decay(kf) ? kf * kf : 1.0f - z;
                     dx[e] = G * (z * rs) * gate;
                     const float t = dx[e] * pair_at<S>(xr[f], e);
                     dg[e] = t - t * gate;
-                    c[e] = __builtin_fmaf(-df, G, G);
+                    c[e] = decayed(kf, G);
                     // G i x a^2 / m = t a^2 / m^2
-                    const float q = w[f][e] * (t * (v - z * v) - c[e] * h);
+                    const float q = w[f][e] * (t * (a2 * (rs * rs)) - c[e] * h);
                     const float s = w[f][e] * unrate[e];
                     dr[e] = q * (0.69314718f - 0.69314718f * s);
                     sum[e] += span.full || p.seg * FR + f < valid ? q : 0.0f;

@@ -681,9 +681,10 @@ size_t dwscan_fwd_workspace_bytes(const dw_scan *shape);
  * stream's next call, which may be the same buffer.  Inputs at or past the
  * length are not read.
  *
- * decay: [C] float; h0, h_last: [B][C] float, dense.  The state, the gates and
- * 1 - a (taken without cancellation) are float32 whatever the storage type; y
- * is rounded once.  Repeated calls agree bit for bit.  The workspace serves one
+ * decay: [C] float; h0, h_last: [B][C] float, dense.  The state, the gates, and
+ * 1 - a or a, whichever is below 1/2 (neither taken by cancellation), are float32
+ * whatever the storage type; decays below 2^-126 are 0, and y is rounded once.  A
+ * state that overflows is an infinity or a NaN for the rest of its item.  Repeated calls agree bit for bit.  The workspace serves one
  * call at a time: calls that may overlap (on two streams, or captured into graphs
  * that may) take one each.
  * Errors: DW_ERR_INVALID_ARG for a null pointer that holds elements, a negative
