@@ -149,11 +149,22 @@ __device__ __forceinline__ void store_pair(S* p, int have, pair_raw<S> q) {
 // ---------------------------------------------------------------------------
 // The step's functions
 // ---------------------------------------------------------------------------
-// 1 / (1 + exp(-v)).  The exponent is one rounded product, so the result is off by
-// up to |v| 2^-24 of itself for negative v; an exponential that reduces its
-// argument cost 2 us of 25 ([2,6001,512] float).  Results below 2^-126 are zero.
+// exp(-v).  float: the rounding of the exponent's product, and what the constant
+// leaves out, come back as a factor (bounded, so that infinite exponents stay what
+// they are): off by 4 2^-24 of itself.  bf16: one rounded product, off by up to |v| 2^-24, which
+// its inputs' own 2^-9 hide.
+template <typename S>
+__device__ __forceinline__ float exp_minus(float v) {
+    const float t = v * -1.44269502f, p = __builtin_amdgcn_exp2f(t);
+    if constexpr (sizeof(S) == 2) return p;
+    const float left = __builtin_fmaf(v, -1.92596299e-8f, __builtin_fmaf(v, -1.44269502f, -t));
+    return p * __builtin_fmaf(__builtin_amdgcn_fmed3f(left, -1.0f, 1.0f), 0.69314718f, 1.0f);
+}
+
+// 1 / (1 + exp(-v)).  Results below 2^-126 are zero.
+template <typename S>
 __device__ __forceinline__ float sigmoid(float v) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+    return __builtin_amdgcn_rcpf(1.0f + exp_minus<S>(v));
 }
 
 // What the decay a = 2^-v (v = w / log 2) does to a state, as the one of 1 - a and a
@@ -541,10 +552,10 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
             for (int f = 0; f < FR; ++f) {
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
-                    const float wf = rate[e] * sigmoid(pair_at<S>(rr[f], e));
+                    const float wf = rate[e] * sigmoid<S>(pair_at<S>(rr[f], e));
                     const float kf = decay_factor(wf);
                     const float m = __builtin_amdgcn_sqrtf(lost_power(kf));
-                    const float uf = m * (sigmoid(pair_at<S>(gr[f], e)) * pair_at<S>(xr[f], e));
+                    const float uf = m * (sigmoid<S>(pair_at<S>(gr[f], e)) * pair_at<S>(xr[f], e));
                     k[f][e] = kf;
                     u[f][e] = uf;
                     w[e] += wf;
@@ -632,7 +643,7 @@ __global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd
             for (int f = FR - 1; f >= 0; --f) {
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
-                    const float wf = rate[e] * sigmoid(pair_at<S>(rr[f], e));
+                    const float wf = rate[e] * sigmoid<S>(pair_at<S>(rr[f], e));
                     w[f][e] = wf;
                     k[f][e] = decay_factor(wf);
                     c[e] = decayed(k[f][e], pair_at<S>(dyr[f], e) + c[e]);
@@ -656,7 +667,7 @@ __global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
                     const float G = pair_at<S>(dyr[f], e) + c[e];
-                    const float gate = sigmoid(pair_at<S>(gr[f], e));
+                    const float gate = sigmoid<S>(pair_at<S>(gr[f], e));
                     const float h = f == 0 && start ? h0[e] : pair_at<S>(prev[f], e);
                     const float kf = k[f][e], z = lost_power(kf);                           // 1 - a^2 = m^2
                     const float rs = __builtin_amdgcn_rsqf(z > 0x1p-126f ? z : 0x1p-126f);  // m = z rs, 0 where z is

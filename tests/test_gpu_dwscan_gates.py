@@ -1,5 +1,5 @@
-"""The recurrence where its decays are near 0, against the definition in 64
-bits.
+"""The recurrence where its decays are near 0, and its gates by themselves,
+against the definition in 64 bits.
 
 Tolerances count roundings of 2^-24 (U), as in test_gpu_dwscan.py, in sums that
 keep no term above what is left of it.  In float32 a gate is off by 8 U: its
@@ -88,3 +88,30 @@ def test_what_one_step_leaves(w):
     bound = U * (40 + 40 * rate * (1 + np.arange(T))[:, None]) * np.abs(left) + 1e-31  # 2^-126 of a million is where decays end
     assert (np.abs(h(y) - left) <= bound).all()
     assert (np.abs(h(last) - left[:, -1]) <= bound[:, -1]).all() and (np.abs(h(dh0) - left[:, -1]) <= bound[:, -1]).all()
+
+
+def test_float_gates():
+    """Both gates by themselves, from -80 to 80.  With a = 0 and x = 1 an output is sigmoid(g): 8 U.  With g = 100 it is
+    sqrt(1 - a^2): w is off by 8 of the gate and 2 of rate and product, the series and 1 - a^2 by 6, the root halves both and adds 2:
+    10 U (softplus(30) is 30 and 1e-13)."""
+    C = 4096
+    v = datagen.uniform((1, 1, C), -80.0, 80.0, "gate/v", device=DEV)
+    one = torch.ones_like(v)
+    y, _ = lib().dwscan_fwd(one, one * 100, v, torch.full((C,), 1e4, device=DEV))
+    want = exact.sigmoid(h(v))
+    assert (np.abs(h(y) - want) <= 8 * U * want).all()
+    y, _ = lib().dwscan_fwd(one, v, one * 100, torch.full((C,), 30.0, device=DEV), scale=1.0)
+    want = np.sqrt(-np.expm1(-60 * want))
+    assert (np.abs(h(y) - want) <= 10 * U * want).all()
+
+
+def test_float_gates_of_infinity_and_nan():
+    v = torch.tensor([float("inf"), -float("inf"), float("nan"), 3e38, -3e38, 200.0, -200.0], device=DEV).view(1, 1, 7)
+    one, decay = torch.ones_like(v), torch.full((7,), 1e4, device=DEV)
+    y, _ = lib().dwscan_fwd(one, one, v, decay)
+    assert y[0, 0, [0, 3, 5]].tolist() == [1.0] * 3 and y[0, 0, [1, 4, 6]].tolist() == [0.0] * 3 and y[0, 0, 2].isnan()
+    y, _ = lib().dwscan_fwd(one * 0, v, one, decay, h0=torch.ones((1, 7), device=DEV))
+    assert y[0, 0, [0, 3, 5]].tolist() == [0.0] * 3 and y[0, 0, [1, 4, 6]].tolist() == [1.0] * 3 and y[0, 0, 2].isnan()
+    back = lib().dwscan_bwd(one, v, v, decay, y, one)
+    for t in back[:3]:
+        assert t[0, 0, [0, 1, 3, 4, 5, 6]].isfinite().all()
