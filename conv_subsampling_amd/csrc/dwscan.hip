@@ -161,11 +161,17 @@ __device__ __forceinline__ float exp_minus(float v) {
     return p * __builtin_fmaf(__builtin_amdgcn_fmed3f(left, -1.0f, 1.0f), 0.69314718f, 1.0f);
 }
 
-// 1 / (1 + exp(-v)).  Results below 2^-126 are zero.
+// 1 / (1 + exp(-v)), given the exponential.  Results below 2^-126 are zero.
+__device__ __forceinline__ float sigmoid_of(float e) { return __builtin_amdgcn_rcpf(1.0f + e); }
+
 template <typename S>
 __device__ __forceinline__ float sigmoid(float v) {
-    return __builtin_amdgcn_rcpf(1.0f + exp_minus<S>(v));
+    return sigmoid_of(exp_minus<S>(v));
 }
+
+// 1 - sigmoid(v) = exp(-v) sigmoid(v), without cancellation.  Where the gate is zero, so
+// is this, which then scales nothing but zeros.
+__device__ __forceinline__ float shut_of(float e, float open) { return fminf(e, 0x1p126f) * open; }
 
 // What the decay a = 2^-v (v = w / log 2) does to a state, as the one of 1 - a and a
 // that a float holds without loss of digits: d = 1 - a where a > 1/2, a polynomial in
@@ -622,9 +628,9 @@ __global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd
     const int end = LINKED ? at + 1 : !item ? 0 : scan_loops<SEGS, FR, LINKED>() ? a.tiles : 1;
     const int row = LINKED ? (int)(p.chain / (uint32_t)a.col_blocks) * a.tiles + at : (int)(p.chain / (uint32_t)a.col_blocks);
     const f32x2 rate = *(const f32x2*)&shared.rate[p.lane];
-    f32x2 unrate;  // w * unrate is the gate; where the rate is 0 nothing comes of it
+    f32x2 unrate;  // w * unrate is the gate
 #pragma unroll
-    for (int e = 0; e < kScanPair; ++e) unrate[e] = rate[e] > 1e-30f ? __builtin_amdgcn_rcpf(rate[e]) : 0.0f;
+    for (int e = 0; e < kScanPair; ++e) unrate[e] = __builtin_amdgcn_rcpf(fmaxf(rate[e], 0x1p-126f));
     f32x2 carry = item && at == 0 ? load_state(a.start, p.b, a.C, p) : f32x2(0.0f), sum = {0.0f, 0.0f};
     int turn = 0;
     for (; at < end; ++at) {
@@ -667,19 +673,20 @@ __global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd
 #pragma unroll
                 for (int e = 0; e < kScanPair; ++e) {
                     const float G = pair_at<S>(dyr[f], e) + c[e];
-                    const float gate = sigmoid<S>(pair_at<S>(gr[f], e));
+                    const float eg = exp_minus<S>(pair_at<S>(gr[f], e)), gate = sigmoid_of(eg);
+                    // again, rather than kept: float gradients [32,1500,512] 168 us, 176 with it in registers
+                    const float er = exp_minus<S>(pair_at<S>(rr[f], e));
                     const float h = f == 0 && start ? h0[e] : pair_at<S>(prev[f], e);
                     const float kf = k[f][e], z = lost_power(kf);                           // 1 - a^2 = m^2
                     const float rs = __builtin_amdgcn_rsqf(z > 0x1p-126f ? z : 0x1p-126f);  // m = z rs, 0 where z is
                     const float a2 = is_decay(kf) ? kf * kf : 1.0f - z;
                     dx[e] = G * (z * rs) * gate;
                     const float t = dx[e] * pair_at<S>(xr[f], e);
-                    dg[e] = t - t * gate;
+                    dg[e] = t * shut_of(eg, gate);
                     c[e] = decayed(kf, G);
                     // G i x a^2 / m = t a^2 / m^2
                     const float q = w[f][e] * (t * (a2 * (rs * rs)) - c[e] * h);
-                    const float s = w[f][e] * unrate[e];
-                    dr[e] = q * (0.69314718f - 0.69314718f * s);
+                    dr[e] = 0.69314718f * q * shut_of(er, w[f][e] * unrate[e]);
                     sum[e] += span.full || p.seg * FR + f < valid ? q : 0.0f;
                 }
                 xr[f] = pack_pair<S>(dx);  // the gradients take their inputs' places

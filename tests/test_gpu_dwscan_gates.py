@@ -1,5 +1,5 @@
-"""The recurrence where its decays are near 0, and its gates by themselves,
-against the definition in 64 bits.
+"""The recurrence where its factors are small: decays near 0, closed halves of
+the gates, and the gates themselves, against the definition in 64 bits.
 
 Tolerances count roundings of 2^-24 (U), as in test_gpu_dwscan.py, in sums that
 keep no term above what is left of it.  In float32 a gate is off by 8 U: its
@@ -88,6 +88,35 @@ def test_what_one_step_leaves(w):
     bound = U * (40 + 40 * rate * (1 + np.arange(T))[:, None]) * np.abs(left) + 1e-31  # 2^-126 of a million is where decays end
     assert (np.abs(h(y) - left) <= bound).all()
     assert (np.abs(h(last) - left[:, -1]) <= bound[:, -1]).all() and (np.abs(h(dh0) - left[:, -1]) <= bound[:, -1]).all()
+
+
+@pytest.mark.parametrize("dt,top", [(F32, 80.0), (F32, 20.0), (BF16, 20.0)], ids=["f32-80", "f32-20", "bf16-20"])
+@pytest.mark.parametrize("T", [1, 12, 130, 700])
+def test_the_closed_halves_of_gates_keep_their_digits(T, dt, top):
+    """Gates of both signs up to 20 and 80: 1 - sigmoid of down to 2e-35 scales their gradients."""
+    B, C = 2, 70
+
+    def gate(name):
+        v = datagen.uniform((B, T, C), 4.0, top, f"shut/{T}/{top}/{name}", device=DEV)
+        return (v * torch.sign(datagen.normal((B, T, C), 1.0, f"shut/{T}/{top}/{name}/sign", device=DEV))).to(dt)
+    n = lambda name: datagen.normal((B, T, C), 1.0, f"shut/{T}/{name}", device=DEV).to(dt)  # noqa: E731
+    s = dict(B=B, T=T, C=C, dt=dt, r=gate("r"), g=gate("g"), x=n("x"), dy=n("dy"), lengths=None,
+             decay=datagen.uniform((C,), -8.0, 0.0, "shut/decay", device=DEV))
+    s["h0"], s["dh_last"] = (datagen.normal((B, C), 1.0, f"shut/{k}", device=DEV) for k in ("h0", "dh"))
+    say("scan closed halves", T, dt, top)
+    check(s)
+
+
+def test_a_slow_channel_has_the_whole_gate():
+    """softplus(decay) = 1e-31: a rate that small is still w's own, and 1 - sigmoid(r) does not come from it."""
+    C = 64
+    r = datagen.uniform((1, 1, C), -3.0, 12.0, "slow/r", device=DEV)
+    one, decay = torch.ones((1, 1, C), device=DEV), torch.full((C,), -71.4, device=DEV)
+    h0 = torch.zeros((1, C), device=DEV)
+    y, _ = lib().dwscan_fwd(one, r, one, decay, h0=h0)
+    _, dr, _, _, _ = lib().dwscan_bwd(one, r, one, decay, y, one, h0=h0)
+    want = exact.scan_bwd(h(one), h(r), h(one), h(decay), h(y), h(one), None, h(h0))
+    within(dr, want["dr"], U * 144 * want["dr_size"], F32, "dr")
 
 
 def test_float_gates():
