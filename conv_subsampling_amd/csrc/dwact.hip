@@ -47,18 +47,23 @@ struct ActArgs {
     int32_t C;
 };
 
-// 1 / (1 + exp(-v)), kept below 2^-126 too, from where the activation's input lifts
-// it back into the range.  float: exp(-|v|), within a few units in the last place,
-// does not overflow.  bf16: the exponent is one rounded product (off by |v| 2^-24
-// of the result), the reciprocal is taken 2^24 higher.
+// open = 1 / (1 + exp(-v)) and shut = 1 - open, without cancellation.  The smaller of
+// them is kept below 2^-126 too, from where the activation's input lifts it back into the range.  float:
+// exp(-|v|), within a few units in the last place.  bf16: the exponent is one rounded product (off by |v|
+// 2^-24 of the result), and all is taken 2^24 higher.
+struct ActGate {
+    float open, shut;
+};
+
 template <typename S>
-__device__ __forceinline__ float tail_sigmoid(float v) {
+__device__ __forceinline__ ActGate act_gate(float v) {
     if constexpr (sizeof(S) == 4) {
         const float e = expf(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.0f + e);
-        return v < 0.0f ? e * r : r;
+        return {v < 0.0f ? e * r : r, v < 0.0f ? r : e * r};
     } else {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(v, -1.44269504f, -24.0f));
-        return __builtin_amdgcn_rcpf(0x1p-24f + e) * 0x1p-24f;
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(fabsf(v), -1.44269504f, 24.0f));
+        const float r = __builtin_amdgcn_rcpf(0x1p24f + e), less = e * r, more = r * 0x1p24f;
+        return {v < 0.0f ? less : more, v < 0.0f ? more : less};
     }
 }
 
@@ -186,7 +191,7 @@ __global__ __launch_bounds__(kActThreads) void act_fwd_kernel(const ActArgs a) {
             Vf<kGroup> o = v[0];
             if constexpr (ACT != 0) {
 #pragma unroll
-                for (int e = 0; e < kGroup; ++e) o.v[e] *= tail_sigmoid<S>(v[kParts - 1].v[e]);
+                for (int e = 0; e < kGroup; ++e) o.v[e] *= act_gate<S>(v[kParts - 1].v[e]).open;
             }
             store_group<S, TAIL>((S*)a.y + p[j].row * C, col, C, o);  // 0 past the length: x reads as 0 there
         }
@@ -226,9 +231,9 @@ __global__ __launch_bounds__(kActThreads) void act_bwd_kernel(const ActArgs a) {
         if constexpr (ACT == 1) {
 #pragma unroll
             for (int e = 0; e < kGroup; ++e) {
-                const float s = tail_sigmoid<S>(x.v[e]);
-                y.v[e] = x.v[e] * s;
-                dx.v[e] = dy.v[e] * (s + y.v[e] * (1.0f - s));
+                const ActGate s = act_gate<S>(x.v[e]);
+                y.v[e] = x.v[e] * s.open;
+                dx.v[e] = dy.v[e] * (s.open + y.v[e] * s.shut);
             }
         }
         if constexpr (ACT == 2) {
@@ -236,10 +241,10 @@ __global__ __launch_bounds__(kActThreads) void act_bwd_kernel(const ActArgs a) {
             Vf<kGroup> db;
 #pragma unroll
             for (int e = 0; e < kGroup; ++e) {
-                const float s = tail_sigmoid<S>(gate.v[e]);
-                y.v[e] = x.v[e] * s;
-                dx.v[e] = dy.v[e] * s;
-                db.v[e] = dx.v[e] * x.v[e] * (1.0f - s);
+                const ActGate s = act_gate<S>(gate.v[e]);
+                y.v[e] = x.v[e] * s.open;
+                dx.v[e] = dy.v[e] * s.open;
+                db.v[e] = dx.v[e] * x.v[e] * s.shut;
             }
             if (a.dx) store_group<S, TAIL>((S*)a.dx + p[j].row * W + C, col, C, db);
         }

@@ -1,4 +1,4 @@
-"""The recurrence in 64 bits, with sums of
+"""The recurrence and the kept activations' gradients in 64 bits, with sums of
 absolute terms that decay and vanish as the terms themselves do: every factor
 of a term, a, a^2 and both halves of a gate, is in its sum, so that an error in
 it counts in units of what is left of the term."""
@@ -64,3 +64,13 @@ def scan_bwd(x, r, g, decay, y, dy, lengths=None, h0=None, dh_last=None, scale=8
     o["dh0"], o["dh0_size"], o["dh0_bent"] = G, size, bent
     return o
 
+
+def act_grad(x, dy, kind):
+    """(dx, its sums of absolute terms)."""
+    if kind == "silu":
+        s, o = sigmoid(x), sigmoid(-x)
+        return dy * (s + x * s * o), np.abs(dy) * (s + np.abs(x) * s * o)
+    C = x.shape[-1] // 2
+    a, s, o = x[..., :C], sigmoid(x[..., C:]), sigmoid(-x[..., C:])
+    dx = np.concatenate([dy * s, dy * a * s * o], -1)
+    return dx, np.abs(dx)
