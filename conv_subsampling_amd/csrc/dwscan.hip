@@ -46,12 +46,13 @@ constexpr int kScanCols = kScanLanes * kScanPair;             // channels of a w
 constexpr int kScanRun = 8, kScanLongRun = 16;                // frames of a thread in a tile
 constexpr int kScanGroup = 16;                                // tiles whose composition is published too
 constexpr int kScanTicket = 32;                               // words from one chain's counter to the next: a cache line
-// Polls of a word, about a microsecond each.  A word that is read belongs to a
-// workgroup that has started and waits for nothing before it publishes, so it
-// comes within microseconds; only where the workspace is overwritten meanwhile
-// (two calls at once on one) does it not, and then the wait ends with a NaN.
-// Nothing is written outside the call's tensors then: tickets past the last tile
-// end their workgroups.
+// Polls of a lane for its words, about a microsecond each.  A word that is read
+// belongs to a workgroup that has started and waits for earlier ones alone, so it
+// comes within microseconds.  Only where the workspace is overwritten meanwhile
+// (two calls at once on one, which is not allowed) does it not: then the wait ends, a
+// ticket past the last tile ends its workgroup, and nothing is written outside the
+// call's tensors, but what is in them is undefined: NaN behind a wait that ended,
+// anything in tiles that no workgroup took and in the sums of ddecay over them.
 constexpr int kScanPolls = 1 << 16;
 
 struct ScanArgs {
