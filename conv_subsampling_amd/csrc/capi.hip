@@ -738,8 +738,8 @@ dw_status dwscan_fwd(const dw_scan* shape, const void* x, const void* r, const v
     if (!nonempty(s.B, s.C) || (s.T == 0 && !h_last)) return ok();
     if (!decay || (s.T > 0 && (!x || !r || !g || !y)))
         return fail(DW_ERR_INVALID_ARG, "%s: x, r, g, decay and y must not be NULL (unless empty)", fn);
-    if (s.T > 0 && (y == x || y == r || y == g)) return fail(DW_ERR_INVALID_ARG, "%s: y must not alias an input", fn);
-    if (among(h_last, {decay}) || (s.T > 0 && among(h_last, {x, r, g, y})))
+    if (s.T > 0 && among(y, {x, r, g, decay, lengths, h0})) return fail(DW_ERR_INVALID_ARG, "%s: y must not alias an input", fn);
+    if (among(h_last, {decay, lengths}) || (s.T > 0 && among(h_last, {x, r, g, y})))
         return fail(DW_ERR_INVALID_ARG, "%s: h_last must not alias y, nor an input but h0", fn);
     if (s.T > 0 && !frames_apart(s.y, s.B, s.T, s.C)) return fail(DW_ERR_INVALID_ARG, "%s: frames of y overlap", fn);
     const dw_status w = check_workspace(fn, workspace, workspace_bytes, dw::dwscan_fwd_workspace(s));
@@ -768,7 +768,7 @@ dw_status dwscan_bwd(const dw_scan* shape, const void* x, const void* r, const v
         if (!x || !r || !g || !y || !dy)
             return fail(DW_ERR_INVALID_ARG, "%s: x, r, g, y and dy must not be NULL (unless empty)", fn);
         for (const void* o : {(const void*)dx, (const void*)dr, (const void*)dg})
-            if (o && (o == x || o == r || o == g || o == y || o == dy))
+            if (among(o, {x, r, g, y, dy, decay, lengths, h0, dh_last}))
                 return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
         if ((dx && (dx == dr || dx == dg)) || (dr && dr == dg))
             return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
@@ -777,7 +777,7 @@ dw_status dwscan_bwd(const dw_scan* shape, const void* x, const void* r, const v
             return fail(DW_ERR_INVALID_ARG, "%s: frames of a gradient overlap", fn);
     }
     if (s.B > 0) {
-        if (among(ddecay, {decay, h0, dh_last}) || among(dh0, {decay, h0}) ||
+        if (among(ddecay, {decay, lengths, h0, dh_last}) || among(dh0, {decay, lengths, h0}) ||
             (s.T > 0 && (among(ddecay, {x, r, g, y, dy}) || among(dh0, {x, r, g, y, dy}))))
             return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias an input", fn);
         if (among(ddecay, {dh0}) || (s.T > 0 && (among(ddecay, {dx, dr, dg}) || among(dh0, {dx, dr, dg}))))
@@ -807,6 +807,9 @@ dw_status dwrope_fwd(const dw_rope* shape, const void* q, const void* k, const v
         return fail(DW_ERR_INVALID_ARG, "%s: k_out must not alias another tensor", fn);
     if (any_k && v && (v_out == v || v_out == k || (any_q && v_out == q)))
         return fail(DW_ERR_INVALID_ARG, "%s: v_out must not alias another tensor", fn);
+    for (const void* o : {any_q ? (const void*)q_out : nullptr, any_k ? (const void*)k_out : nullptr, any_k ? (const void*)v_out : nullptr})
+        if (among(o, {q_gamma, k_gamma, freq, lengths, pos, place}))
+            return fail(DW_ERR_INVALID_ARG, "%s: an output must not alias another tensor", fn);
     const int64_t rows = place ? s.S : s.T;
     if ((any_q && !heads_apart(shape->q_out, s.B, s.T, s.H, s.D)) || (any_k && !heads_apart(shape->k_out, s.B, rows, s.Hkv, s.D)) ||
         (any_k && v && !heads_apart(shape->v_out, s.B, rows, s.Hkv, s.D)))
@@ -846,6 +849,12 @@ dw_status dwrope_bwd(const dw_rope* shape, const void* q, const void* k, const v
         return fail(DW_ERR_INVALID_ARG, "%s: dk must not alias another tensor", fn);
     if ((any_q && dq && !heads_apart(shape->dq, s.B, s.T, s.H, s.D)) || (any_k && dk && !heads_apart(shape->dk, s.B, s.T, s.Hkv, s.D)))
         return fail(DW_ERR_INVALID_ARG, "%s: heads of a gradient overlap", fn);
+    for (const void* o : {any_q ? (const void*)dq : nullptr, any_k ? (const void*)dk : nullptr, (const void*)dq_gamma, (const void*)dk_gamma})
+        if (among(o, {q_gamma, k_gamma, freq, lengths, pos}))
+            return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias another tensor", fn);
+    for (const void* o : {(const void*)dq_gamma, (const void*)dk_gamma})
+        if ((any_q && among(o, {q, dq_out})) || (any_k && among(o, {k, dk_out})))
+            return fail(DW_ERR_INVALID_ARG, "%s: a gradient must not alias another tensor", fn);
     if (among(dq_gamma, {dk_gamma}) || (any_q && (among(dq_gamma, {dq}) || among(dk_gamma, {dq}))) ||
         (any_k && (among(dq_gamma, {dk}) || among(dk_gamma, {dk}))))
         return fail(DW_ERR_INVALID_ARG, "%s: the gradients must not alias each other", fn);
@@ -867,6 +876,8 @@ dw_status dwact_fwd(dw_act act, const void* x, const int32_t* lengths, void* y, 
     if (!nonempty(B, T, C) || (!y && !kept)) return ok();
     if (!x) return fail(DW_ERR_INVALID_ARG, "%s: x must not be NULL", fn);
     if (y == x && act == DW_ACT_GLU) return fail(DW_ERR_INVALID_ARG, "%s: y must not alias x", fn);
+    if (among(y, {lengths}) || among(kept, {lengths}) || among(codes, {lengths}))
+        return fail(DW_ERR_INVALID_ARG, "%s: an output must not alias another tensor", fn);
     if (kept && ((const void*)kept == x || (const void*)codes == x || kept == y || codes == y || (const void*)kept == (const void*)codes))
         return fail(DW_ERR_INVALID_ARG, "%s: kept and codes must not alias another tensor", fn);
     return from_hip(dw::launch_dwact_fwd((int)act, x, lengths, y, kept, codes, B, T, C, dtype == DW_BF16, (hipStream_t)stream), fn);
@@ -882,7 +893,7 @@ dw_status dwact_bwd(dw_act act, const int8_t* kept, const uint8_t* codes, const 
     if (dx && ((dx == dy && act == DW_ACT_GLU) || dx == y))
         return fail(DW_ERR_INVALID_ARG, "%s: dx must not alias y, nor dy with DW_ACT_GLU", fn);
     for (const void* o : {(const void*)dx, (const void*)y})
-        if (o && (o == (const void*)kept || o == (const void*)codes || (o == dy && o != dx)))
+        if (among(o, {kept, codes, lengths}) || (o && o == dy && o != dx))
             return fail(DW_ERR_INVALID_ARG, "%s: an output must not alias an input", fn);
     return from_hip(dw::launch_dwact_bwd((int)act, kept, codes, lengths, dy, dx, y, B, T, C, dtype == DW_BF16, (hipStream_t)stream), fn);
 }

@@ -112,3 +112,53 @@ def test_gammas_gradients_that_alias(lib):  # noqa: F811
 
 def test_far_distances_do_not_wrap(lib):  # noqa: F811
     assert scan_bwd(lib, scan(B=3, T=600, strides=[4800, 8] * 5 + [1 << 58, 8] * 3)) == UNSUPPORTED
+
+
+def test_outputs_in_a_small_operand(lib):  # noqa: F811
+    """decay, lengths, states, weights, frequencies, positions: no output starts where one of them does."""
+    long = scan(B=2, T=600, strides=[4800, 8] * 8)
+    names = ["x", "r", "g", "decay", "lengths", "h0", "y", "h_last"]
+
+    def fwd(**kw):
+        given = dict(zip(names, A)) | kw
+        return lib.dwscan_fwd(long, *[given[k] for k in names], N, 0, N)
+    assert fwd() == WORKSPACE and fwd(h_last=A[5]) == WORKSPACE
+    for k in ("decay", "lengths", "h0"):
+        assert fwd(y=A[names.index(k)]) == INVALID and "alias" in err(lib), k
+    for k in ("decay", "lengths", "y"):
+        assert fwd(h_last=A[names.index(k)]) == INVALID and "alias" in err(lib), k
+
+    back = ["x", "r", "g", "decay", "lengths", "h0", "y", "dy", "dh_last", "dx", "dr", "dg", "ddecay", "dh0"]
+
+    def bwd(**kw):
+        given = dict(zip(back, A)) | kw
+        return lib.dwscan_bwd(long, *[given[k] for k in back], N, 0, N)
+    assert bwd() == WORKSPACE and bwd(dh0=A[8]) == WORKSPACE
+    for o in ("dx", "dr", "dg", "ddecay", "dh0"):
+        for k in ("decay", "lengths", "h0", "dh_last"):
+            if (o, k) != ("dh0", "dh_last"):
+                assert bwd(**{o: A[back.index(k)]}) == INVALID and "alias" in err(lib), (o, k)
+
+    heads = ["q", "k", "v", "q_gamma", "k_gamma", "freq", "lengths", "pos", "place", "q_out", "k_out", "v_out"]
+    for o in ("q_out", "k_out", "v_out"):  # the forward has no workspace to end at: refusals alone
+        for k in ("q_gamma", "k_gamma", "freq", "lengths", "pos", "place"):
+            given = dict(zip(heads, A)) | {o: A[heads.index(k)]}
+            got = lib.dwrope_fwd(rope(H=4, Hkv=4, strides=[320, 64, 16] * 8), *[given[n] for n in heads], N)
+            assert got == INVALID and "alias" in err(lib), (o, k)
+
+    hback = ["q", "k", "q_gamma", "k_gamma", "freq", "lengths", "pos", "dq_out", "dk_out", "dq", "dk", "dq_gamma", "dk_gamma"]
+
+    def heads_bwd(**kw):
+        given = dict(zip(hback, A)) | kw
+        return lib.dwrope_bwd(rope(H=4, Hkv=4, strides=[320, 64, 16] * 8), *[given[k] for k in hback], N, 0, N)
+    assert heads_bwd() == WORKSPACE and heads_bwd(dq=A[7], dk=A[8]) == WORKSPACE and heads_bwd(dq=A[0], dk=A[1]) == WORKSPACE
+    for o in ("dq", "dk", "dq_gamma", "dk_gamma"):
+        for k in ("q_gamma", "k_gamma", "freq", "lengths", "pos") + (("q", "k", "dq_out", "dk_out") if "gamma" in o else ()):
+            assert heads_bwd(**{o: A[hback.index(k)]}) == INVALID and "alias" in err(lib), (o, k)
+
+    for o in range(3):  # y, kept, codes
+        out = [A[2 + j] if j != o else A[1] for j in range(3)]
+        assert lib.dwact_fwd(1, A[0], A[1], *out, 2, 3, 8, 0, N) == INVALID and "alias" in err(lib)
+    for o in range(2):  # dx, y
+        out = [A[4 + j] if j != o else A[2] for j in range(2)]
+        assert lib.dwact_bwd(1, A[0], A[1], A[2], A[3], *out, 2, 3, 8, 0, N) == INVALID and "alias" in err(lib)
