@@ -10,7 +10,7 @@
 // Bound by memory.  With lengths of half to all of the frames: [16,750,2 x 1024]
 // bf16 GLU forward with the checkpoint 19 us and gradients 18 us for 87 MB each (37
 // together, 4.7 TB/s; a large copy reaches 5.1); [16,750,4096] SiLU gradients and
-// activation 63 us for 311 MB (4.9 TB/s).  17 to 29 vector operations an element
+// activation 62 us for 311 MB (5.0 TB/s).  19 to 33 vector operations an element
 // take half to two thirds of that time in issue slots, beside it.
 #include "launch.h"
 #include "rowops.h"

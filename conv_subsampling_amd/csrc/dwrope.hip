@@ -11,12 +11,12 @@
 // turns, reduced in 64 bits, then a float polynomial on [-1, 1].
 //
 // Bound by memory.  12000 frames of 8 + 8 heads of 128 in bf16: forward 86.8 MB in
-// 18.7 us (4.6 TB/s; a large copy reaches 5.1), about 19 vector operations an element,
+// 18.6 us (4.7 TB/s; a large copy reaches 5.1), about 19 vector operations an element,
 // which take 9 us of issue slots; gradients 124.5 MB in 29 us and 4 us for the
 // sum of the gammas' partial rows, 32 together.  Two heads of both tensors in
 // flight (134 registers, three waves a SIMD, so all workgroups at once); with four
 // 40 us, with one 33, with the next two read ahead 33.  One frame of 64 items
-// takes 11.6 us, which is the host's call and launch: the kernel is 6, a chain of
+// takes 11.5 us, which is the host's call and launch: the kernel is 6, a chain of
 // loads, the angle's 64-bit reduction and two sums across a team.
 #include "launch.h"
 #include "rowops.h"
@@ -26,7 +26,11 @@ namespace dw {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeFly = 4;                 // heads whose loads are in flight together
-constexpr int64_t kRopeBwdBlocks = 1024;    // workgroups (and partial rows) of the backward at most
+// Workgroups (and partial rows) of the backward at most.  8 + 8 heads of 128 in bf16, us
+// with at most 768, 1024 and 2048: 12000 frames 34.3, 34.2, 34.4, 16000 44.1, 48.7, 48.8,
+// 22000 55.0, 55.0, 58.7, 32000 84.1, 91.2, 84.9: 768 are in flight together, and 769 to
+// 1024 in one turn run a round and a rest.
+constexpr int64_t kRopeBwdBlocks = 1024;
 
 struct RopeStride {
     int64_t item, frame, head;
@@ -50,9 +54,9 @@ struct RopeArgs {
 // neighbouring elements, so vector accesses serve it: halves, the pairs' firsts
 // and their seconds (a lane that is not rotated pairs the two quads of its 8
 // elements in a row); neighbours, 8 elements in a row.  kTail: the head may end
-// inside a quad (gradients of [9,1197,32+8 heads of 50] bf16, neighbours, 58 us;
+// inside a quad (gradients of [9,1197,32+8 heads of 50] bf16, neighbours, 59 us;
 // 144 element by element).  kLoose: each element has a place of its own, D standing
-// for none.
+// for none (heads of 50 turned whole, halves: 177 us; [16,750,8+8 heads of 44] 38 and 68).
 constexpr int kLoose = 0, kWhole = 1, kTail = 2;
 
 template <int PACKED, bool HALVES>
@@ -453,10 +457,12 @@ __global__ __launch_bounds__(kGammaCols* kGammaRows) void rope_gamma_reduce(cons
 static int rope_lanes(int64_t D) { return D <= 32 ? 4 : D <= 64 ? 8 : 16; }
 
 // Teams that share a frame's heads: one where the frames alone fill the GPU
-// (its cosines then serve all heads), else as many as there are heads.  12000
-// frames of 8 + 8 heads of 128 in bf16 (192000 lanes), 1 and 2 teams a frame, us:
-// forward 19.7 and 18.7, gradients 31.8 and 38.4 (750 workgroups are in flight
-// together, 1500 are not).
+// (its cosines then serve all heads), else as many as there are heads.  8 + 8 heads of
+// 128, 1 and 2 teams a frame, and this rule, us: bf16 4000 frames 11.3, 10.5 and 14.7,
+// 8000 14.1, 13.9 and 15.9, 12000 18.4, 18.5 and 18.5 (float 16.5, 13.4 and 14.4, 28.8, 22.6 and
+// 22.5, 43.3, 34.4 and 34.6), gradients 4000 20.3, 20.7 and 21.8, 8000 25.5, 27.9 and 28.1,
+// 12000 34.3, 35.9 and 34.2 (750 workgroups are in flight together, 1500 are not).
+// One team loses in float forward, several in bf16 at 4000 and 8000 frames.
 static int64_t rope_split(const RopeShape& s, bool backward) {
     const int64_t heads = s.H > s.Hkv ? s.H : s.Hkv, lanes = s.B * s.T * rope_lanes(s.D);
     const int64_t enough = backward ? 128 * 1024 : 256 * 1024;

@@ -25,13 +25,13 @@
 // workgroup that has started, and that one waits for earlier ones alone.
 //
 // Bound by memory in float, by memory and vector operations side by side in bf16
-// (about 45 operations an element, 6 of them transcendental, 80 in the gradients;
+// (about 50 operations an element, 6 of them transcendental, 95 in the gradients;
 // lengths of half to all):
-// bf16 [16,750,1024] 81 MB in 25.6 us a call, 14 of them issue slots (3.2 TB/s; a
+// bf16 [16,750,1024] 81 MB in 26.9 us a call, 15 of them issue slots (3.0 TB/s; a
 // large copy reaches 5.1, the loads and stores alone take 18 us), float [2,6001,512]
-// 89 MB in 22.0 (4.0 TB/s), all of [32,1500,512] 393 MB in 85.6 (4.6 TB/s).  Gradients
-// bf16 [16,750,1024] 168 MB in 49.3 (3.4 TB/s, 21 us of issue slots), float
-// [32,1500,512] 787 MB in 166 (4.7 TB/s).  One frame of 64 items takes 8.8 us, which is
+// 89 MB in 23.5 (3.8 TB/s), all of [32,1500,512] 393 MB in 86.2 (4.6 TB/s).  Gradients
+// bf16 [16,750,1024] 168 MB in 51.0 (3.3 TB/s, 25 us of issue slots), float
+// [32,1500,512] 787 MB in 170 (4.6 TB/s).  One frame of 64 items takes 8.7 us, which is
 // the host's call; the kernel is 3.5.
 #include "launch.h"
 #include "rowops.h"
@@ -92,10 +92,10 @@ using pair_raw = typename PairRaw<S>::type;
 
 // have: channels from p on; TAIL: it may be one.  STREAM: read without claiming a
 // place in the caches.  The gradients read so what a training step reads for the
-// last time, us without and with: bf16 [32,1500,512] 115.9 and 107.2, float 185.5
-// and 170.2, between the kernels that write dy and read their results 183.5 and
-// 172.1, 334.1 and 308.7; the forward loses by it (52.4 and 52.6, [16,750,1024]
-// 30.0 and 31.5).
+// last time, us without and with: bf16 [32,1500,512] 113.5 and 108.1, float 186.0
+// and 176.2, between the kernels that write dy and read their results 184.9 and
+// 178.2, 412.7 and 372.6.  The forward loses by it in bf16 ([16,750,1024] 29.0 and
+// 31.8, [32,1500,512] 55.5 and 55.6; float 43.4 and 43.1, 86.1 and 77.6).
 template <typename S, bool TAIL, bool STREAM>
 __device__ __forceinline__ pair_raw<S> load_pair(const S* p, int have) {
     typedef typename PairRaw<S>::access access;
@@ -596,9 +596,10 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanArgs a
 // the frames before them.
 // ---------------------------------------------------------------------------
 //
-// Waves that share a SIMD at least: linked tiles 3 (168 registers; bf16
-// [16,750,1024] 57.4 us against 59.3 with 4, [2,6001,512] 37.4 and 39.3, float 85.1
-// against 86.6 with 2, [8,375,1024] 26.7 and 32.2), in turn 2.
+// Waves that share a SIMD at least: linked tiles 3 (168 registers; bf16 takes 135,
+// [16,750,1024] 58.9 us against 61.1 with 4, [2,6001,512] 39.0 and 40.9; float spills 7,
+// and 86.5 against 90.2 with 2, [8,375,1024] 28.4 and 33.2, [2,6001,512] 55.1 and 53.3), in
+// turn 2 (bf16 176 registers, 180 us for [16,1500,2048] against 182 with 3; float 217).
 constexpr int scan_bwd_waves(bool linked) { return linked ? 3 : 2; }
 
 template <typename S, bool TAIL, int SEGS, int FR, bool LINKED>
@@ -613,7 +614,7 @@ __global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd
     begin_scan<LINKED>(a, p, shared);
     pair_raw<S> rr[FR], dyr[FR], xr[FR], gr[FR], prev[FR];
     // A step by itself, which the compiler does not join with what is made of them: in
-    // turn [16,1500,2048] bf16 169 us and 175, [64,200,256] float 33.5 and 35.0.
+    // turn bf16 [16,1500,2048] 180 us and 182, [64,200,512] 36.6 and 37.2, float alike.
     const auto load = [&](const TileSpan& s) {
         if (s.valid <= 0) return;
         load_run<S, TAIL, true, FR>(rr, a.r, a.rs, p, s.t0, s.valid, s.full);
@@ -675,7 +676,8 @@ __global__ __launch_bounds__(kScanThreads, scan_bwd_waves(LINKED)) void scan_bwd
                 for (int e = 0; e < kScanPair; ++e) {
                     const float G = pair_at<S>(dyr[f], e) + c[e];
                     const float eg = exp_minus<S>(pair_at<S>(gr[f], e)), gate = sigmoid_of(eg);
-                    // again, rather than kept: float gradients [32,1500,512] 168 us, 176 with it in registers
+                    // again, rather than kept: float [32,1500,512] linked 168 us, 176 with it in registers
+                    // ([16,750,1024] 88 and 94; in turn [16,1500,2048] 331 and 330, bf16 181 and 180)
                     const float er = exp_minus<S>(pair_at<S>(rr[f], e));
                     const float h = f == 0 && start ? h0[e] : pair_at<S>(prev[f], e);
                     const float kf = k[f][e], z = lost_power(kf);                           // 1 - a^2 = m^2
@@ -736,19 +738,24 @@ struct ScanPlan {
 // two waves a SIMD) make one tile of up to 128 frames, and in longer sequences
 // halve the words that a tile reads of those before it; with 8, sequences waste
 // less where they end.  us for 16 and 8: bf16 [16,750,1024] with lengths of half
-// to all 28.8 and 26.8, [64,750,256] 29.6 and 28.2, [2,6001,512] 19.9 and 20.2,
-// float 23.0 and 25.6, [1,20000,512] bf16 31.2 and 29.5, float 42.0 and 44.4.
+// to all 29.3 and 27.0, [64,750,256] 29.0 and 27.3.  Two sequences of 512 channels, all
+// valid: 1000 to 2000 frames alike (14.1), 4000 bf16 16.7 and 14.8, float 19.9 and 18.9,
+// 6001 20.5 and 20.1, 23.8 and 25.6, one of 20000 32.0 and 29.9, 43.3 and 44.6; with
+// lengths 6001 19.5 and 20.1, 22.6 and 24.4, 20000 in its first half 23.1 and 23.3, 26.6 and
+// 28.4.  One bound serves both types: float gains by it from 6000 frames on, bf16 does
+// not, and around 4000 both lose a microsecond or two.
 //
-// Linked or in turn, us: 256 chains, [16,750,1024] bf16 30 and 32, float 42 and 53;
-// 512 chains, [16,1500,2048] bf16 100 and 95, float 163 and 155, [32,130,1024] 17
-// and 15.  Gradients: [16,1500,2048] bf16 191 and 170, float 334 and 325,
-// [32,130,1024] 31 and 27.  One chain a CU, all of one length, does better in turn
-// (bf16 [16,750,1024] 59 and 56, float 85 and 80), but not with lengths of half to
-// all (51 and 53), nor do a few more chains (320, [20,750,1024], 70 and 83, float
-// 102 and 119) or fewer (192, [24,1500,512], 85 and 99).
+// Linked or in turn, us: 256 chains, [16,750,1024] bf16 31 and 35, float 44 and 57;
+// 512 chains, [16,1500,2048] bf16 102 and 100, float 164 and 158, [32,330,1024] 28 and
+// 26.  Gradients: [16,1500,2048] bf16 190 and 181, float 337 and 330, [32,330,1024] 55
+// and 52.  One chain a CU, all of one length, is near in turn (bf16 [16,750,1024] 58.9 and
+// 59.3, float 87.4 and 86.5), but not with lengths of half to all (51 and 57), nor are
+// a few more chains (320, [20,750,1024], 69 and 90, float 104 and 127) or fewer (192,
+// [24,1500,512], 84 and 105).
 // Up to 4 tiles in turn save the launch that clears the words: calls of [8,256,512]
-// bf16 15.6 and 11.1, [1,200,64] 15.1 and 10.7 (gradients 23.3 and 20.5), where 5 to
-// 8 tiles cost more than it: [4,500,1024] bf16 15.6 and 20.9.
+// bf16 14.9 and 11.2, [1,200,64] 15.0 and 11.1 (gradients 23.2 and 22.0, 23.1 and 21.0);
+// float [8,256,512] loses by it (15.2 and 16.4, gradients 23.8 and 27.9), [1,200,64] does
+// not (15.0 and 13.4, 23.3 and 24.1).
 static ScanPlan scan_plan(const ScanShape& s, bool backward) {
     ScanPlan p = {};
     const int64_t one = kScanRows * kScanRun;
