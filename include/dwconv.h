@@ -684,7 +684,9 @@ size_t dwscan_fwd_workspace_bytes(const dw_scan *shape);
  * decay: [C] float; h0, h_last: [B][C] float, dense.  The state, the gates, and
  * 1 - a or a, whichever is below 1/2 (neither taken by cancellation), are float32
  * whatever the storage type; decays below 2^-126 are 0, and y is rounded once.  A
- * state that overflows is an infinity or a NaN for the rest of its item.
+ * gate is within 8 * 2^-24 of itself with float32 tensors, |r| (|g|) * 2^-24 more
+ * with bfloat16 ones.  A state that overflows is an infinity or a NaN for the rest
+ * of its item.
  * Repeated calls agree bit for bit.  The workspace serves one call at a time:
  * calls that may overlap (on two streams, or captured into graphs that may) take
  * one each; with one between them, what they write is undefined, and no error tells.
